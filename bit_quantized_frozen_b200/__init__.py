@@ -12,6 +12,7 @@ The layer (SquareQ README, section "SquareQ v3 -- W4"):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -45,6 +46,11 @@ SQ_STAGE_ACT_QUANT = 2
 SQ_CHECK_FINITE = 0x10
 SQ_OP_LINEAR_BWD_DX = 9
 SQ_OP_SVD_INIT = 10
+SQ_OP_LINEAR_FWD_W8A8 = 11
+SQ_OP_LINEAR_BWD_DX_W8A8 = 12
+SQ_OP_GROUPED_FWD_W8A8 = 13
+SQ_OP_GROUPED_BWD_DX_W8A8 = 14
+SQ_ZERO_UNGROUPED = 0x20
 RANK = 32
 
 EXPORTED = [
@@ -53,6 +59,8 @@ EXPORTED = [
     "sq_reconstruct_bf16",
     "sq_check_device_status", "sq_set_gemm_events", "sq_set_stage_events", "sq_linear_fwd_noalloc", "sq_linear_bwd_dx",
     "sq_selftest_wait_timeout", "sq_svd_init",
+    "sq_linear_fwd_w8a8", "sq_linear_bwd_dx_w8a8", "sq_grouped_fwd_w8a8", "sq_grouped_bwd_dx_w8a8",
+    "sq_grouped_workspace_bytes",
 ]
 
 
@@ -101,6 +109,15 @@ _SIGS = {
                                ctypes.POINTER(ctypes.c_void_p), _P], ctypes.c_int),
     "sq_reconstruct_bf16": ([ctypes.POINTER(sq_weight), _P, ctypes.c_uint32, _P], ctypes.c_int),
     "sq_linear_bwd_dx": ([ctypes.POINTER(sq_weight), _P, _I64, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "sq_linear_fwd_w8a8": ([ctypes.POINTER(sq_weight), _P, _I64, _P, ctypes.c_uint32, _P, ctypes.c_size_t, _P],
+                           ctypes.c_int),
+    "sq_linear_bwd_dx_w8a8": ([ctypes.POINTER(sq_weight), _P, _I64, _P, ctypes.c_uint32, _P, ctypes.c_size_t, _P],
+                              ctypes.c_int),
+    "sq_grouped_fwd_w8a8": ([ctypes.POINTER(sq_weight), _I64, _P, _I64, _P, _P, ctypes.c_uint32, _P,
+                             ctypes.c_size_t, _P], ctypes.c_int),
+    "sq_grouped_bwd_dx_w8a8": ([ctypes.POINTER(sq_weight), _I64, _P, _I64, _P, _P, ctypes.c_uint32, _P,
+                                ctypes.c_size_t, _P], ctypes.c_int),
+    "sq_grouped_workspace_bytes": ([ctypes.c_int, _I64, _I64, _I64, _I64], ctypes.c_size_t),
     "sq_check_device_status": ([_P, _P], ctypes.c_int),
     "sq_selftest_wait_timeout": ([_P, ctypes.c_uint32, _P], ctypes.c_int),
     "sq_set_gemm_events": ([_P, _P], ctypes.c_int),
@@ -314,6 +331,63 @@ def sq_linear_bwd_dx(w: "Weight", dy, dx, ws, stream=None):
                                                       _numel_bytes(ws), _stream(stream)))
 
 
+def _rows(fn: str, name: str, t, width: int):
+    """A bf16 matrix [M, width] on the current device."""
+    if t.dim() != 2 or t.shape[1] != width or t.dtype != torch.bfloat16:
+        raise ValueError(f"{fn}: {name} must be bfloat16 [M, {width}], got {t.dtype} {list(t.shape)}")
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{fn}: {name} is on {t.device}, the current device is {torch.cuda.current_device()}")
+    return t.shape[0]
+
+
+def _w8a8(fn: str, w, x, y, flags, ws, stream, backward: bool, offsets=None):
+    """Checks and call of the four 8-bit integer products; w: a Weight, or a GroupedWeight with offsets."""
+    if w.fmt != SQ_FMT_INT8_ROW:
+        raise ValueError(f"{fn}: the weight must be SQ_FMT_INT8_ROW")
+    N, K, E = int(w.N), int(w.K), getattr(w, "E", None)
+    wide, out = (N, K) if backward else (K, N)
+    xn, yn = ("dy", "dx") if backward else ("x", "y")
+    M = _rows(fn, xn, x, wide)
+    experts = 1 if E is None else E
+    _need(fn, "codes", w.codes, experts * N * K)
+    _need(fn, "scales", w.scales, 4 * experts * N)
+    _need(fn, "lora_up", w.lora_up, 2 * experts * N * RANK_INT8)
+    _need(fn, "lora_down", w.lora_down, 2 * experts * K * RANK_INT8)
+    _need(fn, yn, y, M * out * (2 if flags & SQ_OUT_BF16 else 4))
+    if y.dtype != (torch.bfloat16 if flags & SQ_OUT_BF16 else torch.float32):
+        raise ValueError(f"{fn}: {yn} is {y.dtype}, the flags ask for the other type")
+    grouped = ()
+    if E is not None:
+        if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] != E + 1:
+            raise ValueError(f"{fn}: offsets must be int32 [{E + 1}], got {offsets.dtype} {list(offsets.shape)}")
+        if M == 0:
+            return
+        grouped = (_ptr(offsets),)
+    cw = w.as_c()
+    _check(fn, getattr(lib(), fn)(ctypes.byref(cw), *(() if E is None else (E,)), _ptr(x), M, *grouped, _ptr(y), flags,
+                                  _ptr(ws), 0 if ws is None else _numel_bytes(ws), _stream(stream)))
+
+
+def sq_linear_fwd_w8a8(w: "Weight", x, y, flags: int = 0, ws=None, stream=None):
+    _w8a8("sq_linear_fwd_w8a8", w, x, y, flags, ws, stream, False)
+
+
+def sq_linear_bwd_dx_w8a8(w: "Weight", dy, dx, flags: int = 0, ws=None, stream=None):
+    _w8a8("sq_linear_bwd_dx_w8a8", w, dy, dx, flags, ws, stream, True)
+
+
+def sq_grouped_fwd_w8a8(w: "GroupedWeight", x, offsets, y, flags: int = 0, ws=None, stream=None):
+    _w8a8("sq_grouped_fwd_w8a8", w, x, y, flags, ws, stream, False, offsets)
+
+
+def sq_grouped_bwd_dx_w8a8(w: "GroupedWeight", dy, offsets, dx, flags: int = 0, ws=None, stream=None):
+    _w8a8("sq_grouped_bwd_dx_w8a8", w, dy, dx, flags, ws, stream, True, offsets)
+
+
+def sq_grouped_workspace_bytes(op: int, E: int, M: int, N: int, K: int) -> int:
+    return lib().sq_grouped_workspace_bytes(op, E, M, N, K)
+
+
 def sq_debug_checks() -> int:
     """1 if the loaded library was built with the device-side index checks (libsq_debug.so)."""
     return lib().sq_debug_checks()
@@ -368,6 +442,29 @@ class Weight:
     def as_c(self) -> sq_weight:
         return sq_weight(self.fmt, self.N, self.K, _ptr(self.codes), _ptr(self.scales), _ptr(self.g_w),
                          _ptr(self.lora_up), _ptr(self.lora_down))
+
+
+@dataclass
+class GroupedWeight:
+    """E int8 per-row weights of the same shape, one per expert."""
+    E: int
+    N: int
+    K: int
+    codes: torch.Tensor                  # int8 [E, N, K]
+    scales: torch.Tensor                 # float32 [E, N]
+    lora_up: torch.Tensor | None = None  # bf16 [E, N, 16]
+    lora_down: torch.Tensor | None = None  # bf16 [E, K, 16]
+    fmt: int = SQ_FMT_INT8_ROW
+
+    def as_c(self) -> sq_weight:
+        return sq_weight(self.fmt, self.N, self.K, _ptr(self.codes), _ptr(self.scales), None,
+                         _ptr(self.lora_up), _ptr(self.lora_down))
+
+    def expert(self, e: int) -> Weight:
+        """The weight of one expert (views of the same memory)."""
+        pick = lambda t: None if t is None else t[e]  # noqa: E731
+        return Weight(self.fmt, self.N, self.K, self.codes[e], self.scales[e], None, pick(self.lora_up),
+                      pick(self.lora_down))
 
 
 def workspace(op: int, M: int, N: int, K: int, device=None) -> torch.Tensor:
@@ -449,3 +546,63 @@ def linear_bwd_dx(w: Weight, dy: torch.Tensor, ws=None, stream=None) -> torch.Te
     ws = ws if ws is not None else workspace(SQ_OP_LINEAR_BWD_DX, M, w.N, w.K, dy.device)
     sq_linear_bwd_dx(w, dy, dx, ws, stream=stream)
     return dx
+
+
+def build_int8_grouped(R: torch.Tensor, lora_up=None, lora_down=None, stream=None) -> GroupedWeight:
+    """int8 per-row weights of E experts from their residuals R [E, N, K] fp32; lora_up [E, N, 16] /
+    lora_down [E, K, 16] or None."""
+    E, N, K = R.shape
+    codes = torch.empty((E, N, K), dtype=torch.int8, device=R.device)
+    scales = torch.empty((E, N), dtype=torch.float32, device=R.device)
+    for e in range(E):
+        sq_build_int8(R[e], codes[e], scales[e], None, stream=stream)
+    return GroupedWeight(E, N, K, codes, scales, lora_up, lora_down)
+
+
+def _allocating_on(stream):
+    """Context in which a call's own tensors belong to the stream it runs on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
+def _w8a8_out(fn, op, w, x, offsets, width, ws, flags, out_bf16, stream):
+    if out_bf16:
+        flags |= SQ_OUT_BF16
+    M, E = x.shape[0], getattr(w, "E", None)
+    with _allocating_on(stream):
+        y = torch.empty((M, width), dtype=torch.bfloat16 if flags & SQ_OUT_BF16 else torch.float32, device=x.device)
+        if ws is None:
+            n = (sq_workspace_bytes(op, M, w.N, w.K) if E is None
+                 else sq_grouped_workspace_bytes(op, E, M, w.N, w.K))
+            ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+        if E is None:
+            fn(w, x, y, flags=flags, ws=ws, stream=stream)
+        else:
+            fn(w, x, offsets, y, flags=flags | SQ_ZERO_UNGROUPED, ws=ws, stream=stream)
+    return y
+
+
+def linear_fwd_w8a8(w: Weight, x: torch.Tensor, ws=None, flags: int = 0, out_bf16: bool = False,
+                    stream=None) -> torch.Tensor:
+    """y [M, N] = x W^T in 8-bit integers (int8 weight, int8 codes per token), fp32 or bf16."""
+    return _w8a8_out(sq_linear_fwd_w8a8, SQ_OP_LINEAR_FWD_W8A8, w, x, None, w.N, ws, flags, out_bf16, stream)
+
+
+def linear_bwd_dx_w8a8(w: Weight, dy: torch.Tensor, ws=None, flags: int = 0, out_bf16: bool = False,
+                       stream=None) -> torch.Tensor:
+    """dx [M, K] = dy W in 8-bit integers, fp32 or bf16."""
+    return _w8a8_out(sq_linear_bwd_dx_w8a8, SQ_OP_LINEAR_BWD_DX_W8A8, w, dy, None, w.K, ws, flags, out_bf16, stream)
+
+
+def grouped_fwd_w8a8(w: GroupedWeight, x: torch.Tensor, offsets: torch.Tensor, ws=None, flags: int = 0,
+                     out_bf16: bool = False, stream=None) -> torch.Tensor:
+    """y [M, N]: rows offsets[e] .. offsets[e + 1] - 1 of x times expert e's W^T; rows of no expert are 0."""
+    return _w8a8_out(sq_grouped_fwd_w8a8, SQ_OP_GROUPED_FWD_W8A8, w, x, offsets, w.N, ws, flags, out_bf16, stream)
+
+
+def grouped_bwd_dx_w8a8(w: GroupedWeight, dy: torch.Tensor, offsets: torch.Tensor, ws=None, flags: int = 0,
+                        out_bf16: bool = False, stream=None) -> torch.Tensor:
+    """dx [M, K]: rows offsets[e] .. offsets[e + 1] - 1 of dy times expert e's W; rows of no expert are 0."""
+    return _w8a8_out(sq_grouped_bwd_dx_w8a8, SQ_OP_GROUPED_BWD_DX_W8A8, w, dy, offsets, w.K, ws, flags, out_bf16,
+                     stream)

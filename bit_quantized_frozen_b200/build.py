@@ -13,7 +13,7 @@ LIB = os.path.join(PKG, "libsq.so")
 # the same library with the device-side index checks on (-DSQ_DEBUG_CHECKS): every checked store
 # tests its index against its buffer, skips it when outside and reports SQ_ERR_INDEX
 LIB_DEBUG = os.path.join(PKG, "libsq_debug.so")
-SOURCES = ["sq_api.cu", "sq_quant.cu", "sq_gemm.cu", "sq_svd.cu"]
+SOURCES = ["sq_api.cu", "sq_quant.cu", "sq_gemm.cu", "sq_svd.cu", "sq_w8a8_quant.cu", "sq_w8a8.cu"]
 HEADERS = ["sq_device.cuh", "sq_ptx.cuh", "sq_kernels.h"]
 
 NVCC_FLAGS = [

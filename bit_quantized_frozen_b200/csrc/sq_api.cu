@@ -200,6 +200,34 @@ FwdLayout fwd_layout(int fmt, int64_t M, int64_t N, int64_t K)
     return L;
 }
 
+// 8-bit integer products: header, the product's counters, the row operand (codes, scales,
+// low-rank input) and the partial sums of split tiles
+struct I8Layout {
+    size_t counters = 0, codes = 0, scales = 0, low = 0, slabs = 0, total = 0;
+};
+
+I8Layout i8_layout(bool bwd, int E, int64_t M, int64_t N, int64_t K)
+{
+    I8Layout L;
+    size_t off = kHeader;
+    auto take = [&](size_t bytes) {
+        off = round_up(off, kAlign);
+        size_t at = off;
+        off += bytes;
+        return at;
+    };
+    L.counters = take((size_t)sq::kI8Counters * 4);
+    L.codes = take((size_t)M * (size_t)(bwd ? N : K));
+    L.scales = take((size_t)M * 4);
+    L.low = take((size_t)M * 16 * 4);
+    L.slabs = take(sq::i8_slab_bytes(bwd, E, M, N, K));
+    L.total = round_up(off, kAlign);
+    return L;
+}
+
+constexpr int64_t kMaxExperts = 1024;
+constexpr int64_t kMaxSumI8 = int64_t(1) << 17;   // 127 * 128 * 2^17 < 2^31: the 32-bit sums are exact
+
 uint8_t *ws_at(void *ws, size_t off)
 {
     return reinterpret_cast<uint8_t *>(ws) + off;
@@ -246,6 +274,88 @@ sq_status check_weight(const sq_weight *w)
     if (!aligned(w->codes, 16) || !aligned(w->scales, 16) || !aligned(w->g_w, 4) ||
         !aligned(w->lora_up, 16) || !aligned(w->lora_down, 16))
         return SQ_ERR_ALIGN;
+    return SQ_OK;
+}
+
+// The integer products, forward and backward, dense (E == 0) and grouped.
+sq_status i8_product(bool bwd, int64_t E, const sq_weight *w, const uint16_t *x, int64_t M, const int32_t *offsets,
+                     void *y, uint32_t flags, void *ws, size_t ws_bytes, void *stream)
+{
+    sq_status st = check_weight(w);
+    if (st != SQ_OK)
+        return st;
+    if (w->fmt != SQ_FMT_INT8_ROW || (flags & ~(SQ_OUT_BF16 | SQ_CHECK_FINITE | (E > 0 ? SQ_ZERO_UNGROUPED : 0u))))
+        return SQ_ERR_ARG;
+    if ((w->lora_up == nullptr) != (w->lora_down == nullptr))
+        return SQ_ERR_NULL;
+    const int64_t N = w->N, K = w->K;
+    if (M < 0 || M > kMaxM || (E == 0 && M == 0) || (bwd && N > kMaxSumI8))
+        return SQ_ERR_SHAPE;
+    if (E > 0 && !offsets)
+        return SQ_ERR_NULL;
+    if (E > 0 && M == 0)                              // no rows: nothing to do
+        return SQ_OK;
+    if (!x || !y || !ws)
+        return SQ_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(y, 16) || !aligned(offsets, 4) || !aligned(ws, 256))
+        return SQ_ERR_ALIGN;
+    const I8Layout L = i8_layout(bwd, (int)E, M, N, K);
+    if (ws_bytes < L.total)
+        return SQ_ERR_WORKSPACE;
+    int sms = 0;
+    st = check_device(&sms);
+    if (st != SQ_OK)
+        return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    uint32_t *status = reinterpret_cast<uint32_t *>(ws_at(ws, 0));
+    const int64_t width = bwd ? K : N;
+    sq::I8QuantArgs q;
+    memset(&q, 0, sizeof(q));
+    q.x = x;
+    q.col_scale = reinterpret_cast<const float *>(w->scales);
+    q.factor = bwd ? w->lora_up : w->lora_down;
+    q.offsets = offsets;
+    q.codes = reinterpret_cast<int8_t *>(ws_at(ws, L.codes));
+    q.scales = reinterpret_cast<float *>(ws_at(ws, L.scales));
+    q.low = w->lora_up ? reinterpret_cast<float *>(ws_at(ws, L.low)) : nullptr;
+    q.status = status;
+    q.counters = reinterpret_cast<uint32_t *>(ws_at(ws, L.counters));
+    q.y_zero = (flags & SQ_ZERO_UNGROUPED) ? reinterpret_cast<uint8_t *>(y) : nullptr;
+    q.y_row_bytes = width * ((flags & SQ_OUT_BF16) ? 2 : 4);
+    q.M = M;
+    q.K = bwd ? N : K;
+    q.E = (int)E;
+    q.n_counters = sq::kI8Counters;
+    q.finite_check = (flags & SQ_CHECK_FINITE) ? 1 : 0;
+    // the first block of the quantisation writes the status word; with a finite check any block
+    // may set it, so it is cleared first
+    if (q.finite_check)
+        SQ_CUDA(cudaMemsetAsync(status, 0, 4, s), "memset");
+    SQ_CUDA(stage_event(SQ_STAGE_ACT_QUANT, 0, s), "event record");
+    SQ_CUDA(sq::launch_i8_quant(q, bwd, sms, s), "int8 row quantisation");
+    SQ_CUDA(stage_event(SQ_STAGE_ACT_QUANT, 1, s), "event record");
+    sq::I8GemmLaunch g;
+    memset(&g, 0, sizeof(g));
+    g.bwd = bwd;
+    g.E = (int)E;
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    g.offsets = offsets;
+    g.codes = q.codes;
+    g.scales = q.scales;
+    g.low = q.low;
+    g.wcodes = w->codes;
+    g.wscales = q.col_scale;
+    g.factor = bwd ? w->lora_down : w->lora_up;
+    g.y = y;
+    g.out_bf16 = (flags & SQ_OUT_BF16) ? 1 : 0;
+    g.slabs = reinterpret_cast<int32_t *>(ws_at(ws, L.slabs));
+    g.counters = q.counters;
+    g.status = status;
+    SQ_CUDA(stage_event(SQ_STAGE_GEMM, 0, s), "event record");
+    SQ_CUDA(sq::launch_i8_gemm(g, sms, s), "int8 product");
+    SQ_CUDA(stage_event(SQ_STAGE_GEMM, 1, s), "event record");
     return SQ_OK;
 }
 
@@ -324,6 +434,24 @@ size_t sq_workspace_bytes(int op, int64_t M, int64_t N, int64_t K)
         return kAlign + round_up((size_t)N * (size_t)K * 2, kAlign);
     case SQ_OP_SVD_INIT:
         return sq::svd_workspace_bytes(N, K);
+    case SQ_OP_LINEAR_FWD_W8A8:
+        return i8_layout(false, 0, M, N, K).total;
+    case SQ_OP_LINEAR_BWD_DX_W8A8:
+        return i8_layout(true, 0, M, N, K).total;
+    default:
+        return 0;
+    }
+}
+
+size_t sq_grouped_workspace_bytes(int op, int64_t E, int64_t M, int64_t N, int64_t K)
+{
+    if (E < 1 || E > kMaxExperts || M < 0 || N < 0 || K < 0)
+        return 0;
+    switch (op) {
+    case SQ_OP_GROUPED_FWD_W8A8:
+        return i8_layout(false, (int)E, M, N, K).total;
+    case SQ_OP_GROUPED_BWD_DX_W8A8:
+        return i8_layout(true, (int)E, M, N, K).total;
     default:
         return 0;
     }
@@ -695,6 +823,35 @@ sq_status sq_linear_bwd_dx(const sq_weight *w, const uint16_t *dy, int64_t M, fl
     SQ_CUDA(sq::launch_gemm(g, sms, s), "gemm");
     SQ_CUDA(stage_event(SQ_STAGE_GEMM, 1, s), "event record");
     return SQ_OK;
+}
+
+sq_status sq_linear_fwd_w8a8(const sq_weight *w, const uint16_t *x, int64_t M, void *y, uint32_t flags, void *ws,
+                             size_t ws_bytes, void *stream)
+{
+    return i8_product(false, 0, w, x, M, nullptr, y, flags, ws, ws_bytes, stream);
+}
+
+sq_status sq_linear_bwd_dx_w8a8(const sq_weight *w, const uint16_t *dy, int64_t M, void *dx, uint32_t flags,
+                                void *ws, size_t ws_bytes, void *stream)
+{
+    return i8_product(true, 0, w, dy, M, nullptr, dx, flags, ws, ws_bytes, stream);
+}
+
+sq_status sq_grouped_fwd_w8a8(const sq_weight *w, int64_t E, const uint16_t *x, int64_t M, const int32_t *offsets,
+                              void *y, uint32_t flags, void *ws, size_t ws_bytes, void *stream)
+{
+    if (E < 1 || E > kMaxExperts)
+        return SQ_ERR_SHAPE;
+    return i8_product(false, E, w, x, M, offsets, y, flags, ws, ws_bytes, stream);
+}
+
+sq_status sq_grouped_bwd_dx_w8a8(const sq_weight *w, int64_t E, const uint16_t *dy, int64_t M,
+                                 const int32_t *offsets, void *dx, uint32_t flags, void *ws, size_t ws_bytes,
+                                 void *stream)
+{
+    if (E < 1 || E > kMaxExperts)
+        return SQ_ERR_SHAPE;
+    return i8_product(true, E, w, dy, M, offsets, dx, flags, ws, ws_bytes, stream);
 }
 
 sq_status sq_set_stage_events(int32_t stage, void *start_event, void *stop_event)

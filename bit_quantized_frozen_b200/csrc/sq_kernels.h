@@ -94,6 +94,52 @@ struct GemmLaunch {
 
 cudaError_t launch_gemm(const GemmLaunch &g, int sms, cudaStream_t stream);
 
+// ---- 8-bit integer products (sq_w8a8_quant.cu, sq_w8a8.cu) ----------------------
+// The row operand: K values of each of M rows become int8 codes and one scale (see the
+// head of sq_w8a8_quant.cu).  Forward: K input features; backward: K output features.
+struct I8QuantArgs {
+    const uint16_t *x;          // [M, K] bf16
+    const float *col_scale;     // backward: fp32 [max(E, 1), K] channel scales
+    const uint16_t *factor;     // low-rank factor [max(E, 1), K, 16] bf16
+    const int32_t *offsets;     // [E + 1], E > 0
+    int8_t *codes;              // [M, K]
+    float *scales;              // [M]
+    float *low;                 // [M, 16] = x factor, or NULL
+    uint32_t *status;
+    uint32_t *counters;         // zeroed for the product
+    uint8_t *y_zero;            // output whose rows outside every expert become 0, or NULL
+    int64_t y_row_bytes;
+    int64_t M, K;
+    int E;                      // experts, 0: one layer
+    int n_counters;
+    int finite_check;           // 1: a row with a NaN or an infinity sets kStatusNonfinite
+};
+cudaError_t launch_i8_quant(const I8QuantArgs &a, bool bwd, int sms, cudaStream_t s);
+
+// The product itself.  Forward: y[m, n] = s_x[m] s_w[n] sum_k q_x[m, k] Q[n, k] + low[m] . lora_up[n];
+// backward: dx[m, :] = H256(s_g[m] sum_n q_g[m, n] Q[n, :]) + low[m] . lora_down[k].
+struct I8GemmLaunch {
+    bool bwd;
+    int E;                      // experts, 0: one layer
+    int64_t M, N, K;
+    const int32_t *offsets;     // [E + 1] (device), E > 0
+    const int8_t *codes;        // row operand [M, K] (backward [M, N])
+    const float *scales;        // [M]
+    const float *low;           // [M, 16] or NULL
+    const uint8_t *wcodes;      // [max(E, 1) N, K]
+    const float *wscales;       // forward: [max(E, 1), N]
+    const uint16_t *factor;     // lora_up [., N, 16] (forward) or lora_down [., K, 16] (backward)
+    void *y;                    // [M, N] (backward [M, K]) fp32 or bf16
+    int out_bf16;
+    int32_t *slabs;             // partial sums of split tiles, i8_slab_bytes
+    uint32_t *counters;         // kI8Counters, zero at the launch
+    uint32_t *status;
+};
+constexpr int kI8Counters = 512;
+// bytes of the partial sums a product of this shape may need (0: it never splits a tile)
+size_t i8_slab_bytes(bool bwd, int E, int64_t M, int64_t N, int64_t K);
+cudaError_t launch_i8_gemm(const I8GemmLaunch &g, int sms, cudaStream_t stream);
+
 // ID of the current CUDA context (unique for the life of the process; a context created
 // after cudaDeviceReset gets a new one), 0 if it cannot be read.  Per-device caches of
 // symbol addresses and function attributes are keyed on it: a new context loads the
