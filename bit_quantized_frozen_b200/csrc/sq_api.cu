@@ -219,7 +219,7 @@ I8Layout i8_layout(bool bwd, int E, int64_t M, int64_t N, int64_t K)
     L.counters = take((size_t)sq::kI8Counters * 4);
     L.codes = take((size_t)M * (size_t)(bwd ? N : K));
     L.scales = take((size_t)M * 4);
-    L.low = take((size_t)M * 16 * 4);
+    L.low = take((size_t)M * 3 * 16 * 2);
     L.slabs = take(sq::i8_slab_bytes(bwd, E, M, N, K));
     L.total = round_up(off, kAlign);
     return L;
@@ -317,7 +317,7 @@ sq_status i8_product(bool bwd, int64_t E, const sq_weight *w, const uint16_t *x,
     q.offsets = offsets;
     q.codes = reinterpret_cast<int8_t *>(ws_at(ws, L.codes));
     q.scales = reinterpret_cast<float *>(ws_at(ws, L.scales));
-    q.low = w->lora_up ? reinterpret_cast<float *>(ws_at(ws, L.low)) : nullptr;
+    q.low = w->lora_up ? reinterpret_cast<uint16_t *>(ws_at(ws, L.low)) : nullptr;
     q.status = status;
     q.counters = reinterpret_cast<uint32_t *>(ws_at(ws, L.counters));
     q.y_zero = (flags & SQ_ZERO_UNGROUPED) ? reinterpret_cast<uint8_t *>(y) : nullptr;

@@ -17,8 +17,8 @@
 //             transposed).  A thread holds a whole 256-block of its token, so the
 //             rotation is done on the accumulator.
 //
-// CTA (CG = 1) or CTA pair (CG = 2, 256 x 256 tiles) per SM, persistent, 6 warps:
-// 0-3 epilogue, 4 TMA producer, 5 MMA issuer and tensor-memory allocator.  Two
+// CTA (CG = 1) or CTA pair (CG = 2, 256 x 256 tiles) per SM, persistent: 4 or 8 epilogue
+// warps, a TMA producer, an MMA issuer that also allocates tensor memory.  Two
 // accumulators in tensor memory: the next tile's MMAs run while one drains.
 // Weight tiles of the first stages are fetched before the kernel waits for the
 // quantisation kernel in front of it.
@@ -32,13 +32,11 @@
 #include "sq_device.cuh"
 #include "sq_kernels.h"
 #include "sq_ptx.cuh"
+#include "sq_w8a8.cuh"
 
 namespace sq {
 
-constexpr int kI8Rank = 16;
 constexpr int kChunk = 128;                       // summed values (bytes) per stage
-constexpr int kI8Threads = 192;
-constexpr int kMaxExperts = 1024;
 constexpr int kMinSplitChunks = 4;                // a split sums at least 512 values
 
 template <int NT, int CG, bool BWD>
@@ -48,9 +46,19 @@ struct I8Cfg {
     static constexpr int kABytes = 128 * kChunk;
     static constexpr int kBBytes = kColsPerCta * kChunk;
     static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kStages = (192 * 1024) / kStageBytes < 10 ? (192 * 1024) / kStageBytes : 10;
-    static constexpr int kLowOff = kStages * kStageBytes;            // column factors [NT][16] fp32
-    static constexpr int kScaleOff = kLowOff + NT * kI8Rank * 4;     // column scales [NT] fp32 (forward)
+    // epilogue warps: one per 32 lanes and, in wide tiles, per half of the columns
+    static constexpr int kColHalves = NT >= 64 ? 2 : 1;
+    static constexpr int kEpiThreads = 128 * kColHalves;
+    static constexpr int kThreads = kEpiThreads + 64;                // + producer, MMA issuer
+    // low-rank values of a column in shared memory: three bf16 terms of a token (forward), the
+    // bf16 row of lora_down (backward); an odd number of 16-byte pieces apart (ldmatrix rows)
+    static constexpr int kLowPitch = BWD ? 48 : 112;
+    static constexpr int kPatchBytes = BWD ? 0 : 2 * 8 * 36 * 4;     // a warp's two store patches
+    static constexpr int kRing = (BWD ? 192 : NT == 256 ? 160 : 176) * 1024;
+    static constexpr int kStages = kRing / kStageBytes < 10 ? kRing / kStageBytes : 10;
+    static constexpr int kPatchOff = kStages * kStageBytes;
+    static constexpr int kLowOff = kPatchOff + (kEpiThreads / 32) * kPatchBytes;
+    static constexpr int kScaleOff = kLowOff + NT * kLowPitch;       // column scales [NT] fp32 (forward)
     static constexpr int kPlanOff = kScaleOff + NT * 4;              // start and prefix of every expert
     static constexpr int kBarOff = kPlanOff + (2 * kMaxExperts + 4) * 4;
     static constexpr int kNumBars = 2 * kStages + 5;                 // full, empty, acc_full[2], acc_empty[2], drain
@@ -64,7 +72,7 @@ struct I8Cfg {
 struct I8Args {
     const int32_t *offsets;
     const float *scales;      // per token
-    const float *low;         // per token [M, 16] or NULL
+    const uint16_t *low;      // per token, three bf16 terms [M, 3, 16], or NULL
     const float *wscales;     // per channel (forward)
     const uint16_t *factor;   // lane-side (forward: lora_up) or column-side (backward: lora_down) factor
     void *y;
@@ -75,80 +83,6 @@ struct I8Args {
     int E;
     int out_bf16;
     int slab_items;           // slabs there is room for
-};
-
-// where an item's tile lies
-struct I8Tile {
-    int e;                    // expert
-    int row0, rows;           // first token and tokens of the tile
-    int wt;                   // tile along the weight: channels (forward) or input features (backward)
-};
-
-// The tiles of all experts in a row: expert e has ceil(rows / tok_tile) token tiles, each times
-// `wts` weight tiles; the token tile changes fastest, so that the tiles which share a weight
-// tile run together.  Offsets are clamped to [0, M] and to their running maximum, so that the
-// experts' rows never overlap or leave the matrix, whatever the offsets hold.
-struct I8Plan {
-    int32_t *start;           // [E + 1] first row of each expert
-    int32_t *prefix;          // [E + 1] token tiles before each expert
-    int E, wts, tok_tile;
-
-    __device__ __forceinline__ void build(const int32_t *__restrict__ offsets, int64_t M, int tid, int threads)
-    {
-        for (int i = tid; i <= E; i += threads) {
-            const int64_t o = offsets ? (int64_t)__ldg(offsets + i) : i == 0 ? 0 : M;
-            start[i] = (int32_t)(o < 0 ? 0 : o > M ? M : o);
-        }
-        __syncthreads();
-        if (tid < 32) {
-            int32_t top = 0, sum = 0;             // running maximum and token tiles up to here
-            for (int base = 0; base <= E; base += 32) {
-                const int i = base + tid;
-                int32_t v = i <= E ? start[i] : 0;
-#pragma unroll
-                for (int x = 1; x < 32; x <<= 1) {
-                    const int32_t up = __shfl_up_sync(0xffffffffu, v, x);
-                    v = tid >= x ? max(v, up) : v;
-                }
-                v = max(v, top);
-                const int32_t left = __shfl_up_sync(0xffffffffu, v, 1);
-                int32_t n = i == 0 || i > E ? 0 : (v - (tid == 0 ? top : left) + tok_tile - 1) / tok_tile;
-                top = __shfl_sync(0xffffffffu, v, 31);
-#pragma unroll
-                for (int x = 1; x < 32; x <<= 1) {
-                    const int32_t up = __shfl_up_sync(0xffffffffu, n, x);
-                    n += tid >= x ? up : 0;
-                }
-                n += sum;
-                sum = __shfl_sync(0xffffffffu, n, 31);
-                if (i <= E) {
-                    start[i] = v;
-                    prefix[i] = n;
-                }
-            }
-        }
-        __syncthreads();
-    }
-
-    __device__ __forceinline__ int tiles() const
-    {
-        return prefix[E] * wts;
-    }
-
-    // tile number `tile`, below tiles(); e: a role's own walk, starting at 0 (its tiles only grow)
-    __device__ __forceinline__ I8Tile find(int tile, int &e) const
-    {
-        while (tile >= prefix[e + 1] * wts)
-            ++e;
-        const int tts = prefix[e + 1] - prefix[e];
-        const int i = tile - prefix[e] * wts;
-        I8Tile t;
-        t.e = e;
-        t.wt = i / tts;
-        t.row0 = start[e] + (i % tts) * tok_tile;
-        t.rows = min(start[e + 1] - t.row0, tok_tile);
-        return t;
-    }
 };
 
 // Items per tile: with at most half as many tiles as units (CTAs or CTA pairs), the summed
@@ -170,29 +104,13 @@ __device__ __forceinline__ bool acc_wait(uint32_t bar, uint32_t parity, volatile
     return CG == 2 ? mbar_wait_cluster(bar, parity, abort_flag, status) : mbar_wait(bar, parity, abort_flag, status);
 }
 
-// sum over r of low[r] f[r], pairs of neighbouring r in packed arithmetic
-__device__ __forceinline__ float dot16(const uint64_t (&f)[8], const float *__restrict__ low)
-{
-    uint64_t s = f2_pack(0.0f, 0.0f);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float4 v = *reinterpret_cast<const float4 *>(low + 4 * j);
-        s = f2_fma(f2_pack(v.x, v.y), f[2 * j], s);
-        s = f2_fma(f2_pack(v.z, v.w), f[2 * j + 1], s);
-    }
-    float a, b;
-    f2_unpack(s, a, b);
-    return __fadd_rn(a, b);
-}
-
 template <int NT, int CG, bool BWD>
-__global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kI8Threads, 1)
+__global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>::kThreads, 1)
     sq_i8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const I8Args args)
 {
     using Cfg = I8Cfg<NT, CG, BWD>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float *col_low = reinterpret_cast<float *>(smem + Cfg::kLowOff);
     float *col_scale = reinterpret_cast<float *>(smem + Cfg::kScaleOff);
     int32_t *plan_mem = reinterpret_cast<int32_t *>(smem + Cfg::kPlanOff);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kBarOff);
@@ -218,13 +136,14 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kI8Threads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar_acc_full + 8 * i, 1);
-            mbar_init(bar_acc_empty + 8 * i, 4 * CG);
+            mbar_init(bar_acc_empty + 8 * i, CG * Cfg::kEpiThreads / 32);
         }
         mbar_init(bar_drain, 1);
         *abort_flag = 0u;
         fence_mbar_init();
     }
-    if (warp == 5) {
+    constexpr int kProducer = Cfg::kEpiThreads / 32, kIssuer = kProducer + 1;      // warps
+    if (warp == kIssuer) {
         if (CG == 2) {
             tmem_alloc2(smem_u32(tmem_holder), Cfg::kTmemCols);
             tmem_relinquish2();
@@ -233,7 +152,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kI8Threads, 1)
             tmem_relinquish();
         }
     }
-    if (warp == 4 && lane == 0) {
+    if (warp == kProducer && lane == 0) {
         prefetch_tmap(&tmA);
         prefetch_tmap(&tmB);
     }
@@ -244,7 +163,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kI8Threads, 1)
     plan.prefix = plan_mem + kMaxExperts + 1;
     plan.wts = BWD ? (int)(args.K / NT) : (int)((args.N + Cfg::kLaneTile - 1) / Cfg::kLaneTile);
     plan.tok_tile = BWD ? Cfg::kLaneTile : NT;
-    plan.build(args.E > 0 ? args.offsets : nullptr, args.M, threadIdx.x, kI8Threads);
+    plan.build(args.E > 0 ? args.offsets : nullptr, args.M, threadIdx.x, Cfg::kThreads);
     tc_fence_before();
     if (CG == 2)
         cluster_sync();                           // barriers of both CTAs initialised, TMEM allocated
@@ -260,7 +179,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kI8Threads, 1)
     const int splits = i8_splits(tiles, units, chunks, args.slab_items);
     const int items = tiles * splits;
 
-    if (warp == 4) {
+    if (warp == kProducer) {
         // ------------------------------------------------------------ producer (every CTA)
         if (lane == 0) {
             // weight operand of stage `stage`, chunk c of tile t, and the row operand
@@ -336,7 +255,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kI8Threads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == 5) {
+    } else if (warp == kIssuer) {
         // ------------------------------------------------------------ MMA issuer (leader)
         if (leader && lane == 0) {
             const uint32_t s0 = smem_u32(smem);
@@ -391,13 +310,20 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kI8Threads, 1)
         __syncwarp();
     } else {
         // ------------------------------------------------------------ epilogue (every CTA)
-        // Thread 0 alone waits (bounded); the 128 threads meet at named barrier 1, so that they
-        // always take the same way out.
+        // Thread 0 alone waits (bounded); the epilogue's threads meet at named barrier 1, so that
+        // they always take the same way out.
         const int et = threadIdx.x;
+        constexpr int ET = Cfg::kEpiThreads;
+        const int wq = warp & 3;                           // lanes 32 wq .. + 31 of tensor memory
+        const int wh = warp >> 2;                          // half of the columns
+        const int g = lane >> 2, q = lane & 3;             // place in a fragment
         const uint32_t acc_empty_leader = CG == 2 ? mapa_shared(bar_acc_empty, 0) : bar_acc_empty;
+        const uint32_t col_low = smem_u32(smem + Cfg::kLowOff);
+        uint8_t *patch = smem + Cfg::kPatchOff + warp * Cfg::kPatchBytes;
         const bool ybf = args.out_bf16 != 0;
         const bool with_low = args.low != nullptr;
         const int64_t width = BWD ? args.K : args.N;      // columns of y
+        constexpr int64_t kSlab = (int64_t)NT * 128;
         grid_dep_wait();
         int e = 0;
         int count = 0;
@@ -405,211 +331,304 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kI8Threads, 1)
             const int tile = item / splits, split = item % splits;
             const I8Tile t = plan.find(tile, e);
             const int slot = count & 1;
-            named_barrier_sync(1, 128);                    // the previous tile's column factors are used up
-            if (BWD) {
-                if (with_low)
-                    for (int c = et; c < NT; c += 128) {
-                        const uint4 *src = reinterpret_cast<const uint4 *>(
-                            args.factor + ((int64_t)t.e * args.K + t.wt * NT + c) * kI8Rank);
-                        const uint4 p = __ldg(src), q = __ldg(src + 1);
-                        const uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            *reinterpret_cast<float2 *>(col_low + c * kI8Rank + 2 * j) =
-                                make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
-                    }
-            } else {
-                for (int c = et; c < NT; c += 128)
+            named_barrier_sync(1, ET);                     // the previous tile's column factors are used up
+            if (with_low) {
+                // 16-byte pieces of the columns' low-rank values
+                constexpr int kPieces = BWD ? 2 : 2 * kLowParts;
+                const int cols = BWD ? NT : t.rows;
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    BWD ? args.factor + ((int64_t)t.e * args.K + (int64_t)t.wt * NT) * kI8Rank
+                        : args.low + (int64_t)t.row0 * kLowRow);
+                for (int i = et; i < cols * kPieces; i += ET)
+                    *reinterpret_cast<uint4 *>(smem + Cfg::kLowOff + (i / kPieces) * Cfg::kLowPitch +
+                                               16 * (i % kPieces)) = BWD ? __ldg(src + i) : src[i];
+            }
+            if (!BWD)
+                for (int c = et; c < NT; c += ET)
                     col_scale[c] = c < t.rows ? args.scales[t.row0 + c] : 0.0f;
-                if (with_low)
-                    for (int i = et; i < NT * 4; i += 128)
-                        if ((i >> 2) < t.rows)
-                            reinterpret_cast<float4 *>(col_low)[i] =
-                                reinterpret_cast<const float4 *>(args.low + (int64_t)t.row0 * kI8Rank)[i];
-            }
-            // this lane's channel (forward) or token (backward): scale and low-rank values
-            const int in_tile = (int)rank * 128 + et;
-            const int64_t at = BWD ? (int64_t)t.row0 + in_tile : (int64_t)t.wt * Cfg::kLaneTile + in_tile;
-            const bool live = BWD ? in_tile < t.rows : at < args.N;
-            float lane_scale = 0.0f;
-            uint64_t lane_low[8];
+            // the lanes' scales and low-rank values (lane r of a fragment half: 16 h + g + 8 i)
+            const int lane0 = (int)rank * 128 + 32 * wq;   // first lane of the warp in the tile
+            const int64_t base = BWD ? (int64_t)t.row0 + lane0 : (int64_t)t.wt * Cfg::kLaneTile + lane0;
+            float fscale[2][2];                            // forward: per fragment row
+            float lscale = 0.0f;                           // backward: of this thread's lane
+            uint32_t ufrag[2][BWD ? kLowParts : 1][4];     // A operand of the low-rank product
+            if (BWD)
+                lscale = lane0 + lane < t.rows ? args.scales[base + lane] : 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                lane_low[j] = 0;
-            if (live) {
-                if (BWD) {
-                    lane_scale = args.scales[at];
-                    if (with_low)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float4 v = reinterpret_cast<const float4 *>(args.low + at * kI8Rank)[j];
-                            lane_low[2 * j] = f2_pack(v.x, v.y);
-                            lane_low[2 * j + 1] = f2_pack(v.z, v.w);
+                for (int i = 0; i < 2; ++i) {
+                    const int r = 16 * h + g + 8 * i;
+                    const bool live = BWD ? lane0 + r < t.rows : base + r < args.N;
+                    if (!BWD)
+                        fscale[h][i] = live ? __ldg(args.wscales + (int64_t)t.e * args.N + base + r) : 0.0f;
+#pragma unroll
+                    for (int p = 0; p < (BWD ? kLowParts : 1); ++p)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            uint32_t v = 0u;
+                            if (with_low && live)
+                                v = BWD ? reinterpret_cast<const uint32_t *>(args.low + (base + r) * kLowRow)[8 * p + q + 4 * k]
+                                        : __ldg(reinterpret_cast<const uint32_t *>(
+                                                    args.factor + ((int64_t)t.e * args.N + base + r) * kI8Rank) +
+                                                q + 4 * k);
+                            ufrag[h][p][i + 2 * k] = v;
                         }
-                } else {
-                    lane_scale = __ldg(args.wscales + (int64_t)t.e * args.N + at);
-                    if (with_low) {
-                        const uint4 *src =
-                            reinterpret_cast<const uint4 *>(args.factor + ((int64_t)t.e * args.N + at) * kI8Rank);
-                        const uint4 p = __ldg(src), q = __ldg(src + 1);
-                        const uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            lane_low[j] = f2_pack(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
-                    }
                 }
-            }
             if (et == 0)
                 *verdict = acc_wait<CG>(bar_acc_full + 8 * slot, (uint32_t)((count >> 1) & 1), abort_flag, args.status)
                                ? 1u
                                : 0u;
-            named_barrier_sync(1, 128);
+            named_barrier_sync(1, ET);
             if (*verdict == 0u)
                 break;
             tc_fence_after();
-            const uint32_t acc = tmem_base + ((uint32_t)(32 * warp) << 16) + (slot ? (uint32_t)NT : 0u);
-            constexpr int CH = NT < 32 ? NT : 32;
-            const int live_cols = BWD ? NT : t.rows;
-
-            // the raw sums of CH columns, column q * CH on
-            auto load_acc = [&](int q, uint32_t (&r)[CH]) {
-                __syncwarp();
-                if constexpr (CH == 16)
-                    tmem_ld_16cols(acc + CH * q, r);
-                else
-                    tmem_ld_32cols(acc + CH * q, r);
-                tmem_wait_ld();
-            };
-            constexpr int64_t kSlab = (int64_t)NT * 128;
-            int32_t *slab0 = args.slabs + ((int64_t)tile * splits * CG + rank) * kSlab + et;   // + split CG kSlab + 128 c
-            bool finish = true;
-            if (splits > 1) {
-                int32_t *mine = slab0 + (int64_t)split * CG * kSlab;
-                for (int q = 0; q * CH < live_cols; ++q) {
-                    uint32_t r[CH];
-                    load_acc(q, r);
-#pragma unroll
-                    for (int i = 0; i < CH; ++i)
-                        mine[128 * (CH * q + i)] = (int32_t)r[i];
-                }
+            const uint32_t acc = tmem_base + ((uint32_t)(32 * wq) << 16) + (slot ? (uint32_t)NT : 0u);
+            int32_t *slab0 = args.slabs + ((int64_t)tile * splits * CG + rank) * kSlab;   // + split CG kSlab
+            // publish this item's partial sums (already stored); true in the item that comes last
+            auto last_of_tile = [&]() {
                 __threadfence();
-                named_barrier_sync(1, 128);
+                named_barrier_sync(1, ET);
                 if (et == 0) {
                     *last_item = atomicAdd(args.counters + tile * CG + rank, 1u) == (uint32_t)(splits - 1) ? 1u : 0u;
                     __threadfence();
                 }
-                named_barrier_sync(1, 128);
-                finish = *last_item != 0u;
-            }
-            // ... and with the other items' partial sums
-            auto load_sum = [&](int q, uint32_t (&r)[CH]) {
-                load_acc(q, r);
-                if (splits > 1)
-                    for (int s = 0; s < splits; ++s)
-                        if (s != split) {
-                            const int32_t *p = slab0 + (int64_t)s * CG * kSlab + 128 * CH * q;
-#pragma unroll
-                            for (int i = 0; i < CH; ++i)
-                                r[i] += (uint32_t)__ldcg(p + 128 * i);
-                        }
+                named_barrier_sync(1, ET);
+                return *last_item != 0u;
             };
+
             if constexpr (BWD) {
+                // raw sums of columns 32 c .. 32 c + 31 of this thread's lane
+                auto load_acc = [&](int c, uint32_t (&r)[32]) {
+                    __syncwarp();
+                    tmem_ld_32cols(acc + 32 * c, r);
+                    tmem_wait_ld();
+                };
+                const int l = 32 * wq + lane;
+                bool finish = true;
+                if (splits > 1) {
+                    int32_t *mine = slab0 + (int64_t)split * CG * kSlab + l;
+                    for (int c = 4 * wh; c < 4 * wh + 4; ++c) {
+                        uint32_t r[32];
+                        load_acc(c, r);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            mine[128 * (32 * c + i)] = (int32_t)r[i];
+                    }
+                    finish = last_of_tile();
+                }
                 if (finish) {
                     // strides 1 .. 16 inside each 32 columns, back into tensor memory
-                    for (int q = 0; q < NT / 32; ++q) {
+                    for (int c = 4 * wh; c < 4 * wh + 4; ++c) {
                         uint32_t r[32];
-                        load_sum(q, r);
-                        float v[32];
+                        load_acc(c, r);
+                        if (splits > 1)
+                            for (int s = 0; s < splits; ++s)
+                                if (s != split) {
+                                    const int32_t *p = slab0 + (int64_t)s * CG * kSlab + l + 128 * 32 * c;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            v[i] = __fmul_rn(__int2float_rn((int32_t)r[i]), lane_scale);
+                                    for (int i = 0; i < 32; ++i)
+                                        r[i] += (uint32_t)__ldcg(p + 128 * i);
+                                }
+                        uint64_t v[16];
 #pragma unroll
-                        for (int h = 1; h <= 16; h <<= 1)
+                        for (int i = 0; i < 16; ++i) {
+                            const float a = __fmul_rn(__int2float_rn((int32_t)r[2 * i]), lscale);
+                            const float b = __fmul_rn(__int2float_rn((int32_t)r[2 * i + 1]), lscale);
+                            v[i] = f2_pack(__fadd_rn(a, b), __fsub_rn(a, b));
+                        }
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
+                        for (int h = 1; h <= 8; h <<= 1)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
                                 if ((i & h) == 0) {
-                                    const float a = v[i], b = v[i + h];
-                                    v[i] = __fadd_rn(a, b);
-                                    v[i + h] = __fsub_rn(a, b);
+                                    const uint64_t a = v[i], b = v[i + h];
+                                    v[i] = f2_add(a, b);
+                                    v[i + h] = f2_sub(a, b);
                                 }
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            r[i] = __float_as_uint(v[i]);
-                        tmem_st_32cols(acc + 32 * q, r);
+                        for (int i = 0; i < 16; ++i) {
+                            float a, b;
+                            f2_unpack(v[i], a, b);
+                            r[2 * i] = __float_as_uint(a);
+                            r[2 * i + 1] = __float_as_uint(b);
+                        }
+                        tmem_st_32cols(acc + 32 * c, r);
                     }
                     tmem_wait_st();
-                    // strides 32, 64, 128 over four columns of each 32, the low-rank term, the store
-                    for (int c4 = 0; c4 < 32; c4 += 4) {
-                        uint32_t r[8][4];
+                    tc_fence_before();
+                    named_barrier_sync(1, ET);             // both halves of the columns are written
+                    tc_fence_after();
+                    // strides 32, 64, 128 over columns 16 wh .. + 15 of each 32, as fragments of
+                    // 16 tokens; the low-rank term; the store (32-byte runs of a row)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t r[8][2][4];
                         __syncwarp();
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            tmem_ld_4cols(acc + 32 * j + c4, r[j]);
+                            tmem_ld_frag2(acc + ((uint32_t)(16 * h) << 16) + 32 * j + 16 * wh, r[j]);
                         tmem_wait_ld();
-                        float v[8][4];
+                        uint64_t v[8][2][2];
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                v[j][i] = __uint_as_float(r[j][i]);
+                                v[j][i >> 1][i & 1] = f2_pack(__uint_as_float(r[j][i >> 1][2 * (i & 1)]),
+                                                              __uint_as_float(r[j][i >> 1][2 * (i & 1) + 1]));
 #pragma unroll
-                        for (int h = 1; h <= 4; h <<= 1)
+                        for (int x = 1; x <= 4; x <<= 1)
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
-                                if ((j & h) == 0)
+                                if ((j & x) == 0)
 #pragma unroll
                                     for (int i = 0; i < 4; ++i) {
-                                        const float a = v[j][i], b = v[j + h][i];
-                                        v[j][i] = __fadd_rn(a, b);
-                                        v[j + h][i] = __fsub_rn(a, b);
+                                        const uint64_t a = v[j][i >> 1][i & 1], b = v[j + x][i >> 1][i & 1];
+                                        v[j][i >> 1][i & 1] = f2_add(a, b);
+                                        v[j + x][i >> 1][i & 1] = f2_sub(a, b);
                                     }
-                        if (!live)
-                            continue;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            float o[4];
+                            const int col = 32 * j + 16 * wh;
+                            float low[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+                            if (with_low) {                // B: 16 columns (two groups of 8) x 16 ranks
+                                uint32_t b[4];
+                                ldmatrix_x4<false>(col_low + (col + 8 * (lane >> 4) + (lane & 7)) * Cfg::kLowPitch +
+                                                       16 * ((lane >> 3) & 1),
+                                                   b);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                o[i] = __fmul_rn(v[j][i], 0.0625f);
-                                if (with_low)
-                                    o[i] = __fadd_rn(o[i], dot16(lane_low, col_low + (32 * j + c4 + i) * kI8Rank));
+                                for (int p = kLowParts - 1; p >= 0; --p) {
+                                    mma_16816(low[0], ufrag[h][p], b[0], b[1]);
+                                    mma_16816(low[1], ufrag[h][p], b[2], b[3]);
+                                }
                             }
-                            const int64_t col = (int64_t)t.wt * NT + 32 * j + c4;
-                            if (!SQ_DCHECK(at < args.M && col + 4 <= width, args.status))
-                                continue;
-                            if (ybf)
-                                *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(args.y) + at * width + col) =
-                                    make_uint2(f32x2_to_bf16x2_bits(o[0], o[1]), f32x2_to_bf16x2_bits(o[2], o[3]));
-                            else
-                                *reinterpret_cast<float4 *>(reinterpret_cast<float *>(args.y) + at * width + col) =
-                                    make_float4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {  // group i >> 1, fragment rows g + 8 (i & 1)
+                                const int row = 16 * h + g + 8 * (i & 1);
+                                float a, b;
+                                f2_unpack(v[j][i >> 1][i & 1], a, b);
+                                a = __fmaf_rn(a, 0.0625f, low[i >> 1][2 * (i & 1)]);
+                                b = __fmaf_rn(b, 0.0625f, low[i >> 1][2 * (i & 1) + 1]);
+                                const int64_t at = (base + row) * width + (int64_t)t.wt * NT + col + 8 * (i >> 1) + 2 * q;
+                                if (lane0 + row < t.rows && SQ_DCHECK(at + 2 <= args.M * width, args.status)) {
+                                    if (ybf)
+                                        *reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(args.y) + at) =
+                                            f32x2_to_bf16x2_bits(a, b);
+                                    else
+                                        *reinterpret_cast<float2 *>(reinterpret_cast<float *>(args.y) + at) =
+                                            make_float2(a, b);
+                                }
+                            }
                         }
                     }
                 }
             } else {
-                if (finish)
-                    for (int q = 0; q * CH < live_cols; ++q) {
-                        uint32_t r[CH];
-                        load_sum(q, r);
-                        if (!live)
-                            continue;
+                constexpr int CW = NT / Cfg::kColHalves;   // this warp's columns, 16 at a time
+                const int c_end = min(CW * (wh + 1), t.rows);
+                // the sums of 16 columns as fragments [16 channels][8 tokens][4]
+                auto load_acc = [&](int c, uint32_t (&r)[2][2][4]) {
+                    __syncwarp();
+                    tmem_ld_frag2(acc + c, r[0]);
+                    tmem_ld_frag2(acc + (16u << 16) + c, r[1]);
+                };
+                bool finish = true;
+                if (splits > 1) {
+                    int32_t *mine = slab0 + (int64_t)split * CG * kSlab + 32 * wq + lane;
+                    for (int c = CW * wh; c < c_end; c += 16) {
+                        uint32_t r[2][2][4];
+                        load_acc(c, r);
+                        tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < CH; ++i) {
-                            const int c = CH * q + i;
-                            if (c >= t.rows)
-                                break;
-                            float o = __fmul_rn(__int2float_rn((int32_t)r[i]), __fmul_rn(col_scale[c], lane_scale));
-                            if (with_low)
-                                o = __fadd_rn(o, dot16(lane_low, col_low + c * kI8Rank));
-                            const int64_t row = (int64_t)t.row0 + c;
-                            if (!SQ_DCHECK(row < args.M && at < width, args.status))
-                                continue;
-                            if (ybf)
-                                reinterpret_cast<uint16_t *>(args.y)[row * width + at] = (uint16_t)f32_to_bf16_bits(o);
-                            else
-                                reinterpret_cast<float *>(args.y)[row * width + at] = o;
+                        for (int i = 0; i < 16; ++i)
+                            mine[128 * (c + i)] = (int32_t)r[i >> 3][(i >> 2) & 1][i & 3];
+                    }
+                    finish = last_of_tile();
+                }
+                const bool live = finish && base < args.N; // (N % 128 == 0: the same in the whole warp)
+                auto finish16 = [&](int c, const uint32_t (&r)[2][2][4]) {
+                    uint32_t b[3][4];                      // terms 0, 1 of both groups; term 2 of both
+                    if (with_low) {
+                        const uint32_t row = col_low + (c + (lane & 7)) * Cfg::kLowPitch;
+                        ldmatrix_x4<false>(row + 16 * (lane >> 3), b[0]);
+                        ldmatrix_x4<false>(row + 8 * Cfg::kLowPitch + 16 * (lane >> 3), b[1]);
+                        ldmatrix_x4<false>(row + 8 * (lane >> 4) * Cfg::kLowPitch + 64 + 16 * ((lane >> 3) & 1), b[2]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {          // 8 tokens
+                        float o[2][4];
+                        const float2 sx = *reinterpret_cast<const float2 *>(col_scale + c + 8 * n + 2 * q);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float low[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                            if (with_low) {
+                                mma_16816(low, ufrag[h][0], b[2][2 * n], b[2][2 * n + 1]);
+                                mma_16816(low, ufrag[h][0], b[n][2], b[n][3]);
+                                mma_16816(low, ufrag[h][0], b[n][0], b[n][1]);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                o[h][i] = __fmaf_rn(__int2float_rn((int32_t)r[h][n][i]),
+                                                    __fmul_rn(i & 1 ? sx.y : sx.x, fscale[h][i >> 1]), low[i]);
+                        }
+                        // through the warp's patch, so that a token's 32 channels leave in one run
+                        uint8_t *buf = patch + n * (8 * 36 * 4);
+                        const int64_t y0 = ((int64_t)t.row0 + c + 8 * n) * width + base;
+                        if (ybf) {                         // [8 tokens] rows of 80 bytes
+                            const uint32_t w[4] = {f32x2_to_bf16x2_bits(o[0][0], o[0][1]),
+                                                   f32x2_to_bf16x2_bits(o[0][2], o[0][3]),
+                                                   f32x2_to_bf16x2_bits(o[1][0], o[1][1]),
+                                                   f32x2_to_bf16x2_bits(o[1][2], o[1][3])};
+                            stmatrix_x4_trans(smem_u32(buf) + (lane & 7) * 80 + (lane >> 3) * 16, w);
+                            __syncwarp();
+                            const int tok = lane >> 2, piece = lane & 3;
+                            const uint4 v = *reinterpret_cast<const uint4 *>(buf + tok * 80 + piece * 16);
+                            const int64_t at = y0 + tok * width + 8 * piece;
+                            if (c + 8 * n + tok < t.rows && SQ_DCHECK(at + 8 <= args.M * width, args.status))
+                                *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(args.y) + at) = v;
+                        } else {                           // [8 tokens] rows of 36 floats
+                            float *f = reinterpret_cast<float *>(buf);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    f[(2 * q + (i & 1)) * 36 + 16 * h + g + 8 * (i >> 1)] = o[h][i];
+                            __syncwarp();
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const int tok = (lane >> 3) + 4 * k, piece = lane & 7;
+                                const float4 v = *reinterpret_cast<const float4 *>(f + tok * 36 + 4 * piece);
+                                const int64_t at = y0 + tok * width + 4 * piece;
+                                if (c + 8 * n + tok < t.rows && SQ_DCHECK(at + 4 <= args.M * width, args.status))
+                                    *reinterpret_cast<float4 *>(reinterpret_cast<float *>(args.y) + at) = v;
+                            }
                         }
                     }
+                };
+                if (live) {
+                    uint32_t r[2][2][4];
+                    if (CW * wh < c_end) {
+                        load_acc(CW * wh, r);
+                        tmem_wait_ld();
+                    }
+                    for (int c = CW * wh; c < c_end; c += 16) {
+                        uint32_t now[2][2][4];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            now[i >> 3][(i >> 2) & 1][i & 3] = r[i >> 3][(i >> 2) & 1][i & 3];
+                        if (c + 16 < c_end)
+                            load_acc(c + 16, r);           // on its way while these 16 are finished
+                        if (splits > 1)
+                            for (int s = 0; s < splits; ++s)
+                                if (s != split) {
+                                    const int32_t *p = slab0 + (int64_t)s * CG * kSlab + 32 * wq + lane + 128 * c;
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i)
+                                        now[i >> 3][(i >> 2) & 1][i & 3] += (uint32_t)__ldcg(p + 128 * i);
+                                }
+                        finish16(c, now);
+                        tmem_wait_ld();
+                    }
+                }
             }
             tc_fence_before();
             __syncwarp();
@@ -628,7 +647,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kI8Threads, 1)
     else
         __syncthreads();
     tc_fence_after();
-    if (warp == 5) {
+    if (warp == kIssuer) {
         if (CG == 2)
             tmem_dealloc2(tmem_base, Cfg::kTmemCols);
         else
@@ -699,7 +718,7 @@ cudaError_t launch_shape(const I8GemmLaunch &g, int sms, cudaStream_t stream)
         if (CG == 2) {                            // not every SM can pair up inside its GPC
             cudaLaunchConfig_t q = {};
             q.gridDim = dim3(2 * units);
-            q.blockDim = dim3(kI8Threads);
+            q.blockDim = dim3(Cfg::kThreads);
             q.dynamicSmemBytes = Cfg::kSmemBytes;
             int resident = 0;
             e = cudaOccupancyMaxActiveClusters(&resident, sq_i8_kernel<NT, CG, BWD>, &q);
@@ -738,7 +757,7 @@ cudaError_t launch_shape(const I8GemmLaunch &g, int sms, cudaStream_t stream)
     // dependent launch: set-up and the first weight tiles overlap the quantisation in front
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(resident_units[dev] * CG));
-    cfg.blockDim = dim3(kI8Threads);
+    cfg.blockDim = dim3(Cfg::kThreads);
     cfg.dynamicSmemBytes = Cfg::kSmemBytes;
     cfg.stream = stream;
     cudaLaunchAttribute at[1];

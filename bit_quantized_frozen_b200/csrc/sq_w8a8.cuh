@@ -1,0 +1,137 @@
+// sq_w8a8.cuh -- what the row quantisation (sq_w8a8_quant.cu) and the integer
+// product (sq_w8a8.cu) share: the plan of tiles over the experts' rows, and the
+// low-rank values as three bf16 terms.
+#pragma once
+
+#include <cstdint>
+
+#include "sq_device.cuh"
+
+namespace sq {
+
+constexpr int kI8Rank = 16;                       // rank of the int8 layer's low-rank branch
+constexpr int kLowParts = 3;                      // bf16 terms of an fp32 low-rank value
+constexpr int kLowRow = kLowParts * kI8Rank;      // bf16 values per token
+constexpr int kMaxExperts = 1024;
+
+// where a tile lies
+struct I8Tile {
+    int e;                    // expert
+    int row0, rows;           // first token and tokens of the tile
+    int wt;                   // tile along the weight (product only)
+};
+
+// The tiles of all experts in a row: expert e has ceil(rows / tok_tile) token tiles, each times
+// `wts` weight tiles; the token tile changes fastest, so that the tiles which share a weight
+// tile run together.  Offsets are clamped to [0, M] and to their running maximum, so that the
+// experts' rows never overlap or leave the matrix, whatever the offsets hold.
+struct I8Plan {
+    int32_t *start;           // [E + 1] first row of each expert (shared memory)
+    int32_t *prefix;          // [E + 1] token tiles before each expert
+    int E, wts, tok_tile;
+
+    // every thread of the CTA; offsets NULL: one expert with all M rows
+    __device__ __forceinline__ void build(const int32_t *__restrict__ offsets, int64_t M, int tid, int threads)
+    {
+        for (int i = tid; i <= E; i += threads) {
+            const int64_t o = offsets ? (int64_t)__ldg(offsets + i) : i == 0 ? 0 : M;
+            start[i] = (int32_t)(o < 0 ? 0 : o > M ? M : o);
+        }
+        __syncthreads();
+        if (tid < 32) {
+            int32_t top = 0, sum = 0;             // running maximum and token tiles up to here
+            for (int base = 0; base <= E; base += 32) {
+                const int i = base + tid;
+                int32_t v = i <= E ? start[i] : 0;
+#pragma unroll
+                for (int x = 1; x < 32; x <<= 1) {
+                    const int32_t up = __shfl_up_sync(0xffffffffu, v, x);
+                    v = tid >= x ? max(v, up) : v;
+                }
+                v = max(v, top);
+                const int32_t left = __shfl_up_sync(0xffffffffu, v, 1);
+                int32_t n = i == 0 || i > E ? 0 : (v - (tid == 0 ? top : left) + tok_tile - 1) / tok_tile;
+                top = __shfl_sync(0xffffffffu, v, 31);
+#pragma unroll
+                for (int x = 1; x < 32; x <<= 1) {
+                    const int32_t up = __shfl_up_sync(0xffffffffu, n, x);
+                    n += tid >= x ? up : 0;
+                }
+                n += sum;
+                sum = __shfl_sync(0xffffffffu, n, 31);
+                if (i <= E) {
+                    start[i] = v;
+                    prefix[i] = n;
+                }
+            }
+        }
+        __syncthreads();
+    }
+
+    __device__ __forceinline__ int tiles() const
+    {
+        return prefix[E] * wts;
+    }
+
+    // tile number `tile`, below tiles(); e: a role's own walk, starting at 0 (its tiles only grow)
+    __device__ __forceinline__ I8Tile find(int tile, int &e) const
+    {
+        while (tile >= prefix[e + 1] * wts)
+            ++e;
+        const int tts = prefix[e + 1] - prefix[e];
+        const int i = tile - prefix[e] * wts;
+        I8Tile t;
+        t.e = e;
+        t.wt = i / tts;
+        t.row0 = start[e] + (i % tts) * tok_tile;
+        t.rows = min(start[e + 1] - t.row0, tok_tile);
+        return t;
+    }
+};
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p)
+{
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+
+// four 8x8 matrices of 16-bit values from shared memory (each lane gives one row's address);
+// with TRANS each is transposed on the way
+template <bool TRANS>
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4])
+{
+    if (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t (&r)[4])
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+                 ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
+
+// c[16 x 8] += a[16 x 16] b[16 x 8], bf16 inputs, fp32 sums (one warp; the small low-rank
+// products only -- the large ones run on tcgen05)
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// v as the sum of three bf16 terms, largest first (24 significant bits: exact but for
+// subnormal remainders)
+__device__ __forceinline__ void split3(float v, uint32_t (&p)[kLowParts])
+{
+#pragma unroll
+    for (int i = 0; i < kLowParts; ++i) {
+        p[i] = f32_to_bf16_bits(v);
+        v = __fsub_rn(v, bf16_bits_to_f32(p[i]));
+    }
+}
+
+}  // namespace sq

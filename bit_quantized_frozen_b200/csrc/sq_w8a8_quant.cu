@@ -4,38 +4,53 @@
 //
 //   forward   r = H256 x            low = x lora_down   [M, 16]
 //   backward  r = RN(dy s_w)        low = dy lora_up    [M, 16]
-//   s = RN(max|r| / 127),  code = clamp(rint(RN(r RN(1 / s))), -127, 127)
+//   s = RN(max|r| / 127),  code = rint(RN(r RN(1 / s)))
 //
-// A scale below 2^-120 is stored as 0 with zero codes (1 / s would leave fp32's
-// range); a row with a NaN or an infinity in r gets the scale NaN, so its
-// outputs are NaN.  Each product is rounded once, in the order written, so the
-// codes are the same bits whatever kernel forms them.  With experts (E > 0) the
-// row's expert, found from the offsets, picks the lora and scale arrays.
+// A code never leaves [-127, 127]: |r| <= max|r| and the three roundings move
+// 127 by less than 2^-16.  A scale below 2^-120 is stored as 0 with zero codes
+// (1 / s would leave fp32's range); a row with a NaN or an infinity in r gets
+// the scale NaN, so its outputs are NaN.  Each product is rounded once, in the
+// order written, so the codes are the same bits in any kernel.
+//
+// One kernel for both directions and any number of rows.  A warp takes 8 rows x
+// 256 columns in registers: lane 4 g + q holds of row g the 16-byte pieces q,
+// q + 4, ..., q + 28 of the block, so that a load touches whole 64-byte runs,
+// strides 1, 2, 4 and 32, 64, 128 of the transform stay in a lane and strides 8
+// and 16 pair lanes q ^ 1 and q ^ 2.  The same words, as loaded, are the B
+// operand of mma m16n8k16 (8 rows, 16 values of K in the lanes' own order); the
+// A operand is the block's 256 x 16 low-rank factor from shared memory, its rows
+// picked in that order by ldmatrix.  A cluster of up to 8 CTAs with 8 warps each
+// covers K <= 16384, so a row group is read once, its maximum and low-rank sums
+// meet over distributed shared memory, and the codes leave from registers.  The
+// clusters are persistent: a warp keeps its block's factor in shared memory from
+// row group to row group (of one expert) and loads the next group while it
+// transforms this one.  Longer rows (backward, N > 16384) take their blocks in
+// turns and read them a second time for the codes.
 #include <cuda.h>
 
 #include "sq_device.cuh"
 #include "sq_kernels.h"
 #include "sq_ptx.cuh"
+#include "sq_w8a8.cuh"
 
 namespace sq {
 
-constexpr int kLow = 16;                          // rank of the int8 layer's low-rank branch
 constexpr uint32_t kInfBits = 0x7F800000u;
+constexpr int kQRows = 8;                         // rows of a group
+constexpr int kQWarps = 8;                        // warps of a CTA at most
+constexpr int kQMaxCluster = 8;
+constexpr int kQFactorBytes = kHad * kI8Rank * 2; // 8 KB: a block's factor
 
-// expert of row m: the e with offsets[e] <= m < offsets[e + 1], -1 if there is none.  Every
-// lane of the warp takes part; valid offsets do not decrease, and with others the answer is
-// still in range.  E == 0: one layer, expert 0 for every row.
-__device__ __forceinline__ int expert_of(const int32_t *__restrict__ offsets, int E, int64_t m, int lane)
-{
-    if (E == 0)
-        return 0;
-    int below = 0;
-    for (int i = 0; i <= E; i += 32)
-        below += __popc(__ballot_sync(0xffffffffu, i + lane <= E && (int64_t)__ldg(offsets + i + lane) <= m));
-    return below == 0 || below == E + 1 ? -1 : below - 1;
-}
+struct QShared {
+    uint32_t warp_max[kQWarps][kQRows];
+    float warp_low[kQWarps][kI8Rank * kQRows];
+    // from every CTA of the cluster, for even and odd groups
+    uint32_t max[2][kQMaxCluster][kQRows];
+    float low[2][kQMaxCluster][kI8Rank * kQRows]; // (the leader's is used)
+    int32_t start[kMaxExperts + 1], prefix[kMaxExperts + 1];
+};
 
-// scale and reciprocal of a row from the largest |r| (bit pattern, NaN and infinity on top)
+// scale and reciprocal of a row from the largest |r| (NaN and infinity on top)
 __device__ __forceinline__ void row_scale(uint32_t amax_bits, float &s, float &inv)
 {
     s = __fdiv_rn(__uint_as_float(amax_bits), 127.0f);
@@ -50,42 +65,153 @@ __device__ __forceinline__ void row_scale(uint32_t amax_bits, float &s, float &i
     }
 }
 
-__device__ __forceinline__ uint32_t code8(float r, float inv)
+// max(a, |b|, |c|), NaN if any is
+__device__ __forceinline__ float absmax3(float a, float b, float c)
 {
-    // (a NaN r comes with inv = 0: fminf and fmaxf drop the NaN, the code is some number)
-    return (uint32_t)__float2int_rn(fminf(fmaxf(__fmul_rn(r, inv), -127.0f), 127.0f)) & 0xFFu;
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+    return r;
 }
 
-__device__ __forceinline__ uint32_t abs_bits(float v)
+// 16 bytes, or 16 zero bytes with live = false (src is then not read)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live)
 {
-    return __float_as_uint(v) & 0x7FFFFFFFu;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 
-// sums a[0..15] over the 32 lanes; lane l returns the total of a[l / 2]
-__device__ __forceinline__ float reduce16(float (&a)[16], int lane)
+__device__ __forceinline__ void cp_async_wait_all()
+{
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// a 16-byte chunk (factor row k, half h) of a block sits at chunk 2 k + h with bits 0 and 2
+// flipped by bits 3 and 4 of k: the eight rows an ldmatrix matrix takes (k = 8 q + b and
+// the next, q = 0..3) then lie in eight different bank groups
+__device__ __forceinline__ uint32_t factor_chunk(uint32_t c)
+{
+    const uint32_t q = c >> 4;                    // (k >> 3)
+    return c ^ ((q & 1u) | ((q & 2u) << 1));
+}
+
+// the lane's pieces q + 4 j of its row, x at piece q; the first `pieces` of them (8, or 4 in a
+// half block at the end of a row), the others 0
+__device__ __forceinline__ void load_block(const uint16_t *__restrict__ x, int pieces, uint4 (&w)[8])
 {
 #pragma unroll
-    for (int h = 8; h >= 1; h >>= 1) {            // lanes with bit 2h keep the upper half
-        const bool up = lane & (2 * h);
+    for (int j = 0; j < 8; ++j)
+        w[j] = j < pieces ? __ldg(reinterpret_cast<const uint4 *>(x) + 4 * j) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+// acc[16 ranks x 8 rows] += factor^T x of the block
+__device__ __forceinline__ void low_block(const uint4 (&w)[8], uint32_t factor, int lane, float (&acc)[4])
+{
+    const uint32_t m = lane >> 3, s = lane & 7;
 #pragma unroll
-        for (int i = 0; i < h; ++i) {
-            const float mine = up ? a[i + h] : a[i];
-            const float other = __shfl_xor_sync(0xffffffffu, up ? a[i] : a[i + h], 2 * h);
-            a[i] = __fadd_rn(mine, other);
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t k = 8 * ((s >> 1) + 4 * j) + 4 * h + (s & 1) + 2 * (m >> 1);
+            uint32_t a[4];
+            ldmatrix_x4<true>(factor + 16 * factor_chunk(2 * k + (m & 1)), a);
+            mma_16816(acc, a, h ? w[j].z : w[j].x, h ? w[j].w : w[j].y);
         }
-    }
-    return __fadd_rn(a[0], __shfl_xor_sync(0xffffffffu, a[0], 1));
 }
 
-// a[j] += x * (16 bf16 of one row of a low-rank factor)
-__device__ __forceinline__ void low_fma(float x, const uint16_t *__restrict__ row, float (&a)[16])
+// the lane's 64 values as pairs p[4 j + i], widened from bf16
+__device__ __forceinline__ void widen(const uint4 (&w)[8], uint64_t (&p)[32])
 {
-    const uint4 p = __ldg(reinterpret_cast<const uint4 *>(row)), q = __ldg(reinterpret_cast<const uint4 *>(row) + 1);
-    const uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        a[2 * j] = __fmaf_rn(x, __uint_as_float(w[j] << 16), a[2 * j]);
-        a[2 * j + 1] = __fmaf_rn(x, __uint_as_float(w[j] & 0xFFFF0000u), a[2 * j + 1]);
+        const uint32_t v[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            p[4 * j + i] = f2_pack(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xFFFF0000u));
+    }
+}
+
+// H256 without the final 1/16, strides 1, 2, 4 | 8, 16 | 32, 64, 128
+__device__ __forceinline__ void fwht_rows8(uint64_t (&p)[32], int lane)
+{
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        float a, b;
+        f2_unpack(p[j], a, b);
+        p[j] = f2_pack(__fadd_rn(a, b), __fsub_rn(a, b));
+    }
+#pragma unroll
+    for (int h = 1; h <= 2; h <<= 1)              // strides 2, 4
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if ((j & h) == 0) {
+                const uint64_t a = p[j], b = p[j + h];
+                p[j] = f2_add(a, b);
+                p[j + h] = f2_sub(a, b);
+            }
+#pragma unroll
+    for (int x = 1; x <= 2; x <<= 1) {            // strides 8, 16
+        const float sg = (lane & x) == 0 ? 1.0f : -1.0f;
+        const uint64_t sg2 = f2_pack(sg, sg);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            float lo, hi;
+            f2_unpack(p[j], lo, hi);
+            const uint64_t o = f2_pack(__shfl_xor_sync(0xffffffffu, lo, x), __shfl_xor_sync(0xffffffffu, hi, x));
+            p[j] = f2_fma(sg2, p[j], o);          // lower lane own + partner, upper partner - own
+        }
+    }
+#pragma unroll
+    for (int h = 4; h <= 16; h <<= 1)             // strides 32, 64, 128
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if ((j & h) == 0) {
+                const uint64_t a = p[j], b = p[j + h];
+                p[j] = f2_add(a, b);
+                p[j + h] = f2_sub(a, b);
+            }
+}
+
+// p *= the block's channel scales (shared memory, 256 floats)
+__device__ __forceinline__ void scale_rows8(uint64_t (&p)[32], const float *sw, int q)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 v = *reinterpret_cast<const float4 *>(sw + 8 * (q + 4 * j) + 4 * i);
+            p[4 * j + 2 * i] = f2_mul(p[4 * j + 2 * i], f2_pack(v.x, v.y));
+            p[4 * j + 2 * i + 1] = f2_mul(p[4 * j + 2 * i + 1], f2_pack(v.z, v.w));
+        }
+}
+
+// the codes of the lane's values: RN(p inv) + 1.5 2^23 rounds to the integer, whose low byte
+// is then the value's low byte (finite rows; |RN(p inv)| < 128).  The product is the scalar
+// instruction: a packed product and sum in a row come out fused, rounded once instead of
+// twice, which moves the values that RN puts on a tie.
+__device__ __forceinline__ void store_codes(const uint64_t (&p)[32], float inv, int pieces, int8_t *dst)
+{
+    auto scaled = [&](uint64_t v, uint32_t &a, uint32_t &b) {
+        float x, y;
+        f2_unpack(v, x, y);
+        a = __float_as_uint(__fadd_rn(__fmul_rn(x, inv), 12582912.0f));
+        b = __float_as_uint(__fadd_rn(__fmul_rn(y, inv), 12582912.0f));
+    };
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        uint32_t w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t a, b, c, d;
+            scaled(p[4 * j + 2 * i], a, b);
+            scaled(p[4 * j + 2 * i + 1], c, d);
+            w[i] = __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+        }
+        if (j < pieces)
+            *reinterpret_cast<uint2 *>(dst + 32 * j) = make_uint2(w[0], w[1]);
     }
 }
 
@@ -95,7 +221,7 @@ __device__ __forceinline__ void begin_call(const I8QuantArgs &a)
     for (int i = threadIdx.x; i < a.n_counters; i += blockDim.x)
         a.counters[i] = 0u;
     bool bad = false;
-    for (int i = threadIdx.x; i <= a.E && a.E > 0; i += blockDim.x) {
+    for (int i = threadIdx.x; a.E > 0 && i <= a.E; i += blockDim.x) {
         const int32_t o = a.offsets[i];
         bad |= o < 0 || o > a.M || (i > 0 && o < a.offsets[i - 1]);
     }
@@ -110,211 +236,275 @@ __device__ __forceinline__ void begin_call(const I8QuantArgs &a)
     }
 }
 
-// rows of y that belong to no expert become 0
-__device__ __forceinline__ void zero_row(const I8QuantArgs &a, int64_t m)
+template <bool BWD, bool TURNS>
+__global__ void __launch_bounds__(32 * kQWarps, 2) i8_quant_kernel(const I8QuantArgs a, int cluster)
 {
-    if (!a.y_zero)
-        return;
-    uint4 *row = reinterpret_cast<uint4 *>(a.y_zero + m * a.y_row_bytes);
-    for (int64_t i = threadIdx.x; i < a.y_row_bytes / 16; i += blockDim.x)
-        row[i] = make_uint4(0u, 0u, 0u, 0u);
-}
+    extern __shared__ __align__(16) uint8_t q_smem[];
+    __shared__ QShared sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    const int g = lane >> 2, q = lane & 3;
+    const int rank = cluster > 1 ? (int)cluster_ctarank() : 0;
+    const int unit = (int)blockIdx.x / cluster, units = (int)gridDim.x / cluster;
+    const int nb = (int)((a.K + kHad - 1) / kHad);
+    const int lanes_of_k = cluster * warps;       // blocks a cluster holds at once
+    const int block0 = rank * warps + warp;       // this warp's (first) block
+    // the warp's factor and channel scales
+    uint8_t *my_factor = q_smem + warp * kQFactorBytes;
+    float *my_scale = reinterpret_cast<float *>(q_smem + warps * kQFactorBytes) + warp * kHad;
+    const bool with_low = a.low != nullptr;
 
-// the row's partial maxima and low-rank sums of the CTA's warps, combined in order
-struct RowShared {
-    uint32_t amax[32];
-    float low[32][kLow];
-};
-
-__device__ __forceinline__ uint32_t combine_row(const I8QuantArgs &a, RowShared &sh, int64_t m, uint32_t amax,
-                                                float (&low)[16], int warps)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    amax = __reduce_max_sync(0xffffffffu, amax);
-    if (lane == 0)
-        sh.amax[warp] = amax;
-    if (a.low) {
-        const float v = reduce16(low, lane);
-        if ((lane & 1) == 0)
-            sh.low[warp][lane >> 1] = v;
-    }
-    __syncthreads();
-    amax = 0;
-    for (int w = 0; w < warps; ++w)
-        amax = max(amax, sh.amax[w]);
-    if (a.low && threadIdx.x < kLow) {
-        float v = sh.low[0][threadIdx.x];
-        for (int w = 1; w < warps; ++w)
-            v = __fadd_rn(v, sh.low[w][threadIdx.x]);
-        if (SQ_DCHECK(m < a.M, a.status))
-            a.low[m * kLow + threadIdx.x] = v;
-    }
-    if (threadIdx.x == 0 && a.finite_check && amax >= kInfBits)
-        atomicOr(a.status, kStatusNonfinite);
-    return amax;
-}
-
-// ---------------------------------------------------------------------------
-// Forward, one row per CTA, UNITS 256-blocks per warp held in registers: x is
-// read once.
-// ---------------------------------------------------------------------------
-template <int UNITS>
-__global__ void __launch_bounds__(1024) i8_quant_row_kernel(const I8QuantArgs a)
-{
-    __shared__ RowShared sh;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int64_t m = blockIdx.x;
-    const int nb = (int)(a.K / kHad);
     grid_dep_launch();
     if (blockIdx.x == 0)
         begin_call(a);
-    const int e = expert_of(a.offsets, a.E, m, lane);
-    if (e < 0) {
-        zero_row(a, m);
-        return;
-    }
-    const uint16_t *factor = a.factor + (int64_t)e * a.K * kLow;
-    float v[UNITS][8];
-    float low[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        low[i] = 0.0f;
-#pragma unroll
-    for (int u = 0; u < UNITS; ++u) {
-        const int b = warp + u * warps;
-        uint2 p = make_uint2(0u, 0u), q = p;
-        if (b < nb) {
-            const uint2 *src = reinterpret_cast<const uint2 *>(a.x + m * a.K + (int64_t)b * kHad);
-            p = __ldg(src + lane);
-            q = __ldg(src + 32 + lane);
-        }
-        const uint32_t w[4] = {p.x, p.y, q.x, q.y};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[u][2 * j] = __uint_as_float(w[j] << 16);
-            v[u][2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    I8Plan plan;
+    plan.start = sh.start;
+    plan.prefix = sh.prefix;
+    plan.E = a.E > 0 ? a.E : 1;
+    plan.wts = 1;
+    plan.tok_tile = kQRows;
+    plan.build(a.E > 0 ? a.offsets : nullptr, a.M, tid, blockDim.x);
+    const int tiles = plan.tiles();
+    if (cluster > 1)
+        cluster_sync();                               // every CTA of the cluster has started
+
+    // rows of no expert: 0
+    if (a.y_zero) {
+        const int64_t head = plan.start[0], tail = a.M - plan.start[plan.E], n16 = a.y_row_bytes / 16;
+        for (int64_t i = blockIdx.x; i < head + tail; i += gridDim.x) {
+            const int64_t m = i < head ? i : plan.start[plan.E] + (i - head);
+            uint4 *row = reinterpret_cast<uint4 *>(a.y_zero + m * a.y_row_bytes);
+            for (int64_t c = tid; c < n16; c += blockDim.x)
+                if (SQ_DCHECK(m < a.M, a.status))
+                    row[c] = make_uint4(0u, 0u, 0u, 0u);
         }
     }
-    uint32_t amax = 0;
+
+    // columns of block b: 256, 128 (the last one, backward), or 0 behind the row's end
+    auto columns = [&](int b) {
+        const int64_t left = a.K - (int64_t)b * kHad;
+        return left <= 0 ? 0 : left < kHad ? (int)left : kHad;
+    };
+    // factor and scales of block b of expert e on their way into shared memory, 0 behind the end
+    auto fetch = [&](int e, int b) {
+        const int cols = columns(b);
+        if (with_low) {
+            const uint8_t *src =
+                reinterpret_cast<const uint8_t *>(a.factor + ((int64_t)e * a.K + (int64_t)b * kHad) * kI8Rank);
+#pragma unroll 4
+            for (uint32_t c = lane; c < kQFactorBytes / 16; c += 32)
+                cp_async16(smem_u32(my_factor) + 16 * factor_chunk(c), (int)c < 2 * cols ? src + 16 * c : (const void *)a.factor,
+                           (int)c < 2 * cols);
+        }
+        if (BWD) {
+            const float *src = a.col_scale + (int64_t)e * a.K + (int64_t)b * kHad;
+            for (int c = lane; c < kHad / 4; c += 32)
+                cp_async16(smem_u32(my_scale) + 16 * c, 4 * c < cols ? src + 4 * c : a.col_scale, 4 * c < cols);
+        }
+    };
+    auto fetched = [&]() {
+        cp_async_wait_all();
+        __syncwarp();
+    };
+    // this lane's first piece of its row in block b, and how many it has
+    auto pieces_of = [&](const I8Tile &t, int b) { return g < t.rows ? columns(b) / 32 : 0; };
+    auto row_of = [&](const I8Tile &t, int b) {
+        return a.x + (int64_t)(t.row0 + g) * a.K + (int64_t)b * kHad + 8 * q;
+    };
+    auto spread = [&](const uint4(&w)[8], uint64_t(&p)[32]) {
+        widen(w, p);
+        if (BWD)
+            scale_rows8(p, my_scale, q);
+        else
+            fwht_rows8(p, lane);
+    };
+
+    int e = 0, have = -1;                             // expert walked to; expert whose factor is here
+    uint4 w[8];
+    I8Tile t = {0, 0, 0, 0};
+    if (unit < tiles) {
+        t = plan.find(unit, e);
+        if (!TURNS)
+            load_block(row_of(t, block0), pieces_of(t, block0), w);
+    }
+    int parity = 0;
+    for (int tile = unit; tile < tiles; tile += units, parity ^= 1) {
+        const bool live = g < t.rows;
+        float low[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float amax = 0.0f;
+        uint64_t p[32];
+        I8Tile next = t;
+        if (TURNS) {
+            for (int b = block0; b < nb; b += lanes_of_k) {
+                fetch(t.e, b);
+                load_block(row_of(t, b), pieces_of(t, b), w);
+                fetched();
+                if (with_low)
+                    low_block(w, smem_u32(my_factor), lane, low);
+                spread(w, p);
 #pragma unroll
-    for (int u = 0; u < UNITS; ++u) {
-        const int b = warp + u * warps;
-        if (b >= nb)
-            continue;
-        if (a.low) {
+                for (int j = 0; j < 32; ++j) {
+                    float x0, x1;
+                    f2_unpack(p[j], x0, x1);
+                    amax = absmax3(amax, x0, x1);
+                }
+                __syncwarp();                         // the next block's factor takes this one's place
+            }
+        } else {
+            if (have != t.e) {
+                __syncwarp();
+                fetch(t.e, block0);
+                fetched();
+                have = t.e;
+            }
+            if (with_low && block0 < nb)
+                low_block(w, smem_u32(my_factor), lane, low);
+            spread(w, p);
+            if (tile + units < tiles) {               // the next group's values, while this one's are transformed
+                next = plan.find(tile + units, e);
+                load_block(row_of(next, block0), pieces_of(next, block0), w);
+            }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int k = b * kHad + 4 * lane + (j & 3) + 128 * (j >> 2);
-                low_fma(v[u][j], factor + (int64_t)k * kLow, low);
+            for (int j = 0; j < 32; ++j) {
+                float x0, x1;
+                f2_unpack(p[j], x0, x1);
+                amax = absmax3(amax, x0, x1);
             }
         }
-        fwht256_warp(v[u], lane);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            amax = max(amax, abs_bits(v[u][j]));
-    }
-    amax = combine_row(a, sh, m, amax, low, warps);
-    float s, inv;
-    row_scale(amax, s, inv);
-    if (threadIdx.x == 0 && SQ_DCHECK(m < a.M, a.status))
-        a.scales[m] = s;
-#pragma unroll
-    for (int u = 0; u < UNITS; ++u) {
-        const int b = warp + u * warps;
-        if (b >= nb || !SQ_DCHECK(m < a.M, a.status))
-            continue;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(a.codes + m * a.K + (int64_t)b * kHad);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            dst[lane + 32 * h] = code8(v[u][4 * h], inv) | code8(v[u][4 * h + 1], inv) << 8 |
-                                 code8(v[u][4 * h + 2], inv) << 16 | code8(v[u][4 * h + 3], inv) << 24;
-    }
-}
-
-// ---------------------------------------------------------------------------
-// Backward, one row per CTA: a pass for the maximum and the low-rank input, a
-// pass for the codes (the row comes from L1 or L2 the second time).
-// ---------------------------------------------------------------------------
-constexpr int kBwdThreads = 256;
-
-__device__ __forceinline__ void scaled8(const uint16_t *__restrict__ x, const float *__restrict__ s, float (&raw)[8],
-                                        float (&r)[8])
-{
-    const uint4 p = __ldg(reinterpret_cast<const uint4 *>(x));
-    const float4 s0 = __ldg(reinterpret_cast<const float4 *>(s)), s1 = __ldg(reinterpret_cast<const float4 *>(s) + 1);
-    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
-    const float sc[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        raw[2 * j] = __uint_as_float(w[j] << 16);
-        raw[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        r[j] = __fmul_rn(raw[j], sc[j]);
-}
-
-__global__ void __launch_bounds__(kBwdThreads) i8_quant_row_bwd_kernel(const I8QuantArgs a)
-{
-    __shared__ RowShared sh;
-    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    const int64_t m = blockIdx.x;
-    grid_dep_launch();
-    if (blockIdx.x == 0)
-        begin_call(a);
-    const int e = expert_of(a.offsets, a.E, m, lane);
-    if (e < 0) {
-        zero_row(a, m);
-        return;
-    }
-    const uint16_t *x = a.x + m * a.K;
-    const float *sw = a.col_scale + (int64_t)e * a.K;
-    const uint16_t *factor = a.factor + (int64_t)e * a.K * kLow;
-    float low[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        low[i] = 0.0f;
-    uint32_t amax = 0;
-    for (int64_t k = 8 * threadIdx.x; k < a.K; k += 8 * kBwdThreads) {
-        float raw[8], r[8];
-        scaled8(x + k, sw + k, raw, r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            amax = max(amax, abs_bits(r[j]));
-            if (a.low)
-                low_fma(raw[j], factor + (k + j) * kLow, low);
+        // the row's maximum: 4 lanes, the CTA's warps, the cluster's CTAs (max of bit patterns:
+        // not below zero, NaN above infinity above all others)
+        uint32_t m = __float_as_uint(amax);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        if (q == 0)
+            sh.warp_max[warp][g] = m;
+        if (with_low) {                               // low[0..3]: ranks g, g + 8; rows 2 q, 2 q + 1
+            float *wl = sh.warp_low[warp];
+            wl[(2 * q) * kI8Rank + g] = low[0];
+            wl[(2 * q + 1) * kI8Rank + g] = low[1];
+            wl[(2 * q) * kI8Rank + g + 8] = low[2];
+            wl[(2 * q + 1) * kI8Rank + g + 8] = low[3];
         }
-    }
-    amax = combine_row(a, sh, m, amax, low, warps);
-    float s, inv;
-    row_scale(amax, s, inv);
-    if (threadIdx.x == 0 && SQ_DCHECK(m < a.M, a.status))
-        a.scales[m] = s;
-    for (int64_t k = 8 * threadIdx.x; k < a.K; k += 8 * kBwdThreads) {
-        float raw[8], r[8];
-        scaled8(x + k, sw + k, raw, r);
-        uint32_t w[2] = {0u, 0u};
+        __syncthreads();
+        if (tid < kQRows) {
+            uint32_t v = 0;
+            for (int i = 0; i < warps; ++i)
+                v = max(v, sh.warp_max[i][tid]);
+            if (cluster == 1)
+                sh.max[parity][0][tid] = v;
+            else
+                for (int r = 0; r < cluster; ++r)
+                    st_cluster(mapa_shared(smem_u32(&sh.max[parity][rank][tid]), r), v);
+        }
+        if (with_low)
+            for (int i = tid; i < kI8Rank * kQRows; i += blockDim.x) {
+                float v = sh.warp_low[0][i];
+                for (int k = 1; k < warps; ++k)
+                    v = __fadd_rn(v, sh.warp_low[k][i]);
+                if (cluster == 1)
+                    sh.low[parity][0][i] = v;
+                else
+                    st_cluster(mapa_shared(smem_u32(&sh.low[parity][rank][i]), 0), __float_as_uint(v));
+            }
+        __syncwarp();
+        if (cluster > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+        if (rank == 0 && with_low)
+            for (int i = tid; i < kI8Rank * kQRows; i += blockDim.x) {
+                float v = sh.low[parity][0][i];
+                for (int r = 1; r < cluster; ++r)
+                    v = __fadd_rn(v, sh.low[parity][r][i]);
+                const int row = i / kI8Rank, k = i % kI8Rank;
+                if (row < t.rows && SQ_DCHECK(t.row0 + row < a.M, a.status)) {
+                    uint32_t part[kLowParts];
+                    split3(v, part);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            w[j >> 2] |= code8(r[j], inv) << (8 * (j & 3));
-        if (SQ_DCHECK(m < a.M, a.status))
-            *reinterpret_cast<uint2 *>(a.codes + m * a.K + k) = make_uint2(w[0], w[1]);
+                    for (int j = 0; j < kLowParts; ++j)
+                        a.low[(int64_t)(t.row0 + row) * kLowRow + j * kI8Rank + k] = (uint16_t)part[j];
+                }
+            }
+        uint32_t top = 0;
+        for (int r = 0; r < cluster; ++r)
+            top = max(top, sh.max[parity][r][g]);
+        if (!BWD && top < kInfBits)                   // the transform's 1/16 (exact where the scale is not 0)
+            top = __float_as_uint(__fmul_rn(__uint_as_float(top), 0.0625f));
+        float s, inv;
+        row_scale(top, s, inv);
+        if (!BWD)
+            inv *= 0.0625f;                           // exact: 1 / s is above 2^-122
+        if (rank == 0 && tid < 32 && q == 0 && live && SQ_DCHECK(t.row0 + g < a.M, a.status)) {
+            a.scales[t.row0 + g] = s;
+            if (a.finite_check && top >= kInfBits)
+                atomicOr(a.status, kStatusNonfinite);
+        }
+        if (TURNS) {
+            for (int b = block0; b < nb; b += lanes_of_k) {
+                if (BWD)
+                    fetch(t.e, b);
+                load_block(row_of(t, b), pieces_of(t, b), w);
+                fetched();
+                spread(w, p);
+                if (live && SQ_DCHECK(t.row0 + g < a.M, a.status))
+                    store_codes(p, inv, pieces_of(t, b),
+                                a.codes + (int64_t)(t.row0 + g) * a.K + (int64_t)b * kHad + 8 * q);
+                __syncwarp();
+            }
+        } else if (live && SQ_DCHECK(t.row0 + g < a.M, a.status)) {
+            store_codes(p, inv, pieces_of(t, block0), a.codes + (int64_t)(t.row0 + g) * a.K + (int64_t)block0 * kHad + 8 * q);
+        }
+        t = TURNS && tile + units < tiles ? plan.find(tile + units, e) : next;
     }
+}
+
+template <bool BWD, bool TURNS>
+static cudaError_t launch_quant_v(const I8QuantArgs &a, int cluster, int warps, int sms, cudaStream_t s)
+{
+    constexpr int kMaxDev = 64;
+    static unsigned long long attr_ctx[kMaxDev];
+    constexpr int kMaxSmem = kQWarps * (kQFactorBytes + kHad * 4);
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev)
+        return cudaErrorInvalidDevice;
+    const unsigned long long ctx = current_context_id();
+    if (ctx == 0 || attr_ctx[dev] != ctx) {
+        cudaError_t e = cudaFuncSetAttribute(i8_quant_kernel<BWD, TURNS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kMaxSmem);
+        if (e != cudaSuccess)
+            return e;
+        attr_ctx[dev] = ctx;
+    }
+    // persistent: two CTAs per SM
+    const int64_t groups = (a.M + kQRows - 1) / kQRows + a.E;
+    const int64_t room = 2 * sms / cluster;
+    const int units = (int)(groups < room ? groups : room);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * cluster));
+    cfg.blockDim = dim3(32 * warps);
+    cfg.dynamicSmemBytes = warps * (kQFactorBytes + (BWD ? kHad * 4 : 0));
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)cluster;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, i8_quant_kernel<BWD, TURNS>, a, cluster);
 }
 
 cudaError_t launch_i8_quant(const I8QuantArgs &a, bool bwd, int sms, cudaStream_t s)
 {
-    (void)sms;
-    if (bwd) {
-        i8_quant_row_bwd_kernel<<<(unsigned)a.M, kBwdThreads, 0, s>>>(a);
-        return cudaGetLastError();
-    }
-    const int nb = (int)(a.K / kHad);             // <= 64
-    if (nb <= 32)
-        i8_quant_row_kernel<1><<<(unsigned)a.M, 32 * nb, 0, s>>>(a);
-    else
-        i8_quant_row_kernel<2><<<(unsigned)a.M, 32 * ((nb + 1) / 2), 0, s>>>(a);
-    return cudaGetLastError();
+    const int nb = (int)(a.K + kHad - 1) / kHad;
+    int cluster = (nb + kQWarps - 1) / kQWarps;
+    cluster = cluster < kQMaxCluster ? cluster : kQMaxCluster;
+    int warps = (nb + cluster - 1) / cluster;
+    const bool turns = warps > kQWarps;
+    warps = turns ? kQWarps : warps;
+    if (bwd)
+        return turns ? launch_quant_v<true, true>(a, cluster, warps, sms, s)
+                     : launch_quant_v<true, false>(a, cluster, warps, sms, s);
+    return launch_quant_v<false, false>(a, cluster, warps, sms, s);
 }
 
 }  // namespace sq
