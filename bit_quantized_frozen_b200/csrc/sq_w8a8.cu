@@ -23,10 +23,14 @@
 // Weight tiles of the first stages are fetched before the kernel waits for the
 // quantisation kernel in front of it.
 //
-// Few tiles: each is split over the summed axis into as many items as there are
-// idle CTAs; an item writes its 32-bit partial sums to its own slab and counts up,
-// and the one that counts last adds them all and finishes the tile.  Integer sums
-// do not depend on the order, so the result does not either.
+// A tile's MMAs and loads cover only the boxes of tokens that it has (the instruction's
+// column count is set per tile), so that an expert with few rows costs few.
+//
+// Where the last round of tiles would leave many SMs idle, the work is dealt out in
+// equal shares of the summed axis instead (I8Deal): a unit stores the 32-bit partial
+// sums of a tile that it shares, counts up, and the one that counts last adds them
+// all and finishes the tile.  Integer sums do not depend on the order, so neither
+// does the result.
 #include <cuda.h>
 
 #include "sq_device.cuh"
@@ -37,12 +41,13 @@
 namespace sq {
 
 constexpr int kChunk = 128;                       // summed values (bytes) per stage
-constexpr int kMinSplitChunks = 4;                // a split sums at least 512 values
+constexpr int kMinSplitChunks = 4;                // a unit's share is at least this many
 
 template <int NT, int CG, bool BWD>
 struct I8Cfg {
     static constexpr int kLaneTile = 128 * CG;                       // A rows of the tile
     static constexpr int kColsPerCta = NT / CG;                      // B rows (or columns) each CTA loads
+    static constexpr int kBox = NT >= 64 ? 32 : 16;                  // token rows per TMA box (forward)
     static constexpr int kABytes = 128 * kChunk;
     static constexpr int kBBytes = kColsPerCta * kChunk;
     static constexpr int kStageBytes = kABytes + kBBytes;
@@ -65,7 +70,7 @@ struct I8Cfg {
     static constexpr int kSmemBytes = kBarOff + 8 * kNumBars + 32 + 1024;
     static constexpr uint32_t kTmemCols = 2 * NT < 32 ? 32 : 2 * NT;
     static constexpr uint32_t kIdesc = (2u << 4) | (1u << 7) | (1u << 10) | (BWD ? 1u << 16 : 0u) |
-                                       ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(kLaneTile >> 4) << 24);
+                                       ((uint32_t)(kLaneTile >> 4) << 24);   // + columns / 8 << 17
     static constexpr uint32_t kBStep16 = BWD ? (32u * 128u) >> 4 : 2u;   // B descriptor step per MMA (32 values)
 };
 
@@ -82,20 +87,77 @@ struct I8Args {
     int64_t M, N, K;          // N, K of one expert
     int E;
     int out_bf16;
-    int slab_items;           // slabs there is room for
+    int slab_units;           // units there are slabs for (two each), 0: none
 };
 
-// Items per tile: with at most half as many tiles as units (CTAs or CTA pairs), the summed
-// axis is split so that every unit has one, into at least kMinSplitChunks chunks each.
-__host__ __device__ __forceinline__ int i8_splits(int tiles, int units, int chunks, int slab_items)
+// chunks' worth of time that joining split tiles of nt columns costs (a fixed latency and the slab)
+__host__ __device__ constexpr int split_cost(int nt)
 {
-    if (tiles <= 0)
-        return 1;
-    int s = units / tiles;
-    s = s < chunks / kMinSplitChunks ? s : chunks / kMinSplitChunks;
-    s = s < slab_items / tiles ? s : slab_items / tiles;
-    return s < 1 ? 1 : s;
+    return 8 + nt / 16;
 }
+
+// How the tiles are spread over the units (CTAs or CTA pairs).  Whole tiles in turn, unless the
+// last, partly filled round wastes more than `cost` chunks a unit: then the chunks of all tiles
+// are dealt out evenly as one row of chunks, and a tile that crosses a border is summed from
+// the partial sums of its units.
+struct I8Deal {
+    int tiles, units, chunks;
+    bool even;                // chunks dealt out evenly over `units`
+
+    __host__ __device__ __forceinline__ I8Deal(int tiles_, int units_, int chunks_, int cost, bool slabs)
+        : tiles(tiles_), units(units_), chunks(chunks_), even(false)
+    {
+        if (!slabs || tiles <= 0 || tiles >= 8 * units)
+            return;
+        const int rounds = (tiles + units - 1) / units;
+        if ((rounds * units - tiles) * (int64_t)chunks <= (int64_t)cost * units)
+            return;
+        const int64_t most = (int64_t)tiles * chunks / kMinSplitChunks;
+        units = most < units ? (most < 1 ? 1 : (int)most) : units;
+        even = true;
+    }
+
+    // even: first chunk of unit u; the unit that has chunk i
+    __host__ __device__ __forceinline__ int begin(int u) const
+    {
+        return (int)((int64_t)tiles * chunks * u / units);
+    }
+    __device__ __forceinline__ int owner(int i) const
+    {
+        return (int)(((int64_t)(i + 1) * units - 1) / ((int64_t)tiles * chunks));
+    }
+};
+
+// one unit's way through its work: (tile, chunks c0 .. c1 - 1) in turn
+struct I8Walk {
+    int pos, end, step, chunks;
+    bool even;
+    int tile, c0, c1;
+
+    __device__ __forceinline__ I8Walk(const I8Deal &d, int unit) : chunks(d.chunks), even(d.even), tile(0), c0(0), c1(0)
+    {
+        pos = even ? (unit < d.units ? d.begin(unit) : 0) : unit;
+        end = even ? (unit < d.units ? d.begin(unit + 1) : 0) : d.tiles;
+        step = d.units;
+    }
+    __device__ __forceinline__ bool next()
+    {
+        if (pos >= end)
+            return false;
+        if (even) {
+            tile = pos / chunks;
+            c0 = pos - tile * chunks;
+            c1 = min(chunks, c0 + end - pos);
+            pos += c1 - c0;
+        } else {
+            tile = pos;
+            c0 = 0;
+            c1 = chunks;
+            pos += step;
+        }
+        return true;
+    }
+};
 
 template <int CG>
 __device__ __forceinline__ bool acc_wait(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag,
@@ -106,7 +168,8 @@ __device__ __forceinline__ bool acc_wait(uint32_t bar, uint32_t parity, volatile
 
 template <int NT, int CG, bool BWD>
 __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>::kThreads, 1)
-    sq_i8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const I8Args args)
+    sq_i8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                 const __grid_constant__ CUtensorMap tmBox, const I8Args args)
 {
     using Cfg = I8Cfg<NT, CG, BWD>;
     extern __shared__ uint8_t smem_raw[];
@@ -155,6 +218,8 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
     if (warp == kProducer && lane == 0) {
         prefetch_tmap(&tmA);
         prefetch_tmap(&tmB);
+        if (!BWD)
+            prefetch_tmap(&tmBox);
     }
     // the offsets are an input of the call: they are there before the kernel in front starts
     I8Plan plan;
@@ -173,69 +238,74 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
     const uint32_t tmem_base = *tmem_holder;
 
     const int tiles = plan.tiles();
-    const int units = (int)gridDim.x / CG;
     const int unit = (int)blockIdx.x / CG;
-    const int chunks = (int)((BWD ? args.N : args.K) / kChunk);
-    const int splits = i8_splits(tiles, units, chunks, args.slab_items);
-    const int items = tiles * splits;
+    const int units = (int)gridDim.x / CG;
+    const I8Deal deal(tiles, args.slab_units > 0 ? min(units, args.slab_units) : units,
+                      (int)((BWD ? args.N : args.K) / kChunk), split_cost(NT), args.slab_units > 0);
+    // columns of the accumulator a tile uses (forward: its tokens, in whole boxes of both CTAs)
+    auto columns = [&](const I8Tile &t) {
+        return BWD ? NT : (t.rows + CG * Cfg::kBox - 1) / (CG * Cfg::kBox) * (CG * Cfg::kBox);
+    };
 
     if (warp == kProducer) {
         // ------------------------------------------------------------ producer (every CTA)
         if (lane == 0) {
             // weight operand of stage `stage`, chunk c of tile t, and the row operand
+            auto load = [&](const void *tm, uint32_t dst, int x, int y, uint32_t bar) {
+                if (CG == 2)
+                    tma_load_2d_pair(dst, tm, x, y, bar);
+                else
+                    tma_load_2d(dst, tm, x, y, bar);
+            };
             auto load_w = [&](int stage, const I8Tile &t, int c) {
                 const uint32_t sA = smem_u32(smem + stage * Cfg::kStageBytes), fb = bar_full + 8 * stage;
                 const int n0 = t.e * (int)args.N;
-                const uint32_t dst = BWD ? sA + Cfg::kABytes : sA;
-                const void *tm = BWD ? &tmB : &tmA;
-                const int x = BWD ? t.wt * NT + (int)rank * Cfg::kColsPerCta : c * kChunk;
-                const int y = BWD ? n0 + c * kChunk : n0 + t.wt * Cfg::kLaneTile + (int)rank * 128;
-                if (CG == 2)
-                    tma_load_2d_pair(dst, tm, x, y, fb);
+                if (leader)
+                    mbar_arrive_expect_tx(fb, CG * Cfg::kABytes + columns(t) * kChunk);
+                if (BWD)
+                    load(&tmB, sA + Cfg::kABytes, t.wt * NT + (int)rank * Cfg::kColsPerCta, n0 + c * kChunk, fb);
                 else
-                    tma_load_2d(dst, tm, x, y, fb);
+                    load(&tmA, sA, c * kChunk, n0 + t.wt * Cfg::kLaneTile + (int)rank * 128, fb);
             };
             auto load_x = [&](int stage, const I8Tile &t, int c) {
                 const uint32_t sA = smem_u32(smem + stage * Cfg::kStageBytes), fb = bar_full + 8 * stage;
-                const uint32_t dst = BWD ? sA : sA + Cfg::kABytes;
-                const void *tm = BWD ? &tmA : &tmB;
-                const int y = t.row0 + (int)rank * (BWD ? 128 : Cfg::kColsPerCta);
-                if (CG == 2)
-                    tma_load_2d_pair(dst, tm, c * kChunk, y, fb);
-                else
-                    tma_load_2d(dst, tm, c * kChunk, y, fb);
+                if (BWD) {
+                    load(&tmA, sA, c * kChunk, t.row0 + (int)rank * 128, fb);
+                } else {
+                    const int mine = columns(t) / CG;          // this CTA's half of the tokens
+                    if (mine == Cfg::kColsPerCta) {            // a full tile: one copy
+                        load(&tmB, sA + Cfg::kABytes, c * kChunk, t.row0 + (int)rank * mine, fb);
+                        return;
+                    }
+                    for (int r = 0; r < mine; r += Cfg::kBox)
+                        load(&tmBox, sA + Cfg::kABytes + r * kChunk, c * kChunk, t.row0 + (int)rank * mine + r, fb);
+                }
             };
             int e = 0;
             int early = 0;                        // stages whose weight operand is on its way
-            if (unit < items) {
-                const I8Tile t = plan.find(unit / splits, e);
-                const int s = unit % splits;
-                const int c0 = (int)((int64_t)chunks * s / splits), c1 = (int)((int64_t)chunks * (s + 1) / splits);
-                early = min(c1 - c0, Cfg::kStages);
-                for (int i = 0; i < early; ++i) {
-                    if (leader)
-                        mbar_arrive_expect_tx(bar_full + 8 * i, CG * Cfg::kStageBytes);
-                    load_w(i, t, c0 + i);
+            {
+                I8Walk walk(deal, unit);
+                if (walk.next()) {
+                    const I8Tile t = plan.find(walk.tile, e);
+                    early = min(walk.c1 - walk.c0, Cfg::kStages);
+                    for (int i = 0; i < early; ++i)
+                        load_w(i, t, walk.c0 + i);
                 }
             }
             grid_dep_wait();                      // codes, scales and low-rank input of the rows
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int item = unit; item < items && ok; item += units) {
-                const I8Tile t = plan.find(item / splits, e);
-                const int s = item % splits;
-                const int c0 = (int)((int64_t)chunks * s / splits), c1 = (int)((int64_t)chunks * (s + 1) / splits);
-                for (int c = c0; c < c1; ++c) {
-                    if (early > 0) {              // the first stages of the first item
+            for (I8Walk walk(deal, unit); ok && walk.next();) {
+                const I8Tile t = plan.find(walk.tile, e);
+                for (int c = walk.c0; c < walk.c1; ++c) {
+                    if (early > 0) {              // the first stages of the first tile
                         --early;
                     } else {
                         if (!mbar_wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag, args.status)) {
                             ok = false;
                             break;
                         }
-                        if (leader)
-                            mbar_arrive_expect_tx(bar_full + 8 * stage, CG * Cfg::kStageBytes);
                         load_w(stage, t, c);
                     }
                     load_x(stage, t, c);
@@ -265,9 +335,10 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
             uint32_t phase = 0;
             int count = 0;
             bool ok = true;
-            for (int item = unit; item < items && ok; item += units, ++count) {
-                const int s = item % splits;
-                const int n = (int)((int64_t)chunks * (s + 1) / splits) - (int)((int64_t)chunks * s / splits);
+            int e = 0;
+            for (I8Walk walk(deal, unit); ok && walk.next(); ++count) {
+                const int n = walk.c1 - walk.c0;
+                const uint32_t idesc = Cfg::kIdesc | (uint32_t)(columns(plan.find(walk.tile, e)) >> 3) << 17;
                 const uint32_t acc = tmem_base + ((count & 1) ? (uint32_t)NT : 0u);
                 // the tile before last (same accumulator) has left tensor memory
                 if (count >= 2 && !acc_wait<CG>(bar_acc_empty + 8 * (count & 1), (uint32_t)(((count >> 1) - 1) & 1),
@@ -283,7 +354,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                     const uint64_t a = dA0 + stage * kStage16, b = dB0 + stage * kStage16;
 #pragma unroll
                     for (int k = 0; k < kChunk / 32; ++k)
-                        mma_i8<CG>(acc, a + 2 * k, b + Cfg::kBStep16 * k, Cfg::kIdesc, (c > 0 || k > 0) ? 1u : 0u);
+                        mma_i8<CG>(acc, a + 2 * k, b + Cfg::kBStep16 * k, idesc, (c > 0 || k > 0) ? 1u : 0u);
                     if (CG == 2)
                         tc_commit2_both(bar_empty + 8 * stage);
                     else
@@ -315,7 +386,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
         const int et = threadIdx.x;
         constexpr int ET = Cfg::kEpiThreads;
         const int wq = warp & 3;                           // lanes 32 wq .. + 31 of tensor memory
-        const int wh = warp >> 2;                          // half of the columns
+        const int wh = warp >> 2;                          // which warp of those lanes
         const int g = lane >> 2, q = lane & 3;             // place in a fragment
         const uint32_t acc_empty_leader = CG == 2 ? mapa_shared(bar_acc_empty, 0) : bar_acc_empty;
         const uint32_t col_low = smem_u32(smem + Cfg::kLowOff);
@@ -327,9 +398,8 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
         grid_dep_wait();
         int e = 0;
         int count = 0;
-        for (int item = unit; item < items; item += units, ++count) {
-            const int tile = item / splits, split = item % splits;
-            const I8Tile t = plan.find(tile, e);
+        for (I8Walk walk(deal, unit); walk.next(); ++count) {
+            const I8Tile t = plan.find(walk.tile, e);
             const int slot = count & 1;
             named_barrier_sync(1, ET);                     // the previous tile's column factors are used up
             if (with_low) {
@@ -384,13 +454,21 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                 break;
             tc_fence_after();
             const uint32_t acc = tmem_base + ((uint32_t)(32 * wq) << 16) + (slot ? (uint32_t)NT : 0u);
-            int32_t *slab0 = args.slabs + ((int64_t)tile * splits * CG + rank) * kSlab;   // + split CG kSlab
-            // publish this item's partial sums (already stored); true in the item that comes last
+            // a tile of several units u0 .. u1: each but whole ones stores its sums in a slab (a
+            // unit has two: of the tile it starts in the middle of, or at the head of, and of the
+            // tile it ends in); the unit that counts last adds the others' to its own
+            const bool split = walk.c1 - walk.c0 < walk.chunks;
+            const int t0 = walk.tile * walk.chunks;
+            const int u0 = split ? deal.owner(t0) : unit, u1 = split ? deal.owner(t0 + walk.chunks - 1) : unit;
+            auto slab = [&](int u) {
+                return args.slabs + ((int64_t)(2 * u + (deal.begin(u) >= t0 ? 0 : 1)) * CG + rank) * kSlab;
+            };
+            // publish this unit's partial sums (already stored); true in the unit that comes last
             auto last_of_tile = [&]() {
                 __threadfence();
                 named_barrier_sync(1, ET);
                 if (et == 0) {
-                    *last_item = atomicAdd(args.counters + tile * CG + rank, 1u) == (uint32_t)(splits - 1) ? 1u : 0u;
+                    *last_item = atomicAdd(args.counters + u0 * CG + rank, 1u) == (uint32_t)(u1 - u0) ? 1u : 0u;
                     __threadfence();
                 }
                 named_barrier_sync(1, ET);
@@ -406,8 +484,8 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                 };
                 const int l = 32 * wq + lane;
                 bool finish = true;
-                if (splits > 1) {
-                    int32_t *mine = slab0 + (int64_t)split * CG * kSlab + l;
+                if (split) {
+                    int32_t *mine = slab(unit) + l;
                     for (int c = 4 * wh; c < 4 * wh + 4; ++c) {
                         uint32_t r[32];
                         load_acc(c, r);
@@ -422,10 +500,10 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                     for (int c = 4 * wh; c < 4 * wh + 4; ++c) {
                         uint32_t r[32];
                         load_acc(c, r);
-                        if (splits > 1)
-                            for (int s = 0; s < splits; ++s)
-                                if (s != split) {
-                                    const int32_t *p = slab0 + (int64_t)s * CG * kSlab + l + 128 * 32 * c;
+                        if (split)
+                            for (int u = u0; u <= u1; ++u)
+                                if (u != unit) {
+                                    const int32_t *p = slab(u) + l + 128 * 32 * c;
 #pragma unroll
                                     for (int i = 0; i < 32; ++i)
                                         r[i] += (uint32_t)__ldcg(p + 128 * i);
@@ -523,8 +601,9 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                     }
                 }
             } else {
-                constexpr int CW = NT / Cfg::kColHalves;   // this warp's columns, 16 at a time
-                const int c_end = min(CW * (wh + 1), t.rows);
+                // this warp's columns: 16 at a time, in turn with the other warp of its lanes
+                constexpr int kStep = 16 * Cfg::kColHalves;
+                const int c_begin = 16 * wh, c_end = t.rows;
                 // the sums of 16 columns as fragments [16 channels][8 tokens][4]
                 auto load_acc = [&](int c, uint32_t (&r)[2][2][4]) {
                     __syncwarp();
@@ -532,9 +611,9 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                     tmem_ld_frag2(acc + (16u << 16) + c, r[1]);
                 };
                 bool finish = true;
-                if (splits > 1) {
-                    int32_t *mine = slab0 + (int64_t)split * CG * kSlab + 32 * wq + lane;
-                    for (int c = CW * wh; c < c_end; c += 16) {
+                if (split) {
+                    int32_t *mine = slab(unit) + 32 * wq + lane;
+                    for (int c = c_begin; c < c_end; c += kStep) {
                         uint32_t r[2][2][4];
                         load_acc(c, r);
                         tmem_wait_ld();
@@ -606,21 +685,21 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                 };
                 if (live) {
                     uint32_t r[2][2][4];
-                    if (CW * wh < c_end) {
-                        load_acc(CW * wh, r);
+                    if (c_begin < c_end) {
+                        load_acc(c_begin, r);
                         tmem_wait_ld();
                     }
-                    for (int c = CW * wh; c < c_end; c += 16) {
+                    for (int c = c_begin; c < c_end; c += kStep) {
                         uint32_t now[2][2][4];
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             now[i >> 3][(i >> 2) & 1][i & 3] = r[i >> 3][(i >> 2) & 1][i & 3];
-                        if (c + 16 < c_end)
-                            load_acc(c + 16, r);           // on its way while these 16 are finished
-                        if (splits > 1)
-                            for (int s = 0; s < splits; ++s)
-                                if (s != split) {
-                                    const int32_t *p = slab0 + (int64_t)s * CG * kSlab + 32 * wq + lane + 128 * c;
+                        if (c + kStep < c_end)
+                            load_acc(c + kStep, r);           // on its way while these 16 are finished
+                        if (split)
+                            for (int u = u0; u <= u1; ++u)
+                                if (u != unit) {
+                                    const int32_t *p = slab(u) + 32 * wq + lane + 128 * c;
 #pragma unroll
                                     for (int i = 0; i < 16; ++i)
                                         now[i >> 3][(i >> 2) & 1][i & 3] += (uint32_t)__ldcg(p + 128 * i);
@@ -664,8 +743,8 @@ struct Shape {
     int nt, cg;
 };
 
-// Token tile by the rows of one product (experts: their mean).  Up to 128 rows one tile takes
-// them all, the narrowest that does; above, 256 x 256 tiles of a CTA pair.
+// Token tile by the rows of one product (experts: their mean).  Few rows: the narrowest tile of
+// one CTA that takes them; above 64, 256 x 256 tiles of a CTA pair.
 Shape pick_shape(bool bwd, int E, int64_t M)
 {
     if (bwd)
@@ -684,7 +763,8 @@ Shape pick_shape(bool bwd, int E, int64_t M)
 
 constexpr int kSlabSms = 148;                     // CTAs the slabs are sized for (a B200's SMs)
 
-int64_t slab_items(bool bwd, int E, int64_t M, int64_t N, int64_t K)
+// units the workspace has slabs for: 0 where no tile can be split
+int slab_units(bool bwd, int E, int64_t M, int64_t N, int64_t K)
 {
     const Shape sh = pick_shape(bwd, E, M);
     const int units = kSlabSms / sh.cg;
@@ -692,10 +772,7 @@ int64_t slab_items(bool bwd, int E, int64_t M, int64_t N, int64_t K)
         return units;
     const int64_t tok = bwd ? 128 * sh.cg : sh.nt, tts = (M + tok - 1) / tok;
     const int64_t wts = bwd ? K / sh.nt : (N + 128 * sh.cg - 1) / (128 * sh.cg);
-    if (tts * wts > units)
-        return 0;
-    const int s = i8_splits((int)(tts * wts), units, (int)((bwd ? N : K) / kChunk), units);
-    return s > 1 ? tts * wts * s : 0;
+    return I8Deal((int)(tts * wts), units, (int)((bwd ? N : K) / kChunk), split_cost(sh.nt), true).even ? units : 0;
 }
 
 template <int NT, int CG, bool BWD>
@@ -730,12 +807,15 @@ cudaError_t launch_shape(const I8GemmLaunch &g, int sms, cudaStream_t stream)
         ctx_seen[dev] = ctx;
     }
     const int64_t Em = g.E > 0 ? g.E : 1;
-    // 128-byte wide boxes: weight codes [E N, K], row codes [M, K] (backward [M, N])
-    CUtensorMap tmW, tmX;
+    // 128-byte wide boxes: weight codes [E N, K], row codes [M, K] (backward [M, N]) by whole tiles
+    // and by kBox tokens
+    CUtensorMap tmW, tmX, tmBox;
     bool ok = make_tmap(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.wcodes, (uint64_t)g.K, (uint64_t)(Em * g.N), 128,
                         128, CU_TENSOR_MAP_SWIZZLE_128B);
     ok &= make_tmap(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.codes, (uint64_t)(BWD ? g.N : g.K), (uint64_t)g.M, 128,
                     BWD ? 128 : Cfg::kColsPerCta, CU_TENSOR_MAP_SWIZZLE_128B);
+    ok &= make_tmap(&tmBox, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.codes, (uint64_t)(BWD ? g.N : g.K), (uint64_t)g.M, 128,
+                    Cfg::kBox, CU_TENSOR_MAP_SWIZZLE_128B);
     if (!ok)
         return cudaErrorInvalidValue;
     I8Args a;
@@ -753,7 +833,7 @@ cudaError_t launch_shape(const I8GemmLaunch &g, int sms, cudaStream_t stream)
     a.K = g.K;
     a.E = g.E;
     a.out_bf16 = g.out_bf16;
-    a.slab_items = (int)slab_items(BWD, g.E, g.M, g.N, g.K);
+    a.slab_units = slab_units(BWD, g.E, g.M, g.N, g.K);
     // dependent launch: set-up and the first weight tiles overlap the quantisation in front
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(resident_units[dev] * CG));
@@ -765,7 +845,7 @@ cudaError_t launch_shape(const I8GemmLaunch &g, int sms, cudaStream_t stream)
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, sq_i8_kernel<NT, CG, BWD>, BWD ? tmX : tmW, BWD ? tmW : tmX, a);
+    return cudaLaunchKernelEx(&cfg, sq_i8_kernel<NT, CG, BWD>, BWD ? tmX : tmW, BWD ? tmW : tmX, tmBox, a);
 }
 
 }  // namespace
@@ -773,7 +853,7 @@ cudaError_t launch_shape(const I8GemmLaunch &g, int sms, cudaStream_t stream)
 size_t i8_slab_bytes(bool bwd, int E, int64_t M, int64_t N, int64_t K)
 {
     const Shape sh = pick_shape(bwd, E, M);
-    return (size_t)slab_items(bwd, E, M, N, K) * sh.cg * 128 * sh.nt * 4;
+    return (size_t)slab_units(bwd, E, M, N, K) * 2 * sh.cg * 128 * sh.nt * 4;
 }
 
 cudaError_t launch_i8_gemm(const I8GemmLaunch &g, int sms, cudaStream_t stream)

@@ -107,19 +107,30 @@ __device__ __forceinline__ void load_block(const uint16_t *__restrict__ x, int p
         w[j] = j < pieces ? __ldg(reinterpret_cast<const uint4 *>(x) + 4 * j) : make_uint4(0u, 0u, 0u, 0u);
 }
 
-// acc[16 ranks x 8 rows] += factor^T x of the block
-__device__ __forceinline__ void low_block(const uint4 (&w)[8], uint32_t factor, int lane, float (&acc)[4])
+// this lane's row address for the ldmatrix of step (j, h): matrix m = lane / 8 takes rows
+// k = 8 ((s >> 1) + 4 j) + 4 h + (s & 1) + 2 (m >> 1), s = lane % 8, half m & 1; steps lie a
+// constant 1024 j + 128 h apart (they leave the flipped bits alone)
+__device__ __forceinline__ uint32_t factor_lane(uint32_t factor, int lane)
 {
     const uint32_t m = lane >> 3, s = lane & 7;
+    return factor + 16 * factor_chunk(16 * (s >> 1) + 2 * (s & 1) + 4 * (m >> 1) + (m & 1));
+}
+
+// acc[16 ranks x 8 rows] += factor^T x of the block (two chains of sums, added at the end)
+__device__ __forceinline__ void low_block(const uint4 (&w)[8], uint32_t lane_addr, float (&acc)[4])
+{
+    float odd[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 8; ++j) {
+        uint32_t a[4], b[4];
+        ldmatrix_x4<true>(lane_addr + 1024 * j, a);
+        ldmatrix_x4<true>(lane_addr + 1024 * j + 128, b);
+        mma_16816(acc, a, w[j].x, w[j].y);
+        mma_16816(odd, b, w[j].z, w[j].w);
+    }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t k = 8 * ((s >> 1) + 4 * j) + 4 * h + (s & 1) + 2 * (m >> 1);
-            uint32_t a[4];
-            ldmatrix_x4<true>(factor + 16 * factor_chunk(2 * k + (m & 1)), a);
-            mma_16816(acc, a, h ? w[j].z : w[j].x, h ? w[j].w : w[j].y);
-        }
+    for (int i = 0; i < 4; ++i)
+        acc[i] = __fadd_rn(acc[i], odd[i]);
 }
 
 // the lane's 64 values as pairs p[4 j + i], widened from bf16
@@ -252,6 +263,7 @@ __global__ void __launch_bounds__(32 * kQWarps, 2) i8_quant_kernel(const I8Quant
     uint8_t *my_factor = q_smem + warp * kQFactorBytes;
     float *my_scale = reinterpret_cast<float *>(q_smem + warps * kQFactorBytes) + warp * kHad;
     const bool with_low = a.low != nullptr;
+    const uint32_t factor_at = factor_lane(smem_u32(my_factor), lane);
 
     grid_dep_launch();
     if (blockIdx.x == 0)
@@ -339,7 +351,7 @@ __global__ void __launch_bounds__(32 * kQWarps, 2) i8_quant_kernel(const I8Quant
                 load_block(row_of(t, b), pieces_of(t, b), w);
                 fetched();
                 if (with_low)
-                    low_block(w, smem_u32(my_factor), lane, low);
+                    low_block(w, factor_at, low);
                 spread(w, p);
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
@@ -357,7 +369,7 @@ __global__ void __launch_bounds__(32 * kQWarps, 2) i8_quant_kernel(const I8Quant
                 have = t.e;
             }
             if (with_low && block0 < nb)
-                low_block(w, smem_u32(my_factor), lane, low);
+                low_block(w, factor_at, low);
             spread(w, p);
             if (tile + units < tiles) {               // the next group's values, while this one's are transformed
                 next = plan.find(tile + units, e);
@@ -462,6 +474,8 @@ static cudaError_t launch_quant_v(const I8QuantArgs &a, int cluster, int warps, 
 {
     constexpr int kMaxDev = 64;
     static unsigned long long attr_ctx[kMaxDev];
+    static unsigned long long room_ctx[kMaxDev][kQMaxCluster][kQWarps];
+    static int room[kMaxDev][kQMaxCluster][kQWarps];
     constexpr int kMaxSmem = kQWarps * (kQFactorBytes + kHad * 4);
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev)
@@ -474,12 +488,7 @@ static cudaError_t launch_quant_v(const I8QuantArgs &a, int cluster, int warps, 
             return e;
         attr_ctx[dev] = ctx;
     }
-    // persistent: two CTAs per SM
-    const int64_t groups = (a.M + kQRows - 1) / kQRows + a.E;
-    const int64_t room = 2 * sms / cluster;
-    const int units = (int)(groups < room ? groups : room);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * cluster));
     cfg.blockDim = dim3(32 * warps);
     cfg.dynamicSmemBytes = warps * (kQFactorBytes + (BWD ? kHad * 4 : 0));
     cfg.stream = s;
@@ -488,6 +497,21 @@ static cudaError_t launch_quant_v(const I8QuantArgs &a, int cluster, int warps, 
     at[0].val.clusterDim.x = (unsigned)cluster;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
+    // persistent: as many clusters as are resident at once (clusters left over for a second
+    // wave would double the time), but never more than row groups
+    if (ctx == 0 || room_ctx[dev][cluster - 1][warps - 1] != ctx) {
+        cfg.gridDim = dim3((unsigned)(2 * sms / cluster * cluster));
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, i8_quant_kernel<BWD, TURNS>, &cfg);
+        (void)cudaGetLastError();
+        room[dev][cluster - 1][warps - 1] = e == cudaSuccess && n > 0 ? n : 1;
+        room_ctx[dev][cluster - 1][warps - 1] = ctx;
+    }
+    const int64_t groups = (a.M + kQRows - 1) / kQRows + a.E;
+    const int64_t fit = room[dev][cluster - 1][warps - 1];
+    cfg.gridDim = dim3((unsigned)((groups < fit ? groups : fit) * cluster));
     cfg.attrs = at;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, i8_quant_kernel<BWD, TURNS>, a, cluster);

@@ -121,13 +121,13 @@ def test_binding_refusals():
 
 def test_workspace_covers_its_parts():
     """Header, counters, row codes, scales and low-rank input; partial sums only where tiles can be split."""
-    base = lambda M, width: 2048 + M * (width + 4 + 64)  # noqa: E731
+    base = lambda M, width: 2048 + M * (width + 4 + 96)  # noqa: E731
     assert sq.sq_workspace_bytes(sq.SQ_OP_LINEAR_FWD_W8A8, 1, 6144, 6144) >= base(1, 6144)
     big = sq.sq_workspace_bytes(sq.SQ_OP_LINEAR_FWD_W8A8, 4480, 16384, 6144)
     assert base(4480, 6144) <= big <= base(4480, 6144) + 8192                    # more tiles than SMs: none split
     big = sq.sq_workspace_bytes(sq.SQ_OP_LINEAR_BWD_DX_W8A8, 4480, 16384, 6144)
     assert base(4480, 16384) <= big <= base(4480, 16384) + 8192
-    # 48 weight tiles of 16 tokens on 148 SMs: three items each
+    # 48 weight tiles of 16 tokens on 148 SMs are split
     one = sq.sq_workspace_bytes(sq.SQ_OP_LINEAR_FWD_W8A8, 1, 6144, 6144)
     assert one >= base(1, 6144) + 48 * 3 * 128 * 16 * 4
 
