@@ -26,11 +26,14 @@
 // A tile's MMAs and loads cover only the boxes of tokens that it has (the instruction's
 // column count is set per tile), so that an expert with few rows costs few.
 //
-// Where the last round of tiles would leave many SMs idle, the work is dealt out in
-// equal shares of the summed axis instead (I8Deal): a unit stores the 32-bit partial
-// sums of a tile that it shares, counts up, and the one that counts last adds them
-// all and finishes the tile.  Integer sums do not depend on the order, so neither
-// does the result.
+// Tiles of a CTA pair whose last round would leave many SMs idle are dealt out in equal
+// shares of the summed axis instead (I8Deal): a unit stores the 32-bit partial sums of a
+// tile that it shares, counts up, and the one that counts last adds them all and
+// finishes the tile.  Integer sums do not depend on the order, so neither does the
+// result.  Few tokens (CG = 1) are bound by the weight's bytes: each CTA takes an equal
+// share of all channels, to four of them, as tiles of up to 128, so that every SM reads
+// the same amount and nothing has to be joined.  (Splitting the summed axis over the SMs
+// instead cost 3 to 4 us for storing, counting and adding: M = 1, N = K = 6144 16 us.)
 #include <cuda.h>
 
 #include "sq_device.cuh"
@@ -54,14 +57,20 @@ struct I8Cfg {
     // epilogue warps: one per 32 lanes and, in wide tiles, per half of the columns
     static constexpr int kColHalves = NT >= 64 ? 2 : 1;
     static constexpr int kEpiThreads = 128 * kColHalves;
-    static constexpr int kThreads = kEpiThreads + 64;                // + producer, MMA issuer
+    // producer warps, each with its own stages: one copy takes a thread about 60 ns to issue, so
+    // tiles that need little time per stage share the work out
+    static constexpr int kProducers = CG == 2 ? 1 : NT <= 32 ? 4 : 2;
+    static constexpr int kThreads = kEpiThreads + 32 * kProducers + 32;   // + MMA issuer
     // low-rank values of a column in shared memory: three bf16 terms of a token (forward), the
     // bf16 row of lora_down (backward); an odd number of 16-byte pieces apart (ldmatrix rows)
     static constexpr int kLowPitch = BWD ? 48 : 112;
     static constexpr int kPatchBytes = BWD ? 0 : 2 * 8 * 36 * 4;     // a warp's two store patches
-    static constexpr int kRing = (BWD ? 192 : NT == 256 ? 160 : 176) * 1024;
-    static constexpr int kStages = kRing / kStageBytes < 10 ? kRing / kStageBytes : 10;
-    static constexpr int kPatchOff = kStages * kStageBytes;
+    // stages: fixed for a CTA pair; with CG = 1 as many as fit with the A rows that the CTA's
+    // tiles have (the MMAs read 128 rows all the same: behind the tile's own lie other bytes of
+    // the CTA's shared memory, and their lanes of the accumulator are not looked at)
+    static constexpr int kRing = (BWD ? 192 : NT == 256 ? 160 : NT == 128 ? 176 : 184) * 1024;
+    static constexpr int kStages = CG == 1 ? 24 : kRing / kStageBytes;
+    static constexpr int kPatchOff = kRing;
     static constexpr int kLowOff = kPatchOff + (kEpiThreads / 32) * kPatchBytes;
     static constexpr int kScaleOff = kLowOff + NT * kLowPitch;       // column scales [NT] fp32 (forward)
     static constexpr int kPlanOff = kScaleOff + NT * 4;              // start and prefix of every expert
@@ -88,6 +97,7 @@ struct I8Args {
     int E;
     int out_bf16;
     int slab_units;           // units there are slabs for (two each), 0: none
+    int box;                  // weight rows of a tmA box
 };
 
 // chunks' worth of time that joining split tiles of nt columns costs (a fixed latency and the slab)
@@ -159,6 +169,97 @@ struct I8Walk {
     }
 };
 
+// CG = 1: a CTA's share of all (token tile, channel) pairs, in tiles of up to 128 channels
+struct I8ChannelWalk {
+    int64_t pos, end;         // in groups of 4 channels, token tile after token tile
+    int per_tile;             // N / 4
+    int tile, n0, channels;
+
+    __device__ __forceinline__ I8ChannelWalk(int tiles, int64_t N, int cta, int ctas)
+        : per_tile((int)(N / 4)), tile(0), n0(0), channels(0)
+    {
+        const int64_t all = (int64_t)tiles * per_tile;
+        pos = all * cta / ctas;
+        end = all * (cta + 1) / ctas;
+    }
+    // channels of the largest tile, at most
+    __device__ __forceinline__ int largest() const
+    {
+        return (int)min((int64_t)128, 4 * (end - pos));
+    }
+    __device__ __forceinline__ bool next()
+    {
+        if (pos >= end)
+            return false;
+        tile = (int)(pos / per_tile);
+        const int first = (int)(pos - (int64_t)tile * per_tile);
+        const int left = (int)min(end - pos, (int64_t)(per_tile - first));
+        const int tiles_left = (left + 31) / 32;
+        const int now = (left + tiles_left - 1) / tiles_left;      // of equal size
+        n0 = 4 * first;
+        channels = 4 * now;
+        pos += now;
+        return true;
+    }
+};
+
+// what a unit does next: tile t, its lanes (channels from n0 on; backward: tokens), chunks c0 .. c1 - 1
+struct I8Work {
+    I8Tile t;
+    int tile, n0, lanes, c0, c1;
+};
+
+template <int NT, int CG, bool BWD>
+struct I8Units {
+    const I8Plan &plan;
+    I8Walk walk;              // CG = 2
+    I8ChannelWalk cwalk;      // CG = 1
+    int64_t N;
+    int e;
+
+    __device__ __forceinline__ I8Units(const I8Plan &p, const I8Deal &d, const I8ChannelWalk &c, int unit, int64_t N_)
+        : plan(p), walk(d, unit), cwalk(c), N(N_), e(0)
+    {
+    }
+    __device__ __forceinline__ bool next(I8Work &w)
+    {
+        if (CG == 1) {
+            if (!cwalk.next())
+                return false;
+            w.tile = cwalk.tile;
+            w.t = plan.find(cwalk.tile, e);
+            w.n0 = cwalk.n0;
+            w.lanes = cwalk.channels;
+            w.c0 = 0;
+            w.c1 = walk.chunks;
+        } else {
+            if (!walk.next())
+                return false;
+            w.tile = walk.tile;
+            w.t = plan.find(walk.tile, e);
+            w.n0 = BWD ? 0 : w.t.wt * 256;
+            w.lanes = BWD ? w.t.rows : (int)min((int64_t)256, N - w.n0);
+            w.c0 = walk.c0;
+            w.c1 = walk.c1;
+        }
+        return true;
+    }
+};
+
+// one lane of the warp
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// the same in every lane (as it is already), told to the compiler
+__device__ __forceinline__ int uniform(int v)
+{
+    return __shfl_sync(0xffffffffu, v, 0);
+}
+
 template <int CG>
 __device__ __forceinline__ bool acc_wait(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag,
                                          uint32_t *status)
@@ -169,7 +270,8 @@ __device__ __forceinline__ bool acc_wait(uint32_t bar, uint32_t parity, volatile
 template <int NT, int CG, bool BWD>
 __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>::kThreads, 1)
     sq_i8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                 const __grid_constant__ CUtensorMap tmBox, const I8Args args)
+                 const __grid_constant__ CUtensorMap tmBox, const __grid_constant__ CUtensorMap tmA64,
+                 const __grid_constant__ CUtensorMap tmA16, const I8Args args)
 {
     using Cfg = I8Cfg<NT, CG, BWD>;
     extern __shared__ uint8_t smem_raw[];
@@ -205,7 +307,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
         *abort_flag = 0u;
         fence_mbar_init();
     }
-    constexpr int kProducer = Cfg::kEpiThreads / 32, kIssuer = kProducer + 1;      // warps
+    constexpr int kProducer = Cfg::kEpiThreads / 32, kIssuer = kProducer + Cfg::kProducers;      // warps
     if (warp == kIssuer) {
         if (CG == 2) {
             tmem_alloc2(smem_u32(tmem_holder), Cfg::kTmemCols);
@@ -220,13 +322,17 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
         prefetch_tmap(&tmB);
         if (!BWD)
             prefetch_tmap(&tmBox);
+        if (CG == 1) {
+            prefetch_tmap(&tmA64);
+            prefetch_tmap(&tmA16);
+        }
     }
     // the offsets are an input of the call: they are there before the kernel in front starts
     I8Plan plan;
     plan.E = args.E > 0 ? args.E : 1;
     plan.start = plan_mem;
     plan.prefix = plan_mem + kMaxExperts + 1;
-    plan.wts = BWD ? (int)(args.K / NT) : (int)((args.N + Cfg::kLaneTile - 1) / Cfg::kLaneTile);
+    plan.wts = CG == 1 ? 1 : BWD ? (int)(args.K / NT) : (int)((args.N + Cfg::kLaneTile - 1) / Cfg::kLaneTile);
     plan.tok_tile = BWD ? Cfg::kLaneTile : NT;
     plan.build(args.E > 0 ? args.offsets : nullptr, args.M, threadIdx.x, Cfg::kThreads);
     tc_fence_before();
@@ -241,104 +347,156 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
     const int unit = (int)blockIdx.x / CG;
     const int units = (int)gridDim.x / CG;
     const I8Deal deal(tiles, args.slab_units > 0 ? min(units, args.slab_units) : units,
-                      (int)((BWD ? args.N : args.K) / kChunk), split_cost(NT), args.slab_units > 0);
+                      (int)((BWD ? args.N : args.K) / kChunk), split_cost(NT), CG == 2 && args.slab_units > 0);
+    const I8ChannelWalk share(CG == 1 ? tiles : 0, args.N, unit, units);
+    using Units = I8Units<NT, CG, BWD>;
+    const int a_bytes = CG == 1 ? min(128, max(args.box < 128 ? args.box : 16, (share.largest() + 7) / 8 * 8)) * kChunk
+                                : Cfg::kABytes;
+    const int stage_bytes = a_bytes + Cfg::kBBytes;
+    const int stages = CG == 1 ? min(Cfg::kStages, Cfg::kRing / stage_bytes) / Cfg::kProducers * Cfg::kProducers
+                               : Cfg::kStages;
     // columns of the accumulator a tile uses (forward: its tokens, in whole boxes of both CTAs)
     auto columns = [&](const I8Tile &t) {
         return BWD ? NT : (t.rows + CG * Cfg::kBox - 1) / (CG * Cfg::kBox) * (CG * Cfg::kBox);
     };
 
-    if (warp == kProducer) {
-        // ------------------------------------------------------------ producer (every CTA)
-        if (lane == 0) {
-            // weight operand of stage `stage`, chunk c of tile t, and the row operand
-            auto load = [&](const void *tm, uint32_t dst, int x, int y, uint32_t bar) {
-                if (CG == 2)
-                    tma_load_2d_pair(dst, tm, x, y, bar);
-                else
-                    tma_load_2d(dst, tm, x, y, bar);
-            };
-            auto load_w = [&](int stage, const I8Tile &t, int c) {
-                const uint32_t sA = smem_u32(smem + stage * Cfg::kStageBytes), fb = bar_full + 8 * stage;
-                const int n0 = t.e * (int)args.N;
-                if (leader)
-                    mbar_arrive_expect_tx(fb, CG * Cfg::kABytes + columns(t) * kChunk);
-                if (BWD)
-                    load(&tmB, sA + Cfg::kABytes, t.wt * NT + (int)rank * Cfg::kColsPerCta, n0 + c * kChunk, fb);
-                else
-                    load(&tmA, sA, c * kChunk, n0 + t.wt * Cfg::kLaneTile + (int)rank * 128, fb);
-            };
-            auto load_x = [&](int stage, const I8Tile &t, int c) {
-                const uint32_t sA = smem_u32(smem + stage * Cfg::kStageBytes), fb = bar_full + 8 * stage;
-                if (BWD) {
-                    load(&tmA, sA, c * kChunk, t.row0 + (int)rank * 128, fb);
-                } else {
-                    const int mine = columns(t) / CG;          // this CTA's half of the tokens
-                    if (mine == Cfg::kColsPerCta) {            // a full tile: one copy
-                        load(&tmB, sA + Cfg::kABytes, c * kChunk, t.row0 + (int)rank * mine, fb);
-                        return;
-                    }
-                    for (int r = 0; r < mine; r += Cfg::kBox)
-                        load(&tmBox, sA + Cfg::kABytes + r * kChunk, c * kChunk, t.row0 + (int)rank * mine + r, fb);
-                }
-            };
-            int e = 0;
-            int early = 0;                        // stages whose weight operand is on its way
-            {
-                I8Walk walk(deal, unit);
-                if (walk.next()) {
-                    const I8Tile t = plan.find(walk.tile, e);
-                    early = min(walk.c1 - walk.c0, Cfg::kStages);
-                    for (int i = 0; i < early; ++i)
-                        load_w(i, t, walk.c0 + i);
+    if (warp >= kProducer && warp < kIssuer) {
+        // ------------------------------------------------------------ producers (every CTA)
+        // Producer p fills stages p, p + P, ... with every P-th chunk of the unit's work.  The whole
+        // warp runs the loop on uniform values and one lane issues, which keeps the address
+        // arithmetic off the path between two copies.
+        constexpr int P = Cfg::kProducers;
+        const int p = warp - kProducer;
+        const bool issue = elect_one();
+        const uint32_t s0 = smem_u32(smem);
+        auto load = [&](const void *tm, uint32_t dst, int x, int y, uint32_t bar) {
+            if (CG == 2)
+                tma_load_2d_pair(dst, tm, x, y, bar);
+            else
+                tma_load_2d(dst, tm, x, y, bar);
+        };
+        // what is the same for every chunk of a tile
+        struct Aim {
+            int wrow, rows;           // weight: first row, rows (forward; in whole 8-row groups)
+            int xrow, mine;           // row operand: first row, rows
+            uint32_t bytes;           // of a stage (both CTAs)
+        };
+        auto aim_at = [&](const I8Work &w) {
+            Aim m;
+            const int cols = columns(w.t);
+            // rows and the bytes of their copies: one box where it is not much more, else boxes of
+            // 64 or 16 rows that may overlap (the same bytes to the same place)
+            m.rows = 128;
+            int copied = 128;
+            if (CG == 1) {
+                m.rows = max(16, (w.lanes + 7) / 8 * 8);
+                if (m.rows <= args.box && m.rows + 16 >= args.box)
+                    m.rows = args.box;
+                copied = m.rows == args.box ? args.box : m.rows > 64 ? 128 : (m.rows + 15) / 16 * 16;
+            }
+            m.wrow = w.t.e * (int)args.N + (BWD ? 0 : w.n0 + (int)rank * 128);
+            m.mine = BWD ? 128 : cols / CG;
+            m.xrow = w.t.row0 + (int)rank * m.mine;
+            m.bytes = CG * copied * kChunk + cols * kChunk;
+            m.wrow = uniform(m.wrow);
+            m.rows = uniform(m.rows);
+            m.xrow = uniform(m.xrow);
+            m.mine = uniform(m.mine);
+            m.bytes = (uint32_t)uniform((int)m.bytes);
+            return m;
+        };
+        auto load_w = [&](int stage, const Aim &m, int wt, int c) {
+            const uint32_t sA = s0 + stage * stage_bytes, fb = bar_full + 8 * stage;
+            if (leader)
+                mbar_arrive_expect_tx(fb, m.bytes);
+            if (BWD) {
+                load(&tmB, sA + a_bytes, wt * NT + (int)rank * Cfg::kColsPerCta, m.wrow + c * kChunk, fb);
+            } else if (CG == 2 || m.rows == args.box) {
+                load(&tmA, sA, c * kChunk, m.wrow, fb);
+            } else if (m.rows > 64) {             // two boxes, the second one back from the end
+                load(&tmA64, sA, c * kChunk, m.wrow, fb);
+                load(&tmA64, sA + (m.rows - 64) * kChunk, c * kChunk, m.wrow + m.rows - 64, fb);
+            } else {
+                for (int r = 0; r < m.rows; r += 16) {
+                    const int at = min(r, m.rows - 16);
+                    load(&tmA16, sA + at * kChunk, c * kChunk, m.wrow + at, fb);
                 }
             }
-            grid_dep_wait();                      // codes, scales and low-rank input of the rows
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (I8Walk walk(deal, unit); ok && walk.next();) {
-                const I8Tile t = plan.find(walk.tile, e);
-                for (int c = walk.c0; c < walk.c1; ++c) {
-                    if (early > 0) {              // the first stages of the first tile
-                        --early;
-                    } else {
-                        if (!mbar_wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag, args.status)) {
-                            ok = false;
-                            break;
-                        }
-                        load_w(stage, t, c);
-                    }
-                    load_x(stage, t, c);
-                    if (++stage == Cfg::kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
+        };
+        auto load_x = [&](int stage, const Aim &m, int c) {
+            const uint32_t sX = s0 + stage * stage_bytes + (BWD ? 0 : a_bytes), fb = bar_full + 8 * stage;
+            if (BWD || m.mine == Cfg::kColsPerCta) {
+                load(BWD ? &tmA : &tmB, sX, c * kChunk, m.xrow, fb);
+            } else {
+                for (int r = 0; r < m.mine; r += Cfg::kBox)
+                    load(&tmBox, sX + r * kChunk, c * kChunk, m.xrow + r, fb);
             }
-            // let every load that was issued land (and be consumed) before the CTA exits
-            for (int st = 0; st < Cfg::kStages; ++st) {
-                (void)mbar_wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag, args.status);
-                if (++stage == Cfg::kStages) {
-                    stage = 0;
+        };
+        I8Work w;
+        int early = 0;                            // chunks of the first tile whose weight operand is on its way
+        if (Units first(plan, deal, share, unit, args.N); first.next(w)) {
+            early = uniform(min(w.c1 - w.c0, stages));
+            const Aim m = aim_at(w);
+            const int c0 = uniform(w.c0), wt = uniform(w.t.wt);
+            if (issue)
+                for (int i = p; i < early; i += P)
+                    load_w(i, m, wt, c0 + i);
+        }
+        grid_dep_wait();                          // codes, scales and low-rank input of the rows
+        int stage = p;
+        uint32_t phase = 0;
+        bool ok = true;
+        int skip = p;                             // chunks of the others before this producer's next one
+        for (Units work(plan, deal, share, unit, args.N); ok && work.next(w);) {
+            const Aim m = aim_at(w);
+            const int c1 = uniform(w.c1), wt = uniform(w.t.wt);
+            int c = uniform(w.c0) + skip;
+            for (; c < c1; c += P) {
+                const bool fresh = early <= p;
+                if (fresh && !mbar_wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag, args.status)) {
+                    ok = false;
+                    break;
+                }
+                early -= P;
+                if (issue) {
+                    if (fresh)
+                        load_w(stage, m, wt, c);
+                    load_x(stage, m, c);
+                }
+                stage += P;
+                if (stage >= stages) {
+                    stage = p;
                     phase ^= 1u;
                 }
+            }
+            skip = c - c1;
+        }
+        // let every load that was issued land (and be consumed) before the CTA exits
+        for (int st = p; st < stages; st += P) {
+            (void)mbar_wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag, args.status);
+            stage += P;
+            if (stage >= stages) {
+                stage = p;
+                phase ^= 1u;
             }
         }
         __syncwarp();
     } else if (warp == kIssuer) {
         // ------------------------------------------------------------ MMA issuer (leader)
-        if (leader && lane == 0) {
+        if (leader) {
+            const bool issue = elect_one();
             const uint32_t s0 = smem_u32(smem);
-            const uint64_t dA0 = sdesc_sw128(s0), dB0 = sdesc_sw128(s0 + Cfg::kABytes);
-            constexpr uint32_t kStage16 = Cfg::kStageBytes >> 4;
+            const uint64_t dA0 = sdesc_sw128(s0), dB0 = sdesc_sw128(s0 + a_bytes);
+            const uint32_t stage16 = stage_bytes >> 4;
             int stage = 0;
             uint32_t phase = 0;
+            uint64_t dA = dA0, dB = dB0;
             int count = 0;
             bool ok = true;
-            int e = 0;
-            for (I8Walk walk(deal, unit); ok && walk.next(); ++count) {
-                const int n = walk.c1 - walk.c0;
-                const uint32_t idesc = Cfg::kIdesc | (uint32_t)(columns(plan.find(walk.tile, e)) >> 3) << 17;
+            I8Work w;
+            for (Units work(plan, deal, share, unit, args.N); ok && work.next(w); ++count) {
+                const int n = uniform(w.c1 - w.c0);
+                const uint32_t idesc = Cfg::kIdesc | (uint32_t)uniform(columns(w.t) >> 3) << 17;
                 const uint32_t acc = tmem_base + ((count & 1) ? (uint32_t)NT : 0u);
                 // the tile before last (same accumulator) has left tensor memory
                 if (count >= 2 && !acc_wait<CG>(bar_acc_empty + 8 * (count & 1), (uint32_t)(((count >> 1) - 1) & 1),
@@ -351,20 +509,25 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t a = dA0 + stage * kStage16, b = dB0 + stage * kStage16;
+                    if (issue) {
 #pragma unroll
-                    for (int k = 0; k < kChunk / 32; ++k)
-                        mma_i8<CG>(acc, a + 2 * k, b + Cfg::kBStep16 * k, idesc, (c > 0 || k > 0) ? 1u : 0u);
-                    if (CG == 2)
-                        tc_commit2_both(bar_empty + 8 * stage);
-                    else
-                        tc_commit(bar_empty + 8 * stage);
-                    if (++stage == Cfg::kStages) {
+                        for (int k = 0; k < kChunk / 32; ++k)
+                            mma_i8<CG>(acc, dA + 2 * k, dB + Cfg::kBStep16 * k, idesc, (c > 0 || k > 0) ? 1u : 0u);
+                        if (CG == 2)
+                            tc_commit2_both(bar_empty + 8 * stage);
+                        else
+                            tc_commit(bar_empty + 8 * stage);
+                    }
+                    dA += stage16;
+                    dB += stage16;
+                    if (++stage == stages) {
                         stage = 0;
+                        dA = dA0;
+                        dB = dB0;
                         phase ^= 1u;
                     }
                 }
-                if (ok) {
+                if (ok && issue) {
                     if (CG == 2)
                         tc_commit2_both(bar_acc_full + 8 * (count & 1));
                     else
@@ -372,10 +535,12 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                 }
             }
             // all issued MMAs must finish before tensor memory is released
-            if (CG == 2)
-                tc_commit2_local(bar_drain);
-            else
-                tc_commit(bar_drain);
+            if (issue) {
+                if (CG == 2)
+                    tc_commit2_local(bar_drain);
+                else
+                    tc_commit(bar_drain);
+            }
             (void)mbar_wait(bar_drain, 0, abort_flag, args.status);
         }
         __syncwarp();
@@ -396,10 +561,10 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
         const int64_t width = BWD ? args.K : args.N;      // columns of y
         constexpr int64_t kSlab = (int64_t)NT * 128;
         grid_dep_wait();
-        int e = 0;
         int count = 0;
-        for (I8Walk walk(deal, unit); walk.next(); ++count) {
-            const I8Tile t = plan.find(walk.tile, e);
+        I8Work w;
+        for (Units work(plan, deal, share, unit, args.N); work.next(w); ++count) {
+            const I8Tile &t = w.t;
             const int slot = count & 1;
             named_barrier_sync(1, ET);                     // the previous tile's column factors are used up
             if (with_low) {
@@ -418,18 +583,18 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                     col_scale[c] = c < t.rows ? args.scales[t.row0 + c] : 0.0f;
             // the lanes' scales and low-rank values (lane r of a fragment half: 16 h + g + 8 i)
             const int lane0 = (int)rank * 128 + 32 * wq;   // first lane of the warp in the tile
-            const int64_t base = BWD ? (int64_t)t.row0 + lane0 : (int64_t)t.wt * Cfg::kLaneTile + lane0;
+            const int64_t base = (BWD ? t.row0 : w.n0) + lane0;
             float fscale[2][2];                            // forward: per fragment row
             float lscale = 0.0f;                           // backward: of this thread's lane
             uint32_t ufrag[2][BWD ? kLowParts : 1][4];     // A operand of the low-rank product
             if (BWD)
-                lscale = lane0 + lane < t.rows ? args.scales[base + lane] : 0.0f;
+                lscale = lane0 + lane < w.lanes ? args.scales[base + lane] : 0.0f;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int r = 16 * h + g + 8 * i;
-                    const bool live = BWD ? lane0 + r < t.rows : base + r < args.N;
+                    const bool live = lane0 + r < w.lanes;
                     if (!BWD)
                         fscale[h][i] = live ? __ldg(args.wscales + (int64_t)t.e * args.N + base + r) : 0.0f;
 #pragma unroll
@@ -457,9 +622,9 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
             // a tile of several units u0 .. u1: each but whole ones stores its sums in a slab (a
             // unit has two: of the tile it starts in the middle of, or at the head of, and of the
             // tile it ends in); the unit that counts last adds the others' to its own
-            const bool split = walk.c1 - walk.c0 < walk.chunks;
-            const int t0 = walk.tile * walk.chunks;
-            const int u0 = split ? deal.owner(t0) : unit, u1 = split ? deal.owner(t0 + walk.chunks - 1) : unit;
+            const bool split = CG == 2 && w.c1 - w.c0 < deal.chunks;
+            const int t0 = w.tile * deal.chunks;
+            const int u0 = split ? deal.owner(t0) : unit, u1 = split ? deal.owner(t0 + deal.chunks - 1) : unit;
             auto slab = [&](int u) {
                 return args.slabs + ((int64_t)(2 * u + (deal.begin(u) >= t0 ? 0 : 1)) * CG + rank) * kSlab;
             };
@@ -588,7 +753,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                                 a = __fmaf_rn(a, 0.0625f, low[i >> 1][2 * (i & 1)]);
                                 b = __fmaf_rn(b, 0.0625f, low[i >> 1][2 * (i & 1) + 1]);
                                 const int64_t at = (base + row) * width + (int64_t)t.wt * NT + col + 8 * (i >> 1) + 2 * q;
-                                if (lane0 + row < t.rows && SQ_DCHECK(at + 2 <= args.M * width, args.status)) {
+                                if (lane0 + row < w.lanes && SQ_DCHECK(at + 2 <= args.M * width, args.status)) {
                                     if (ybf)
                                         *reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(args.y) + at) =
                                             f32x2_to_bf16x2_bits(a, b);
@@ -623,7 +788,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                     }
                     finish = last_of_tile();
                 }
-                const bool live = finish && base < args.N; // (N % 128 == 0: the same in the whole warp)
+                const bool live = finish && lane0 < w.lanes;
                 auto finish16 = [&](int c, const uint32_t (&r)[2][2][4]) {
                     uint32_t b[3][4];                      // terms 0, 1 of both groups; term 2 of both
                     if (with_low) {
@@ -653,17 +818,29 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                         uint8_t *buf = patch + n * (8 * 36 * 4);
                         const int64_t y0 = ((int64_t)t.row0 + c + 8 * n) * width + base;
                         if (ybf) {                         // [8 tokens] rows of 80 bytes
-                            const uint32_t w[4] = {f32x2_to_bf16x2_bits(o[0][0], o[0][1]),
-                                                   f32x2_to_bf16x2_bits(o[0][2], o[0][3]),
-                                                   f32x2_to_bf16x2_bits(o[1][0], o[1][1]),
-                                                   f32x2_to_bf16x2_bits(o[1][2], o[1][3])};
-                            stmatrix_x4_trans(smem_u32(buf) + (lane & 7) * 80 + (lane >> 3) * 16, w);
+                            const uint32_t pairs[4] = {f32x2_to_bf16x2_bits(o[0][0], o[0][1]),
+                                                       f32x2_to_bf16x2_bits(o[0][2], o[0][3]),
+                                                       f32x2_to_bf16x2_bits(o[1][0], o[1][1]),
+                                                       f32x2_to_bf16x2_bits(o[1][2], o[1][3])};
+                            stmatrix_x4_trans(smem_u32(buf) + (lane & 7) * 80 + (lane >> 3) * 16, pairs);
                             __syncwarp();
-                            const int tok = lane >> 2, piece = lane & 3;
-                            const uint4 v = *reinterpret_cast<const uint4 *>(buf + tok * 80 + piece * 16);
-                            const int64_t at = y0 + tok * width + 8 * piece;
-                            if (c + 8 * n + tok < t.rows && SQ_DCHECK(at + 8 <= args.M * width, args.status))
-                                *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(args.y) + at) = v;
+                            if (CG == 2) {                 // (whole 32 channels: N % 128 == 0)
+                                const int tok = lane >> 2, piece = lane & 3;
+                                const uint4 v = *reinterpret_cast<const uint4 *>(buf + tok * 80 + piece * 16);
+                                const int64_t at = y0 + tok * width + 8 * piece;
+                                if (c + 8 * n + tok < t.rows && SQ_DCHECK(at + 8 <= args.M * width, args.status))
+                                    *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(args.y) + at) = v;
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const int tok = (lane >> 3) + 4 * k, piece = lane & 7;
+                                    const uint2 v = *reinterpret_cast<const uint2 *>(buf + tok * 80 + piece * 8);
+                                    const int64_t at = y0 + tok * width + 4 * piece;
+                                    if (c + 8 * n + tok < t.rows && lane0 + 4 * piece < w.lanes &&
+                                        SQ_DCHECK(at + 4 <= args.M * width, args.status))
+                                        *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(args.y) + at) = v;
+                                }
+                            }
                         } else {                           // [8 tokens] rows of 36 floats
                             float *f = reinterpret_cast<float *>(buf);
 #pragma unroll
@@ -677,7 +854,8 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                                 const int tok = (lane >> 3) + 4 * k, piece = lane & 7;
                                 const float4 v = *reinterpret_cast<const float4 *>(f + tok * 36 + 4 * piece);
                                 const int64_t at = y0 + tok * width + 4 * piece;
-                                if (c + 8 * n + tok < t.rows && SQ_DCHECK(at + 4 <= args.M * width, args.status))
+                                if (c + 8 * n + tok < t.rows && lane0 + 4 * piece < w.lanes &&
+                                    SQ_DCHECK(at + 4 <= args.M * width, args.status))
                                     *reinterpret_cast<float4 *>(reinterpret_cast<float *>(args.y) + at) = v;
                             }
                         }
@@ -743,8 +921,8 @@ struct Shape {
     int nt, cg;
 };
 
-// Token tile by the rows of one product (experts: their mean).  Few rows: the narrowest tile of
-// one CTA that takes them; above 64, 256 x 256 tiles of a CTA pair.
+// Token tile by the rows of one product (experts: their mean): up to 128 the narrowest tile of
+// one CTA that takes them, above 256 x 256 tiles of a CTA pair.
 Shape pick_shape(bool bwd, int E, int64_t M)
 {
     if (bwd)
@@ -767,12 +945,27 @@ constexpr int kSlabSms = 148;                     // CTAs the slabs are sized fo
 int slab_units(bool bwd, int E, int64_t M, int64_t N, int64_t K)
 {
     const Shape sh = pick_shape(bwd, E, M);
+    if (sh.cg == 1)
+        return 0;
     const int units = kSlabSms / sh.cg;
     if (E > 0)                                    // how the rows spread is known on the device only
         return units;
     const int64_t tok = bwd ? 128 * sh.cg : sh.nt, tts = (M + tok - 1) / tok;
     const int64_t wts = bwd ? K / sh.nt : (N + 128 * sh.cg - 1) / (128 * sh.cg);
     return I8Deal((int)(tts * wts), units, (int)((bwd ? N : K) / kChunk), split_cost(sh.nt), true).even ? units : 0;
+}
+
+// CG = 1: rows of the box that takes a CTA's whole tile in one copy.  Dense: the shares are known
+// and nearly equal; experts: 128.
+int whole_box(const I8GemmLaunch &g, int ctas, int nt)
+{
+    if (g.E > 0)
+        return 128;
+    const int64_t all = (g.M + nt - 1) / nt * (g.N / 4), share = (all + ctas - 1) / ctas;
+    const int64_t most = share < g.N / 4 ? share : g.N / 4;          // a tile never leaves its token tile
+    const int64_t tiles = (most + 31) / 32, groups = (most + tiles - 1) / tiles;
+    const int64_t rows = (4 * groups + 7) / 8 * 8;
+    return rows < 16 ? 16 : (int)rows;
 }
 
 template <int NT, int CG, bool BWD>
@@ -809,13 +1002,18 @@ cudaError_t launch_shape(const I8GemmLaunch &g, int sms, cudaStream_t stream)
     const int64_t Em = g.E > 0 ? g.E : 1;
     // 128-byte wide boxes: weight codes [E N, K], row codes [M, K] (backward [M, N]) by whole tiles
     // and by kBox tokens
-    CUtensorMap tmW, tmX, tmBox;
+    const int box = CG == 1 ? whole_box(g, resident_units[dev], NT) : 128;
+    CUtensorMap tmW, tmX, tmBox, tmW64, tmW16;
     bool ok = make_tmap(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.wcodes, (uint64_t)g.K, (uint64_t)(Em * g.N), 128,
-                        128, CU_TENSOR_MAP_SWIZZLE_128B);
+                        box, CU_TENSOR_MAP_SWIZZLE_128B);
     ok &= make_tmap(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.codes, (uint64_t)(BWD ? g.N : g.K), (uint64_t)g.M, 128,
                     BWD ? 128 : Cfg::kColsPerCta, CU_TENSOR_MAP_SWIZZLE_128B);
     ok &= make_tmap(&tmBox, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.codes, (uint64_t)(BWD ? g.N : g.K), (uint64_t)g.M, 128,
                     Cfg::kBox, CU_TENSOR_MAP_SWIZZLE_128B);
+    ok &= make_tmap(&tmW64, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.wcodes, (uint64_t)g.K, (uint64_t)(Em * g.N), 128, 64,
+                    CU_TENSOR_MAP_SWIZZLE_128B);
+    ok &= make_tmap(&tmW16, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.wcodes, (uint64_t)g.K, (uint64_t)(Em * g.N), 128, 16,
+                    CU_TENSOR_MAP_SWIZZLE_128B);
     if (!ok)
         return cudaErrorInvalidValue;
     I8Args a;
@@ -833,6 +1031,7 @@ cudaError_t launch_shape(const I8GemmLaunch &g, int sms, cudaStream_t stream)
     a.K = g.K;
     a.E = g.E;
     a.out_bf16 = g.out_bf16;
+    a.box = box;
     a.slab_units = slab_units(BWD, g.E, g.M, g.N, g.K);
     // dependent launch: set-up and the first weight tiles overlap the quantisation in front
     cudaLaunchConfig_t cfg = {};
@@ -845,7 +1044,7 @@ cudaError_t launch_shape(const I8GemmLaunch &g, int sms, cudaStream_t stream)
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, sq_i8_kernel<NT, CG, BWD>, BWD ? tmX : tmW, BWD ? tmW : tmX, tmBox, a);
+    return cudaLaunchKernelEx(&cfg, sq_i8_kernel<NT, CG, BWD>, BWD ? tmX : tmW, BWD ? tmW : tmX, tmBox, tmW64, tmW16, a);
 }
 
 }  // namespace

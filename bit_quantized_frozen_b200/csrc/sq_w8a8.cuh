@@ -18,7 +18,7 @@ constexpr int kMaxExperts = 1024;
 struct I8Tile {
     int e;                    // expert
     int row0, rows;           // first token and tokens of the tile
-    int wt;                   // tile along the weight (product only)
+    int wt;                   // tile along the weight (0 with wts = 1)
 };
 
 // The tiles of all experts in a row: expert e has ceil(rows / tok_tile) token tiles, each times
