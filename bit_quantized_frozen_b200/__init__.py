@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -59,6 +60,9 @@ EXPORTED = [
     "sq_reconstruct_bf16",
     "sq_check_device_status", "sq_set_gemm_events", "sq_set_stage_events", "sq_linear_fwd_noalloc", "sq_linear_bwd_dx",
     "sq_selftest_wait_timeout", "sq_svd_init",
+]
+# include/sq_w8a8.h: the products of 8-bit integers
+EXPORTED_W8A8 = [
     "sq_linear_fwd_w8a8", "sq_linear_bwd_dx_w8a8", "sq_grouped_fwd_w8a8", "sq_grouped_bwd_dx_w8a8",
     "sq_grouped_workspace_bytes",
 ]
@@ -331,41 +335,56 @@ def sq_linear_bwd_dx(w: "Weight", dy, dx, ws, stream=None):
                                                       _numel_bytes(ws), _stream(stream)))
 
 
-def _rows(fn: str, name: str, t, width: int):
-    """A bf16 matrix [M, width] on the current device."""
-    if t.dim() != 2 or t.shape[1] != width or t.dtype != torch.bfloat16:
-        raise ValueError(f"{fn}: {name} must be bfloat16 [M, {width}], got {t.dtype} {list(t.shape)}")
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{fn}: {name} is on {t.device}, the current device is {torch.cuda.current_device()}")
-    return t.shape[0]
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_W8A8 = {}                               # entry point by name, looked up once
 
 
 def _w8a8(fn: str, w, x, y, flags, ws, stream, backward: bool, offsets=None):
     """Checks and call of the four 8-bit integer products; w: a Weight, or a GroupedWeight with offsets."""
+    N, K, E = w.N, w.K, getattr(w, "E", None)
+    wide, out = (N, K) if backward else (K, N)
     if w.fmt != SQ_FMT_INT8_ROW:
         raise ValueError(f"{fn}: the weight must be SQ_FMT_INT8_ROW")
-    N, K, E = int(w.N), int(w.K), getattr(w, "E", None)
-    wide, out = (N, K) if backward else (K, N)
-    xn, yn = ("dy", "dx") if backward else ("x", "y")
-    M = _rows(fn, xn, x, wide)
+    if x.dim() != 2 or x.shape[1] != wide or x.dtype != torch.bfloat16:
+        raise ValueError(f"{fn}: {'dy' if backward else 'x'} must be bfloat16 [M, {wide}], "
+                         f"got {x.dtype} {list(x.shape)}")
+    M = x.shape[0]
     experts = 1 if E is None else E
     _need(fn, "codes", w.codes, experts * N * K)
     _need(fn, "scales", w.scales, 4 * experts * N)
-    _need(fn, "lora_up", w.lora_up, 2 * experts * N * RANK_INT8)
-    _need(fn, "lora_down", w.lora_down, 2 * experts * K * RANK_INT8)
-    _need(fn, yn, y, M * out * (2 if flags & SQ_OUT_BF16 else 4))
-    if y.dtype != (torch.bfloat16 if flags & SQ_OUT_BF16 else torch.float32):
-        raise ValueError(f"{fn}: {yn} is {y.dtype}, the flags ask for the other type")
-    grouped = ()
+    if w.lora_up is not None:
+        _need(fn, "lora_up", w.lora_up, 2 * experts * N * RANK_INT8)
+    if w.lora_down is not None:
+        _need(fn, "lora_down", w.lora_down, 2 * experts * K * RANK_INT8)
+    bf16 = flags & SQ_OUT_BF16
+    _need(fn, "dx" if backward else "y", y, M * out * (2 if bf16 else 4))
+    if y.dtype != (torch.bfloat16 if bf16 else torch.float32):
+        raise ValueError(f"{fn}: {'dx' if backward else 'y'} is {y.dtype}, the flags ask for the other type")
     if E is not None:
         if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] != E + 1:
             raise ValueError(f"{fn}: offsets must be int32 [{E + 1}], got {offsets.dtype} {list(offsets.shape)}")
         if M == 0:
             return
-        grouped = (_ptr(offsets),)
-    cw = w.as_c()
-    _check(fn, getattr(lib(), fn)(ctypes.byref(cw), *(() if E is None else (E,)), _ptr(x), M, *grouped, _ptr(y), flags,
-                                  _ptr(ws), 0 if ws is None else _numel_bytes(ws), _stream(stream)))
+    xp, yp = _ptr(x), _ptr(y)
+    dev = x.device.index
+    for t in (y, w.codes, w.scales, w.lora_up, w.lora_down, ws, offsets):
+        if t is not None and not isinstance(t, int) and t.is_cuda and t.device.index != dev:
+            raise ValueError(f"{fn}: tensors on {t.device} and on {x.device}")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{fn}: the tensors are on {x.device}, the current device is {torch.cuda.current_device()}")
+    if stream is None and _raw_stream is not None:
+        stream = _raw_stream(dev)
+    f = _W8A8.get(fn)
+    if f is None:
+        f = _W8A8[fn] = getattr(lib(), fn)
+    nb = 0 if ws is None else _numel_bytes(ws)
+    cw = ctypes.byref(w.as_c())
+    if E is None:
+        st = f(cw, xp, M, yp, flags, _ptr(ws), nb, _stream(stream))
+    else:
+        st = f(cw, E, xp, M, _ptr(offsets), yp, flags, _ptr(ws), nb, _stream(stream))
+    if st != SQ_OK:
+        _check(fn, st)
 
 
 def sq_linear_fwd_w8a8(w: "Weight", x, y, flags: int = 0, ws=None, stream=None):
@@ -566,43 +585,52 @@ def _allocating_on(stream):
     return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
+@functools.lru_cache(maxsize=4096)
+def _w8a8_bytes(op, E, M, N, K):
+    """Workspace size of a shape (a pure function of it)."""
+    return sq_workspace_bytes(op, M, N, K) if E is None else sq_grouped_workspace_bytes(op, E, M, N, K)
+
+
 def _w8a8_out(fn, op, w, x, offsets, width, ws, flags, out_bf16, stream):
+    if stream is not None:
+        with _allocating_on(stream):
+            return _w8a8_out_here(fn, op, w, x, offsets, width, ws, flags, out_bf16, stream)
+    return _w8a8_out_here(fn, op, w, x, offsets, width, ws, flags, out_bf16, None)
+
+
+def _w8a8_out_here(fn, op, w, x, offsets, width, ws, flags, out_bf16, stream):
     if out_bf16:
         flags |= SQ_OUT_BF16
-    M, E = x.shape[0], getattr(w, "E", None)
-    with _allocating_on(stream):
-        y = torch.empty((M, width), dtype=torch.bfloat16 if flags & SQ_OUT_BF16 else torch.float32, device=x.device)
-        if ws is None:
-            n = (sq_workspace_bytes(op, M, w.N, w.K) if E is None
-                 else sq_grouped_workspace_bytes(op, E, M, w.N, w.K))
-            ws = torch.empty(n, dtype=torch.uint8, device=x.device)
-        if E is None:
-            fn(w, x, y, flags=flags, ws=ws, stream=stream)
-        else:
-            fn(w, x, offsets, y, flags=flags | SQ_ZERO_UNGROUPED, ws=ws, stream=stream)
+    M, E, dev = x.shape[0], getattr(w, "E", None), x.device
+    y = torch.empty((M, width), dtype=torch.bfloat16 if flags & SQ_OUT_BF16 else torch.float32, device=dev)
+    if ws is None:
+        ws = torch.empty(_w8a8_bytes(op, E, M, w.N, w.K), dtype=torch.uint8, device=dev)
+    if E is not None:
+        flags |= SQ_ZERO_UNGROUPED
+    _w8a8(fn, w, x, y, flags, ws, stream, "bwd" in fn, offsets)
     return y
 
 
 def linear_fwd_w8a8(w: Weight, x: torch.Tensor, ws=None, flags: int = 0, out_bf16: bool = False,
                     stream=None) -> torch.Tensor:
     """y [M, N] = x W^T in 8-bit integers (int8 weight, int8 codes per token), fp32 or bf16."""
-    return _w8a8_out(sq_linear_fwd_w8a8, SQ_OP_LINEAR_FWD_W8A8, w, x, None, w.N, ws, flags, out_bf16, stream)
+    return _w8a8_out("sq_linear_fwd_w8a8", SQ_OP_LINEAR_FWD_W8A8, w, x, None, w.N, ws, flags, out_bf16, stream)
 
 
 def linear_bwd_dx_w8a8(w: Weight, dy: torch.Tensor, ws=None, flags: int = 0, out_bf16: bool = False,
                        stream=None) -> torch.Tensor:
     """dx [M, K] = dy W in 8-bit integers, fp32 or bf16."""
-    return _w8a8_out(sq_linear_bwd_dx_w8a8, SQ_OP_LINEAR_BWD_DX_W8A8, w, dy, None, w.K, ws, flags, out_bf16, stream)
+    return _w8a8_out("sq_linear_bwd_dx_w8a8", SQ_OP_LINEAR_BWD_DX_W8A8, w, dy, None, w.K, ws, flags, out_bf16, stream)
 
 
 def grouped_fwd_w8a8(w: GroupedWeight, x: torch.Tensor, offsets: torch.Tensor, ws=None, flags: int = 0,
                      out_bf16: bool = False, stream=None) -> torch.Tensor:
     """y [M, N]: rows offsets[e] .. offsets[e + 1] - 1 of x times expert e's W^T; rows of no expert are 0."""
-    return _w8a8_out(sq_grouped_fwd_w8a8, SQ_OP_GROUPED_FWD_W8A8, w, x, offsets, w.N, ws, flags, out_bf16, stream)
+    return _w8a8_out("sq_grouped_fwd_w8a8", SQ_OP_GROUPED_FWD_W8A8, w, x, offsets, w.N, ws, flags, out_bf16, stream)
 
 
 def grouped_bwd_dx_w8a8(w: GroupedWeight, dy: torch.Tensor, offsets: torch.Tensor, ws=None, flags: int = 0,
                         out_bf16: bool = False, stream=None) -> torch.Tensor:
     """dx [M, K]: rows offsets[e] .. offsets[e + 1] - 1 of dy times expert e's W; rows of no expert are 0."""
-    return _w8a8_out(sq_grouped_bwd_dx_w8a8, SQ_OP_GROUPED_BWD_DX_W8A8, w, dy, offsets, w.K, ws, flags, out_bf16,
+    return _w8a8_out("sq_grouped_bwd_dx_w8a8", SQ_OP_GROUPED_BWD_DX_W8A8, w, dy, offsets, w.K, ws, flags, out_bf16,
                      stream)

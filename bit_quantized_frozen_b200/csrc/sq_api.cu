@@ -10,6 +10,7 @@
 #include <cstring>
 
 #include "sq.h"
+#include "sq_w8a8.h"
 #include "sq_device.cuh"
 #include "sq_kernels.h"
 #include "sq_ptx.cuh"
@@ -200,13 +201,12 @@ FwdLayout fwd_layout(int fmt, int64_t M, int64_t N, int64_t K)
     return L;
 }
 
-// 8-bit integer products: header, the product's counters, the row operand (codes, scales,
-// low-rank input) and the partial sums of split tiles
+// 8-bit integer products: header and the row operand (codes, scales, low-rank input)
 struct I8Layout {
-    size_t counters = 0, codes = 0, scales = 0, low = 0, slabs = 0, total = 0;
+    size_t codes = 0, scales = 0, low = 0, total = 0;
 };
 
-I8Layout i8_layout(bool bwd, int E, int64_t M, int64_t N, int64_t K)
+I8Layout i8_layout(bool bwd, int64_t M, int64_t N, int64_t K)
 {
     I8Layout L;
     size_t off = kHeader;
@@ -216,11 +216,9 @@ I8Layout i8_layout(bool bwd, int E, int64_t M, int64_t N, int64_t K)
         off += bytes;
         return at;
     };
-    L.counters = take((size_t)sq::kI8Counters * 4);
     L.codes = take((size_t)M * (size_t)(bwd ? N : K));
     L.scales = take((size_t)M * 4);
     L.low = take((size_t)M * 3 * 16 * 2);
-    L.slabs = take(sq::i8_slab_bytes(bwd, E, M, N, K));
     L.total = round_up(off, kAlign);
     return L;
 }
@@ -299,7 +297,7 @@ sq_status i8_product(bool bwd, int64_t E, const sq_weight *w, const uint16_t *x,
         return SQ_ERR_NULL;
     if (!aligned(x, 16) || !aligned(y, 16) || !aligned(offsets, 4) || !aligned(ws, 256))
         return SQ_ERR_ALIGN;
-    const I8Layout L = i8_layout(bwd, (int)E, M, N, K);
+    const I8Layout L = i8_layout(bwd, M, N, K);
     if (ws_bytes < L.total)
         return SQ_ERR_WORKSPACE;
     int sms = 0;
@@ -319,13 +317,11 @@ sq_status i8_product(bool bwd, int64_t E, const sq_weight *w, const uint16_t *x,
     q.scales = reinterpret_cast<float *>(ws_at(ws, L.scales));
     q.low = w->lora_up ? reinterpret_cast<uint16_t *>(ws_at(ws, L.low)) : nullptr;
     q.status = status;
-    q.counters = reinterpret_cast<uint32_t *>(ws_at(ws, L.counters));
     q.y_zero = (flags & SQ_ZERO_UNGROUPED) ? reinterpret_cast<uint8_t *>(y) : nullptr;
     q.y_row_bytes = width * ((flags & SQ_OUT_BF16) ? 2 : 4);
     q.M = M;
     q.K = bwd ? N : K;
     q.E = (int)E;
-    q.n_counters = sq::kI8Counters;
     q.finite_check = (flags & SQ_CHECK_FINITE) ? 1 : 0;
     // the first block of the quantisation writes the status word; with a finite check any block
     // may set it, so it is cleared first
@@ -350,8 +346,6 @@ sq_status i8_product(bool bwd, int64_t E, const sq_weight *w, const uint16_t *x,
     g.factor = bwd ? w->lora_down : w->lora_up;
     g.y = y;
     g.out_bf16 = (flags & SQ_OUT_BF16) ? 1 : 0;
-    g.slabs = reinterpret_cast<int32_t *>(ws_at(ws, L.slabs));
-    g.counters = q.counters;
     g.status = status;
     SQ_CUDA(stage_event(SQ_STAGE_GEMM, 0, s), "event record");
     SQ_CUDA(sq::launch_i8_gemm(g, sms, s), "int8 product");
@@ -435,9 +429,9 @@ size_t sq_workspace_bytes(int op, int64_t M, int64_t N, int64_t K)
     case SQ_OP_SVD_INIT:
         return sq::svd_workspace_bytes(N, K);
     case SQ_OP_LINEAR_FWD_W8A8:
-        return i8_layout(false, 0, M, N, K).total;
+        return i8_layout(false, M, N, K).total;
     case SQ_OP_LINEAR_BWD_DX_W8A8:
-        return i8_layout(true, 0, M, N, K).total;
+        return i8_layout(true, M, N, K).total;
     default:
         return 0;
     }
@@ -449,9 +443,9 @@ size_t sq_grouped_workspace_bytes(int op, int64_t E, int64_t M, int64_t N, int64
         return 0;
     switch (op) {
     case SQ_OP_GROUPED_FWD_W8A8:
-        return i8_layout(false, (int)E, M, N, K).total;
+        return i8_layout(false, M, N, K).total;
     case SQ_OP_GROUPED_BWD_DX_W8A8:
-        return i8_layout(true, (int)E, M, N, K).total;
+        return i8_layout(true, M, N, K).total;
     default:
         return 0;
     }

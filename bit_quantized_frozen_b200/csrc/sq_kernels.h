@@ -106,12 +106,10 @@ struct I8QuantArgs {
     float *scales;              // [M]
     uint16_t *low;              // x factor [M, 16] as three bf16 terms, [M, 3, 16], or NULL
     uint32_t *status;
-    uint32_t *counters;         // zeroed for the product
     uint8_t *y_zero;            // output whose rows outside every expert become 0, or NULL
     int64_t y_row_bytes;
     int64_t M, K;               // K % 256 == 0 (backward: % 128)
     int E;                      // experts, 0: one layer
-    int n_counters;
     int finite_check;           // 1: a row with a NaN or an infinity sets kStatusNonfinite
 };
 cudaError_t launch_i8_quant(const I8QuantArgs &a, bool bwd, int sms, cudaStream_t s);
@@ -131,13 +129,8 @@ struct I8GemmLaunch {
     const uint16_t *factor;     // lora_up [., N, 16] (forward) or lora_down [., K, 16] (backward)
     void *y;                    // [M, N] (backward [M, K]) fp32 or bf16
     int out_bf16;
-    int32_t *slabs;             // partial sums of split tiles, i8_slab_bytes
-    uint32_t *counters;         // kI8Counters, zero at the launch
     uint32_t *status;
 };
-constexpr int kI8Counters = 512;
-// bytes of the partial sums a product of this shape may need (0: it never splits a tile)
-size_t i8_slab_bytes(bool bwd, int E, int64_t M, int64_t N, int64_t K);
 cudaError_t launch_i8_gemm(const I8GemmLaunch &g, int sms, cudaStream_t stream);
 
 // ID of the current CUDA context (unique for the life of the process; a context created

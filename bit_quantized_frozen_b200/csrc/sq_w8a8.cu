@@ -26,14 +26,10 @@
 // A tile's MMAs and loads cover only the boxes of tokens that it has (the instruction's
 // column count is set per tile), so that an expert with few rows costs few.
 //
-// Tiles of a CTA pair whose last round would leave many SMs idle are dealt out in equal
-// shares of the summed axis instead (I8Deal): a unit stores the 32-bit partial sums of a
-// tile that it shares, counts up, and the one that counts last adds them all and
-// finishes the tile.  Integer sums do not depend on the order, so neither does the
-// result.  Few tokens (CG = 1) are bound by the weight's bytes: each CTA takes an equal
-// share of all channels, to four of them, as tiles of up to 128, so that every SM reads
-// the same amount and nothing has to be joined.  (Splitting the summed axis over the SMs
-// instead cost 3 to 4 us for storing, counting and adding: M = 1, N = K = 6144 16 us.)
+// Few tokens (CG = 1) are bound by the weight's bytes: each CTA takes an equal share of
+// all channels, to four of them, as tiles of up to 128, so that every SM reads the same
+// amount.  (Splitting the summed axis over idle SMs instead, with the partial sums joined
+// through L2, cost 4 us at 16 tokens and 15 us and more with 256-column tiles.)
 #include <cuda.h>
 
 #include "sq_device.cuh"
@@ -43,14 +39,16 @@
 
 namespace sq {
 
-constexpr int kChunk = 128;                       // summed values (bytes) per stage
-constexpr int kMinSplitChunks = 4;                // a unit's share is at least this many
+constexpr int kChunk = 128;                       // summed values (bytes) of a shared-memory row
 
 template <int NT, int CG, bool BWD>
 struct I8Cfg {
     static constexpr int kLaneTile = 128 * CG;                       // A rows of the tile
     static constexpr int kColsPerCta = NT / CG;                      // B rows (or columns) each CTA loads
     static constexpr int kBox = NT >= 64 ? 32 : 16;                  // token rows per TMA box (forward)
+    // chunks per stage: a stage costs the MMA issuer about 85 ns (wait, commit) beside 28 ns for each
+    // of the chunk's four narrow MMAs (K is a multiple of two chunks)
+    static constexpr int kPer = CG == 1 && NT <= 32 ? 2 : 1;
     static constexpr int kABytes = 128 * kChunk;
     static constexpr int kBBytes = kColsPerCta * kChunk;
     static constexpr int kStageBytes = kABytes + kBBytes;
@@ -90,83 +88,12 @@ struct I8Args {
     const float *wscales;     // per channel (forward)
     const uint16_t *factor;   // lane-side (forward: lora_up) or column-side (backward: lora_down) factor
     void *y;
-    int32_t *slabs;
-    uint32_t *counters;
     uint32_t *status;
     int64_t M, N, K;          // N, K of one expert
     int E;
     int out_bf16;
-    int slab_units;           // units there are slabs for (two each), 0: none
+    int tok;                  // tokens of a tile (forward; at most NT)
     int box;                  // weight rows of a tmA box
-};
-
-// chunks' worth of time that joining split tiles of nt columns costs (a fixed latency and the slab)
-__host__ __device__ constexpr int split_cost(int nt)
-{
-    return 8 + nt / 16;
-}
-
-// How the tiles are spread over the units (CTAs or CTA pairs).  Whole tiles in turn, unless the
-// last, partly filled round wastes more than `cost` chunks a unit: then the chunks of all tiles
-// are dealt out evenly as one row of chunks, and a tile that crosses a border is summed from
-// the partial sums of its units.
-struct I8Deal {
-    int tiles, units, chunks;
-    bool even;                // chunks dealt out evenly over `units`
-
-    __host__ __device__ __forceinline__ I8Deal(int tiles_, int units_, int chunks_, int cost, bool slabs)
-        : tiles(tiles_), units(units_), chunks(chunks_), even(false)
-    {
-        if (!slabs || tiles <= 0 || tiles >= 8 * units)
-            return;
-        const int rounds = (tiles + units - 1) / units;
-        if ((rounds * units - tiles) * (int64_t)chunks <= (int64_t)cost * units)
-            return;
-        const int64_t most = (int64_t)tiles * chunks / kMinSplitChunks;
-        units = most < units ? (most < 1 ? 1 : (int)most) : units;
-        even = true;
-    }
-
-    // even: first chunk of unit u; the unit that has chunk i
-    __host__ __device__ __forceinline__ int begin(int u) const
-    {
-        return (int)((int64_t)tiles * chunks * u / units);
-    }
-    __device__ __forceinline__ int owner(int i) const
-    {
-        return (int)(((int64_t)(i + 1) * units - 1) / ((int64_t)tiles * chunks));
-    }
-};
-
-// one unit's way through its work: (tile, chunks c0 .. c1 - 1) in turn
-struct I8Walk {
-    int pos, end, step, chunks;
-    bool even;
-    int tile, c0, c1;
-
-    __device__ __forceinline__ I8Walk(const I8Deal &d, int unit) : chunks(d.chunks), even(d.even), tile(0), c0(0), c1(0)
-    {
-        pos = even ? (unit < d.units ? d.begin(unit) : 0) : unit;
-        end = even ? (unit < d.units ? d.begin(unit + 1) : 0) : d.tiles;
-        step = d.units;
-    }
-    __device__ __forceinline__ bool next()
-    {
-        if (pos >= end)
-            return false;
-        if (even) {
-            tile = pos / chunks;
-            c0 = pos - tile * chunks;
-            c1 = min(chunks, c0 + end - pos);
-            pos += c1 - c0;
-        } else {
-            tile = pos;
-            c0 = 0;
-            c1 = chunks;
-            pos += step;
-        }
-        return true;
-    }
 };
 
 // CG = 1: a CTA's share of all (token tile, channel) pairs, in tiles of up to 128 channels
@@ -203,44 +130,40 @@ struct I8ChannelWalk {
     }
 };
 
-// what a unit does next: tile t, its lanes (channels from n0 on; backward: tokens), chunks c0 .. c1 - 1
+// what a unit does next: tile t, its lanes (channels from n0 on; backward: tokens)
 struct I8Work {
     I8Tile t;
-    int tile, n0, lanes, c0, c1;
+    int n0, lanes;
 };
 
-template <int NT, int CG, bool BWD>
+// CG = 2: every units-th tile; CG = 1: the CTA's share of the channels
+template <int CG, bool BWD>
 struct I8Units {
     const I8Plan &plan;
-    I8Walk walk;              // CG = 2
-    I8ChannelWalk cwalk;      // CG = 1
+    I8ChannelWalk share;
+    int tile, tiles, units, e;
     int64_t N;
-    int e;
 
-    __device__ __forceinline__ I8Units(const I8Plan &p, const I8Deal &d, const I8ChannelWalk &c, int unit, int64_t N_)
-        : plan(p), walk(d, unit), cwalk(c), N(N_), e(0)
+    __device__ __forceinline__ I8Units(const I8Plan &p, const I8ChannelWalk &c, int tiles_, int unit, int units_,
+                                       int64_t N_)
+        : plan(p), share(c), tile(unit), tiles(tiles_), units(units_), e(0), N(N_)
     {
     }
     __device__ __forceinline__ bool next(I8Work &w)
     {
         if (CG == 1) {
-            if (!cwalk.next())
+            if (!share.next())
                 return false;
-            w.tile = cwalk.tile;
-            w.t = plan.find(cwalk.tile, e);
-            w.n0 = cwalk.n0;
-            w.lanes = cwalk.channels;
-            w.c0 = 0;
-            w.c1 = walk.chunks;
+            w.t = plan.find(share.tile, e);
+            w.n0 = share.n0;
+            w.lanes = share.channels;
         } else {
-            if (!walk.next())
+            if (tile >= tiles)
                 return false;
-            w.tile = walk.tile;
-            w.t = plan.find(walk.tile, e);
+            w.t = plan.find(tile, e);
             w.n0 = BWD ? 0 : w.t.wt * 256;
             w.lanes = BWD ? w.t.rows : (int)min((int64_t)256, N - w.n0);
-            w.c0 = walk.c0;
-            w.c1 = walk.c1;
+            tile += units;
         }
         return true;
     }
@@ -287,7 +210,6 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + Cfg::kNumBars);
     volatile uint32_t *abort_flag = tmem_holder + 1;
     volatile uint32_t *verdict = tmem_holder + 2;
-    volatile uint32_t *last_item = tmem_holder + 3;
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -327,13 +249,14 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
             prefetch_tmap(&tmA16);
         }
     }
+    grid_dep_launch();                            // the next call's quantisation may be set up
     // the offsets are an input of the call: they are there before the kernel in front starts
     I8Plan plan;
     plan.E = args.E > 0 ? args.E : 1;
     plan.start = plan_mem;
     plan.prefix = plan_mem + kMaxExperts + 1;
     plan.wts = CG == 1 ? 1 : BWD ? (int)(args.K / NT) : (int)((args.N + Cfg::kLaneTile - 1) / Cfg::kLaneTile);
-    plan.tok_tile = BWD ? Cfg::kLaneTile : NT;
+    plan.tok_tile = BWD ? Cfg::kLaneTile : args.tok;
     plan.build(args.E > 0 ? args.offsets : nullptr, args.M, threadIdx.x, Cfg::kThreads);
     tc_fence_before();
     if (CG == 2)
@@ -346,13 +269,14 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
     const int tiles = plan.tiles();
     const int unit = (int)blockIdx.x / CG;
     const int units = (int)gridDim.x / CG;
-    const I8Deal deal(tiles, args.slab_units > 0 ? min(units, args.slab_units) : units,
-                      (int)((BWD ? args.N : args.K) / kChunk), split_cost(NT), CG == 2 && args.slab_units > 0);
+    const int steps = (int)((BWD ? args.N : args.K) / (kChunk * Cfg::kPer));      // stages of a tile
     const I8ChannelWalk share(CG == 1 ? tiles : 0, args.N, unit, units);
-    using Units = I8Units<NT, CG, BWD>;
+    using Units = I8Units<CG, BWD>;
+    auto all_work = [&]() { return Units(plan, share, tiles, unit, units, args.N); };
     const int a_bytes = CG == 1 ? min(128, max(args.box < 128 ? args.box : 16, (share.largest() + 7) / 8 * 8)) * kChunk
                                 : Cfg::kABytes;
-    const int stage_bytes = a_bytes + Cfg::kBBytes;
+    const int chunk_bytes = a_bytes + Cfg::kBBytes;
+    const int stage_bytes = Cfg::kPer * chunk_bytes;
     const int stages = CG == 1 ? min(Cfg::kStages, Cfg::kRing / stage_bytes) / Cfg::kProducers * Cfg::kProducers
                                : Cfg::kStages;
     // columns of the accumulator a tile uses (forward: its tokens, in whole boxes of both CTAs)
@@ -362,7 +286,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
 
     if (warp >= kProducer && warp < kIssuer) {
         // ------------------------------------------------------------ producers (every CTA)
-        // Producer p fills stages p, p + P, ... with every P-th chunk of the unit's work.  The whole
+        // Producer p fills stages p, p + P, ... with every P-th step of the unit's work.  The whole
         // warp runs the loop on uniform values and one lane issues, which keeps the address
         // arithmetic off the path between two copies.
         constexpr int P = Cfg::kProducers;
@@ -375,7 +299,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
             else
                 tma_load_2d(dst, tm, x, y, bar);
         };
-        // what is the same for every chunk of a tile
+        // what is the same for every step of a tile
         struct Aim {
             int wrow, rows;           // weight: first row, rows (forward; in whole 8-row groups)
             int xrow, mine;           // row operand: first row, rows
@@ -397,7 +321,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
             m.wrow = w.t.e * (int)args.N + (BWD ? 0 : w.n0 + (int)rank * 128);
             m.mine = BWD ? 128 : cols / CG;
             m.xrow = w.t.row0 + (int)rank * m.mine;
-            m.bytes = CG * copied * kChunk + cols * kChunk;
+            m.bytes = Cfg::kPer * (CG * copied + cols) * kChunk;
             m.wrow = uniform(m.wrow);
             m.rows = uniform(m.rows);
             m.xrow = uniform(m.xrow);
@@ -405,53 +329,63 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
             m.bytes = (uint32_t)uniform((int)m.bytes);
             return m;
         };
-        auto load_w = [&](int stage, const Aim &m, int wt, int c) {
-            const uint32_t sA = s0 + stage * stage_bytes, fb = bar_full + 8 * stage;
+        auto load_w = [&](int stage, const Aim &m, int wt, int step) {
+            const uint32_t fb = bar_full + 8 * stage;
             if (leader)
                 mbar_arrive_expect_tx(fb, m.bytes);
-            if (BWD) {
-                load(&tmB, sA + a_bytes, wt * NT + (int)rank * Cfg::kColsPerCta, m.wrow + c * kChunk, fb);
-            } else if (CG == 2 || m.rows == args.box) {
-                load(&tmA, sA, c * kChunk, m.wrow, fb);
-            } else if (m.rows > 64) {             // two boxes, the second one back from the end
-                load(&tmA64, sA, c * kChunk, m.wrow, fb);
-                load(&tmA64, sA + (m.rows - 64) * kChunk, c * kChunk, m.wrow + m.rows - 64, fb);
-            } else {
-                for (int r = 0; r < m.rows; r += 16) {
-                    const int at = min(r, m.rows - 16);
-                    load(&tmA16, sA + at * kChunk, c * kChunk, m.wrow + at, fb);
+#pragma unroll
+            for (int u = 0; u < Cfg::kPer; ++u) {
+                const uint32_t sA = s0 + stage * stage_bytes + u * chunk_bytes;
+                const int x = (step * Cfg::kPer + u) * kChunk;
+                if (BWD) {
+                    load(&tmB, sA + a_bytes, wt * NT + (int)rank * Cfg::kColsPerCta, m.wrow + x, fb);
+                } else if (CG == 2 || m.rows == args.box) {
+                    load(&tmA, sA, x, m.wrow, fb);
+                } else if (m.rows > 64) {         // two boxes, the second one back from the end
+                    load(&tmA64, sA, x, m.wrow, fb);
+                    load(&tmA64, sA + (m.rows - 64) * kChunk, x, m.wrow + m.rows - 64, fb);
+                } else {
+                    for (int r = 0; r < m.rows; r += 16) {
+                        const int at = min(r, m.rows - 16);
+                        load(&tmA16, sA + at * kChunk, x, m.wrow + at, fb);
+                    }
                 }
             }
         };
-        auto load_x = [&](int stage, const Aim &m, int c) {
-            const uint32_t sX = s0 + stage * stage_bytes + (BWD ? 0 : a_bytes), fb = bar_full + 8 * stage;
-            if (BWD || m.mine == Cfg::kColsPerCta) {
-                load(BWD ? &tmA : &tmB, sX, c * kChunk, m.xrow, fb);
-            } else {
-                for (int r = 0; r < m.mine; r += Cfg::kBox)
-                    load(&tmBox, sX + r * kChunk, c * kChunk, m.xrow + r, fb);
+        auto load_x = [&](int stage, const Aim &m, int step) {
+            const uint32_t fb = bar_full + 8 * stage;
+#pragma unroll
+            for (int u = 0; u < Cfg::kPer; ++u) {
+                const uint32_t sX = s0 + stage * stage_bytes + u * chunk_bytes + (BWD ? 0 : a_bytes);
+                const int x = (step * Cfg::kPer + u) * kChunk;
+                if (BWD || m.mine == Cfg::kColsPerCta) {
+                    load(BWD ? &tmA : &tmB, sX, x, m.xrow, fb);
+                } else {
+                    for (int r = 0; r < m.mine; r += Cfg::kBox)
+                        load(&tmBox, sX + r * kChunk, x, m.xrow + r, fb);
+                }
             }
         };
         I8Work w;
-        int early = 0;                            // chunks of the first tile whose weight operand is on its way
-        if (Units first(plan, deal, share, unit, args.N); first.next(w)) {
-            early = uniform(min(w.c1 - w.c0, stages));
+        int early = 0;                            // steps of the first tile whose weight operand is on its way
+        if (Units first = all_work(); first.next(w)) {
+            early = min(steps, stages);
             const Aim m = aim_at(w);
-            const int c0 = uniform(w.c0), wt = uniform(w.t.wt);
+            const int wt = uniform(w.t.wt);
             if (issue)
                 for (int i = p; i < early; i += P)
-                    load_w(i, m, wt, c0 + i);
+                    load_w(i, m, wt, i);
         }
         grid_dep_wait();                          // codes, scales and low-rank input of the rows
         int stage = p;
         uint32_t phase = 0;
         bool ok = true;
-        int skip = p;                             // chunks of the others before this producer's next one
-        for (Units work(plan, deal, share, unit, args.N); ok && work.next(w);) {
+        int skip = p;                             // steps of the others before this producer's next one
+        for (Units work = all_work(); ok && work.next(w);) {
             const Aim m = aim_at(w);
-            const int c1 = uniform(w.c1), wt = uniform(w.t.wt);
-            int c = uniform(w.c0) + skip;
-            for (; c < c1; c += P) {
+            const int wt = uniform(w.t.wt);
+            int c = skip;
+            for (; c < steps; c += P) {
                 const bool fresh = early <= p;
                 if (fresh && !mbar_wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag, args.status)) {
                     ok = false;
@@ -469,7 +403,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                     phase ^= 1u;
                 }
             }
-            skip = c - c1;
+            skip = c - steps;
         }
         // let every load that was issued land (and be consumed) before the CTA exits
         for (int st = p; st < stages; st += P) {
@@ -487,15 +421,14 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
             const bool issue = elect_one();
             const uint32_t s0 = smem_u32(smem);
             const uint64_t dA0 = sdesc_sw128(s0), dB0 = sdesc_sw128(s0 + a_bytes);
-            const uint32_t stage16 = stage_bytes >> 4;
+            const uint32_t stage16 = stage_bytes >> 4, chunk16 = chunk_bytes >> 4;
             int stage = 0;
             uint32_t phase = 0;
             uint64_t dA = dA0, dB = dB0;
             int count = 0;
             bool ok = true;
             I8Work w;
-            for (Units work(plan, deal, share, unit, args.N); ok && work.next(w); ++count) {
-                const int n = uniform(w.c1 - w.c0);
+            for (Units work = all_work(); ok && work.next(w); ++count) {
                 const uint32_t idesc = Cfg::kIdesc | (uint32_t)uniform(columns(w.t) >> 3) << 17;
                 const uint32_t acc = tmem_base + ((count & 1) ? (uint32_t)NT : 0u);
                 // the tile before last (same accumulator) has left tensor memory
@@ -503,7 +436,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                                                 abort_flag, args.status))
                     break;
                 tc_fence_after();
-                for (int c = 0; c < n; ++c) {
+                for (int c = 0; c < steps; ++c) {
                     if (!acc_wait<CG>(bar_full + 8 * stage, phase, abort_flag, args.status)) {
                         ok = false;
                         break;
@@ -511,8 +444,11 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                     tc_fence_after();
                     if (issue) {
 #pragma unroll
-                        for (int k = 0; k < kChunk / 32; ++k)
-                            mma_i8<CG>(acc, dA + 2 * k, dB + Cfg::kBStep16 * k, idesc, (c > 0 || k > 0) ? 1u : 0u);
+                        for (int u = 0; u < Cfg::kPer; ++u)
+#pragma unroll
+                            for (int k = 0; k < kChunk / 32; ++k)
+                                mma_i8<CG>(acc, dA + u * chunk16 + 2 * k, dB + u * chunk16 + Cfg::kBStep16 * k, idesc,
+                                           (c > 0 || u > 0 || k > 0) ? 1u : 0u);
                         if (CG == 2)
                             tc_commit2_both(bar_empty + 8 * stage);
                         else
@@ -559,11 +495,10 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
         const bool ybf = args.out_bf16 != 0;
         const bool with_low = args.low != nullptr;
         const int64_t width = BWD ? args.K : args.N;      // columns of y
-        constexpr int64_t kSlab = (int64_t)NT * 128;
         grid_dep_wait();
         int count = 0;
         I8Work w;
-        for (Units work(plan, deal, share, unit, args.N); work.next(w); ++count) {
+        for (Units work = all_work(); work.next(w); ++count) {
             const I8Tile &t = w.t;
             const int slot = count & 1;
             named_barrier_sync(1, ET);                     // the previous tile's column factors are used up
@@ -619,148 +554,100 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                 break;
             tc_fence_after();
             const uint32_t acc = tmem_base + ((uint32_t)(32 * wq) << 16) + (slot ? (uint32_t)NT : 0u);
-            // a tile of several units u0 .. u1: each but whole ones stores its sums in a slab (a
-            // unit has two: of the tile it starts in the middle of, or at the head of, and of the
-            // tile it ends in); the unit that counts last adds the others' to its own
-            const bool split = CG == 2 && w.c1 - w.c0 < deal.chunks;
-            const int t0 = w.tile * deal.chunks;
-            const int u0 = split ? deal.owner(t0) : unit, u1 = split ? deal.owner(t0 + deal.chunks - 1) : unit;
-            auto slab = [&](int u) {
-                return args.slabs + ((int64_t)(2 * u + (deal.begin(u) >= t0 ? 0 : 1)) * CG + rank) * kSlab;
-            };
-            // publish this unit's partial sums (already stored); true in the unit that comes last
-            auto last_of_tile = [&]() {
-                __threadfence();
-                named_barrier_sync(1, ET);
-                if (et == 0) {
-                    *last_item = atomicAdd(args.counters + u0 * CG + rank, 1u) == (uint32_t)(u1 - u0) ? 1u : 0u;
-                    __threadfence();
-                }
-                named_barrier_sync(1, ET);
-                return *last_item != 0u;
-            };
-
             if constexpr (BWD) {
-                // raw sums of columns 32 c .. 32 c + 31 of this thread's lane
-                auto load_acc = [&](int c, uint32_t (&r)[32]) {
+                // strides 1 .. 16 inside each 32 columns, back into tensor memory
+                for (int c = 4 * wh; c < 4 * wh + 4; ++c) {
+                    uint32_t r[32];
                     __syncwarp();
                     tmem_ld_32cols(acc + 32 * c, r);
                     tmem_wait_ld();
-                };
-                const int l = 32 * wq + lane;
-                bool finish = true;
-                if (split) {
-                    int32_t *mine = slab(unit) + l;
-                    for (int c = 4 * wh; c < 4 * wh + 4; ++c) {
-                        uint32_t r[32];
-                        load_acc(c, r);
+                    uint64_t v[16];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            mine[128 * (32 * c + i)] = (int32_t)r[i];
+                    for (int i = 0; i < 16; ++i) {
+                        const float a = __fmul_rn(__int2float_rn((int32_t)r[2 * i]), lscale);
+                        const float b = __fmul_rn(__int2float_rn((int32_t)r[2 * i + 1]), lscale);
+                        v[i] = f2_pack(__fadd_rn(a, b), __fsub_rn(a, b));
                     }
-                    finish = last_of_tile();
-                }
-                if (finish) {
-                    // strides 1 .. 16 inside each 32 columns, back into tensor memory
-                    for (int c = 4 * wh; c < 4 * wh + 4; ++c) {
-                        uint32_t r[32];
-                        load_acc(c, r);
-                        if (split)
-                            for (int u = u0; u <= u1; ++u)
-                                if (u != unit) {
-                                    const int32_t *p = slab(u) + l + 128 * 32 * c;
 #pragma unroll
-                                    for (int i = 0; i < 32; ++i)
-                                        r[i] += (uint32_t)__ldcg(p + 128 * i);
-                                }
-                        uint64_t v[16];
+                    for (int h = 1; h <= 8; h <<= 1)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float a = __fmul_rn(__int2float_rn((int32_t)r[2 * i]), lscale);
-                            const float b = __fmul_rn(__int2float_rn((int32_t)r[2 * i + 1]), lscale);
-                            v[i] = f2_pack(__fadd_rn(a, b), __fsub_rn(a, b));
-                        }
-#pragma unroll
-                        for (int h = 1; h <= 8; h <<= 1)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if ((i & h) == 0) {
-                                    const uint64_t a = v[i], b = v[i + h];
-                                    v[i] = f2_add(a, b);
-                                    v[i + h] = f2_sub(a, b);
-                                }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float a, b;
-                            f2_unpack(v[i], a, b);
-                            r[2 * i] = __float_as_uint(a);
-                            r[2 * i + 1] = __float_as_uint(b);
-                        }
-                        tmem_st_32cols(acc + 32 * c, r);
-                    }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    named_barrier_sync(1, ET);             // both halves of the columns are written
-                    tc_fence_after();
-                    // strides 32, 64, 128 over columns 16 wh .. + 15 of each 32, as fragments of
-                    // 16 tokens; the low-rank term; the store (32-byte runs of a row)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t r[8][2][4];
-                        __syncwarp();
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            tmem_ld_frag2(acc + ((uint32_t)(16 * h) << 16) + 32 * j + 16 * wh, r[j]);
-                        tmem_wait_ld();
-                        uint64_t v[8][2][2];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                v[j][i >> 1][i & 1] = f2_pack(__uint_as_float(r[j][i >> 1][2 * (i & 1)]),
-                                                              __uint_as_float(r[j][i >> 1][2 * (i & 1) + 1]));
-#pragma unroll
-                        for (int x = 1; x <= 4; x <<= 1)
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if ((j & x) == 0)
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        const uint64_t a = v[j][i >> 1][i & 1], b = v[j + x][i >> 1][i & 1];
-                                        v[j][i >> 1][i & 1] = f2_add(a, b);
-                                        v[j + x][i >> 1][i & 1] = f2_sub(a, b);
-                                    }
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int col = 32 * j + 16 * wh;
-                            float low[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-                            if (with_low) {                // B: 16 columns (two groups of 8) x 16 ranks
-                                uint32_t b[4];
-                                ldmatrix_x4<false>(col_low + (col + 8 * (lane >> 4) + (lane & 7)) * Cfg::kLowPitch +
-                                                       16 * ((lane >> 3) & 1),
-                                                   b);
-#pragma unroll
-                                for (int p = kLowParts - 1; p >= 0; --p) {
-                                    mma_16816(low[0], ufrag[h][p], b[0], b[1]);
-                                    mma_16816(low[1], ufrag[h][p], b[2], b[3]);
-                                }
+                        for (int i = 0; i < 16; ++i)
+                            if ((i & h) == 0) {
+                                const uint64_t a = v[i], b = v[i + h];
+                                v[i] = f2_add(a, b);
+                                v[i + h] = f2_sub(a, b);
                             }
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {  // group i >> 1, fragment rows g + 8 (i & 1)
-                                const int row = 16 * h + g + 8 * (i & 1);
-                                float a, b;
-                                f2_unpack(v[j][i >> 1][i & 1], a, b);
-                                a = __fmaf_rn(a, 0.0625f, low[i >> 1][2 * (i & 1)]);
-                                b = __fmaf_rn(b, 0.0625f, low[i >> 1][2 * (i & 1) + 1]);
-                                const int64_t at = (base + row) * width + (int64_t)t.wt * NT + col + 8 * (i >> 1) + 2 * q;
-                                if (lane0 + row < w.lanes && SQ_DCHECK(at + 2 <= args.M * width, args.status)) {
-                                    if (ybf)
-                                        *reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(args.y) + at) =
-                                            f32x2_to_bf16x2_bits(a, b);
-                                    else
-                                        *reinterpret_cast<float2 *>(reinterpret_cast<float *>(args.y) + at) =
-                                            make_float2(a, b);
+                    for (int i = 0; i < 16; ++i) {
+                        float a, b;
+                        f2_unpack(v[i], a, b);
+                        r[2 * i] = __float_as_uint(a);
+                        r[2 * i + 1] = __float_as_uint(b);
+                    }
+                    tmem_st_32cols(acc + 32 * c, r);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                named_barrier_sync(1, ET);             // both halves of the columns are written
+                tc_fence_after();
+                // strides 32, 64, 128 over columns 16 wh .. + 15 of each 32, as fragments of
+                // 16 tokens; the low-rank term; the store (32-byte runs of a row)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t r[8][2][4];
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        tmem_ld_frag2(acc + ((uint32_t)(16 * h) << 16) + 32 * j + 16 * wh, r[j]);
+                    tmem_wait_ld();
+                    uint64_t v[8][2][2];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[j][i >> 1][i & 1] = f2_pack(__uint_as_float(r[j][i >> 1][2 * (i & 1)]),
+                                                          __uint_as_float(r[j][i >> 1][2 * (i & 1) + 1]));
+#pragma unroll
+                    for (int x = 1; x <= 4; x <<= 1)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if ((j & x) == 0)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const uint64_t a = v[j][i >> 1][i & 1], b = v[j + x][i >> 1][i & 1];
+                                    v[j][i >> 1][i & 1] = f2_add(a, b);
+                                    v[j + x][i >> 1][i & 1] = f2_sub(a, b);
                                 }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int col = 32 * j + 16 * wh;
+                        float low[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+                        if (with_low) {                // B: 16 columns (two groups of 8) x 16 ranks
+                            uint32_t b[4];
+                            ldmatrix_x4<false>(col_low + (col + 8 * (lane >> 4) + (lane & 7)) * Cfg::kLowPitch +
+                                                   16 * ((lane >> 3) & 1),
+                                               b);
+#pragma unroll
+                            for (int p = kLowParts - 1; p >= 0; --p) {
+                                mma_16816(low[0], ufrag[h][p], b[0], b[1]);
+                                mma_16816(low[1], ufrag[h][p], b[2], b[3]);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {  // group i >> 1, fragment rows g + 8 (i & 1)
+                            const int row = 16 * h + g + 8 * (i & 1);
+                            float a, b;
+                            f2_unpack(v[j][i >> 1][i & 1], a, b);
+                            a = __fmaf_rn(a, 0.0625f, low[i >> 1][2 * (i & 1)]);
+                            b = __fmaf_rn(b, 0.0625f, low[i >> 1][2 * (i & 1) + 1]);
+                            const int64_t at = (base + row) * width + (int64_t)t.wt * NT + col + 8 * (i >> 1) + 2 * q;
+                            if (lane0 + row < w.lanes && SQ_DCHECK(at + 2 <= args.M * width, args.status)) {
+                                if (ybf)
+                                    *reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(args.y) + at) =
+                                        f32x2_to_bf16x2_bits(a, b);
+                                else
+                                    *reinterpret_cast<float2 *>(reinterpret_cast<float *>(args.y) + at) =
+                                        make_float2(a, b);
                             }
                         }
                     }
@@ -775,20 +662,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                     tmem_ld_frag2(acc + c, r[0]);
                     tmem_ld_frag2(acc + (16u << 16) + c, r[1]);
                 };
-                bool finish = true;
-                if (split) {
-                    int32_t *mine = slab(unit) + 32 * wq + lane;
-                    for (int c = c_begin; c < c_end; c += kStep) {
-                        uint32_t r[2][2][4];
-                        load_acc(c, r);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            mine[128 * (c + i)] = (int32_t)r[i >> 3][(i >> 2) & 1][i & 3];
-                    }
-                    finish = last_of_tile();
-                }
-                const bool live = finish && lane0 < w.lanes;
+                const bool live = lane0 < w.lanes;
                 auto finish16 = [&](int c, const uint32_t (&r)[2][2][4]) {
                     uint32_t b[3][4];                      // terms 0, 1 of both groups; term 2 of both
                     if (with_low) {
@@ -874,14 +748,6 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                             now[i >> 3][(i >> 2) & 1][i & 3] = r[i >> 3][(i >> 2) & 1][i & 3];
                         if (c + kStep < c_end)
                             load_acc(c + kStep, r);           // on its way while these 16 are finished
-                        if (split)
-                            for (int u = u0; u <= u1; ++u)
-                                if (u != unit) {
-                                    const int32_t *p = slab(u) + 32 * wq + lane + 128 * c;
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i)
-                                        now[i >> 3][(i >> 2) & 1][i & 3] += (uint32_t)__ldcg(p + 128 * i);
-                                }
                         finish16(c, now);
                         tmem_wait_ld();
                     }
@@ -939,32 +805,38 @@ Shape pick_shape(bool bwd, int E, int64_t M)
     return {256, 2};
 }
 
-constexpr int kSlabSms = 148;                     // CTAs the slabs are sized for (a B200's SMs)
-
-// units the workspace has slabs for: 0 where no tile can be split
-int slab_units(bool bwd, int E, int64_t M, int64_t N, int64_t K)
+// CTA pairs: tokens of a tile.  Dense: of 256, 192, 128 and 64 the size with the least time, rounds
+// of tiles times a chunk's cycles: the larger of the MMAs (2 a column) and the copies (16 KB of
+// weight and 64 bytes a token per CTA, at about 64 bytes a cycle).  Experts: 256 (a tile's cost
+// follows its rows).
+int pair_tokens(int E, int64_t M, int64_t N, int pairs)
 {
-    const Shape sh = pick_shape(bwd, E, M);
-    if (sh.cg == 1)
-        return 0;
-    const int units = kSlabSms / sh.cg;
-    if (E > 0)                                    // how the rows spread is known on the device only
-        return units;
-    const int64_t tok = bwd ? 128 * sh.cg : sh.nt, tts = (M + tok - 1) / tok;
-    const int64_t wts = bwd ? K / sh.nt : (N + 128 * sh.cg - 1) / (128 * sh.cg);
-    return I8Deal((int)(tts * wts), units, (int)((bwd ? N : K) / kChunk), split_cost(sh.nt), true).even ? units : 0;
+    if (E > 0)
+        return 256;
+    int best = 256;
+    int64_t best_cost = INT64_MAX;
+    for (int tok = 256; tok >= 64; tok -= 64) {
+        const int64_t tiles = (M + tok - 1) / tok * ((N + 255) / 256);
+        const int64_t cost = (tiles + pairs - 1) / pairs * (2 * tok > 256 + tok ? 2 * tok : 256 + tok);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = tok;
+        }
+    }
+    return best;
 }
 
 // CG = 1: rows of the box that takes a CTA's whole tile in one copy.  Dense: the shares are known
-// and nearly equal; experts: 128.
-int whole_box(const I8GemmLaunch &g, int ctas, int nt)
+// and nearly equal; experts: 128.  `only`: every tile is taken so.
+int whole_box(const I8GemmLaunch &g, int ctas, int nt, bool *only)
 {
+    *only = false;
     if (g.E > 0)
         return 128;
     const int64_t all = (g.M + nt - 1) / nt * (g.N / 4), share = (all + ctas - 1) / ctas;
-    const int64_t most = share < g.N / 4 ? share : g.N / 4;          // a tile never leaves its token tile
-    const int64_t tiles = (most + 31) / 32, groups = (most + tiles - 1) / tiles;
+    const int64_t tiles = (share + 31) / 32, groups = (share + tiles - 1) / tiles;
     const int64_t rows = (4 * groups + 7) / 8 * 8;
+    *only = g.M <= nt && (all / ctas + 31) / 32 == tiles;            // (sizes then differ by 4 channels)
     return rows < 16 ? 16 : (int)rows;
 }
 
@@ -1002,18 +874,27 @@ cudaError_t launch_shape(const I8GemmLaunch &g, int sms, cudaStream_t stream)
     const int64_t Em = g.E > 0 ? g.E : 1;
     // 128-byte wide boxes: weight codes [E N, K], row codes [M, K] (backward [M, N]) by whole tiles
     // and by kBox tokens
-    const int box = CG == 1 ? whole_box(g, resident_units[dev], NT) : 128;
+    const int tok = BWD || CG == 1 ? NT : pair_tokens(g.E, g.M, g.N, resident_units[dev]);
+    bool one_box = true;
+    const int box = CG == 1 ? whole_box(g, resident_units[dev], NT, &one_box) : 128;
+    // 128-byte wide boxes: weight codes [E N, K], row codes [M, K] (backward [M, N]) by whole tiles
+    // and by kBox tokens; maps that this call cannot use are not encoded
     CUtensorMap tmW, tmX, tmBox, tmW64, tmW16;
-    bool ok = make_tmap(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.wcodes, (uint64_t)g.K, (uint64_t)(Em * g.N), 128,
-                        box, CU_TENSOR_MAP_SWIZZLE_128B);
-    ok &= make_tmap(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.codes, (uint64_t)(BWD ? g.N : g.K), (uint64_t)g.M, 128,
-                    BWD ? 128 : Cfg::kColsPerCta, CU_TENSOR_MAP_SWIZZLE_128B);
-    ok &= make_tmap(&tmBox, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.codes, (uint64_t)(BWD ? g.N : g.K), (uint64_t)g.M, 128,
-                    Cfg::kBox, CU_TENSOR_MAP_SWIZZLE_128B);
-    ok &= make_tmap(&tmW64, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.wcodes, (uint64_t)g.K, (uint64_t)(Em * g.N), 128, 64,
-                    CU_TENSOR_MAP_SWIZZLE_128B);
-    ok &= make_tmap(&tmW16, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.wcodes, (uint64_t)g.K, (uint64_t)(Em * g.N), 128, 16,
-                    CU_TENSOR_MAP_SWIZZLE_128B);
+    auto weight_map = [&](CUtensorMap *m, int rows) {
+        return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.wcodes, (uint64_t)g.K, (uint64_t)(Em * g.N), 128, rows,
+                         CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    auto row_map = [&](CUtensorMap *m, int rows) {
+        return make_tmap(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.codes, (uint64_t)(BWD ? g.N : g.K), (uint64_t)g.M, 128,
+                         rows, CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    bool ok = weight_map(&tmW, box) && row_map(&tmX, BWD ? 128 : Cfg::kColsPerCta);
+    tmBox = tmX;
+    tmW64 = tmW16 = tmW;
+    if (!BWD && (g.E > 0 || tok != NT || (g.M % NT != 0 && !(NT <= 32 && g.M <= NT))))
+        ok = ok && row_map(&tmBox, Cfg::kBox);
+    if (!one_box)
+        ok = ok && weight_map(&tmW64, 64) && weight_map(&tmW16, 16);
     if (!ok)
         return cudaErrorInvalidValue;
     I8Args a;
@@ -1023,8 +904,6 @@ cudaError_t launch_shape(const I8GemmLaunch &g, int sms, cudaStream_t stream)
     a.wscales = g.wscales;
     a.factor = g.factor;
     a.y = g.y;
-    a.slabs = g.slabs;
-    a.counters = g.counters;
     a.status = g.status;
     a.M = g.M;
     a.N = g.N;
@@ -1032,7 +911,7 @@ cudaError_t launch_shape(const I8GemmLaunch &g, int sms, cudaStream_t stream)
     a.E = g.E;
     a.out_bf16 = g.out_bf16;
     a.box = box;
-    a.slab_units = slab_units(BWD, g.E, g.M, g.N, g.K);
+    a.tok = tok;
     // dependent launch: set-up and the first weight tiles overlap the quantisation in front
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(resident_units[dev] * CG));
@@ -1048,12 +927,6 @@ cudaError_t launch_shape(const I8GemmLaunch &g, int sms, cudaStream_t stream)
 }
 
 }  // namespace
-
-size_t i8_slab_bytes(bool bwd, int E, int64_t M, int64_t N, int64_t K)
-{
-    const Shape sh = pick_shape(bwd, E, M);
-    return (size_t)slab_units(bwd, E, M, N, K) * 2 * sh.cg * 128 * sh.nt * 4;
-}
 
 cudaError_t launch_i8_gemm(const I8GemmLaunch &g, int sms, cudaStream_t stream)
 {

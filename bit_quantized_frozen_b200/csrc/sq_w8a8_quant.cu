@@ -41,12 +41,14 @@ constexpr int kQWarps = 8;                        // warps of a CTA at most
 constexpr int kQMaxCluster = 8;
 constexpr int kQFactorBytes = kHad * kI8Rank * 2; // 8 KB: a block's factor
 
+// (everything twice: for even and odd groups)
 struct QShared {
-    uint32_t warp_max[kQWarps][kQRows];
-    float warp_low[kQWarps][kI8Rank * kQRows];
-    // from every CTA of the cluster, for even and odd groups
-    uint32_t max[2][kQMaxCluster][kQRows];
-    float low[2][kQMaxCluster][kI8Rank * kQRows]; // (the leader's is used)
+    uint32_t warp_max[2][kQWarps][kQRows];
+    float warp_low[2][kQWarps][kI8Rank * kQRows];
+    uint32_t max[2][kQMaxCluster][kQRows];        // from every CTA of the cluster
+    float low[2][kQMaxCluster][kI8Rank * kQRows]; // (first CTA) from the others
+    uint64_t max_bar[2], low_bar[2];              // count the bytes that have come
+    uint32_t abort_flag;
     int32_t start[kMaxExperts + 1], prefix[kMaxExperts + 1];
 };
 
@@ -84,9 +86,11 @@ __device__ __forceinline__ void cp_async_wait_all()
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v)
+// 4 bytes into another CTA's shared memory, counted on its barrier
+__device__ __forceinline__ void st_async(uint32_t addr, uint32_t v, uint32_t bar)
 {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];"
+                 ::"r"(addr), "r"(v), "r"(bar) : "memory");
 }
 
 // a 16-byte chunk (factor row k, half h) of a block sits at chunk 2 k + h with bits 0 and 2
@@ -145,14 +149,23 @@ __device__ __forceinline__ void widen(const uint4 (&w)[8], uint64_t (&p)[32])
     }
 }
 
-// H256 without the final 1/16, strides 1, 2, 4 | 8, 16 | 32, 64, 128
-__device__ __forceinline__ void fwht_rows8(uint64_t (&p)[32], int lane)
+// H256 of them without the final 1/16, strides 1, 2, 4 | 8, 16 | 32, 64, 128; stride 1 is folded
+// into the widening (mixed bf16 / fp32 arithmetic, one rounding each, the same bits)
+__device__ __forceinline__ void fwht_rows8(const uint4 (&w)[8], uint64_t (&p)[32], int lane)
 {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        float a, b;
-        f2_unpack(p[j], a, b);
-        p[j] = f2_pack(__fadd_rn(a, b), __fsub_rn(a, b));
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t v[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float lo = __uint_as_float(v[i] << 16);
+            float sum, diff;
+            asm("{\n\t.reg .b16 h0, h1, m1;\n\tmov.b32 {h0, h1}, %2;\n\tmov.b16 m1, 0xBF80;\n\t"
+                "add.rn.f32.bf16 %0, h1, %3;\n\t"
+                "fma.rn.f32.bf16 %1, h1, m1, %3;\n\t}"
+                : "=f"(sum), "=f"(diff) : "r"(v[i]), "f"(lo));
+            p[4 * j + i] = f2_pack(sum, diff);
+        }
     }
 #pragma unroll
     for (int h = 1; h <= 2; h <<= 1)              // strides 2, 4
@@ -205,11 +218,13 @@ __device__ __forceinline__ void scale_rows8(uint64_t (&p)[32], const float *sw, 
 // twice, which moves the values that RN puts on a tie.
 __device__ __forceinline__ void store_codes(const uint64_t (&p)[32], float inv, int pieces, int8_t *dst)
 {
+    const uint64_t magic = f2_pack(12582912.0f, 12582912.0f);
     auto scaled = [&](uint64_t v, uint32_t &a, uint32_t &b) {
         float x, y;
         f2_unpack(v, x, y);
-        a = __float_as_uint(__fadd_rn(__fmul_rn(x, inv), 12582912.0f));
-        b = __float_as_uint(__fadd_rn(__fmul_rn(y, inv), 12582912.0f));
+        f2_unpack(f2_add(f2_pack(__fmul_rn(x, inv), __fmul_rn(y, inv)), magic), x, y);
+        a = __float_as_uint(x);
+        b = __float_as_uint(y);
     };
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -226,17 +241,17 @@ __device__ __forceinline__ void store_codes(const uint64_t (&p)[32], float inv, 
     }
 }
 
-// what the first block does for the whole call: the status word and the product's counters
+// what the first block does for the whole call: the status word
 __device__ __forceinline__ void begin_call(const I8QuantArgs &a)
 {
-    for (int i = threadIdx.x; i < a.n_counters; i += blockDim.x)
-        a.counters[i] = 0u;
     bool bad = false;
-    for (int i = threadIdx.x; a.E > 0 && i <= a.E; i += blockDim.x) {
-        const int32_t o = a.offsets[i];
-        bad |= o < 0 || o > a.M || (i > 0 && o < a.offsets[i - 1]);
+    if (a.E > 0) {
+        for (int i = threadIdx.x; i <= a.E; i += blockDim.x) {
+            const int32_t o = a.offsets[i];
+            bad |= o < 0 || o > a.M || (i > 0 && o < a.offsets[i - 1]);
+        }
+        bad = __syncthreads_or(bad);
     }
-    bad = __syncthreads_or(bad);
     if (threadIdx.x == 0) {
         if (a.finite_check) {                     // (the word was cleared before the launch)
             if (bad)
@@ -263,33 +278,41 @@ __global__ void __launch_bounds__(32 * kQWarps, 2) i8_quant_kernel(const I8Quant
     uint8_t *my_factor = q_smem + warp * kQFactorBytes;
     float *my_scale = reinterpret_cast<float *>(q_smem + warps * kQFactorBytes) + warp * kHad;
     const bool with_low = a.low != nullptr;
+    const uint32_t max_bar = smem_u32(sh.max_bar), low_bar = smem_u32(sh.low_bar);
+    if (cluster > 1 && tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(max_bar + 8 * i, 1);
+            mbar_init(low_bar + 8 * i, 1);
+        }
+        sh.abort_flag = 0u;
+        fence_mbar_init();
+    }
     const uint32_t factor_at = factor_lane(smem_u32(my_factor), lane);
 
-    grid_dep_launch();
-    if (blockIdx.x == 0)
-        begin_call(a);
+    if (a.E == 0 && with_low && block0 < nb && (int)blockIdx.x < cluster * 2) {
+        // the factor on its way into L2 (a prefetch: whoever still writes it is not overtaken)
+        const uint8_t *src = reinterpret_cast<const uint8_t *>(a.factor + (int64_t)block0 * kHad * kI8Rank);
+        const int64_t bytes = (a.K - (int64_t)block0 * kHad) * kI8Rank * 2;
+        for (int c = 128 * lane; c < kQFactorBytes && c < bytes; c += 128 * 32)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(src + c));
+    }
+    grid_dep_wait();                                  // x, and the workspace of the call before
+    grid_dep_launch();                                // the product may fetch its first weights
     I8Plan plan;
     plan.start = sh.start;
     plan.prefix = sh.prefix;
-    plan.E = a.E > 0 ? a.E : 1;
+    plan.E = a.E;
     plan.wts = 1;
     plan.tok_tile = kQRows;
-    plan.build(a.E > 0 ? a.offsets : nullptr, a.M, tid, blockDim.x);
-    const int tiles = plan.tiles();
-    if (cluster > 1)
-        cluster_sync();                               // every CTA of the cluster has started
-
-    // rows of no expert: 0
-    if (a.y_zero) {
-        const int64_t head = plan.start[0], tail = a.M - plan.start[plan.E], n16 = a.y_row_bytes / 16;
-        for (int64_t i = blockIdx.x; i < head + tail; i += gridDim.x) {
-            const int64_t m = i < head ? i : plan.start[plan.E] + (i - head);
-            uint4 *row = reinterpret_cast<uint4 *>(a.y_zero + m * a.y_row_bytes);
-            for (int64_t c = tid; c < n16; c += blockDim.x)
-                if (SQ_DCHECK(m < a.M, a.status))
-                    row[c] = make_uint4(0u, 0u, 0u, 0u);
-        }
-    }
+    if (a.E > 0)
+        plan.build(a.offsets, a.M, tid, blockDim.x);
+    const int tiles = a.E > 0 ? plan.tiles() : (int)((a.M + kQRows - 1) / kQRows);
+    auto tile_at = [&](int i, int &e) {
+        if (a.E > 0)
+            return plan.find(i, e);
+        const int64_t row0 = (int64_t)i * kQRows, left = a.M - row0;
+        return I8Tile{0, (int)row0, left < kQRows ? (int)left : kQRows, 0};
+    };
 
     // columns of block b: 256, 128 (the last one, backward), or 0 behind the row's end
     auto columns = [&](int b) {
@@ -323,23 +346,47 @@ __global__ void __launch_bounds__(32 * kQWarps, 2) i8_quant_kernel(const I8Quant
         return a.x + (int64_t)(t.row0 + g) * a.K + (int64_t)b * kHad + 8 * q;
     };
     auto spread = [&](const uint4(&w)[8], uint64_t(&p)[32]) {
-        widen(w, p);
-        if (BWD)
+        if (BWD) {
+            widen(w, p);
             scale_rows8(p, my_scale, q);
-        else
-            fwht_rows8(p, lane);
+        } else {
+            fwht_rows8(w, p, lane);
+        }
     };
 
     int e = 0, have = -1;                             // expert walked to; expert whose factor is here
     uint4 w[8];
     I8Tile t = {0, 0, 0, 0};
     if (unit < tiles) {
-        t = plan.find(unit, e);
-        if (!TURNS)
+        t = tile_at(unit, e);
+        if (!TURNS) {
             load_block(row_of(t, block0), pieces_of(t, block0), w);
+            fetch(t.e, block0);
+            have = t.e;
+        }
     }
-    int parity = 0;
-    for (int tile = unit; tile < tiles; tile += units, parity ^= 1) {
+    if (blockIdx.x == 0)                              // while the first loads are on their way
+        begin_call(a);
+    // rows of no expert: 0
+    if (a.y_zero && a.E > 0) {
+        const int64_t head = plan.start[0], tail = a.M - plan.start[a.E], n16 = a.y_row_bytes / 16;
+        for (int64_t i = blockIdx.x; i < head + tail; i += gridDim.x) {
+            const int64_t m = i < head ? i : plan.start[a.E] + (i - head);
+            uint4 *row = reinterpret_cast<uint4 *>(a.y_zero + m * a.y_row_bytes);
+            for (int64_t c = tid; c < n16; c += blockDim.x)
+                if (SQ_DCHECK(m < a.M, a.status))
+                    row[c] = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+    if (cluster > 1) {
+        __syncwarp();
+        cluster_sync();                               // every CTA has started and set up its barriers
+    }
+    if (!TURNS)
+        fetched();
+    int round = 0;
+    for (int tile = unit; tile < tiles; tile += units, ++round) {
+        const int parity = round & 1;
         const bool live = g < t.rows;
         float low[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         float amax = 0.0f;
@@ -371,74 +418,70 @@ __global__ void __launch_bounds__(32 * kQWarps, 2) i8_quant_kernel(const I8Quant
             if (with_low && block0 < nb)
                 low_block(w, factor_at, low);
             spread(w, p);
-            if (tile + units < tiles) {               // the next group's values, while this one's are transformed
-                next = plan.find(tile + units, e);
-                load_block(row_of(next, block0), pieces_of(next, block0), w);
-            }
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
                 float x0, x1;
                 f2_unpack(p[j], x0, x1);
                 amax = absmax3(amax, x0, x1);
             }
+            if (tile + units < tiles) {               // the next group's values, while this one is finished
+                next = tile_at(tile + units, e);
+                load_block(row_of(next, block0), pieces_of(next, block0), w);
+            }
         }
         // the row's maximum: 4 lanes, the CTA's warps, the cluster's CTAs (max of bit patterns:
-        // not below zero, NaN above infinity above all others)
+        // not below zero, NaN above infinity above all others); the low-rank sums in the same order
+        // of warps and CTAs.  What the CTAs exchange is counted on barriers: a buffer is written
+        // again two groups later, by a CTA that has this one's values of the group between, sent
+        // after this one had read the buffer.
+        const uint32_t bar_phase = (uint32_t)(round >> 1) & 1u;
         uint32_t m = __float_as_uint(amax);
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
         if (q == 0)
-            sh.warp_max[warp][g] = m;
+            sh.warp_max[parity][warp][g] = m;
         if (with_low) {                               // low[0..3]: ranks g, g + 8; rows 2 q, 2 q + 1
-            float *wl = sh.warp_low[warp];
+            float *wl = sh.warp_low[parity][warp];
             wl[(2 * q) * kI8Rank + g] = low[0];
             wl[(2 * q + 1) * kI8Rank + g] = low[1];
             wl[(2 * q) * kI8Rank + g + 8] = low[2];
             wl[(2 * q + 1) * kI8Rank + g + 8] = low[3];
         }
-        __syncthreads();
-        if (tid < kQRows) {
-            uint32_t v = 0;
-            for (int i = 0; i < warps; ++i)
-                v = max(v, sh.warp_max[i][tid]);
-            if (cluster == 1)
-                sh.max[parity][0][tid] = v;
-            else
-                for (int r = 0; r < cluster; ++r)
-                    st_cluster(mapa_shared(smem_u32(&sh.max[parity][rank][tid]), r), v);
+        if (cluster > 1 && tid == 0) {
+            mbar_arrive_expect_tx(max_bar + 8 * parity, cluster * kQRows * 4);
+            if (rank == 0 && with_low)
+                mbar_arrive_expect_tx(low_bar + 8 * parity, (cluster - 1) * kI8Rank * kQRows * 4);
         }
-        if (with_low)
-            for (int i = tid; i < kI8Rank * kQRows; i += blockDim.x) {
-                float v = sh.warp_low[0][i];
-                for (int k = 1; k < warps; ++k)
-                    v = __fadd_rn(v, sh.warp_low[k][i]);
-                if (cluster == 1)
-                    sh.low[parity][0][i] = v;
-                else
-                    st_cluster(mapa_shared(smem_u32(&sh.low[parity][rank][i]), 0), __float_as_uint(v));
-            }
-        __syncwarp();
-        if (cluster > 1)
-            cluster_sync();
-        else
-            __syncthreads();
-        if (rank == 0 && with_low)
-            for (int i = tid; i < kI8Rank * kQRows; i += blockDim.x) {
-                float v = sh.low[parity][0][i];
-                for (int r = 1; r < cluster; ++r)
-                    v = __fadd_rn(v, sh.low[parity][r][i]);
-                const int row = i / kI8Rank, k = i % kI8Rank;
-                if (row < t.rows && SQ_DCHECK(t.row0 + row < a.M, a.status)) {
-                    uint32_t part[kLowParts];
-                    split3(v, part);
-#pragma unroll
-                    for (int j = 0; j < kLowParts; ++j)
-                        a.low[(int64_t)(t.row0 + row) * kLowRow + j * kI8Rank + k] = (uint16_t)part[j];
-                }
-            }
+        __syncthreads();
         uint32_t top = 0;
-        for (int r = 0; r < cluster; ++r)
-            top = max(top, sh.max[parity][r][g]);
+        if (cluster > 1) {
+            for (int i = tid; i < kQRows * cluster; i += blockDim.x) {
+                const int row = i % kQRows, to = i / kQRows;
+                uint32_t v = 0;
+                for (int k = 0; k < warps; ++k)
+                    v = max(v, sh.warp_max[parity][k][row]);
+                st_async(mapa_shared(smem_u32(&sh.max[parity][rank][row]), to), v,
+                         mapa_shared(max_bar + 8 * parity, to));
+            }
+        }
+        auto low_sum = [&](int i) {                   // of the CTA's warps
+            float v = sh.warp_low[parity][0][i];
+            for (int k = 1; k < warps; ++k)
+                v = __fadd_rn(v, sh.warp_low[parity][k][i]);
+            return v;
+        };
+        if (with_low && rank > 0)
+            for (int i = tid; i < kI8Rank * kQRows; i += blockDim.x)
+                st_async(mapa_shared(smem_u32(&sh.low[parity][rank][i]), 0), __float_as_uint(low_sum(i)),
+                         mapa_shared(low_bar + 8 * parity, 0));
+        if (cluster > 1) {
+            (void)mbar_wait(max_bar + 8 * parity, bar_phase, &sh.abort_flag, a.status);
+            for (int r = 0; r < cluster; ++r)
+                top = max(top, sh.max[parity][r][g]);
+        } else {
+            for (int k = 0; k < warps; ++k)
+                top = max(top, sh.warp_max[parity][k][g]);
+        }
         if (!BWD && top < kInfBits)                   // the transform's 1/16 (exact where the scale is not 0)
             top = __float_as_uint(__fmul_rn(__uint_as_float(top), 0.0625f));
         float s, inv;
@@ -465,7 +508,28 @@ __global__ void __launch_bounds__(32 * kQWarps, 2) i8_quant_kernel(const I8Quant
         } else if (live && SQ_DCHECK(t.row0 + g < a.M, a.status)) {
             store_codes(p, inv, pieces_of(t, block0), a.codes + (int64_t)(t.row0 + g) * a.K + (int64_t)block0 * kHad + 8 * q);
         }
-        t = TURNS && tile + units < tiles ? plan.find(tile + units, e) : next;
+        if (with_low && rank == 0)                    // the low-rank input, once the codes are out
+            for (int i = tid; i < kI8Rank * kQRows; i += blockDim.x) {
+                float v = low_sum(i);
+                if (cluster > 1) {
+                    (void)mbar_wait(low_bar + 8 * parity, bar_phase, &sh.abort_flag, a.status);
+                    for (int r = 1; r < cluster; ++r)
+                        v = __fadd_rn(v, sh.low[parity][r][i]);
+                }
+                const int row = i / kI8Rank, k = i % kI8Rank;
+                if (row < t.rows && SQ_DCHECK(t.row0 + row < a.M, a.status)) {
+                    uint32_t part[kLowParts];
+                    split3(v, part);
+#pragma unroll
+                    for (int j = 0; j < kLowParts; ++j)
+                        a.low[(int64_t)(t.row0 + row) * kLowRow + j * kI8Rank + k] = (uint16_t)part[j];
+                }
+            }
+        t = TURNS && tile + units < tiles ? tile_at(tile + units, e) : next;
+    }
+    if (cluster > 1) {
+        __syncwarp();
+        cluster_sync();                               // nobody leaves while another CTA may still write to it
     }
 }
 
@@ -492,11 +556,15 @@ static cudaError_t launch_quant_v(const I8QuantArgs &a, int cluster, int warps, 
     cfg.blockDim = dim3(32 * warps);
     cfg.dynamicSmemBytes = warps * (kQFactorBytes + (BWD ? kHad * 4 : 0));
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)cluster;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
+    // dependent launch: the CTAs are there when the kernel in front (the product of the call
+    // before, perhaps) ends
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     // persistent: as many clusters as are resident at once (clusters left over for a second
     // wave would double the time), but never more than row groups
     if (ctx == 0 || room_ctx[dev][cluster - 1][warps - 1] != ctx) {
@@ -513,7 +581,7 @@ static cudaError_t launch_quant_v(const I8QuantArgs &a, int cluster, int warps, 
     const int64_t fit = room[dev][cluster - 1][warps - 1];
     cfg.gridDim = dim3((unsigned)((groups < fit ? groups : fit) * cluster));
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, i8_quant_kernel<BWD, TURNS>, a, cluster);
 }
 

@@ -120,16 +120,34 @@ def test_binding_refusals():
 
 
 def test_workspace_covers_its_parts():
-    """Header, counters, row codes, scales and low-rank input; partial sums only where tiles can be split."""
-    base = lambda M, width: 2048 + M * (width + 4 + 96)  # noqa: E731
-    assert sq.sq_workspace_bytes(sq.SQ_OP_LINEAR_FWD_W8A8, 1, 6144, 6144) >= base(1, 6144)
-    big = sq.sq_workspace_bytes(sq.SQ_OP_LINEAR_FWD_W8A8, 4480, 16384, 6144)
-    assert base(4480, 6144) <= big <= base(4480, 6144) + 8192                    # more tiles than SMs: none split
-    big = sq.sq_workspace_bytes(sq.SQ_OP_LINEAR_BWD_DX_W8A8, 4480, 16384, 6144)
-    assert base(4480, 16384) <= big <= base(4480, 16384) + 8192
-    # 48 weight tiles of 16 tokens on 148 SMs are split
-    one = sq.sq_workspace_bytes(sq.SQ_OP_LINEAR_FWD_W8A8, 1, 6144, 6144)
-    assert one >= base(1, 6144) + 48 * 3 * 128 * 16 * 4
+    """Header, row codes, scales and low-rank input, and little more."""
+    for op, gop, back in ((sq.SQ_OP_LINEAR_FWD_W8A8, sq.SQ_OP_GROUPED_FWD_W8A8, False),
+                          (sq.SQ_OP_LINEAR_BWD_DX_W8A8, sq.SQ_OP_GROUPED_BWD_DX_W8A8, True)):
+        for M, N, K in ((1, 6144, 6144), (4480, 16384, 6144), (333, 128, 256)):
+            need = 256 + M * ((N if back else K) + 4 + 96)
+            assert need <= sq.sq_workspace_bytes(op, M, N, K) <= need + 5 * 1024
+            for E in (1, 64, 1024):
+                assert sq.sq_grouped_workspace_bytes(gop, E, M, N, K) == sq.sq_workspace_bytes(op, M, N, K)
+
+
+def test_header_is_plain_c_and_exports():
+    """include/sq_w8a8.h compiles as strict C99 beside sq.h, and both libraries export what it declares."""
+    import os
+    import re
+    import shutil
+    import subprocess
+    from bit_quantized_frozen_b200 import build
+    text = open(os.path.join(build.INCLUDE, "sq_w8a8.h")).read()
+    names = sorted(set(re.findall(r"^SQ_API[^;(]*?\b(sq_\w+)\s*\(", text, re.M)))
+    assert names == sorted(sq.EXPORTED_W8A8)
+    for lib in (sq.LIB_PATH, build.build(debug_checks=True)):
+        L = ctypes.CDLL(lib)
+        for n in names:
+            assert hasattr(L, n), n
+    if shutil.which("gcc"):
+        src = '#include "sq_w8a8.h"\nint main(void) { return SQ_ZERO_UNGROUPED == 0u; }\n'
+        subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-pedantic", "-I", build.INCLUDE, "-x", "c",
+                        "-fsyntax-only", "-"], input=src, text=True, check=True)
 
 
 # ---- the reference ------------------------------------------------------------------------------

@@ -1,7 +1,7 @@
 """Reference of the 8-bit integer products on the host, and how far a right result may be from it.
 
 codes(): the row quantisation operation by operation in numpy float32, one rounding each, as the
-contract in include/sq.h states it.  forward() and backward(): the product from those codes in
+contract in include/sq_w8a8.h states it.  forward() and backward(): the product from those codes in
 float64, with a bound on the library's fp32 arithmetic, element by element.  u = 2^-24 is half a
 step of fp32, 2^-8 half a step of bf16 (relative to the value):
   main term   RN(float(acc) RN(s_x s_w)): three roundings, 3 u |main| (4 u with the second-order
