@@ -76,8 +76,8 @@ struct I8Cfg {
     static constexpr int kNumBars = 2 * kStages + 5;                 // full, empty, acc_full[2], acc_empty[2], drain
     static constexpr int kSmemBytes = kBarOff + 8 * kNumBars + 32 + 1024;
     static constexpr uint32_t kTmemCols = 2 * NT < 32 ? 32 : 2 * NT;
-    static constexpr uint32_t kIdesc = (2u << 4) | (1u << 7) | (1u << 10) | (BWD ? 1u << 16 : 0u) |
-                                       ((uint32_t)(kLaneTile >> 4) << 24);   // + columns / 8 << 17
+    // instruction descriptor, without columns / 8 << 17 and rows / 16 << 24
+    static constexpr uint32_t kIdesc = (2u << 4) | (1u << 7) | (1u << 10) | (BWD ? 1u << 16 : 0u);
     static constexpr uint32_t kBStep16 = BWD ? (32u * 128u) >> 4 : 2u;   // B descriptor step per MMA (32 values)
 };
 
@@ -275,6 +275,9 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
     auto all_work = [&]() { return Units(plan, share, tiles, unit, units, args.N); };
     const int a_bytes = CG == 1 ? min(128, max(args.box < 128 ? args.box : 16, (share.largest() + 7) / 8 * 8)) * kChunk
                                 : Cfg::kABytes;
+    // CG = 1: tiles of at most 64 channels take the 64-row MMA, which reads half as much of A and puts
+    // 16 rows into each quarter of the lanes
+    const bool m64 = CG == 1 && a_bytes <= 64 * kChunk;
     const int chunk_bytes = a_bytes + Cfg::kBBytes;
     const int stage_bytes = Cfg::kPer * chunk_bytes;
     const int stages = CG == 1 ? min(Cfg::kStages, Cfg::kRing / stage_bytes) / Cfg::kProducers * Cfg::kProducers
@@ -429,7 +432,8 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
             bool ok = true;
             I8Work w;
             for (Units work = all_work(); ok && work.next(w); ++count) {
-                const uint32_t idesc = Cfg::kIdesc | (uint32_t)uniform(columns(w.t) >> 3) << 17;
+                const uint32_t idesc = Cfg::kIdesc | (uint32_t)uniform(columns(w.t) >> 3) << 17 |
+                                       (uint32_t)(m64 ? 4 : Cfg::kLaneTile >> 4) << 24;
                 const uint32_t acc = tmem_base + ((count & 1) ? (uint32_t)NT : 0u);
                 // the tile before last (same accumulator) has left tensor memory
                 if (count >= 2 && !acc_wait<CG>(bar_acc_empty + 8 * (count & 1), (uint32_t)(((count >> 1) - 1) & 1),
@@ -517,7 +521,8 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                 for (int c = et; c < NT; c += ET)
                     col_scale[c] = c < t.rows ? args.scales[t.row0 + c] : 0.0f;
             // the lanes' scales and low-rank values (lane r of a fragment half: 16 h + g + 8 i)
-            const int lane0 = (int)rank * 128 + 32 * wq;   // first lane of the warp in the tile
+            const int span = m64 ? 16 : 32;                // rows of the tile in a quarter of the lanes
+            const int lane0 = (int)rank * 128 + span * wq; // first row of the warp in the tile
             const int64_t base = (BWD ? t.row0 : w.n0) + lane0;
             float fscale[2][2];                            // forward: per fragment row
             float lscale = 0.0f;                           // backward: of this thread's lane
@@ -529,7 +534,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int r = 16 * h + g + 8 * i;
-                    const bool live = lane0 + r < w.lanes;
+                    const bool live = r < span && lane0 + r < w.lanes;
                     if (!BWD)
                         fscale[h][i] = live ? __ldg(args.wscales + (int64_t)t.e * args.N + base + r) : 0.0f;
 #pragma unroll
@@ -710,7 +715,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                                     const int tok = (lane >> 3) + 4 * k, piece = lane & 7;
                                     const uint2 v = *reinterpret_cast<const uint2 *>(buf + tok * 80 + piece * 8);
                                     const int64_t at = y0 + tok * width + 4 * piece;
-                                    if (c + 8 * n + tok < t.rows && lane0 + 4 * piece < w.lanes &&
+                                    if (c + 8 * n + tok < t.rows && 4 * piece < min(span, w.lanes - lane0) &&
                                         SQ_DCHECK(at + 4 <= args.M * width, args.status))
                                         *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(args.y) + at) = v;
                                 }
@@ -728,7 +733,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                                 const int tok = (lane >> 3) + 4 * k, piece = lane & 7;
                                 const float4 v = *reinterpret_cast<const float4 *>(f + tok * 36 + 4 * piece);
                                 const int64_t at = y0 + tok * width + 4 * piece;
-                                if (c + 8 * n + tok < t.rows && lane0 + 4 * piece < w.lanes &&
+                                if (c + 8 * n + tok < t.rows && 4 * piece < min(span, w.lanes - lane0) &&
                                     SQ_DCHECK(at + 4 <= args.M * width, args.status))
                                     *reinterpret_cast<float4 *>(reinterpret_cast<float *>(args.y) + at) = v;
                             }
@@ -766,7 +771,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
 
     tc_fence_before();
     if (CG == 2)
-        cluster_sync();                               // no CTA leaves while its peer may still signal it
+        cluster_meet();                               // no CTA leaves while its peer may still signal it
     else
         __syncthreads();
     tc_fence_after();

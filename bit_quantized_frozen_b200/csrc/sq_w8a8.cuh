@@ -94,6 +94,14 @@ __device__ __forceinline__ uint32_t smem_addr(const void *p)
     return (uint32_t)__cvta_generic_to_shared(p);
 }
 
+// Every thread of the cluster meets here; nothing written before is published by it (the release
+// of cluster_sync() waits for every global store that the CTA has on its way).  For barriers set up
+// before with fence_mbar_init(), and for CTAs that must not leave before their peers.
+__device__ __forceinline__ void cluster_meet()
+{
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // four 8x8 matrices of 16-bit values from shared memory (each lane gives one row's address);
 // with TRANS each is transposed on the way
 template <bool TRANS>

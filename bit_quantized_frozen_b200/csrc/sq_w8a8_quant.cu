@@ -303,6 +303,10 @@ __global__ void __launch_bounds__(32 * kQWarps, 2) i8_quant_kernel(const I8Quant
         for (int c = 128 * lane; c < kQFactorBytes && c < bytes; c += 128 * 32)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(src + c));
     }
+    if (cluster > 1) {
+        __syncwarp();
+        cluster_meet();                               // every CTA has started and set up its barriers
+    }
     grid_dep_wait();                                  // x, and the workspace of the call before
     grid_dep_launch();                                // the product may fetch its first weights
     I8Plan plan;
@@ -384,10 +388,6 @@ __global__ void __launch_bounds__(32 * kQWarps, 2) i8_quant_kernel(const I8Quant
                 if (SQ_DCHECK(m < a.M, a.status))
                     row[c] = make_uint4(0u, 0u, 0u, 0u);
         }
-    }
-    if (cluster > 1) {
-        __syncwarp();
-        cluster_sync();                               // every CTA has started and set up its barriers
     }
     if (!TURNS)
         fetched();
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(32 * kQWarps, 2) i8_quant_kernel(const I8Quant
     }
     if (cluster > 1) {
         __syncwarp();
-        cluster_sync();                               // nobody leaves while another CTA may still write to it
+        cluster_meet();                               // nobody leaves while another CTA may still write to it
     }
 }
 
