@@ -599,6 +599,10 @@ cudaError_t launch_i8_quant(const I8QuantArgs &a, bool bwd, int sms, cudaStream_
     const int nb = (int)(a.K + kHad - 1) / kHad;
     int cluster = (nb + kQWarps - 1) / kQWarps;
     cluster = cluster < kQMaxCluster ? cluster : kQMaxCluster;
+    // few row groups: more CTAs of fewer warps, while each still has an SM of its own
+    const int64_t groups = (a.M + kQRows - 1) / kQRows + a.E;
+    while (cluster < kQMaxCluster && cluster < nb && groups * (cluster + 1) <= sms)
+        ++cluster;
     int warps = (nb + cluster - 1) / cluster;
     const bool turns = warps > kQWarps;
     warps = turns ? kQWarps : warps;
