@@ -342,47 +342,50 @@ _W8A8 = {}                               # entry point by name, looked up once
 def _w8a8(fn: str, w, x, y, flags, ws, stream, backward: bool, offsets=None):
     """Checks and call of the four 8-bit integer products; w: a Weight, or a GroupedWeight with offsets."""
     N, K, E = w.N, w.K, getattr(w, "E", None)
-    wide, out = (N, K) if backward else (K, N)
+    xn, yn, wide, out = ("dy", "dx", N, K) if backward else ("x", "y", K, N)
     if w.fmt != SQ_FMT_INT8_ROW:
         raise ValueError(f"{fn}: the weight must be SQ_FMT_INT8_ROW")
     if x.dim() != 2 or x.shape[1] != wide or x.dtype != torch.bfloat16:
-        raise ValueError(f"{fn}: {'dy' if backward else 'x'} must be bfloat16 [M, {wide}], "
-                         f"got {x.dtype} {list(x.shape)}")
+        raise ValueError(f"{fn}: {xn} must be bfloat16 [M, {wide}], got {x.dtype} {list(x.shape)}")
     M = x.shape[0]
     experts = 1 if E is None else E
-    _need(fn, "codes", w.codes, experts * N * K)
-    _need(fn, "scales", w.scales, 4 * experts * N)
-    if w.lora_up is not None:
-        _need(fn, "lora_up", w.lora_up, 2 * experts * N * RANK_INT8)
-    if w.lora_down is not None:
-        _need(fn, "lora_down", w.lora_down, 2 * experts * K * RANK_INT8)
     bf16 = flags & SQ_OUT_BF16
-    _need(fn, "dx" if backward else "y", y, M * out * (2 if bf16 else 4))
-    if y.dtype != (torch.bfloat16 if bf16 else torch.float32):
-        raise ValueError(f"{fn}: {'dx' if backward else 'y'} is {y.dtype}, the flags ask for the other type")
-    if E is not None:
-        if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] != E + 1:
-            raise ValueError(f"{fn}: offsets must be int32 [{E + 1}], got {offsets.dtype} {list(offsets.shape)}")
-        if M == 0:
-            return
-    xp, yp = _ptr(x), _ptr(y)
-    dev = x.device.index
-    for t in (y, w.codes, w.scales, w.lora_up, w.lora_down, ws, offsets):
-        if t is not None and not isinstance(t, int) and t.is_cuda and t.device.index != dev:
-            raise ValueError(f"{fn}: tensors on {t.device} and on {x.device}")
+    if E is not None and (offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] != E + 1):
+        raise ValueError(f"{fn}: offsets must be int32 [{E + 1}], got {offsets.dtype} {list(offsets.shape)}")
+    # every tensor: long enough, on one device, contiguous (NULL and raw addresses are the library's to check)
+    dev, at = x.get_device(), {}
+    for name, t, nbytes in (("codes", w.codes, experts * N * K), ("scales", w.scales, 4 * experts * N),
+                            ("lora_up", w.lora_up, 2 * experts * N * RANK_INT8),
+                            ("lora_down", w.lora_down, 2 * experts * K * RANK_INT8),
+                            (yn, y, M * out * (2 if bf16 else 4)), (xn, x, 0), ("offsets", offsets, 0), ("ws", ws, 0)):
+        if t is None or isinstance(t, int):
+            at[name] = t
+            continue
+        if t.nbytes < nbytes:
+            raise ValueError(f"{fn}: {name} holds {t.nbytes} bytes, the call needs {nbytes}")
+        if t.get_device() != dev:
+            raise ValueError(f"{fn}: {name} is on {t.device}, {xn} on {x.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: expected a contiguous tensor for {name}")
+        at[name] = t.data_ptr()
+    if not isinstance(y, int) and y.dtype != (torch.bfloat16 if bf16 else torch.float32):
+        raise ValueError(f"{fn}: {yn} is {y.dtype}, the flags ask for the other type")
+    if dev < 0:
+        raise ValueError(f"{fn}: expected a CUDA tensor")
     if dev != torch.cuda.current_device():
         raise ValueError(f"{fn}: the tensors are on {x.device}, the current device is {torch.cuda.current_device()}")
-    if stream is None and _raw_stream is not None:
-        stream = _raw_stream(dev)
+    if M == 0 and E is not None:
+        return
+    stream = _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
     f = _W8A8.get(fn)
     if f is None:
         f = _W8A8[fn] = getattr(lib(), fn)
+    cw = ctypes.byref(sq_weight(w.fmt, N, K, at["codes"], at["scales"], None, at["lora_up"], at["lora_down"]))
     nb = 0 if ws is None else _numel_bytes(ws)
-    cw = ctypes.byref(w.as_c())
     if E is None:
-        st = f(cw, xp, M, yp, flags, _ptr(ws), nb, _stream(stream))
+        st = f(cw, at[xn], M, at[yn], flags, at["ws"], nb, stream)
     else:
-        st = f(cw, E, xp, M, _ptr(offsets), yp, flags, _ptr(ws), nb, _stream(stream))
+        st = f(cw, E, at[xn], M, at["offsets"], at[yn], flags, at["ws"], nb, stream)
     if st != SQ_OK:
         _check(fn, st)
 
@@ -601,10 +604,10 @@ def _w8a8_out(fn, op, w, x, offsets, width, ws, flags, out_bf16, stream):
 def _w8a8_out_here(fn, op, w, x, offsets, width, ws, flags, out_bf16, stream):
     if out_bf16:
         flags |= SQ_OUT_BF16
-    M, E, dev = x.shape[0], getattr(w, "E", None), x.device
-    y = torch.empty((M, width), dtype=torch.bfloat16 if flags & SQ_OUT_BF16 else torch.float32, device=dev)
+    M, E = x.shape[0], getattr(w, "E", None)
+    y = x.new_empty(M, width, dtype=torch.bfloat16 if flags & SQ_OUT_BF16 else torch.float32)
     if ws is None:
-        ws = torch.empty(_w8a8_bytes(op, E, M, w.N, w.K), dtype=torch.uint8, device=dev)
+        ws = x.new_empty(_w8a8_bytes(op, E, M, w.N, w.K), dtype=torch.uint8)
     if E is not None:
         flags |= SQ_ZERO_UNGROUPED
     _w8a8(fn, w, x, y, flags, ws, stream, "bwd" in fn, offsets)

@@ -26,16 +26,18 @@ extern "C" {
  * product runs on the 8-bit integer tensor cores (32-bit sums, exact):
  *   r = H256 x (per row m),  s_x = RN(max|r| / 127),
  *   q_x[k] = clamp(rint(RN(r_k RN(1 / s_x))), -127, 127),
- *   y[m, n] = RN( RN(float(sum_k q_x[m, k] Q[n, k]) RN(s_x s_w[n])) + t[m] . lora_up[n] ),
- *   t[m] = x[m] lora_down (fp32, fixed order).
+ *   y[m, n] = fma(float(sum_k q_x[m, k] Q[n, k]), RN(s_x s_w[n]), t[m] . lora_up[n]),
+ *   t[m] = x[m] lora_down (fp32 sums).
  * The codes are the same bits as this sequence of fp32 operations gives.  A
  * scale below 2^-120 counts as 0 (zero codes).  A row with a NaN or an infinity
  * in r gives a row of NaN; other rows are not affected.  y [M, N] fp32 (device),
  * or bf16 with SQ_OUT_BF16 (one more rounding); x [M, K] bf16 (device).
- * lora_up and lora_down are both NULL or both given.  Any M >= 1; one token and
- * a few tokens run on narrow tiles that read each weight byte once, with the sum
- * split over idle SMs.  The result does not depend on the split, nor on the
- * other rows: a row's y is the same bits whatever M is.
+ * lora_up and lora_down are both NULL or both given.  Any M >= 1; few tokens run
+ * on narrow tiles that read each weight byte once.  The codes, the scales and
+ * the integer sums of a row are the same bits whatever M is and whichever rows
+ * lie beside it; t is summed in an order fixed by M and K, so equal calls give
+ * equal bits.  t enters the last product as three bf16 terms (24 bits; below
+ * 2^-110 with an absolute error of 2^-134), for a bf16 y as two (2^-17 of t).
  * flags: SQ_OUT_BF16, SQ_CHECK_FINITE (a row whose rotation holds a NaN or an
  * infinity sets SQ_ERR_NONFINITE in the status word).
  * ws: sq_workspace_bytes(SQ_OP_LINEAR_FWD_W8A8, M, N, K) bytes.
@@ -49,7 +51,7 @@ SQ_API sq_status sq_linear_fwd_w8a8(const sq_weight *w, const uint16_t *x, int64
  * through the rounding of x: dx = dy W with the rows of dy quantised,
  *   r[n] = RN(dy[m, n] s_w[n]),  s_g and q_g from r as in sq_linear_fwd_w8a8,
  *   dx[m, :] = H256( RN(float(sum_n q_g[m, n] Q[n, :]) s_g) ) + u[m] . lora_down[k],
- *   u[m] = dy[m] lora_up (fp32, fixed order);
+ *   u[m] = dy[m] lora_up (fp32 sums);
  * the codes are read as they lie, no transposed or reconstructed copy of W is
  * made.  dy [M, N] bf16, dx [M, K] fp32 (bf16 with SQ_OUT_BF16), device.
  * N <= 131072 (the 32-bit sums stay exact).  NaN, infinities, flags and status
@@ -66,9 +68,9 @@ SQ_API sq_status sq_linear_bwd_dx_w8a8(const sq_weight *w, const uint16_t *dy, i
  * [E, N], lora_up [E, N, 16], lora_down [E, K, 16].  offsets [E + 1] int32
  * (device), not decreasing, between 0 and M; an expert may have no rows.  Rows
  * before offsets[0] and from offsets[E] on belong to none: they are left as they
- * were, or become 0 with SQ_ZERO_UNGROUPED.  A row's result is the same bits as
- * the dense call gives with that expert's weight.  M may be 0 (nothing is
- * enqueued).  Offsets outside these rules are clamped, so that no access leaves
+ * were, or become 0 with SQ_ZERO_UNGROUPED.  A row's result is what the dense call
+ * gives with that expert's weight (the same codes and integer sums).  M may be 0
+ * (nothing is enqueued).  Offsets outside these rules are clamped, so that no access leaves
  * the buffers; the rows' results are then unspecified, and
  * sq_check_device_status reports SQ_ERR_INDEX.
  * ws: sq_grouped_workspace_bytes(SQ_OP_GROUPED_FWD_W8A8 or _BWD_DX_W8A8, E, M, N, K).

@@ -425,3 +425,92 @@ def test_debug_library_gives_the_same_bits(tmp_path):
         got.append(np.load(out))
     for name in got[0].files:
         assert np.array_equal(got[0][name], got[1][name]), name
+
+
+def test_offsets_past_32_bits():
+    """Row codes and weight codes of more than 2^31 values: the last rows and the last expert are right."""
+    N, K, M = 128, 8192, 270000
+    rng = np.random.default_rng(12)
+    L = ref.layer(rng, N, K)
+    last = rows(rng, 70, K)
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    x[-70:] = dev(last, torch.bfloat16)
+    y = sq.linear_fwd_w8a8(weight(*L), x)
+    assert not y[:-70].any()
+    ref.check(y[-70:].cpu().numpy(), *ref.forward(last, *L), False)
+    del x, y
+    E, N, K = 600, 1024, 3840
+    Q, sw, up, down = ref.layer(rng, N, K)
+    w = sq.GroupedWeight(E, N, K, torch.zeros(E, N, K, dtype=torch.int8, device="cuda"),
+                         torch.zeros(E, N, device="cuda"),
+                         torch.zeros(E, N, 16, dtype=torch.bfloat16, device="cuda"),
+                         torch.zeros(E, K, 16, dtype=torch.bfloat16, device="cuda"))
+    one = weight(Q, sw, up, down)
+    for a, b in ((w.codes, one.codes), (w.scales, one.scales), (w.lora_up, one.lora_up), (w.lora_down, one.lora_down)):
+        a[-1] = b
+    off = torch.full((E + 1,), 3, dtype=torch.int32, device="cuda")
+    off[0], off[-1] = 0, 13
+    for f, r, width in ((sq.grouped_fwd_w8a8, ref.forward, K), (sq.grouped_bwd_dx_w8a8, ref.backward, N)):
+        x = rows(rng, 13, width)
+        y = f(w, dev(x, torch.bfloat16), off).cpu().numpy()
+        assert not y[:3].any()
+        ref.check(y[3:], *r(x[3:], Q, sw, up, down), False)
+
+
+@pytest.mark.parametrize("N", [32768, 32768 + 128])
+def test_backward_rows_longer_than_a_cluster(N):
+    """Rows of more than 64 blocks are read twice; a half block at the end."""
+    rng = np.random.default_rng(N)
+    for M in (1, 37):
+        L = ref.layer(rng, N, 256)
+        dy = rows(rng, M, N)
+        ref.check(call("bwd", weight(*L), dev(dy, torch.bfloat16)).cpu().numpy(), *ref.backward(dy, *L), False)
+
+
+def test_row_views_and_one_expert():
+    """x and offsets that are views into larger buffers; a grouped call with one expert is the dense call."""
+    rng = np.random.default_rng(21)
+    w = weight(*ref.layer(rng, 256, 768, lora=False, E=1))
+    big = dev(rows(rng, 200, 768), torch.bfloat16)
+    off = torch.tensor([7, 7, 0, 50], dtype=torch.int32, device="cuda")[2:]
+    dense = sq.linear_fwd_w8a8(w.expert(0), big[13:63])
+    assert torch.equal(sq.grouped_fwd_w8a8(w, big[13:63], off), dense)
+    assert torch.equal(dense, sq.linear_fwd_w8a8(w.expert(0), big)[13:63])
+    with pytest.raises(ValueError, match="contiguous"):
+        sq.linear_fwd_w8a8(w.expert(0), big[::2])
+
+
+def test_device_checks(monkeypatch):
+    w = weight(*ref.layer(np.random.default_rng(0), 128, 256))
+    x = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="current device"):
+        sq.linear_fwd_w8a8(w, x, ws=ws)
+    w.codes = w.codes.cpu()
+    with pytest.raises(ValueError, match="codes is on cpu"):
+        sq.linear_fwd_w8a8(w, x)
+
+
+FIRST = r"""
+import sys, torch
+sys.path.insert(0, sys.argv[1])
+import bit_quantized_frozen_b200 as sq
+w = sq.Weight(4, 256, 512, torch.ones(256, 512, dtype=torch.int8, device="cuda"), torch.ones(256, device="cuda"))
+x = torch.ones(300, 512, dtype=torch.bfloat16, device="cuda")
+dy = torch.ones(300, 256, dtype=torch.bfloat16, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    y, z, dx = sq.linear_fwd_w8a8(w, x), sq.linear_fwd_w8a8(w, x[:5]), sq.linear_bwd_dx_w8a8(w, dy)
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(y[:5], z) and torch.equal(y, sq.linear_fwd_w8a8(w, x)) and torch.equal(dx, sq.linear_bwd_dx_w8a8(w, dy))
+print("ok")
+"""
+
+
+def test_first_call_inside_a_capture():
+    """The library's first call of a process may be a captured one."""
+    p = subprocess.run([sys.executable, "-c", FIRST, ROOT], capture_output=True, text=True, timeout=600)
+    assert p.returncode == 0 and p.stdout.strip() == "ok", p.stderr
