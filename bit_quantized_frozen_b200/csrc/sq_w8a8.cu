@@ -634,8 +634,8 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                                                b);
 #pragma unroll
                             for (int p = kLowParts - 1; p >= 0; --p) {
-                                    if (p == 2 && ybf)     // (a bf16 result takes two terms: 2^-17 of u)
-                                        continue;
+                                if (p == 2 && ybf)     // (a bf16 result takes two terms: 2^-16 of u)
+                                    continue;
                                 mma_16816(low[0], ufrag[h][p], b[0], b[1]);
                                 mma_16816(low[1], ufrag[h][p], b[2], b[3]);
                             }
@@ -685,7 +685,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             float low[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            if (with_low) {                // (a bf16 result takes two terms: 2^-17 of t)
+                            if (with_low) {                // (a bf16 result takes two terms: 2^-16 of t)
                                 if (!ybf)
                                     mma_16816(low, ufrag[h][0], b[2][2 * n], b[2][2 * n + 1]);
                                 mma_16816(low, ufrag[h][0], b[n][2], b[n][3]);

@@ -37,7 +37,7 @@ extern "C" {
  * the integer sums of a row are the same bits whatever M is and whichever rows
  * lie beside it; t is summed in an order fixed by M and K, so equal calls give
  * equal bits.  t enters the last product as three bf16 terms (24 bits; below
- * 2^-110 with an absolute error of 2^-134), for a bf16 y as two (2^-17 of t).
+ * 2^-110 with an absolute error of 2^-134), for a bf16 y as two (2^-16 of t).
  * flags: SQ_OUT_BF16, SQ_CHECK_FINITE (a row whose rotation holds a NaN or an
  * infinity sets SQ_ERR_NONFINITE in the status word).
  * ws: sq_workspace_bytes(SQ_OP_LINEAR_FWD_W8A8, M, N, K) bytes.

@@ -90,7 +90,7 @@ def test_forward(M, N, K, lora, bf16):
     L = ref.layer(rng, N, K, lora)
     x = rows(rng, M, K)
     y = call("fwd", weight(*L), dev(x, torch.bfloat16), bf16=bf16)
-    ref.check(y.float().cpu().numpy(), *ref.forward(x, *L), bf16)
+    ref.check(y.float().cpu().numpy(), *ref.forward(x, *L, bf16_out=bf16), bf16)
     assert status() == sq.SQ_OK
 
 
@@ -102,7 +102,7 @@ def test_backward(M, N, K, lora, bf16):
     L = ref.layer(rng, N, K, lora)
     dy = ref.bf16(rows(rng, M, N) * np.exp(rng.standard_normal((M, 1))).astype(np.float32) * 1e-3)
     dx = call("bwd", weight(*L), dev(dy, torch.bfloat16), bf16=bf16)
-    ref.check(dx.float().cpu().numpy(), *ref.backward(dy, *L), bf16)
+    ref.check(dx.float().cpu().numpy(), *ref.backward(dy, *L, bf16_out=bf16), bf16)
     assert status() == sq.SQ_OK
 
 
@@ -181,7 +181,7 @@ def test_grouped(op, name, lora, bf16):
         for e in range(E):
             a, b = off[e], off[e + 1]
             if a < b:
-                r, bound = f(x[a:b], Q[e], sw[e], *((up[e], down[e]) if lora else (None, None)))
+                r, bound = f(x[a:b], Q[e], sw[e], *((up[e], down[e]) if lora else (None, None)), bf16_out=bf16)
                 ref.check(y[a:b], r, bound, bf16)
 
 
@@ -327,7 +327,7 @@ def test_streams_and_graph():
         x.copy_(dev(v, torch.bfloat16))
         g.replay()
         torch.cuda.synchronize()
-        r, b = ref.forward(v, Q, sw, up, down)
+        r, b = ref.forward(v, Q, sw, up, down, bf16_out=True)
         ref.check(y.float().cpu().numpy(), r, b, True)
         r, b = ref.backward(y.float().cpu().numpy(), Q, sw, up, down)
         ref.check(dx.cpu().numpy(), r, b, False)
@@ -364,7 +364,7 @@ def test_experts_forward_and_back():
         if s.start == s.stop:
             continue
         one = lambda L: tuple(v[e] for v in L)  # noqa: E731
-        ref.check(f32(h)[s], *ref.forward(f32(x)[s], *one(gate_up)), True)
+        ref.check(f32(h)[s], *ref.forward(f32(x)[s], *one(gate_up), bf16_out=True), True)
         ref.check(f32(y)[s], *ref.forward(f32(a)[s], *one(down)), False)
         ref.check(f32(da)[s], *ref.backward(f32(dy)[s], *one(down)), False)
         ref.check(f32(dx)[s], *ref.backward(f32(dh)[s], *one(gate_up)), False)

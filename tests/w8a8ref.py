@@ -12,6 +12,8 @@ step of fp32, 2^-8 half a step of bf16 (relative to the value):
   low rank    t: fp32 sum of K products in some order, at most K u sum|x D|; t . U: 16 more
               products.  (K + 20) u |x| |D| |U| covers both (n u / (1 - n u) for n <= 16384 + 20).
   sum         one rounding of the result, u |y|.
+A bf16 result adds its own rounding (2^-8 of the value), and takes t (u) as two bf16 terms: each
+rounding leaves at most 2^-8 of what is left, so 2^-16 |t| . |U|.
 """
 import numpy as np
 
@@ -57,7 +59,7 @@ def codes(r):
     return np.where(np.isfinite(s)[:, None], np.nan_to_num(q), 0).astype(np.float64), s.astype(np.float32)
 
 
-def forward(x, Q, sw, up=None, down=None):
+def forward(x, Q, sw, up=None, down=None, bf16_out=False):
     """x [M, K] (bf16 values as fp32), Q [N, K] int8, sw [N] fp32 -> (y float64, bound on an fp32 y)."""
     q, s = codes(rotate32(x))
     main = (q @ Q.astype(np.float64).T) * s.astype(np.float64)[:, None] * sw.astype(np.float64)[None, :]
@@ -66,10 +68,12 @@ def forward(x, Q, sw, up=None, down=None):
         x64, U, D = x.astype(np.float64), up.astype(np.float64), down.astype(np.float64)
         y = main + (x64 @ D) @ U.T
         bound = bound + (x.shape[1] + 20) * U24 * ((np.abs(x64) @ np.abs(D)) @ np.abs(U).T)
+        if bf16_out:
+            bound = bound + 2.0 ** -16 * (np.abs(x64 @ D) @ np.abs(U).T)
     return y, bound + U24 * np.abs(y)
 
 
-def backward(dy, Q, sw, up=None, down=None):
+def backward(dy, Q, sw, up=None, down=None, bf16_out=False):
     """dy [M, N] (bf16 values as fp32) -> (dx [M, K] float64, bound on an fp32 dx)."""
     q, s = codes(dy.astype(np.float32) * sw[None, :].astype(np.float32))
     main = (q @ Q.astype(np.float64)) * s.astype(np.float64)[:, None]
@@ -79,6 +83,8 @@ def backward(dy, Q, sw, up=None, down=None):
         d64, U, D = dy.astype(np.float64), up.astype(np.float64), down.astype(np.float64)
         dx = dx + (d64 @ U) @ D.T
         bound = bound + (dy.shape[1] + 20) * U24 * ((np.abs(d64) @ np.abs(U)) @ np.abs(D).T)
+        if bf16_out:
+            bound = bound + 2.0 ** -16 * (np.abs(d64 @ U) @ np.abs(D).T)
     return dx, bound + U24 * np.abs(dx)
 
 
