@@ -46,9 +46,6 @@ struct I8Cfg {
     static constexpr int kLaneTile = 128 * CG;                       // A rows of the tile
     static constexpr int kColsPerCta = NT / CG;                      // B rows (or columns) each CTA loads
     static constexpr int kBox = NT >= 64 ? 32 : 16;                  // token rows per TMA box (forward)
-    // chunks per stage: a stage costs the MMA issuer about 85 ns (wait, commit) beside 28 ns for each
-    // of the chunk's four narrow MMAs (K is a multiple of two chunks)
-    static constexpr int kPer = CG == 1 && NT <= 32 ? 2 : 1;
     static constexpr int kABytes = 128 * kChunk;
     static constexpr int kBBytes = kColsPerCta * kChunk;
     static constexpr int kStageBytes = kABytes + kBBytes;
@@ -269,7 +266,6 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
     const int tiles = plan.tiles();
     const int unit = (int)blockIdx.x / CG;
     const int units = (int)gridDim.x / CG;
-    const int steps = (int)((BWD ? args.N : args.K) / (kChunk * Cfg::kPer));      // stages of a tile
     const I8ChannelWalk share(CG == 1 ? tiles : 0, args.N, unit, units);
     using Units = I8Units<CG, BWD>;
     auto all_work = [&]() { return Units(plan, share, tiles, unit, units, args.N); };
@@ -279,7 +275,16 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
     // 16 rows into each quarter of the lanes
     const bool m64 = CG == 1 && a_bytes <= 64 * kChunk;
     const int chunk_bytes = a_bytes + Cfg::kBBytes;
-    const int stage_bytes = Cfg::kPer * chunk_bytes;
+    // chunks per stage: a stage costs the MMA issuer about 85 ns (wait, commit) beside 20 ns for each
+    // of a chunk's four narrow MMAs, so few tokens take several, as long as every producer has a
+    // stage to fill (16 tokens, N = K = 6144: one, two, four chunks 24.5, 17.4, 16.4 us a call).
+    // Chunks behind the end of the summed axis read as 0.
+    int per = 1;
+    if (CG == 1)
+        while (per < 4 && 2 * per * chunk_bytes * max(4, Cfg::kProducers) <= Cfg::kRing)
+            per *= 2;
+    const int stage_bytes = per * chunk_bytes;
+    const int steps = (int)(((BWD ? args.N : args.K) / kChunk + per - 1) / per);      // stages of a tile
     const int stages = CG == 1 ? min(Cfg::kStages, Cfg::kRing / stage_bytes) / Cfg::kProducers * Cfg::kProducers
                                : Cfg::kStages;
     // columns of the accumulator a tile uses (forward: its tokens, in whole boxes of both CTAs)
@@ -324,7 +329,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
             m.wrow = w.t.e * (int)args.N + (BWD ? 0 : w.n0 + (int)rank * 128);
             m.mine = BWD ? 128 : cols / CG;
             m.xrow = w.t.row0 + (int)rank * m.mine;
-            m.bytes = Cfg::kPer * (CG * copied + cols) * kChunk;
+            m.bytes = per * (CG * copied + cols) * kChunk;
             m.wrow = uniform(m.wrow);
             m.rows = uniform(m.rows);
             m.xrow = uniform(m.xrow);
@@ -336,10 +341,9 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
             const uint32_t fb = bar_full + 8 * stage;
             if (leader)
                 mbar_arrive_expect_tx(fb, m.bytes);
-#pragma unroll
-            for (int u = 0; u < Cfg::kPer; ++u) {
+            for (int u = 0; u < per; ++u) {
                 const uint32_t sA = s0 + stage * stage_bytes + u * chunk_bytes;
-                const int x = (step * Cfg::kPer + u) * kChunk;
+                const int x = (step * per + u) * kChunk;
                 if (BWD) {
                     load(&tmB, sA + a_bytes, wt * NT + (int)rank * Cfg::kColsPerCta, m.wrow + x, fb);
                 } else if (CG == 2 || m.rows == args.box) {
@@ -357,10 +361,9 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
         };
         auto load_x = [&](int stage, const Aim &m, int step) {
             const uint32_t fb = bar_full + 8 * stage;
-#pragma unroll
-            for (int u = 0; u < Cfg::kPer; ++u) {
+            for (int u = 0; u < per; ++u) {
                 const uint32_t sX = s0 + stage * stage_bytes + u * chunk_bytes + (BWD ? 0 : a_bytes);
-                const int x = (step * Cfg::kPer + u) * kChunk;
+                const int x = (step * per + u) * kChunk;
                 if (BWD || m.mine == Cfg::kColsPerCta) {
                     load(BWD ? &tmA : &tmB, sX, x, m.xrow, fb);
                 } else {
@@ -447,8 +450,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                     }
                     tc_fence_after();
                     if (issue) {
-#pragma unroll
-                        for (int u = 0; u < Cfg::kPer; ++u)
+                        for (int u = 0; u < per; ++u)
 #pragma unroll
                             for (int k = 0; k < kChunk / 32; ++k)
                                 mma_i8<CG>(acc, dA + u * chunk16 + 2 * k, dB + u * chunk16 + Cfg::kBStep16 * k, idesc,
