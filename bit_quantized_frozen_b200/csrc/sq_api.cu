@@ -218,7 +218,7 @@ I8Layout i8_layout(bool bwd, int64_t M, int64_t N, int64_t K)
     };
     L.codes = take((size_t)M * (size_t)(bwd ? N : K));
     L.scales = take((size_t)M * 4);
-    L.low = take((size_t)M * 3 * 16 * 2);
+    L.low = take((size_t)M * 16 * 4);
     L.total = round_up(off, kAlign);
     return L;
 }
@@ -315,7 +315,7 @@ sq_status i8_product(bool bwd, int64_t E, const sq_weight *w, const uint16_t *x,
     q.offsets = offsets;
     q.codes = reinterpret_cast<int8_t *>(ws_at(ws, L.codes));
     q.scales = reinterpret_cast<float *>(ws_at(ws, L.scales));
-    q.low = w->lora_up ? reinterpret_cast<uint16_t *>(ws_at(ws, L.low)) : nullptr;
+    q.low = w->lora_up ? reinterpret_cast<float *>(ws_at(ws, L.low)) : nullptr;
     q.status = status;
     q.y_zero = (flags & SQ_ZERO_UNGROUPED) ? reinterpret_cast<uint8_t *>(y) : nullptr;
     q.y_row_bytes = width * ((flags & SQ_OUT_BF16) ? 2 : 4);

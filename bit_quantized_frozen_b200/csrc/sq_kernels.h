@@ -104,7 +104,7 @@ struct I8QuantArgs {
     const int32_t *offsets;     // [E + 1], E > 0
     int8_t *codes;              // [M, K]
     float *scales;              // [M]
-    uint16_t *low;              // x factor [M, 16] as three bf16 terms, [M, 3, 16], or NULL
+    float *low;                 // [M, 16] = x factor, or NULL
     uint32_t *status;
     uint8_t *y_zero;            // output whose rows outside every expert become 0, or NULL
     int64_t y_row_bytes;
@@ -123,7 +123,7 @@ struct I8GemmLaunch {
     const int32_t *offsets;     // [E + 1] (device), E > 0
     const int8_t *codes;        // row operand [M, K] (backward [M, N])
     const float *scales;        // [M]
-    const uint16_t *low;        // [M, 3, 16] or NULL
+    const float *low;           // [M, 16] or NULL
     const uint8_t *wcodes;      // [max(E, 1) N, K]
     const float *wscales;       // forward: [max(E, 1), N]
     const uint16_t *factor;     // lora_up [., N, 16] (forward) or lora_down [., K, 16] (backward)

@@ -17,8 +17,15 @@
 //             transposed).  A thread holds a whole 256-block of its token, so the
 //             rotation is done on the accumulator.
 //
+// The low-rank product (rank 16) is part of the epilogue.  Forward it is 8 packed fp32 FMAs a
+// value, with the lane's factors in registers and the tokens' in shared memory; mma.sync on bf16
+// terms would hold up the integer MMAs (4480 tokens, N = 16384, K = 6144: 315 us a call against
+// 360; 6001 rows of 8 experts, 6144 x 4096: 166 against 200).  Backward the FMA units are busy
+// with the rotation and mma.sync on three bf16 terms is faster (8192 rows of 64 experts,
+// 2816 x 2048: 136 us against 150; 509 tokens: 24 against 29).
+//
 // CTA (CG = 1) or CTA pair (CG = 2, 256 x 256 tiles) per SM, persistent: 4 or 8 epilogue
-// warps, a TMA producer, an MMA issuer that also allocates tensor memory.  Two
+// warps, one to four TMA producers, an MMA issuer that also allocates tensor memory.  Two
 // accumulators in tensor memory: the next tile's MMAs run while one drains.
 // Weight tiles of the first stages are fetched before the kernel waits for the
 // quantisation kernel in front of it.
@@ -56,9 +63,9 @@ struct I8Cfg {
     // tiles that need little time per stage share the work out
     static constexpr int kProducers = CG == 2 ? 1 : NT <= 32 ? 4 : 2;
     static constexpr int kThreads = kEpiThreads + 32 * kProducers + 32;   // + MMA issuer
-    // low-rank values of a column in shared memory: three bf16 terms of a token (forward), the
-    // bf16 row of lora_down (backward); an odd number of 16-byte pieces apart (ldmatrix rows)
-    static constexpr int kLowPitch = BWD ? 48 : 112;
+    // bytes from one column's low-rank values to the next in shared memory (bf16 backward, fp32
+    // forward): the four columns that a warp reads at once lie in different banks
+    static constexpr int kLowPitch = BWD ? 48 : 80;
     static constexpr int kPatchBytes = BWD ? 0 : 2 * 8 * 36 * 4;     // a warp's two store patches
     // stages: fixed for a CTA pair; with CG = 1 as many as fit with the A rows that the CTA's
     // tiles have (the MMAs read 128 rows all the same: behind the tile's own lie other bytes of
@@ -81,7 +88,7 @@ struct I8Cfg {
 struct I8Args {
     const int32_t *offsets;
     const float *scales;      // per token
-    const uint16_t *low;      // per token, three bf16 terms [M, 3, 16], or NULL
+    const float *low;         // per token [M, 16] or NULL
     const float *wscales;     // per channel (forward)
     const uint16_t *factor;   // lane-side (forward: lora_up) or column-side (backward: lora_down) factor
     void *y;
@@ -496,7 +503,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
         const int wh = warp >> 2;                          // which warp of those lanes
         const int g = lane >> 2, q = lane & 3;             // place in a fragment
         const uint32_t acc_empty_leader = CG == 2 ? mapa_shared(bar_acc_empty, 0) : bar_acc_empty;
-        const uint32_t col_low = smem_u32(smem + Cfg::kLowOff);
+        uint8_t *col_low = smem + Cfg::kLowOff;
         uint8_t *patch = smem + Cfg::kPatchOff + warp * Cfg::kPatchBytes;
         const bool ybf = args.out_bf16 != 0;
         const bool with_low = args.low != nullptr;
@@ -509,53 +516,91 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
             const int slot = count & 1;
             named_barrier_sync(1, ET);                     // the previous tile's column factors are used up
             if (with_low) {
-                // 16-byte pieces of the columns' low-rank values
-                constexpr int kPieces = BWD ? 2 : 2 * kLowParts;
-                const int cols = BWD ? NT : t.rows;
-                const uint4 *src = reinterpret_cast<const uint4 *>(
-                    BWD ? args.factor + ((int64_t)t.e * args.K + (int64_t)t.wt * NT) * kI8Rank
-                        : args.low + (int64_t)t.row0 * kLowRow);
-                for (int i = et; i < cols * kPieces; i += ET)
-                    *reinterpret_cast<uint4 *>(smem + Cfg::kLowOff + (i / kPieces) * Cfg::kLowPitch +
-                                               16 * (i % kPieces)) = BWD ? __ldg(src + i) : src[i];
+                // the columns' low-rank values: lora_down's rows (backward), the tokens' t (forward)
+                const char *src = BWD ? reinterpret_cast<const char *>(
+                                            args.factor + ((int64_t)t.e * args.K + (int64_t)t.wt * NT) * kI8Rank)
+                                      : reinterpret_cast<const char *>(args.low + (int64_t)t.row0 * kI8Rank);
+                constexpr int kPieces = BWD ? 2 : 4;       // of 16 bytes a column
+                const int pieces = kPieces * (BWD ? NT : t.rows);
+                // (with many tiles a CTA the copies run under the loads below; with one, plain loads
+                // end 1 us earlier)
+                for (int i = et; i < pieces; i += ET) {
+                    uint8_t *dst = col_low + i / kPieces * Cfg::kLowPitch + i % kPieces * 16;
+                    if (CG == 2 && !BWD)
+                        cp_async16(smem_u32(dst), src + 16 * i, true);
+                    else
+                        *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(src + 16 * i);
+                }
             }
-            if (!BWD)
-                for (int c = et; c < NT; c += ET)
-                    col_scale[c] = c < t.rows ? args.scales[t.row0 + c] : 0.0f;
+            static_assert(BWD || NT <= ET, "a token's scale for each thread");
+            const float token_scale = !BWD && et < t.rows ? args.scales[t.row0 + et] : 0.0f;
             // the lanes' scales and low-rank values (lane r of a fragment half: 16 h + g + 8 i)
             const int span = m64 ? 16 : 32;                // rows of the tile in a quarter of the lanes
             const int lane0 = (int)rank * 128 + span * wq; // first row of the warp in the tile
             const int64_t base = (BWD ? t.row0 : w.n0) + lane0;
+            // (rows behind the tile's last one repeat that one; their sums are not stored)
+            const float lscale = BWD ? args.scales[t.row0 + min(lane0 + lane, w.lanes - 1)] : 0.0f;
             float fscale[2][2];                            // forward: per fragment row
-            float lscale = 0.0f;                           // backward: of this thread's lane
-            uint32_t ufrag[2][BWD ? kLowParts : 1][4];     // A operand of the low-rank product
-            if (BWD)
-                lscale = lane0 + lane < w.lanes ? args.scales[base + lane] : 0.0f;
+            uint64_t lane_low[2][2][BWD ? 1 : 8];          // forward: lora_up's rows
+            uint32_t ufrag[2][BWD ? kLowParts : 1][4];     // backward: A operand of the low-rank product
+            int64_t lrow[2][2];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int r = 16 * h + g + 8 * i;
-                    const bool live = r < span && lane0 + r < w.lanes;
+                    lrow[h][i] = min(lane0 + 16 * h + g + 8 * i, w.lanes - 1);
+                    lrow[h][i] += BWD ? (int64_t)t.row0 : (int64_t)t.e * args.N + w.n0;
                     if (!BWD)
-                        fscale[h][i] = live ? __ldg(args.wscales + (int64_t)t.e * args.N + base + r) : 0.0f;
+                        fscale[h][i] = __ldg(args.wscales + lrow[h][i]);
+                }
+            if constexpr (BWD) {
+                float2 v[2][2][2];                         // ranks 2 q + 8 k, 2 q + 8 k + 1
 #pragma unroll
-                    for (int p = 0; p < (BWD ? kLowParts : 1); ++p)
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            v[h][i][k] = with_low ? *reinterpret_cast<const float2 *>(args.low + lrow[h][i] * kI8Rank +
+                                                                                      2 * q + 8 * k)
+                                                  : make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            uint32_t v = 0u;
-                            if (with_low && live)
-                                v = BWD ? reinterpret_cast<const uint32_t *>(args.low + (base + r) * kLowRow)[8 * p + q + 4 * k]
-                                        : __ldg(reinterpret_cast<const uint32_t *>(
-                                                    args.factor + ((int64_t)t.e * args.N + base + r) * kI8Rank) +
-                                                q + 4 * k);
-                            ufrag[h][p][i + 2 * k] = v;
+                            uint32_t x[kLowParts], y[kLowParts];
+                            split3(v[h][i][k].x, x);
+                            split3(v[h][i][k].y, y);
+#pragma unroll
+                            for (int p = 0; p < kLowParts; ++p)
+                                ufrag[h][p][i + 2 * k] = x[p] | y[p] << 16;
                         }
-                }
+            } else {
+                uint4 v[2][2][2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            v[h][i][k] = with_low ? __ldg(reinterpret_cast<const uint4 *>(args.factor + lrow[h][i] * kI8Rank) + k)
+                                                  : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        pairs16(v[h][i][0], v[h][i][1], lane_low[h][i]);
+            }
+            if (!BWD && et < NT)
+                col_scale[et] = token_scale;
             if (et == 0)
                 *verdict = acc_wait<CG>(bar_acc_full + 8 * slot, (uint32_t)((count >> 1) & 1), abort_flag, args.status)
                                ? 1u
                                : 0u;
+            if (CG == 2 && !BWD)
+                cp_async_wait_all();
             named_barrier_sync(1, ET);
             if (*verdict == 0u)
                 break;
@@ -631,7 +676,8 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                         float low[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
                         if (with_low) {                // B: 16 columns (two groups of 8) x 16 ranks
                             uint32_t b[4];
-                            ldmatrix_x4<false>(col_low + (col + 8 * (lane >> 4) + (lane & 7)) * Cfg::kLowPitch +
+                            ldmatrix_x4<false>(smem_u32(col_low) +
+                                                   (col + 8 * (lane >> 4) + (lane & 7)) * Cfg::kLowPitch +
                                                    16 * ((lane >> 3) & 1),
                                                b);
 #pragma unroll
@@ -673,30 +719,23 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                 };
                 const bool live = lane0 < w.lanes;
                 auto finish16 = [&](int c, const uint32_t (&r)[2][2][4]) {
-                    uint32_t b[3][4];                      // terms 0, 1 of both groups; term 2 of both
-                    if (with_low) {
-                        const uint32_t row = col_low + (c + (lane & 7)) * Cfg::kLowPitch;
-                        ldmatrix_x4<false>(row + 16 * (lane >> 3), b[0]);
-                        ldmatrix_x4<false>(row + 8 * Cfg::kLowPitch + 16 * (lane >> 3), b[1]);
-                        ldmatrix_x4<false>(row + 8 * (lane >> 4) * Cfg::kLowPitch + 64 + 16 * ((lane >> 3) & 1), b[2]);
-                    }
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {          // 8 tokens
                         float o[2][4];
                         const float2 sx = *reinterpret_cast<const float2 *>(col_scale + c + 8 * n + 2 * q);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float low[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            if (with_low) {                // (a bf16 result takes two terms: 2^-16 of t)
-                                if (!ybf)
-                                    mma_16816(low, ufrag[h][0], b[2][2 * n], b[2][2 * n + 1]);
-                                mma_16816(low, ufrag[h][0], b[n][2], b[n][3]);
-                                mma_16816(low, ufrag[h][0], b[n][0], b[n][1]);
-                            }
+                        for (int j = 0; j < 2; ++j) {      // token 2 q + j, fragment rows g + 8 i
+                            const float4 *src = reinterpret_cast<const float4 *>(
+                                col_low + (c + 8 * n + 2 * q + j) * Cfg::kLowPitch);
+                            uint64_t f[8];
+                            pairs16(src[0], src[1], src[2], src[3], f);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                o[h][i] = __fmaf_rn(__int2float_rn((int32_t)r[h][n][i]),
-                                                    __fmul_rn(i & 1 ? sx.y : sx.x, fscale[h][i >> 1]), low[i]);
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+                                    o[h][2 * i + j] = __fmaf_rn(__int2float_rn((int32_t)r[h][n][2 * i + j]),
+                                                                __fmul_rn(j ? sx.y : sx.x, fscale[h][i]),
+                                                                with_low ? dot16(lane_low[h][i], f) : 0.0f);
                         }
                         // through the warp's patch, so that a token's 32 channels leave in one run
                         uint8_t *buf = patch + n * (8 * 36 * 4);

@@ -1,6 +1,6 @@
 // sq_w8a8.cuh -- what the row quantisation (sq_w8a8_quant.cu) and the integer
-// product (sq_w8a8.cu) share: the plan of tiles over the experts' rows, and the
-// low-rank values as three bf16 terms.
+// product (sq_w8a8.cu) share: the plan of tiles over the experts' rows, and small
+// products of low-rank values.
 #pragma once
 
 #include <cstdint>
@@ -10,8 +10,6 @@
 namespace sq {
 
 constexpr int kI8Rank = 16;                       // rank of the int8 layer's low-rank branch
-constexpr int kLowParts = 3;                      // bf16 terms of an fp32 low-rank value
-constexpr int kLowRow = kLowParts * kI8Rank;      // bf16 values per token
 constexpr int kMaxExperts = 1024;
 
 // where a tile lies
@@ -121,8 +119,8 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t 
                  ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
 }
 
-// c[16 x 8] += a[16 x 16] b[16 x 8], bf16 inputs, fp32 sums (one warp; the small low-rank
-// products only -- the large ones run on tcgen05)
+// c[16 x 8] += a[16 x 16] b[16 x 8], bf16 inputs, fp32 sums (one warp; the rows' low-rank input
+// only -- the large products run on tcgen05)
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -130,6 +128,33 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+
+// 16 bytes, or 16 zero bytes with live = false (src is then not read)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_wait_all()
+{
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// 16 values as pairs of neighbours, from fp32 (64 bytes) or bf16 (32 bytes)
+__device__ __forceinline__ void pairs16(const float4 &a, const float4 &b, const float4 &c, const float4 &d,
+                                        uint64_t (&f)[8])
+{
+    f[0] = f2_pack(a.x, a.y);
+    f[1] = f2_pack(a.z, a.w);
+    f[2] = f2_pack(b.x, b.y);
+    f[3] = f2_pack(b.z, b.w);
+    f[4] = f2_pack(c.x, c.y);
+    f[5] = f2_pack(c.z, c.w);
+    f[6] = f2_pack(d.x, d.y);
+    f[7] = f2_pack(d.z, d.w);
+}
+
+constexpr int kLowParts = 3;                      // bf16 terms of an fp32 low-rank value
 
 // v as the sum of three bf16 terms, largest first (24 significant bits: exact but for
 // subnormal remainders)
@@ -140,6 +165,26 @@ __device__ __forceinline__ void split3(float v, uint32_t (&p)[kLowParts])
         p[i] = f32_to_bf16_bits(v);
         v = __fsub_rn(v, bf16_bits_to_f32(p[i]));
     }
+}
+
+__device__ __forceinline__ void pairs16(const uint4 &a, const uint4 &b, uint64_t (&f)[8])
+{
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        f[j] = f2_pack(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+}
+
+// sum over r = 0 .. 15 of a[r] b[r]: even and odd r apart, then their sum
+__device__ __forceinline__ float dot16(const uint64_t (&a)[8], const uint64_t (&b)[8])
+{
+    uint64_t s = 0;                               // (0.0f, 0.0f)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        s = f2_fma(a[j], b[j], s);
+    float lo, hi;
+    f2_unpack(s, lo, hi);
+    return __fadd_rn(lo, hi);
 }
 
 }  // namespace sq

@@ -75,17 +75,6 @@ __device__ __forceinline__ float absmax3(float a, float b, float c)
     return r;
 }
 
-// 16 bytes, or 16 zero bytes with live = false (src is then not read)
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-
-__device__ __forceinline__ void cp_async_wait_all()
-{
-    asm volatile("cp.async.wait_all;" ::: "memory");
-}
-
 // 4 bytes into another CTA's shared memory, counted on its barrier
 __device__ __forceinline__ void st_async(uint32_t addr, uint32_t v, uint32_t bar)
 {
@@ -524,13 +513,8 @@ __global__ void __launch_bounds__(32 * kQWarps, 2) i8_quant_kernel(const I8Quant
                         v = __fadd_rn(v, sh.low[parity][r][i]);
                 }
                 const int row = i / kI8Rank, k = i % kI8Rank;
-                if (row < t.rows && SQ_DCHECK(t.row0 + row < a.M, a.status)) {
-                    uint32_t part[kLowParts];
-                    split3(v, part);
-#pragma unroll
-                    for (int j = 0; j < kLowParts; ++j)
-                        a.low[(int64_t)(t.row0 + row) * kLowRow + j * kI8Rank + k] = (uint16_t)part[j];
-                }
+                if (row < t.rows && SQ_DCHECK(t.row0 + row < a.M, a.status))
+                    a.low[(int64_t)(t.row0 + row) * kI8Rank + k] = v;
             }
         t = TURNS && tile + units < tiles ? tile_at(tile + units, e) : next;
     }

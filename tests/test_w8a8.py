@@ -124,7 +124,7 @@ def test_workspace_covers_its_parts():
     for op, gop, back in ((sq.SQ_OP_LINEAR_FWD_W8A8, sq.SQ_OP_GROUPED_FWD_W8A8, False),
                           (sq.SQ_OP_LINEAR_BWD_DX_W8A8, sq.SQ_OP_GROUPED_BWD_DX_W8A8, True)):
         for M, N, K in ((1, 6144, 6144), (4480, 16384, 6144), (333, 128, 256)):
-            need = 256 + M * ((N if back else K) + 4 + 96)
+            need = 256 + M * ((N if back else K) + 4 + 64)
             assert need <= sq.sq_workspace_bytes(op, M, N, K) <= need + 5 * 1024
             for E in (1, 64, 1024):
                 assert sq.sq_grouped_workspace_bytes(gop, E, M, N, K) == sq.sq_workspace_bytes(op, M, N, K)

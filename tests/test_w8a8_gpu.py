@@ -224,10 +224,9 @@ def test_special_rows(M):
     assert (y[0] == 0).all() and np.isnan(y[2:5]).all()
     with np.errstate(all="ignore"):
         r, b = ref.forward(x, *L)
-    # subnormal fp32 sums have an absolute error of half the smallest step each; t = x lora_down is
-    # handed over as three bf16 terms, whose last remainder is below half the smallest bf16 step
-    # (2^-133) where t is this small, so that y is off by up to 2^-134 sum_r |lora_up[n, r]| more
-    off = (K + 20) * 2.0 ** -149 + 2.0 ** -134 * np.abs(L[2].astype(np.float64)).sum(axis=1)
+    # subnormal fp32 sums have an absolute error of half the smallest step (2^-149) each: K of t,
+    # which sum_r |lora_up[n, r]| takes into y, and the 20 behind them
+    off = 2.0 ** -149 * (K * np.abs(L[2].astype(np.float64)).sum(axis=1) + 20)
     ref.check(y[1:2], r[1:2], b[1:2] + off[None, :], False)
     ref.check(y[5:], r[5:], b[5:], False)
     call("fwd", w, dev(x[5:6], torch.bfloat16), flags=sq.SQ_CHECK_FINITE)

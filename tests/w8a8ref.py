@@ -12,8 +12,8 @@ step of fp32, 2^-8 half a step of bf16 (relative to the value):
   low rank    t: fp32 sum of K products in some order, at most K u sum|x D|; t . U: 16 more
               products.  (K + 20) u |x| |D| |U| covers both (n u / (1 - n u) for n <= 16384 + 20).
   sum         one rounding of the result, u |y|.
-A bf16 result adds its own rounding (2^-8 of the value), and takes t (u) as two bf16 terms: each
-rounding leaves at most 2^-8 of what is left, so 2^-16 |t| . |U|.
+A bf16 result adds its own rounding (2^-8 of the value); backward it takes u as two bf16 terms:
+each rounding leaves at most 2^-8 of what is left, so 2^-16 |u| . |D|.
 """
 import numpy as np
 
@@ -60,7 +60,8 @@ def codes(r):
 
 
 def forward(x, Q, sw, up=None, down=None, bf16_out=False):
-    """x [M, K] (bf16 values as fp32), Q [N, K] int8, sw [N] fp32 -> (y float64, bound on an fp32 y)."""
+    """x [M, K] (bf16 values as fp32), Q [N, K] int8, sw [N] fp32 -> (y float64, bound on an fp32 y).
+    bf16_out is backward's and changes nothing here."""
     q, s = codes(rotate32(x))
     main = (q @ Q.astype(np.float64).T) * s.astype(np.float64)[:, None] * sw.astype(np.float64)[None, :]
     y, bound = main, 4 * U24 * np.abs(main)
@@ -68,8 +69,6 @@ def forward(x, Q, sw, up=None, down=None, bf16_out=False):
         x64, U, D = x.astype(np.float64), up.astype(np.float64), down.astype(np.float64)
         y = main + (x64 @ D) @ U.T
         bound = bound + (x.shape[1] + 20) * U24 * ((np.abs(x64) @ np.abs(D)) @ np.abs(U).T)
-        if bf16_out:
-            bound = bound + 2.0 ** -16 * (np.abs(x64 @ D) @ np.abs(U).T)
     return y, bound + U24 * np.abs(y)
 
 
