@@ -23,8 +23,8 @@
 // covers K <= 16384, so a row group is read once, its maximum and low-rank sums
 // meet over distributed shared memory, and the codes leave from registers.  The
 // clusters are persistent: a warp keeps its block's factor in shared memory from
-// row group to row group (of one expert) and loads the next group while it
-// transforms this one.  Longer rows (backward, N > 16384) take their blocks in
+// row group to row group (of one expert) and loads the next group, and its expert's
+// factor where that is another one, while it transforms this one.  Longer rows (backward, N > 16384) take their blocks in
 // turns and read them a second time for the codes.
 #include <cuda.h>
 
@@ -258,7 +258,11 @@ __device__ __forceinline__ void begin_call(const I8QuantArgs &a)
     }
 }
 
-template <bool BWD, bool TURNS>
+// GROUPED: called with E > 0 only.  Dense calls have a kernel of their own (4480 x 16384 backward
+// 78 us against 85); tests of a.E that are always true stay in the grouped one, since without them
+// the compiler keeps fewer of the forward's values in registers (115 us a call against 108, 8192
+// rows of 64 experts, 2816 x 2048).
+template <bool BWD, bool TURNS, bool GROUPED>
 __global__ void __launch_bounds__(32 * kQWarps, 2) i8_quant_kernel(const I8QuantArgs a, int cluster)
 {
     extern __shared__ __align__(16) uint8_t q_smem[];
@@ -285,7 +289,7 @@ __global__ void __launch_bounds__(32 * kQWarps, 2) i8_quant_kernel(const I8Quant
     }
     const uint32_t factor_at = factor_lane(smem_u32(my_factor), lane);
 
-    if (a.E == 0 && with_low && block0 < nb && (int)blockIdx.x < cluster * 2) {
+    if ((!GROUPED || a.E == 0) && with_low && block0 < nb && (int)blockIdx.x < cluster * 2) {
         // the factor on its way into L2 (a prefetch: whoever still writes it is not overtaken)
         const uint8_t *src = reinterpret_cast<const uint8_t *>(a.factor + (int64_t)block0 * kHad * kI8Rank);
         const int64_t bytes = (a.K - (int64_t)block0 * kHad) * kI8Rank * 2;
@@ -304,11 +308,11 @@ __global__ void __launch_bounds__(32 * kQWarps, 2) i8_quant_kernel(const I8Quant
     plan.E = a.E;
     plan.wts = 1;
     plan.tok_tile = kQRows;
-    if (a.E > 0)
+    if (GROUPED && a.E > 0)
         plan.build(a.offsets, a.M, tid, blockDim.x);
-    const int tiles = a.E > 0 ? plan.tiles() : (int)((a.M + kQRows - 1) / kQRows);
+    const int tiles = GROUPED && a.E > 0 ? plan.tiles() : (int)((a.M + kQRows - 1) / kQRows);
     auto tile_at = [&](int i, int &e) {
-        if (a.E > 0)
+        if (GROUPED && a.E > 0)
             return plan.find(i, e);
         const int64_t row0 = (int64_t)i * kQRows, left = a.M - row0;
         return I8Tile{0, (int)row0, left < kQRows ? (int)left : kQRows, 0};
@@ -354,21 +358,26 @@ __global__ void __launch_bounds__(32 * kQWarps, 2) i8_quant_kernel(const I8Quant
         }
     };
 
-    int e = 0, have = -1;                             // expert walked to; expert whose factor is here
+    // dense: the clusters side by side (what they read at a time lies close together; in shares of
+    // neighbouring groups 4480 x 6144 takes 47 us instead of 38); grouped: neighbouring groups,
+    // mostly of one expert, whose factor then stays in shared memory
+    const int first = GROUPED && a.E > 0 ? (int)((int64_t)tiles * unit / units) : unit;
+    const int end = GROUPED && a.E > 0 ? (int)((int64_t)tiles * (unit + 1) / units) : tiles;
+    const int step = GROUPED && a.E > 0 ? 1 : units;
+    int e = 0;                                        // expert walked to
     uint4 w[8];
     I8Tile t = {0, 0, 0, 0};
-    if (unit < tiles) {
-        t = tile_at(unit, e);
+    if (first < end) {
+        t = tile_at(first, e);
         if (!TURNS) {
             load_block<BWD>(row_of(t, block0), pieces_of(t, block0), w);
             fetch(t.e, block0);
-            have = t.e;
         }
     }
     if (blockIdx.x == 0)                              // while the first loads are on their way
         begin_call(a);
     // rows of no expert: 0
-    if (a.y_zero && a.E > 0) {
+    if (GROUPED && a.y_zero && a.E > 0) {
         const int64_t head = plan.start[0], tail = a.M - plan.start[a.E], n16 = a.y_row_bytes / 16;
         for (int64_t i = blockIdx.x; i < head + tail; i += gridDim.x) {
             const int64_t m = i < head ? i : plan.start[a.E] + (i - head);
@@ -378,10 +387,8 @@ __global__ void __launch_bounds__(32 * kQWarps, 2) i8_quant_kernel(const I8Quant
                     row[c] = make_uint4(0u, 0u, 0u, 0u);
         }
     }
-    if (!TURNS)
-        fetched();
     int round = 0;
-    for (int tile = unit; tile < tiles; tile += units, ++round) {
+    for (int tile = first; tile < end; tile += step, ++round) {
         const int parity = round & 1;
         const bool live = g < t.rows;
         float low[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -405,12 +412,7 @@ __global__ void __launch_bounds__(32 * kQWarps, 2) i8_quant_kernel(const I8Quant
                 __syncwarp();                         // the next block's factor takes this one's place
             }
         } else {
-            if (have != t.e) {
-                __syncwarp();
-                fetch(t.e, block0);
-                fetched();
-                have = t.e;
-            }
+            fetched();
             if (with_low && block0 < nb)
                 low_block(w, factor_at, low);
             spread(w, p);
@@ -420,9 +422,13 @@ __global__ void __launch_bounds__(32 * kQWarps, 2) i8_quant_kernel(const I8Quant
                 f2_unpack(p[j], x0, x1);
                 amax = absmax3(amax, x0, x1);
             }
-            if (tile + units < tiles) {               // the next group's values, while this one is finished
-                next = tile_at(tile + units, e);
+            if (tile + step < end) {                  // the next group's values, while this one is finished
+                next = tile_at(tile + step, e);
                 load_block<BWD>(row_of(next, block0), pieces_of(next, block0), w);
+                if (next.e != t.e) {
+                    __syncwarp();
+                    fetch(next.e, block0);
+                }
             }
         }
         // the row's maximum: 4 lanes, the CTA's warps, the cluster's CTAs (max of bit patterns:
@@ -516,7 +522,7 @@ __global__ void __launch_bounds__(32 * kQWarps, 2) i8_quant_kernel(const I8Quant
                 if (row < t.rows && SQ_DCHECK(t.row0 + row < a.M, a.status))
                     a.low[(int64_t)(t.row0 + row) * kI8Rank + k] = v;
             }
-        t = TURNS && tile + units < tiles ? tile_at(tile + units, e) : next;
+        t = TURNS && tile + step < end ? tile_at(tile + step, e) : next;
     }
     if (cluster > 1) {
         __syncwarp();
@@ -524,7 +530,7 @@ __global__ void __launch_bounds__(32 * kQWarps, 2) i8_quant_kernel(const I8Quant
     }
 }
 
-template <bool BWD, bool TURNS>
+template <bool BWD, bool TURNS, bool GROUPED>
 static cudaError_t launch_quant_v(const I8QuantArgs &a, int cluster, int warps, int sms, cudaStream_t s)
 {
     constexpr int kMaxDev = 64;
@@ -537,7 +543,7 @@ static cudaError_t launch_quant_v(const I8QuantArgs &a, int cluster, int warps, 
         return cudaErrorInvalidDevice;
     const unsigned long long ctx = current_context_id();
     if (ctx == 0 || attr_ctx[dev] != ctx) {
-        cudaError_t e = cudaFuncSetAttribute(i8_quant_kernel<BWD, TURNS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(i8_quant_kernel<BWD, TURNS, GROUPED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kMaxSmem);
         if (e != cudaSuccess)
             return e;
@@ -565,7 +571,7 @@ static cudaError_t launch_quant_v(const I8QuantArgs &a, int cluster, int warps, 
         cfg.attrs = at;
         cfg.numAttrs = 1;
         int n = 0;
-        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, i8_quant_kernel<BWD, TURNS>, &cfg);
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, i8_quant_kernel<BWD, TURNS, GROUPED>, &cfg);
         (void)cudaGetLastError();
         room[dev][cluster - 1][warps - 1] = e == cudaSuccess && n > 0 ? n : 1;
         room_ctx[dev][cluster - 1][warps - 1] = ctx;
@@ -575,7 +581,7 @@ static cudaError_t launch_quant_v(const I8QuantArgs &a, int cluster, int warps, 
     cfg.gridDim = dim3((unsigned)((groups < fit ? groups : fit) * cluster));
     cfg.attrs = at;
     cfg.numAttrs = (int64_t)cfg.gridDim.x <= sms ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, i8_quant_kernel<BWD, TURNS>, a, cluster);
+    return cudaLaunchKernelEx(&cfg, i8_quant_kernel<BWD, TURNS, GROUPED>, a, cluster);
 }
 
 cudaError_t launch_i8_quant(const I8QuantArgs &a, bool bwd, int sms, cudaStream_t s)
@@ -590,10 +596,16 @@ cudaError_t launch_i8_quant(const I8QuantArgs &a, bool bwd, int sms, cudaStream_
     int warps = (nb + cluster - 1) / cluster;
     const bool turns = warps > kQWarps;
     warps = turns ? kQWarps : warps;
+    if (a.E > 0) {
+        if (bwd)
+            return turns ? launch_quant_v<true, true, true>(a, cluster, warps, sms, s)
+                         : launch_quant_v<true, false, true>(a, cluster, warps, sms, s);
+        return launch_quant_v<false, false, true>(a, cluster, warps, sms, s);
+    }
     if (bwd)
-        return turns ? launch_quant_v<true, true>(a, cluster, warps, sms, s)
-                     : launch_quant_v<true, false>(a, cluster, warps, sms, s);
-    return launch_quant_v<false, false>(a, cluster, warps, sms, s);
+        return turns ? launch_quant_v<true, true, false>(a, cluster, warps, sms, s)
+                     : launch_quant_v<true, false, false>(a, cluster, warps, sms, s);
+    return launch_quant_v<false, false, false>(a, cluster, warps, sms, s);
 }
 
 }  // namespace sq
