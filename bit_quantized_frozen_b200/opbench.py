@@ -17,6 +17,8 @@ Operations:
   fwd_nvfp4            sq_linear_fwd, NVFP4 weight
   fwd_int4             sq_linear_fwd, int4 group-32 weight
   fwd_int8             sq_linear_fwd, int8 per-row weight (rank-16 low-rank branch)
+  fwd_w8a8             sq_linear_fwd_w8a8, int8 per-row weight, 8-bit integer product
+  bwd_dx_w8a8          sq_linear_bwd_dx_w8a8 on the same weight
   build_nvfp4          sq_build_nvfp4
   build_int4           sq_build_int4, group 32
   build_int4_g64       sq_build_int4, group 64
@@ -64,10 +66,10 @@ import synth_inputs as si  # noqa: E402
 
 FLUSH_BYTES = 256 << 20
 
-OPS = ["act_quant", "act_quant_nolowrank", "fwd_nvfp4", "fwd_int4", "fwd_int8", "build_nvfp4", "build_int4",
+OPS = ["act_quant", "act_quant_nolowrank", "fwd_nvfp4", "fwd_int4", "fwd_int8", "fwd_w8a8", "build_nvfp4", "build_int4",
        "build_int4_g64", "build_int8", "recon_nvfp4", "recon_int4", "recon_int4_g64", "recon_int8",
        "recon_nvfp4_resid", "recon_int4_resid", "recon_int8_resid", "recon_nvfp4_t", "gemm_nvfp4", "gemm_int4",
-       "bwd_dx_nvfp4", "gemm_bwd_dx", "svd_init"]
+       "bwd_dx_nvfp4", "bwd_dx_w8a8", "gemm_bwd_dx", "svd_init"]
 SVD_ITERS = 8
 
 
@@ -208,6 +210,8 @@ def main():
     wn = sq.build_nvfp4(R, U, D)
     w8 = sq.build_int8(R, U[:, :16].contiguous(), D[:, :16].contiguous())
     ws_8 = sq.workspace(sq.SQ_OP_LINEAR_FWD_INT8, M, N, K, dev)
+    ws_q = sq.workspace(sq.SQ_OP_LINEAR_FWD_W8A8, M, N, K, dev)
+    ws_qb = sq.workspace(sq.SQ_OP_LINEAR_BWD_DX_W8A8, M, N, K, dev)
     ws_b = sq.workspace(sq.SQ_OP_BUILD_NVFP4, 0, N, K, dev)
     ws_a = sq.workspace(sq.SQ_OP_ACT_QUANT_NVFP4, M, 0, K, dev)
     ws_n = sq.workspace(sq.SQ_OP_LINEAR_FWD_NVFP4, M, N, K, dev)
@@ -241,6 +245,8 @@ def main():
         "fwd_nvfp4": lambda: sq.sq_linear_fwd(wn, x, y, g_x=gx, ws=ws_n),
         "fwd_int4": lambda: sq.sq_linear_fwd(w4, x, y, ws=ws_i),
         "fwd_int8": lambda: sq.sq_linear_fwd(w8, x, y, ws=ws_8),
+        "fwd_w8a8": lambda: sq.sq_linear_fwd_w8a8(w8, x, y, ws=ws_q),
+        "bwd_dx_w8a8": lambda: sq.sq_linear_bwd_dx_w8a8(w8, dy, dx, ws=ws_qb),
         "build_int8": lambda: sq.sq_build_int8(R, c8, s8, f8),
         "recon_int8": lambda: sq.sq_reconstruct_bf16(w8, W),
         "recon_int8_resid": lambda: sq.sq_reconstruct_bf16(w8, W, RES),
