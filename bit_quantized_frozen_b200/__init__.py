@@ -345,6 +345,10 @@ def _w8a8(fn: str, w, x, y, flags, ws, stream, backward: bool, offsets=None):
     xn, yn, wide, out = ("dy", "dx", N, K) if backward else ("x", "y", K, N)
     if w.fmt != SQ_FMT_INT8_ROW:
         raise ValueError(f"{fn}: the weight must be SQ_FMT_INT8_ROW")
+    if ("grouped" in fn) != (E is not None):
+        raise ValueError(f"{fn}: the weight is a {type(w).__name__}")
+    if E is not None and not isinstance(offsets, torch.Tensor):
+        raise ValueError(f"{fn}: offsets must be an int32 tensor of {E + 1} values")
     if x.dim() != 2 or x.shape[1] != wide or x.dtype != torch.bfloat16:
         raise ValueError(f"{fn}: {xn} must be bfloat16 [M, {wide}], got {x.dtype} {list(x.shape)}")
     M = x.shape[0]

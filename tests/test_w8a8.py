@@ -119,6 +119,20 @@ def test_binding_refusals():
             sq.sq_grouped_fwd_w8a8(w, x, o, y, 0, ws)
 
 
+def test_binding_weight_kinds():
+    """A grouped call wants a GroupedWeight and an offsets tensor, a dense call a Weight."""
+    x, dy, off = t((40, 512)), t((40, 256)), t(4, torch.int32)
+    one, many = weights(), weights(3)
+    for bad, says in ((lambda: sq.linear_fwd_w8a8(many, x), "is a GroupedWeight"),
+                      (lambda: sq.linear_bwd_dx_w8a8(many, dy), "is a GroupedWeight"),
+                      (lambda: sq.grouped_fwd_w8a8(one, x, off), "is a Weight"),
+                      (lambda: sq.grouped_bwd_dx_w8a8(one, dy, off), "is a Weight"),
+                      (lambda: sq.grouped_fwd_w8a8(many, x, None), "offsets must be an int32 tensor"),
+                      (lambda: sq.grouped_bwd_dx_w8a8(many, dy, [0, 7, 7, 40]), "offsets must be an int32 tensor")):
+        with pytest.raises(ValueError, match=says):
+            bad()
+
+
 def test_workspace_covers_its_parts():
     """Header, row codes, scales and low-rank input, and little more."""
     for op, gop, back in ((sq.SQ_OP_LINEAR_FWD_W8A8, sq.SQ_OP_GROUPED_FWD_W8A8, False),
