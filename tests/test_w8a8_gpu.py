@@ -513,3 +513,57 @@ def test_first_call_inside_a_capture():
     """The library's first call of a process may be a captured one."""
     p = subprocess.run([sys.executable, "-c", FIRST, ROOT], capture_output=True, text=True, timeout=600)
     assert p.returncode == 0 and p.stdout.strip() == "ok", p.stderr
+
+
+@pytest.mark.parametrize("op", ["fwd", "bwd"])
+def test_expert_changes_between_row_groups(op):
+    """More row groups than clusters: a cluster's next group is often of another expert, of one a few
+    experts on, or of the same one; a last group of an expert holds 1 to 8 rows."""
+    rng = np.random.default_rng(31)
+    N, K, E = 640, 1024, 160
+    counts = rng.integers(0, 90, E) * (rng.random(E) < 0.7)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    M = int(off[-1])
+    assert sum((c + 7) // 8 for c in counts) > 2 * 148
+    Q, sw, up, down = ref.layer(rng, N, K, E=E)
+    x = rows(rng, M, N if op == "bwd" else K)
+    y = call(op, weight(Q, sw, up, down), dev(x, torch.bfloat16), dev(off)).cpu().numpy()
+    f = ref.backward if op == "bwd" else ref.forward
+    for e in range(E):
+        a, b = off[e], off[e + 1]
+        if a < b:
+            ref.check(y[a:b], *f(x[a:b], Q[e], sw[e], up[e], down[e]), False)
+
+
+def test_captured_grouped_calls_follow_the_offsets():
+    """Two captured graphs that share a workspace, replayed in turn with offsets that change in between:
+    what a replay computes depends on the values it finds, not on those of the capture."""
+    rng = np.random.default_rng(32)
+    M, N, K, E = 333, 256, 512, 6
+    Q, sw, up, down = ref.layer(rng, N, K, E=E)
+    w = weight(Q, sw, up, down)
+    x, dy = rows(rng, M, K), rows(rng, M, N)
+    xd, dyd = dev(x, torch.bfloat16), dev(dy, torch.bfloat16)
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    n = max(sq.sq_grouped_workspace_bytes(o, E, M, N, K)
+            for o in (sq.SQ_OP_GROUPED_FWD_W8A8, sq.SQ_OP_GROUPED_BWD_DX_W8A8))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    sq.grouped_fwd_w8a8(w, xd, offsets, ws=ws)
+    sq.grouped_bwd_dx_w8a8(w, dyd, offsets, ws=ws)
+    torch.cuda.synchronize()
+    gf, gb = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gf):
+        y = sq.grouped_fwd_w8a8(w, xd, offsets, ws=ws)
+    with torch.cuda.graph(gb):
+        dx = sq.grouped_bwd_dx_w8a8(w, dyd, offsets, ws=ws)
+    for off in ([0, 333, 333, 333, 333, 333, 333], [3, 3, 20, 170, 171, 300, 301], [0, 0, 0, 0, 0, 0, 1]):
+        offsets.copy_(torch.tensor(off, dtype=torch.int32))
+        gf.replay()
+        gb.replay()
+        torch.cuda.synchronize()
+        for got, f, v in ((y.cpu().numpy(), ref.forward, x), (dx.cpu().numpy(), ref.backward, dy)):
+            assert (got[:off[0]] == 0).all() and (got[off[-1]:] == 0).all()
+            for e in range(E):
+                a, b = off[e], off[e + 1]
+                if a < b:
+                    ref.check(got[a:b], *f(v[a:b], Q[e], sw[e], up[e], down[e]), False)
