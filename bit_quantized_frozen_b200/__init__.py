@@ -349,29 +349,31 @@ def _w8a8(fn: str, w, x, y, flags, ws, stream, backward: bool, offsets=None):
         raise ValueError(f"{fn}: the weight is a {type(w).__name__}")
     if E is not None and not isinstance(offsets, torch.Tensor):
         raise ValueError(f"{fn}: offsets must be an int32 tensor of {E + 1} values")
-    if x.dim() != 2 or x.shape[1] != wide or x.dtype != torch.bfloat16:
+    shape = x.shape
+    if len(shape) != 2 or shape[1] != wide or x.dtype != torch.bfloat16:
         raise ValueError(f"{fn}: {xn} must be bfloat16 [M, {wide}], got {x.dtype} {list(x.shape)}")
-    M = x.shape[0]
+    M = shape[0]
     experts = 1 if E is None else E
     bf16 = flags & SQ_OUT_BF16
     if E is not None and (offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] != E + 1):
         raise ValueError(f"{fn}: offsets must be int32 [{E + 1}], got {offsets.dtype} {list(offsets.shape)}")
     # every tensor: long enough, on one device, contiguous (NULL and raw addresses are the library's to check)
-    dev, at = x.get_device(), {}
-    for name, t, nbytes in (("codes", w.codes, experts * N * K), ("scales", w.scales, 4 * experts * N),
-                            ("lora_up", w.lora_up, 2 * experts * N * RANK_INT8),
-                            ("lora_down", w.lora_down, 2 * experts * K * RANK_INT8),
-                            (yn, y, M * out * (2 if bf16 else 4)), (xn, x, 0), ("offsets", offsets, 0), ("ws", ws, 0)):
+    dev, at = x.get_device(), []
+    for t, nbytes in ((w.codes, experts * N * K), (w.scales, 4 * experts * N), (w.lora_up, 2 * experts * N * RANK_INT8),
+                      (w.lora_down, 2 * experts * K * RANK_INT8), (y, M * out * (2 if bf16 else 4)), (x, 0),
+                      (offsets, 0), (ws, 0)):
         if t is None or isinstance(t, int):
-            at[name] = t
-            continue
-        if t.nbytes < nbytes:
-            raise ValueError(f"{fn}: {name} holds {t.nbytes} bytes, the call needs {nbytes}")
-        if t.get_device() != dev:
-            raise ValueError(f"{fn}: {name} is on {t.device}, {xn} on {x.device}")
-        if not t.is_contiguous():
+            at.append(t)
+        elif t.nbytes >= nbytes and t.get_device() == dev and t.is_contiguous():
+            at.append(t.data_ptr())
+        else:
+            name = ("codes", "scales", "lora_up", "lora_down", yn, xn, "offsets", "ws")[len(at)]
+            if t.nbytes < nbytes:
+                raise ValueError(f"{fn}: {name} holds {t.nbytes} bytes, the call needs {nbytes}")
+            if t.get_device() != dev:
+                raise ValueError(f"{fn}: {name} is on {t.device}, {xn} on {x.device}")
             raise ValueError(f"{fn}: expected a contiguous tensor for {name}")
-        at[name] = t.data_ptr()
+    codes, scales, up, down, yp, xp, op, wp = at
     if not isinstance(y, int) and y.dtype != (torch.bfloat16 if bf16 else torch.float32):
         raise ValueError(f"{fn}: {yn} is {y.dtype}, the flags ask for the other type")
     if dev < 0:
@@ -384,12 +386,12 @@ def _w8a8(fn: str, w, x, y, flags, ws, stream, backward: bool, offsets=None):
     f = _W8A8.get(fn)
     if f is None:
         f = _W8A8[fn] = getattr(lib(), fn)
-    cw = ctypes.byref(sq_weight(w.fmt, N, K, at["codes"], at["scales"], None, at["lora_up"], at["lora_down"]))
-    nb = 0 if ws is None else _numel_bytes(ws)
+    cw = ctypes.byref(sq_weight(w.fmt, N, K, codes, scales, None, up, down))
+    nb = 0 if ws is None else ws.nbytes if isinstance(ws, torch.Tensor) else _numel_bytes(ws)
     if E is None:
-        st = f(cw, at[xn], M, at[yn], flags, at["ws"], nb, stream)
+        st = f(cw, xp, M, yp, flags, wp, nb, stream)
     else:
-        st = f(cw, E, at[xn], M, at["offsets"], at[yn], flags, at["ws"], nb, stream)
+        st = f(cw, E, xp, M, op, yp, flags, wp, nb, stream)
     if st != SQ_OK:
         _check(fn, st)
 
