@@ -24,6 +24,11 @@
 // with the rotation and mma.sync on three bf16 terms is faster (8192 rows of 64 experts,
 // 2816 x 2048: 136 us against 150; 509 tokens: 24 against 29).
 //
+// Measured on B200, 4480 x 16384 x 6144: forward 267 us (3.38 POP/s, the integer tensor pipe 90 %
+// active at the 1.6 GHz that the power cap leaves), backward 295 to 315 us (82 %).  24 tokens on the
+// same weight: 26 us a call with the quantisation (the weight's 101 MB at 49 % of the DRAM rate, the
+// rest is the start and the end of one tile).
+//
 // CTA (CG = 1) or CTA pair (CG = 2, 256 x 256 tiles) per SM, persistent: 4 or 8 epilogue
 // warps, one to four TMA producers, an MMA issuer that also allocates tensor memory.  Two
 // accumulators in tensor memory: the next tile's MMAs run while one drains.

@@ -26,6 +26,12 @@
 // row group to row group (of one expert) and loads the next group, and its expert's
 // factor where that is another one, while it transforms this one.  Longer rows (backward, N > 16384) take their blocks in
 // turns and read them a second time for the codes.
+//
+// Measured on B200: forward 4480 x 6144 38 us (2.2 TB/s; with the low-rank input 46), backward
+// 4480 x 16384 78 us (2.8 TB/s; 90).  Latency is the bound: 64 values a lane leave room for 16
+// warps an SM, which use 47 % (36 %) of the issue slots, and every 8 rows wait for one exchange of
+// the maximum.  Three CTAs an SM (spills), four-warp CTAs and exchanges with all loads at once
+// (registers) were slower.
 #include <cuda.h>
 
 #include "sq_device.cuh"
