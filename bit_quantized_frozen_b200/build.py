@@ -14,7 +14,7 @@ LIB = os.path.join(PKG, "libsq.so")
 # tests its index against its buffer, skips it when outside and reports SQ_ERR_INDEX
 LIB_DEBUG = os.path.join(PKG, "libsq_debug.so")
 SOURCES = ["sq_api.cu", "sq_quant.cu", "sq_gemm.cu", "sq_svd.cu", "sq_w8a8_quant.cu", "sq_w8a8.cu"]
-HEADERS = ["sq_device.cuh", "sq_ptx.cuh", "sq_kernels.h", "sq_w8a8.cuh"]
+HEADERS = ["sq_device.cuh", "sq_ptx.cuh", "sq_kernels.h", "sq_w8a8.cuh", "sq_w8a8_stage.h"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -48,10 +48,11 @@
 #include "sq_kernels.h"
 #include "sq_ptx.cuh"
 #include "sq_w8a8.cuh"
+#include "sq_w8a8_stage.h"
 
 namespace sq {
 
-constexpr int kChunk = 128;                       // summed values (bytes) of a shared-memory row
+constexpr int kChunk = kI8Chunk;
 
 template <int NT, int CG, bool BWD>
 struct I8Cfg {
@@ -64,9 +65,8 @@ struct I8Cfg {
     // epilogue warps: one per 32 lanes and, in wide tiles, per half of the columns
     static constexpr int kColHalves = NT >= 64 ? 2 : 1;
     static constexpr int kEpiThreads = 128 * kColHalves;
-    // producer warps, each with its own stages: one copy takes a thread about 60 ns to issue, so
-    // tiles that need little time per stage share the work out
-    static constexpr int kProducers = CG == 2 ? 1 : NT <= 32 ? 4 : 2;
+    // producer warps, each with its own stages
+    static constexpr int kProducers = CG == 2 ? 1 : i8_producers(NT);
     static constexpr int kThreads = kEpiThreads + 32 * kProducers + 32;   // + MMA issuer
     // bytes from one column's low-rank values to the next in shared memory (bf16 backward, fp32
     // forward): the four columns that a warp reads at once lie in different banks
@@ -75,8 +75,8 @@ struct I8Cfg {
     // stages: fixed for a CTA pair; with CG = 1 as many as fit with the A rows that the CTA's
     // tiles have (the MMAs read 128 rows all the same: behind the tile's own lie other bytes of
     // the CTA's shared memory, and their lanes of the accumulator are not looked at)
-    static constexpr int kRing = (BWD ? 192 : NT == 256 ? 160 : NT == 128 ? 176 : 184) * 1024;
-    static constexpr int kStages = CG == 1 ? 24 : kRing / kStageBytes;
+    static constexpr int kRing = CG == 1 ? i8_ring_bytes(NT) : (BWD ? 192 : 160) * 1024;
+    static constexpr int kStages = CG == 1 ? kI8MaxStages : kRing / kStageBytes;
     static constexpr int kPatchOff = kRing;
     static constexpr int kLowOff = kPatchOff + (kEpiThreads / 32) * kPatchBytes;
     static constexpr int kScaleOff = kLowOff + NT * kLowPitch;       // column scales [NT] fp32 (forward)
@@ -103,40 +103,6 @@ struct I8Args {
     int out_bf16;
     int tok;                  // tokens of a tile (forward; at most NT)
     int box;                  // weight rows of a tmA box
-};
-
-// CG = 1: a CTA's share of all (token tile, channel) pairs, in tiles of up to 128 channels
-struct I8ChannelWalk {
-    int64_t pos, end;         // in groups of 4 channels, token tile after token tile
-    int per_tile;             // N / 4
-    int tile, n0, channels;
-
-    __device__ __forceinline__ I8ChannelWalk(int tiles, int64_t N, int cta, int ctas)
-        : per_tile((int)(N / 4)), tile(0), n0(0), channels(0)
-    {
-        const int64_t all = (int64_t)tiles * per_tile;
-        pos = all * cta / ctas;
-        end = all * (cta + 1) / ctas;
-    }
-    // channels of the largest tile, at most
-    __device__ __forceinline__ int largest() const
-    {
-        return (int)min((int64_t)128, 4 * (end - pos));
-    }
-    __device__ __forceinline__ bool next()
-    {
-        if (pos >= end)
-            return false;
-        tile = (int)(pos / per_tile);
-        const int first = (int)(pos - (int64_t)tile * per_tile);
-        const int left = (int)min(end - pos, (int64_t)(per_tile - first));
-        const int tiles_left = (left + 31) / 32;
-        const int now = (left + tiles_left - 1) / tiles_left;      // of equal size
-        n0 = 4 * first;
-        channels = 4 * now;
-        pos += now;
-        return true;
-    }
 };
 
 // what a unit does next: tile t, its lanes (channels from n0 on; backward: tokens)
@@ -281,24 +247,16 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
     const I8ChannelWalk share(CG == 1 ? tiles : 0, args.N, unit, units);
     using Units = I8Units<CG, BWD>;
     auto all_work = [&]() { return Units(plan, share, tiles, unit, units, args.N); };
-    const int a_bytes = CG == 1 ? min(128, max(args.box < 128 ? args.box : 16, (share.largest() + 7) / 8 * 8)) * kChunk
-                                : Cfg::kABytes;
+    // stages of equal chunks; CG = 1: as the CTA's share needs them
+    I8Stages lay = {Cfg::kABytes, Cfg::kStageBytes, 1, Cfg::kStageBytes, Cfg::kStages};
+    if (CG == 1)
+        lay = i8_stages(i8_stage_rows(share.largest(), args.box), Cfg::kBBytes, Cfg::kRing, Cfg::kProducers);
+    const int a_bytes = lay.a_bytes, chunk_bytes = lay.chunk_bytes, per = lay.per, stage_bytes = lay.stage_bytes;
+    const int stages = lay.stages;
     // CG = 1: tiles of at most 64 channels take the 64-row MMA, which reads half as much of A and puts
     // 16 rows into each quarter of the lanes
     const bool m64 = CG == 1 && a_bytes <= 64 * kChunk;
-    const int chunk_bytes = a_bytes + Cfg::kBBytes;
-    // chunks per stage: a stage costs the MMA issuer about 85 ns (wait, commit) beside 20 ns for each
-    // of a chunk's four narrow MMAs, so few tokens take several, as long as every producer has a
-    // stage to fill (16 tokens, N = K = 6144: one, two, four chunks 24.5, 17.4, 16.4 us a call).
-    // Chunks behind the end of the summed axis read as 0.
-    int per = 1;
-    if (CG == 1)
-        while (per < 4 && 2 * per * chunk_bytes * max(4, Cfg::kProducers) <= Cfg::kRing)
-            per *= 2;
-    const int stage_bytes = per * chunk_bytes;
     const int steps = (int)(((BWD ? args.N : args.K) / kChunk + per - 1) / per);      // stages of a tile
-    const int stages = CG == 1 ? min(Cfg::kStages, Cfg::kRing / stage_bytes) / Cfg::kProducers * Cfg::kProducers
-                               : Cfg::kStages;
     // columns of the accumulator a tile uses (forward: its tokens, in whole boxes of both CTAs)
     auto columns = [&](const I8Tile &t) {
         return BWD ? NT : (t.rows + CG * Cfg::kBox - 1) / (CG * Cfg::kBox) * (CG * Cfg::kBox);
@@ -328,16 +286,8 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
         auto aim_at = [&](const I8Work &w) {
             Aim m;
             const int cols = columns(w.t);
-            // rows and the bytes of their copies: one box where it is not much more, else boxes of
-            // 64 or 16 rows that may overlap (the same bytes to the same place)
-            m.rows = 128;
-            int copied = 128;
-            if (CG == 1) {
-                m.rows = max(16, (w.lanes + 7) / 8 * 8);
-                if (m.rows <= args.box && m.rows + 16 >= args.box)
-                    m.rows = args.box;
-                copied = m.rows == args.box ? args.box : m.rows > 64 ? 128 : (m.rows + 15) / 16 * 16;
-            }
+            m.rows = CG == 1 ? i8_weight_rows(w.lanes, args.box) : 128;
+            const int copied = CG == 1 ? i8_copied_rows(m.rows, args.box) : 128;
             m.wrow = w.t.e * (int)args.N + (BWD ? 0 : w.n0 + (int)rank * 128);
             m.mine = BWD ? 128 : cols / CG;
             m.xrow = w.t.row0 + (int)rank * m.mine;
@@ -358,16 +308,12 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                 const int x = (step * per + u) * kChunk;
                 if (BWD) {
                     load(&tmB, sA + a_bytes, wt * NT + (int)rank * Cfg::kColsPerCta, m.wrow + x, fb);
-                } else if (CG == 2 || m.rows == args.box) {
+                } else if (CG == 2) {
                     load(&tmA, sA, x, m.wrow, fb);
-                } else if (m.rows > 64) {         // two boxes, the second one back from the end
-                    load(&tmA64, sA, x, m.wrow, fb);
-                    load(&tmA64, sA + (m.rows - 64) * kChunk, x, m.wrow + m.rows - 64, fb);
                 } else {
-                    for (int r = 0; r < m.rows; r += 16) {
-                        const int at = min(r, m.rows - 16);
-                        load(&tmA16, sA + at * kChunk, x, m.wrow + at, fb);
-                    }
+                    i8_weight_copies(m.rows, args.box, [&](int kind, int at) {
+                        load(kind == 0 ? &tmA : kind == 1 ? &tmA64 : &tmA16, sA + at * kChunk, x, m.wrow + at, fb);
+                    });
                 }
             }
         };
@@ -880,20 +826,6 @@ int pair_tokens(int E, int64_t M, int64_t N, int pairs)
     return best;
 }
 
-// CG = 1: rows of the box that takes a CTA's whole tile in one copy.  Dense: the shares are known
-// and nearly equal; experts: 128.  `only`: every tile is taken so.
-int whole_box(const I8GemmLaunch &g, int ctas, int nt, bool *only)
-{
-    *only = false;
-    if (g.E > 0)
-        return 128;
-    const int64_t all = (g.M + nt - 1) / nt * (g.N / 4), share = (all + ctas - 1) / ctas;
-    const int64_t tiles = (share + 31) / 32, groups = (share + tiles - 1) / tiles;
-    const int64_t rows = (4 * groups + 7) / 8 * 8;
-    *only = g.M <= nt && (all / ctas + 31) / 32 == tiles;            // (sizes then differ by 4 channels)
-    return rows < 16 ? 16 : (int)rows;
-}
-
 template <int NT, int CG, bool BWD>
 cudaError_t launch_shape(const I8GemmLaunch &g, int sms, cudaStream_t stream)
 {
@@ -930,7 +862,7 @@ cudaError_t launch_shape(const I8GemmLaunch &g, int sms, cudaStream_t stream)
     // and by kBox tokens
     const int tok = BWD || CG == 1 ? NT : pair_tokens(g.E, g.M, g.N, resident_units[dev]);
     bool one_box = true;
-    const int box = CG == 1 ? whole_box(g, resident_units[dev], NT, &one_box) : 128;
+    const int box = CG == 1 ? i8_whole_box(g.E, g.M, g.N, resident_units[dev], NT, &one_box) : 128;
     // 128-byte wide boxes: weight codes [E N, K], row codes [M, K] (backward [M, N]) by whole tiles
     // and by kBox tokens; maps that this call cannot use are not encoded
     CUtensorMap tmW, tmX, tmBox, tmW64, tmW16;
