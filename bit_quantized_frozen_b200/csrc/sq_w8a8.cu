@@ -633,8 +633,6 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(I8Cfg<NT, CG, BWD>:
                                                b);
 #pragma unroll
                             for (int p = kLowParts - 1; p >= 0; --p) {
-                                if (p == 2 && ybf)     // (a bf16 result takes two terms: 2^-16 of u)
-                                    continue;
                                 mma_16816(low[0], ufrag[h][p], b[0], b[1]);
                                 mma_16816(low[1], ufrag[h][p], b[2], b[3]);
                             }

@@ -51,7 +51,7 @@ SQ_API sq_status sq_linear_fwd_w8a8(const sq_weight *w, const uint16_t *x, int64
  *   r[n] = RN(dy[m, n] s_w[n]),  s_g and q_g from r as in sq_linear_fwd_w8a8,
  *   dx[m, :] = H256( RN(float(sum_n q_g[m, n] Q[n, :]) s_g) ) + u[m] . lora_down[k],
  *   u[m] = dy[m] lora_up (fp32 sums; it enters the last product as three bf16 terms:
- *   24 bits, below 2^-110 with an absolute error of 2^-134; for a bf16 dx as two, 2^-16 of u);
+ *   24 bits, below 2^-110 with an absolute error of 2^-134);
  * the codes are read as they lie, no transposed or reconstructed copy of W is
  * made.  dy [M, N] bf16, dx [M, K] fp32 (bf16 with SQ_OUT_BF16), device.
  * N <= 131072 (the 32-bit sums stay exact).  NaN, infinities, flags and status
