@@ -357,19 +357,26 @@ def _w8a8(fn: str, w, x, y, flags, ws, stream, backward: bool, offsets=None):
     bf16 = flags & SQ_OUT_BF16
     if E is not None and (offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] != E + 1):
         raise ValueError(f"{fn}: offsets must be int32 [{E + 1}], got {offsets.dtype} {list(offsets.shape)}")
-    # every tensor: long enough, on one device, contiguous (NULL and raw addresses are the library's to check)
-    dev, at = x.get_device(), []
-    for t, nbytes in ((w.codes, experts * N * K), (w.scales, 4 * experts * N), (w.lora_up, 2 * experts * N * RANK_INT8),
-                      (w.lora_down, 2 * experts * K * RANK_INT8), (y, M * out * (2 if bf16 else 4)), (x, 0),
-                      (offsets, 0), (ws, 0)):
+    # every tensor: long enough, on one device, contiguous, the weight's of its types and shapes (NULL and
+    # raw addresses are the library's to check)
+    dev, at, lead = x.get_device(), [], () if E is None else (E,)
+    for t, nbytes, dtype, want in ((w.codes, experts * N * K, torch.int8, (*lead, N, K)),
+                                   (w.scales, 4 * experts * N, torch.float32, (*lead, N)),
+                                   (w.lora_up, 2 * experts * N * RANK_INT8, torch.bfloat16, (*lead, N, RANK_INT8)),
+                                   (w.lora_down, 2 * experts * K * RANK_INT8, torch.bfloat16, (*lead, K, RANK_INT8)),
+                                   (y, M * out * (2 if bf16 else 4), None, None), (x, 0, None, None),
+                                   (offsets, 0, None, None), (ws, 0, None, None)):
         if t is None or isinstance(t, int):
             at.append(t)
-        elif t.nbytes >= nbytes and t.get_device() == dev and t.is_contiguous():
+        elif (t.nbytes >= nbytes and t.get_device() == dev and t.is_contiguous()
+              and (dtype is None or (t.dtype is dtype and t.shape == want))):
             at.append(t.data_ptr())
         else:
             name = ("codes", "scales", "lora_up", "lora_down", yn, xn, "offsets", "ws")[len(at)]
             if t.nbytes < nbytes:
                 raise ValueError(f"{fn}: {name} holds {t.nbytes} bytes, the call needs {nbytes}")
+            if dtype is not None and (t.dtype is not dtype or t.shape != want):
+                raise ValueError(f"{fn}: {name} must be {dtype} {list(want)}, got {t.dtype} {list(t.shape)}")
             if t.get_device() != dev:
                 raise ValueError(f"{fn}: {name} is on {t.device}, {xn} on {x.device}")
             raise ValueError(f"{fn}: expected a contiguous tensor for {name}")
