@@ -381,7 +381,7 @@ def _w8a8(fn: str, w, x, y, flags, ws, stream, backward: bool, offsets=None):
                 raise ValueError(f"{fn}: {name} is on {t.device}, {xn} on {x.device}")
             raise ValueError(f"{fn}: expected a contiguous tensor for {name}")
     codes, scales, up, down, yp, xp, op, wp = at
-    if not isinstance(y, int) and y.dtype != (torch.bfloat16 if bf16 else torch.float32):
+    if isinstance(y, torch.Tensor) and y.dtype != (torch.bfloat16 if bf16 else torch.float32):
         raise ValueError(f"{fn}: {yn} is {y.dtype}, the flags ask for the other type")
     if dev < 0:
         raise ValueError(f"{fn}: expected a CUDA tensor")

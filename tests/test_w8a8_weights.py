@@ -48,3 +48,24 @@ def test_types_and_shapes(E):
             for bad in tensors:
                 with pytest.raises(ValueError, match=f"{name} must be torch"):
                     call(weight(E, **{name: bad}))
+
+
+def test_a_missing_output_is_the_librarys_to_refuse():
+    """y = None (NULL) passes the binding's checks of types, as it does in the other entry points."""
+    x, dy, off = t((M, K)), t((M, N)), t(4, torch.int32)
+    for call in (lambda: sq.sq_linear_fwd_w8a8(weight(None), x, None), lambda: sq.sq_linear_bwd_dx_w8a8(weight(None), dy, None),
+                 lambda: sq.sq_grouped_fwd_w8a8(weight(3), x, off, None),
+                 lambda: sq.sq_grouped_bwd_dx_w8a8(weight(3), dy, off, None)):
+        with pytest.raises(ValueError, match="expected a CUDA tensor"):
+            call()
+
+
+@pytest.mark.gpu
+def test_a_missing_output_on_the_device():
+    x = t((M, K)).cuda()
+    w = weight(None)
+    for name in ("codes", "scales", "lora_up", "lora_down"):
+        setattr(w, name, getattr(w, name).cuda())
+    with pytest.raises(sq.SqError) as e:
+        sq.sq_linear_fwd_w8a8(w, x, None, ws=torch.empty(1 << 20, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == 1
