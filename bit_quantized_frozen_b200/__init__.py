@@ -587,8 +587,9 @@ def build_int8_grouped(R: torch.Tensor, lora_up=None, lora_down=None, stream=Non
     """int8 per-row weights of E experts from their residuals R [E, N, K] fp32; lora_up [E, N, 16] /
     lora_down [E, K, 16] or None."""
     E, N, K = R.shape
-    codes = torch.empty((E, N, K), dtype=torch.int8, device=R.device)
-    scales = torch.empty((E, N), dtype=torch.float32, device=R.device)
+    with _allocating_on(stream):
+        codes = torch.empty((E, N, K), dtype=torch.int8, device=R.device)
+        scales = torch.empty((E, N), dtype=torch.float32, device=R.device)
     for e in range(E):
         sq_build_int8(R[e], codes[e], scales[e], None, stream=stream)
     return GroupedWeight(E, N, K, codes, scales, lora_up, lora_down)
