@@ -15,6 +15,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import math
 import os
 from dataclasses import dataclass
 
@@ -337,6 +338,7 @@ def sq_linear_bwd_dx(w: "Weight", dy, dx, ws, stream=None):
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _W8A8 = {}                               # entry point by name, looked up once
+_I8, _F32, _BF16 = torch.int8, torch.float32, torch.bfloat16
 
 
 def _w8a8(fn: str, w, x, y, flags, ws, stream, backward: bool, offsets=None):
@@ -350,38 +352,53 @@ def _w8a8(fn: str, w, x, y, flags, ws, stream, backward: bool, offsets=None):
     if E is not None and not isinstance(offsets, torch.Tensor):
         raise ValueError(f"{fn}: offsets must be an int32 tensor of {E + 1} values")
     shape = x.shape
-    if len(shape) != 2 or shape[1] != wide or x.dtype != torch.bfloat16:
+    if len(shape) != 2 or shape[1] != wide or x.dtype is not _BF16:
         raise ValueError(f"{fn}: {xn} must be bfloat16 [M, {wide}], got {x.dtype} {list(x.shape)}")
     M = shape[0]
-    experts = 1 if E is None else E
     bf16 = flags & SQ_OUT_BF16
     if E is not None and (offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] != E + 1):
         raise ValueError(f"{fn}: offsets must be int32 [{E + 1}], got {offsets.dtype} {list(offsets.shape)}")
-    # every tensor: long enough, on one device, contiguous, the weight's of its types and shapes (NULL and
-    # raw addresses are the library's to check)
-    dev, at, lead = x.get_device(), [], () if E is None else (E,)
-    for t, nbytes, dtype, want in ((w.codes, experts * N * K, torch.int8, (*lead, N, K)),
-                                   (w.scales, 4 * experts * N, torch.float32, (*lead, N)),
-                                   (w.lora_up, 2 * experts * N * RANK_INT8, torch.bfloat16, (*lead, N, RANK_INT8)),
-                                   (w.lora_down, 2 * experts * K * RANK_INT8, torch.bfloat16, (*lead, K, RANK_INT8)),
-                                   (y, M * out * (2 if bf16 else 4), None, None), (x, 0, None, None),
-                                   (offsets, 0, None, None), (ws, 0, None, None)):
-        if t is None or isinstance(t, int):
-            at.append(t)
-        elif (t.nbytes >= nbytes and t.get_device() == dev and t.is_contiguous()
-              and (dtype is None or (t.dtype is dtype and t.shape == want))):
-            at.append(t.data_ptr())
-        else:
-            name = ("codes", "scales", "lora_up", "lora_down", yn, xn, "offsets", "ws")[len(at)]
+    # every tensor: on one device, contiguous, the weight's of its types and shapes, y long enough (NULL and
+    # raw addresses are the library's to check).  One expression for the usual call; the loop names what is wrong.
+    dev, lead, ybytes = x.get_device(), () if E is None else (E,), M * out * (2 if bf16 else 4)
+    c, s, u, d = w.codes, w.scales, w.lora_up, w.lora_down
+    try:
+        usual = (c.dtype is _I8 and c.shape == (*lead, N, K) and c.get_device() == dev and c.is_contiguous()
+                 and s.dtype is _F32 and s.shape == (*lead, N) and s.get_device() == dev and s.is_contiguous()
+                 and (u is None and d is None
+                      or u.dtype is _BF16 and u.shape == (*lead, N, RANK_INT8) and u.get_device() == dev
+                      and u.is_contiguous() and d.dtype is _BF16 and d.shape == (*lead, K, RANK_INT8)
+                      and d.get_device() == dev and d.is_contiguous())
+                 and x.is_contiguous() and y.nbytes >= ybytes and y.get_device() == dev and y.is_contiguous()
+                 and ws.get_device() == dev and ws.is_contiguous()
+                 and (E is None or offsets.get_device() == dev and offsets.is_contiguous()))
+    except AttributeError:
+        usual = False
+    if usual:
+        codes, scales, yp, xp, wp = c.data_ptr(), s.data_ptr(), y.data_ptr(), x.data_ptr(), ws.data_ptr()
+        up, down = (None, None) if u is None else (u.data_ptr(), d.data_ptr())
+        op = None if E is None else offsets.data_ptr()
+    else:
+        at = []
+        for t, name, dtype, want in ((c, "codes", _I8, (*lead, N, K)), (s, "scales", _F32, (*lead, N)),
+                                     (u, "lora_up", _BF16, (*lead, N, RANK_INT8)),
+                                     (d, "lora_down", _BF16, (*lead, K, RANK_INT8)), (y, yn, None, ybytes),
+                                     (x, xn, None, 0), (offsets, "offsets", None, 0), (ws, "ws", None, 0)):
+            if t is None or isinstance(t, int):
+                at.append(t)
+                continue
+            nbytes = want if dtype is None else math.prod(want) * dtype.itemsize
             if t.nbytes < nbytes:
                 raise ValueError(f"{fn}: {name} holds {t.nbytes} bytes, the call needs {nbytes}")
             if dtype is not None and (t.dtype is not dtype or t.shape != want):
                 raise ValueError(f"{fn}: {name} must be {dtype} {list(want)}, got {t.dtype} {list(t.shape)}")
             if t.get_device() != dev:
                 raise ValueError(f"{fn}: {name} is on {t.device}, {xn} on {x.device}")
-            raise ValueError(f"{fn}: expected a contiguous tensor for {name}")
-    codes, scales, up, down, yp, xp, op, wp = at
-    if isinstance(y, torch.Tensor) and y.dtype != (torch.bfloat16 if bf16 else torch.float32):
+            if not t.is_contiguous():
+                raise ValueError(f"{fn}: expected a contiguous tensor for {name}")
+            at.append(t.data_ptr())
+        codes, scales, up, down, yp, xp, op, wp = at
+    if isinstance(y, torch.Tensor) and y.dtype is not (_BF16 if bf16 else _F32):
         raise ValueError(f"{fn}: {yn} is {y.dtype}, the flags ask for the other type")
     if dev < 0:
         raise ValueError(f"{fn}: expected a CUDA tensor")
