@@ -20,14 +20,16 @@
 // The low-rank product (rank 16) is part of the epilogue.  Forward it is 8 packed fp32 FMAs a
 // value, with the lane's factors in registers and the tokens' in shared memory; mma.sync on bf16
 // terms would hold up the integer MMAs (4480 tokens, N = 16384, K = 6144: 315 us a call against
-// 360; 6001 rows of 8 experts, 6144 x 4096: 166 against 200).  Backward the FMA units are busy
-// with the rotation and mma.sync on three bf16 terms is faster (8192 rows of 64 experts,
-// 2816 x 2048: 136 us against 150; 509 tokens: 24 against 29).
+// 360; 6001 rows of 8 experts, 6144 x 4096: 166 against 200, short runs both).  Backward the FMA
+// units are busy with the rotation and mma.sync on three bf16 terms is faster (8192 rows of 64
+// experts, 2816 x 2048: 136 us against 150; 509 tokens: 24 against 29).  Two terms, 16 bits, would
+// take 150.1 us of such a call in a long run instead of 151.1.
 //
-// Measured on B200, 4480 x 16384 x 6144: forward 267 us (3.38 POP/s, the integer tensor pipe 90 %
-// active at the 1.6 GHz that the power cap leaves), backward 295 to 315 us (82 %).  24 tokens on the
-// same weight: 26 us a call with the quantisation (the weight's 101 MB at 49 % of the DRAM rate, the
-// rest is the start and the end of one tile).
+// Measured on B200, 4480 x 16384 x 6144, in a short run: forward 267 us (3.38 POP/s, the integer
+// tensor pipe 90 % active at 1.6 GHz), backward 295 to 315 us (82 %).  With the quantisation a call
+// takes 308 and 378 us in a short run, 365 and 450 us after a second of calls, when the power cap
+// has taken the clocks further down.  24 tokens on the same weight: 26 us a call (the weight's
+// 101 MB at 49 % of the DRAM rate in the product, the rest is the start and the end of one tile).
 //
 // CTA (CG = 1) or CTA pair (CG = 2, 256 x 256 tiles) per SM, persistent: 4 or 8 epilogue
 // warps, one to four TMA producers, an MMA issuer that also allocates tensor memory.  Two
@@ -35,8 +37,9 @@
 // Weight tiles of the first stages are fetched before the kernel waits for the
 // quantisation kernel in front of it.
 //
-// A tile's MMAs and loads cover only the boxes of tokens that it has (the instruction's
-// column count is set per tile), so that an expert with few rows costs few.
+// Forward, a tile's MMAs and loads cover only the boxes of tokens that it has (the instruction's
+// column count is set per tile), so that an expert with few rows costs few.  Backward the tokens
+// are the lanes: a tile is loaded, multiplied and rotated for 256 tokens, however many it has.
 //
 // Few tokens (CG = 1) are bound by the weight's bytes: each CTA takes an equal share of
 // all channels, to four of them, as tiles of up to 128, so that every SM reads the same
@@ -785,8 +788,15 @@ struct Shape {
     int nt, cg;
 };
 
-// Token tile by the rows of one product (experts: their mean): up to 128 the narrowest tile of
-// one CTA that takes them, above 256 x 256 tiles of a CTA pair.
+// Token tile by the rows of one product (experts: the mean over all, since the host does not see
+// the offsets): up to 128 the narrowest tile of one CTA that takes them, above 256 x 256 tiles of a
+// CTA pair.  The two sides of each border, us a call:
+//   rows                     16 | 17      32 | 33      64 | 65      128 | 129
+//   dense, 6144 x 6144       16.4 17.6    19.0 20.2    20.7 23.0    24.8 24.9
+//   dense, 2816 x 2048       11.8 12.3    12.5 13.5    13.8 15.1    16.6 13.1
+//   64 experts, 2816 x 2048  73.9 75.3    77.4 83.1    88.0 94.6    113  109
+// Rows that lie far from their mean pay for it: 2048 rows on one of 128 experts (2816 x 2048) take
+// 16-token tiles and 81 us, on the only one 38 us.
 Shape pick_shape(bool bwd, int E, int64_t M)
 {
     if (bwd)
@@ -856,8 +866,6 @@ cudaError_t launch_shape(const I8GemmLaunch &g, int sms, cudaStream_t stream)
         ctx_seen[dev] = ctx;
     }
     const int64_t Em = g.E > 0 ? g.E : 1;
-    // 128-byte wide boxes: weight codes [E N, K], row codes [M, K] (backward [M, N]) by whole tiles
-    // and by kBox tokens
     const int tok = BWD || CG == 1 ? NT : pair_tokens(g.E, g.M, g.N, resident_units[dev]);
     bool one_box = true;
     const int box = CG == 1 ? i8_whole_box(g.E, g.M, g.N, resident_units[dev], NT, &one_box) : 128;

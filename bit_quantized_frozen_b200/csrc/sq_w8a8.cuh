@@ -87,11 +87,6 @@ struct I8Plan {
     }
 };
 
-__device__ __forceinline__ uint32_t smem_addr(const void *p)
-{
-    return (uint32_t)__cvta_generic_to_shared(p);
-}
-
 // ---- tensor memory and tcgen05 of the integer product ---------------------------
 // D[tmem] (+)= A[smem] * B[smem]^T, signed 8-bit integers, 32-bit integer accumulation
 // (exact while |sum| < 2^31); CG = 1: this CTA, 2: the CTA pair
@@ -164,8 +159,8 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t 
                  ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
 }
 
-// c[16 x 8] += a[16 x 16] b[16 x 8], bf16 inputs, fp32 sums (one warp; the rows' low-rank input
-// only -- the large products run on tcgen05)
+// c[16 x 8] += a[16 x 16] b[16 x 8], bf16 inputs, fp32 sums (one warp; the rows' low-rank input and
+// the gradient's low-rank term -- the large products run on tcgen05)
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "

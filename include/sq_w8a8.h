@@ -35,8 +35,9 @@ extern "C" {
  * lora_up and lora_down are both NULL or both given.  Any M >= 1; few tokens run
  * on narrow tiles that read each weight byte once.  The codes, the scales and
  * the integer sums of a row are the same bits whatever M is and whichever rows
- * lie beside it; t is summed in an order fixed by M and K, so equal calls give
- * equal bits.
+ * lie beside it; t is summed in an order fixed by K, M, the number of experts of
+ * a grouped call and the device's number of SMs, so equal calls on equal devices
+ * give equal bits.
  * flags: SQ_OUT_BF16, SQ_CHECK_FINITE (a row whose rotation holds a NaN or an
  * infinity sets SQ_ERR_NONFINITE in the status word).
  * ws: sq_workspace_bytes(SQ_OP_LINEAR_FWD_W8A8, M, N, K) bytes.
