@@ -53,6 +53,18 @@ SQ_OP_LINEAR_BWD_DX_W8A8 = 12
 SQ_OP_GROUPED_FWD_W8A8 = 13
 SQ_OP_GROUPED_BWD_DX_W8A8 = 14
 SQ_ZERO_UNGROUPED = 0x20
+SQ_FMT_FP8_BLOCK = 5
+SQ_OP_LINEAR_FWD_FP8 = 15
+SQ_OP_LINEAR_BWD_DX_FP8 = 16
+SQ_OP_GATED_FWD_FP8 = 17
+SQ_OP_GATED_BWD_DX_FP8 = 18
+SQ_OP_GROUPED_FWD_FP8 = 19
+SQ_OP_GROUPED_BWD_DX_FP8 = 20
+SQ_OP_GROUPED_GATED_FWD_FP8 = 21
+SQ_OP_GROUPED_GATED_BWD_DX_FP8 = 22
+SQ_IN_BF16 = 0x40
+SQ_ACT_SILU = 0
+SQ_ACT_GELU_TANH = 1
 RANK = 32
 
 EXPORTED = [
@@ -66,6 +78,11 @@ EXPORTED = [
 EXPORTED_W8A8 = [
     "sq_linear_fwd_w8a8", "sq_linear_bwd_dx_w8a8", "sq_grouped_fwd_w8a8", "sq_grouped_bwd_dx_w8a8",
     "sq_grouped_workspace_bytes",
+]
+# include/sq_fp8.h: the products of 8-bit floating point with a scale for each block of 128
+EXPORTED_FP8 = [
+    "sq_build_fp8", "sq_linear_fwd_fp8", "sq_linear_bwd_dx_fp8", "sq_gated_fwd_fp8", "sq_gated_bwd_dx_fp8",
+    "sq_grouped_fwd_fp8", "sq_grouped_bwd_dx_fp8", "sq_grouped_gated_fwd_fp8", "sq_grouped_gated_bwd_dx_fp8",
 ]
 
 
@@ -93,6 +110,8 @@ class sq_weight(ctypes.Structure):
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
+_W = ctypes.POINTER(sq_weight)
+_TAIL = [ctypes.c_uint32, _P, ctypes.c_size_t, _P]      # flags, ws, ws_bytes, stream
 _SIGS = {
     "sq_status_str": ([ctypes.c_int], ctypes.c_char_p),
     "sq_abi_version": ([], ctypes.c_int),
@@ -123,6 +142,15 @@ _SIGS = {
     "sq_grouped_bwd_dx_w8a8": ([ctypes.POINTER(sq_weight), _I64, _P, _I64, _P, _P, ctypes.c_uint32, _P,
                                 ctypes.c_size_t, _P], ctypes.c_int),
     "sq_grouped_workspace_bytes": ([ctypes.c_int, _I64, _I64, _I64, _I64], ctypes.c_size_t),
+    "sq_build_fp8": ([_P, _I64, _I64, ctypes.c_uint32, _P, _P, _P], ctypes.c_int),
+    "sq_linear_fwd_fp8": ([_W, _P, _I64, _P, *_TAIL], ctypes.c_int),
+    "sq_linear_bwd_dx_fp8": ([_W, _P, _I64, _P, *_TAIL], ctypes.c_int),
+    "sq_gated_fwd_fp8": ([_W, _W, _P, _I64, ctypes.c_int32, _P, _P, _P, *_TAIL], ctypes.c_int),
+    "sq_gated_bwd_dx_fp8": ([_W, _W, _P, _P, _P, _I64, ctypes.c_int32, _P, *_TAIL], ctypes.c_int),
+    "sq_grouped_fwd_fp8": ([_W, _I64, _P, _I64, _P, _P, *_TAIL], ctypes.c_int),
+    "sq_grouped_bwd_dx_fp8": ([_W, _I64, _P, _I64, _P, _P, *_TAIL], ctypes.c_int),
+    "sq_grouped_gated_fwd_fp8": ([_W, _W, _I64, _P, _I64, _P, ctypes.c_int32, _P, _P, _P, *_TAIL], ctypes.c_int),
+    "sq_grouped_gated_bwd_dx_fp8": ([_W, _W, _I64, _P, _P, _P, _I64, _P, ctypes.c_int32, _P, *_TAIL], ctypes.c_int),
     "sq_check_device_status": ([_P, _P], ctypes.c_int),
     "sq_selftest_wait_timeout": ([_P, ctypes.c_uint32, _P], ctypes.c_int),
     "sq_set_gemm_events": ([_P, _P], ctypes.c_int),
@@ -440,6 +468,170 @@ def sq_grouped_workspace_bytes(op: int, E: int, M: int, N: int, K: int) -> int:
     return lib().sq_grouped_workspace_bytes(op, E, M, N, K)
 
 
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+_FP8 = {}                                # entry point by name, looked up once
+_FP8_ACTS = {"silu": SQ_ACT_SILU, "gelu": SQ_ACT_GELU_TANH}
+
+
+def _fp8_refuse(fn, weights, rows, outs, offsets, ws):
+    """Names what is wrong with the tensors of a block-scaled call (outs: (tensor, name, dtype, shape))."""
+    w = weights[0]
+    N, K, E = w.N, w.K, getattr(w, "E", None)
+    lead, dev = (() if E is None else (E,)), rows[0][0].get_device()
+    blocks = ((N + 127) // 128, (K + 127) // 128)
+    want = [(t, name, dtype, shape) for v in weights
+            for t, name, dtype, shape in ((v.codes, "codes", _E4M3, (*lead, N, K)), (v.scales, "scales", _E8M0, (*lead, *blocks)))]
+    want += rows + outs
+    if offsets is not None:
+        want.append((offsets, "offsets", torch.int32, (E + 1,)))
+    want.append((ws, "ws", None, None))
+    for t, name, dtype, shape in want:
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{fn}: {name} must be a tensor")
+        if dtype is not None and (t.dtype is not dtype or t.shape != shape):
+            raise ValueError(f"{fn}: {name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+        if t.get_device() != dev:
+            raise ValueError(f"{fn}: {name} is on {t.device}, {rows[0][1]} on {rows[0][0].device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: expected a contiguous tensor for {name}")
+
+
+def _fp8(fn, op, weights, rows, offsets, act, outs, flags, ws, stream):
+    """Checks and call of the block-scaled products.  weights: one Weight or GroupedWeight, or a gated pair;
+    rows: x, dy, or (dh, gate, up); outs: y, dx, or (h, g, u); None among the outs: not wanted."""
+    w, x = weights[0], rows[0]
+    N, K, E = w.N, w.K, getattr(w, "E", None)
+    gated, bwd = len(weights) == 2, "bwd" in fn
+    for v in weights:
+        if v.fmt != SQ_FMT_FP8_BLOCK:
+            raise ValueError(f"{fn}: the weight must be SQ_FMT_FP8_BLOCK")
+        if v.lora_up is not None or v.lora_down is not None:
+            raise ValueError(f"{fn}: a block-scaled weight has no low-rank branch")
+    if ("grouped" in fn) != (E is not None):
+        raise ValueError(f"{fn}: the weight is a {type(w).__name__}")
+    if gated and (weights[1].N != N or weights[1].K != K or getattr(weights[1], "E", None) != E):
+        raise ValueError(f"{fn}: the two weights differ in their sizes")
+    wide, out = (N, K) if bwd else (K, N)
+    shape = x.shape
+    if len(shape) != 2 or shape[1] != wide or x.dtype is not _BF16:
+        raise ValueError(f"{fn}: {('dh' if gated else 'dy') if bwd else 'x'} must be bfloat16 [M, {wide}], "
+                         f"got {x.dtype} {list(x.shape)}")
+    M, dev = shape[0], x.get_device()
+    lead = () if E is None else (E,)
+    codes, blocks = (*lead, N, K), (*lead, (N + 127) // 128, (K + 127) // 128)
+    ydt, yshape = (_BF16 if flags & SQ_OUT_BF16 else _F32), (M, out)
+    # every tensor: its type and shape, on one device, contiguous.  One pass for the usual call; the
+    # loop in _fp8_refuse names what is wrong.
+    ok = x.is_contiguous()
+    for v in weights:
+        c, s = v.codes, v.scales
+        ok = (ok and c.dtype is _E4M3 and c.shape == codes and c.get_device() == dev and c.is_contiguous()
+              and s.dtype is _E8M0 and s.shape == blocks and s.get_device() == dev and s.is_contiguous())
+    for t in rows[1:]:
+        ok = ok and t.dtype is _BF16 and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+    y = outs[0]
+    ok = (ok and y is not None and y.dtype is ydt and y.shape == yshape and y.get_device() == dev and y.is_contiguous()
+          and ws is not None and ws.get_device() == dev and ws.is_contiguous())
+    for t in outs[1:]:
+        ok = ok and (t is None or t.dtype is _BF16 and t.shape == yshape and t.get_device() == dev and t.is_contiguous())
+    if E is not None:
+        ok = (ok and isinstance(offsets, torch.Tensor) and offsets.dtype is torch.int32 and offsets.shape == (E + 1,)
+              and offsets.get_device() == dev and offsets.is_contiguous())
+    if not ok:
+        if E is not None and not isinstance(offsets, torch.Tensor):
+            raise ValueError(f"{fn}: offsets must be an int32 tensor of {E + 1} values")
+        names = ("dh", "gate", "up") if gated and bwd else ("dy",) if bwd else ("x",)
+        onames = ("dx",) if bwd else ("h", "g", "u") if gated else ("y",)
+        _fp8_refuse(fn, weights, [(t, n, _BF16, tuple(shape)) for t, n in zip(rows, names)],
+                    [(t, n, ydt if i == 0 else _BF16, yshape) for i, (t, n) in enumerate(zip(outs, onames))
+                     if i == 0 or t is not None], offsets, ws)
+    if dev < 0:
+        raise ValueError(f"{fn}: expected a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{fn}: the tensors are on {x.device}, the current device is {torch.cuda.current_device()}")
+    if M == 0 and E is not None:
+        return
+    stream = _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
+    f = _FP8.get(fn)
+    if f is None:
+        f = _FP8[fn] = getattr(lib(), fn)
+    args = [ctypes.byref(sq_weight(SQ_FMT_FP8_BLOCK, N, K, v.codes.data_ptr(), v.scales.data_ptr(), None, None, None))
+            for v in weights]
+    if E is not None:
+        args.append(E)
+    args += [t.data_ptr() for t in rows]
+    args.append(M)
+    if E is not None:
+        args.append(offsets.data_ptr())
+    if gated:
+        args.append(act)
+    args += [None if t is None else t.data_ptr() for t in outs]
+    st = f(*args, flags, ws.data_ptr(), ws.nbytes, stream)
+    if st != SQ_OK:
+        _check(fn, st)
+
+
+def _fp8_act(fn, act):
+    code = _FP8_ACTS.get(act)
+    if code is None:
+        raise ValueError(f"{fn}: act must be one of {sorted(_FP8_ACTS)}, got {act!r}")
+    return code
+
+
+def sq_build_fp8(W, codes, scales, stream=None):
+    """W [N, K] fp32 or bf16."""
+    fn = "sq_build_fp8"
+    N, K = W.shape
+    if W.dtype not in (_F32, _BF16):
+        raise ValueError(f"{fn}: W must be float32 or bfloat16, got {W.dtype}")
+    _need(fn, "codes", codes, N * K)
+    _need(fn, "scales", scales, (N + 127) // 128 * ((K + 127) // 128))
+    _check(fn, lib().sq_build_fp8(_ptr(W), N, K, SQ_IN_BF16 if W.dtype is _BF16 else 0, _ptr(codes), _ptr(scales),
+                                  _stream(stream)))
+
+
+def sq_linear_fwd_fp8(w: "Weight", x, y, flags: int = 0, ws=None, stream=None):
+    _fp8("sq_linear_fwd_fp8", SQ_OP_LINEAR_FWD_FP8, (w,), (x,), None, 0, (y,), flags, ws, stream)
+
+
+def sq_linear_bwd_dx_fp8(w: "Weight", dy, dx, flags: int = 0, ws=None, stream=None):
+    _fp8("sq_linear_bwd_dx_fp8", SQ_OP_LINEAR_BWD_DX_FP8, (w,), (dy,), None, 0, (dx,), flags, ws, stream)
+
+
+def sq_gated_fwd_fp8(w_gate: "Weight", w_up: "Weight", x, h, g=None, u=None, act: str = "silu", flags: int = 0,
+                     ws=None, stream=None):
+    fn = "sq_gated_fwd_fp8"
+    _fp8(fn, SQ_OP_GATED_FWD_FP8, (w_gate, w_up), (x,), None, _fp8_act(fn, act), (h, g, u), flags, ws, stream)
+
+
+def sq_gated_bwd_dx_fp8(w_gate: "Weight", w_up: "Weight", dh, g, u, dx, act: str = "silu", flags: int = 0, ws=None,
+                        stream=None):
+    fn = "sq_gated_bwd_dx_fp8"
+    _fp8(fn, SQ_OP_GATED_BWD_DX_FP8, (w_gate, w_up), (dh, g, u), None, _fp8_act(fn, act), (dx,), flags, ws, stream)
+
+
+def sq_grouped_fwd_fp8(w: "GroupedWeight", x, offsets, y, flags: int = 0, ws=None, stream=None):
+    _fp8("sq_grouped_fwd_fp8", SQ_OP_GROUPED_FWD_FP8, (w,), (x,), offsets, 0, (y,), flags, ws, stream)
+
+
+def sq_grouped_bwd_dx_fp8(w: "GroupedWeight", dy, offsets, dx, flags: int = 0, ws=None, stream=None):
+    _fp8("sq_grouped_bwd_dx_fp8", SQ_OP_GROUPED_BWD_DX_FP8, (w,), (dy,), offsets, 0, (dx,), flags, ws, stream)
+
+
+def sq_grouped_gated_fwd_fp8(w_gate: "GroupedWeight", w_up: "GroupedWeight", x, offsets, h, g=None, u=None,
+                             act: str = "silu", flags: int = 0, ws=None, stream=None):
+    fn = "sq_grouped_gated_fwd_fp8"
+    _fp8(fn, SQ_OP_GROUPED_GATED_FWD_FP8, (w_gate, w_up), (x,), offsets, _fp8_act(fn, act), (h, g, u), flags, ws,
+         stream)
+
+
+def sq_grouped_gated_bwd_dx_fp8(w_gate: "GroupedWeight", w_up: "GroupedWeight", dh, g, u, offsets, dx,
+                                act: str = "silu", flags: int = 0, ws=None, stream=None):
+    fn = "sq_grouped_gated_bwd_dx_fp8"
+    _fp8(fn, SQ_OP_GROUPED_GATED_BWD_DX_FP8, (w_gate, w_up), (dh, g, u), offsets, _fp8_act(fn, act), (dx,), flags, ws,
+         stream)
+
+
 def sq_debug_checks() -> int:
     """1 if the loaded library was built with the device-side index checks (libsq_debug.so)."""
     return lib().sq_debug_checks()
@@ -484,8 +676,9 @@ class Weight:
     fmt: int
     N: int
     K: int
-    codes: torch.Tensor                  # uint8 [N, K/2] (int8 format: int8 [N, K])
-    scales: torch.Tensor                 # int4: float16 [N, K/group]; NVFP4: uint8 tiled; int8: float32 [N]
+    codes: torch.Tensor                  # uint8 [N, K/2] (int8 format: int8 [N, K]; block-scaled: float8_e4m3fn [N, K])
+    scales: torch.Tensor                 # int4: float16 [N, K/group]; NVFP4: uint8 tiled; int8: float32 [N];
+                                         # block-scaled: float8_e8m0fnu [ceil(N/128), ceil(K/128)]
     g_w: torch.Tensor | None = None      # float32 [1] (NVFP4)
     lora_up: torch.Tensor | None = None  # bf16 [N, 32] (int8 format: [N, 16])
     lora_down: torch.Tensor | None = None  # bf16 [K, 32] (int8 format: [K, 16])
@@ -498,12 +691,12 @@ class Weight:
 
 @dataclass
 class GroupedWeight:
-    """E int8 per-row weights of the same shape, one per expert."""
+    """E int8 per-row (or, with fmt SQ_FMT_FP8_BLOCK, block-scaled e4m3) weights of the same shape, one per expert."""
     E: int
     N: int
     K: int
-    codes: torch.Tensor                  # int8 [E, N, K]
-    scales: torch.Tensor                 # float32 [E, N]
+    codes: torch.Tensor                  # int8 [E, N, K]; block-scaled: float8_e4m3fn
+    scales: torch.Tensor                 # float32 [E, N]; block-scaled: float8_e8m0fnu [E, ceil(N/128), ceil(K/128)]
     lora_up: torch.Tensor | None = None  # bf16 [E, N, 16]
     lora_down: torch.Tensor | None = None  # bf16 [E, K, 16]
     fmt: int = SQ_FMT_INT8_ROW
@@ -668,3 +861,109 @@ def grouped_bwd_dx_w8a8(w: GroupedWeight, dy: torch.Tensor, offsets: torch.Tenso
     """dx [M, K]: rows offsets[e] .. offsets[e + 1] - 1 of dy times expert e's W; rows of no expert are 0."""
     return _w8a8_out("sq_grouped_bwd_dx_w8a8", SQ_OP_GROUPED_BWD_DX_W8A8, w, dy, offsets, w.K, ws, flags, out_bf16,
                      stream)
+
+
+def build_fp8(W: torch.Tensor, stream=None) -> Weight:
+    """Block-scaled e4m3 weight of W [N, K] (fp32 or bf16); N and K multiples of 16."""
+    N, K = W.shape
+    with _allocating_on(stream):
+        codes = torch.empty((N, K), dtype=_E4M3, device=W.device)
+        scales = torch.empty(((N + 127) // 128, (K + 127) // 128), dtype=_E8M0, device=W.device)
+    sq_build_fp8(W, codes, scales, stream=stream)
+    return Weight(SQ_FMT_FP8_BLOCK, N, K, codes, scales)
+
+
+def build_fp8_grouped(W: torch.Tensor, stream=None) -> GroupedWeight:
+    """Block-scaled e4m3 weights of E experts from W [E, N, K] (fp32 or bf16)."""
+    E, N, K = W.shape
+    with _allocating_on(stream):
+        codes = torch.empty((E, N, K), dtype=_E4M3, device=W.device)
+        scales = torch.empty((E, (N + 127) // 128, (K + 127) // 128), dtype=_E8M0, device=W.device)
+    for e in range(E):
+        sq_build_fp8(W[e], codes[e], scales[e], stream=stream)
+    return GroupedWeight(E, N, K, codes, scales, fmt=SQ_FMT_FP8_BLOCK)
+
+
+def _fp8_out(fn, op, weights, rows, offsets, act, save, ws, flags, out_bf16, stream):
+    """The outputs and workspace of a block-scaled call, and the call."""
+    if stream is not None:
+        with _allocating_on(stream):
+            return _fp8_out_here(fn, op, weights, rows, offsets, act, save, ws, flags, out_bf16, stream)
+    return _fp8_out_here(fn, op, weights, rows, offsets, act, save, ws, flags, out_bf16, None)
+
+
+def _fp8_out_here(fn, op, weights, rows, offsets, act, save, ws, flags, out_bf16, stream):
+    if out_bf16:
+        flags |= SQ_OUT_BF16
+    w, x = weights[0], rows[0]
+    M, E = x.shape[0], getattr(w, "E", None)
+    width = w.K if "bwd" in fn else w.N
+    y = x.new_empty(M, width, dtype=_BF16 if flags & SQ_OUT_BF16 else _F32)
+    if ws is None:
+        ws = x.new_empty(_w8a8_bytes(op, E, M, w.N, w.K), dtype=torch.uint8)
+    if E is not None:
+        flags |= SQ_ZERO_UNGROUPED
+    if act is None:
+        _fp8(fn, op, weights, rows, offsets, 0, (y,), flags, ws, stream)
+        return y
+    outs = (y,) if "bwd" in fn else (y, *((x.new_empty(M, width), x.new_empty(M, width)) if save else (None, None)))
+    _fp8(fn, op, weights, rows, offsets, _fp8_act(fn, act), outs, flags, ws, stream)
+    return outs if save else y
+
+
+def linear_fwd_fp8(w: Weight, x: torch.Tensor, ws=None, flags: int = 0, out_bf16: bool = False,
+                   stream=None) -> torch.Tensor:
+    """y [M, N] = x W^T on a block-scaled weight, x rounded to e4m3 in blocks of 128; fp32 or bf16."""
+    return _fp8_out("sq_linear_fwd_fp8", SQ_OP_LINEAR_FWD_FP8, (w,), (x,), None, None, False, ws, flags, out_bf16, stream)
+
+
+def linear_bwd_dx_fp8(w: Weight, dy: torch.Tensor, ws=None, flags: int = 0, out_bf16: bool = False,
+                      stream=None) -> torch.Tensor:
+    """dx [M, K] = dy W on a block-scaled weight, fp32 or bf16."""
+    return _fp8_out("sq_linear_bwd_dx_fp8", SQ_OP_LINEAR_BWD_DX_FP8, (w,), (dy,), None, None, False, ws, flags, out_bf16,
+                    stream)
+
+
+def gated_fwd_fp8(w_gate: Weight, w_up: Weight, x: torch.Tensor, act: str = "silu", save: bool = False, ws=None,
+                  flags: int = 0, out_bf16: bool = False, stream=None):
+    """h [M, N] = act(x Wgate^T) (x Wup^T), act "silu" or "gelu" (tanh form); with save (h, g, u), the two
+    products in bf16, for gated_bwd_dx_fp8."""
+    return _fp8_out("sq_gated_fwd_fp8", SQ_OP_GATED_FWD_FP8, (w_gate, w_up), (x,), None, act, save, ws, flags, out_bf16,
+                    stream)
+
+
+def gated_bwd_dx_fp8(w_gate: Weight, w_up: Weight, dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor,
+                     act: str = "silu", ws=None, flags: int = 0, out_bf16: bool = False, stream=None) -> torch.Tensor:
+    """dx [M, K] of gated_fwd_fp8 from dh and the g and u that it kept."""
+    return _fp8_out("sq_gated_bwd_dx_fp8", SQ_OP_GATED_BWD_DX_FP8, (w_gate, w_up), (dh, g, u), None, act, False, ws,
+                    flags, out_bf16, stream)
+
+
+def grouped_fwd_fp8(w: GroupedWeight, x: torch.Tensor, offsets: torch.Tensor, ws=None, flags: int = 0,
+                    out_bf16: bool = False, stream=None) -> torch.Tensor:
+    """y [M, N]: rows offsets[e] .. offsets[e + 1] - 1 of x times expert e's W^T; rows of no expert are 0."""
+    return _fp8_out("sq_grouped_fwd_fp8", SQ_OP_GROUPED_FWD_FP8, (w,), (x,), offsets, None, False, ws, flags, out_bf16,
+                    stream)
+
+
+def grouped_bwd_dx_fp8(w: GroupedWeight, dy: torch.Tensor, offsets: torch.Tensor, ws=None, flags: int = 0,
+                       out_bf16: bool = False, stream=None) -> torch.Tensor:
+    """dx [M, K]: rows offsets[e] .. offsets[e + 1] - 1 of dy times expert e's W; rows of no expert are 0."""
+    return _fp8_out("sq_grouped_bwd_dx_fp8", SQ_OP_GROUPED_BWD_DX_FP8, (w,), (dy,), offsets, None, False, ws, flags,
+                    out_bf16, stream)
+
+
+def grouped_gated_fwd_fp8(w_gate: GroupedWeight, w_up: GroupedWeight, x: torch.Tensor, offsets: torch.Tensor,
+                          act: str = "silu", save: bool = False, ws=None, flags: int = 0, out_bf16: bool = False,
+                          stream=None):
+    """gated_fwd_fp8 for the rows of each expert; rows of no expert are 0."""
+    return _fp8_out("sq_grouped_gated_fwd_fp8", SQ_OP_GROUPED_GATED_FWD_FP8, (w_gate, w_up), (x,), offsets, act, save, ws,
+                    flags, out_bf16, stream)
+
+
+def grouped_gated_bwd_dx_fp8(w_gate: GroupedWeight, w_up: GroupedWeight, dh: torch.Tensor, g: torch.Tensor,
+                             u: torch.Tensor, offsets: torch.Tensor, act: str = "silu", ws=None, flags: int = 0,
+                             out_bf16: bool = False, stream=None) -> torch.Tensor:
+    """gated_bwd_dx_fp8 for the rows of each expert; rows of no expert are 0."""
+    return _fp8_out("sq_grouped_gated_bwd_dx_fp8", SQ_OP_GROUPED_GATED_BWD_DX_FP8, (w_gate, w_up), (dh, g, u), offsets,
+                    act, False, ws, flags, out_bf16, stream)

@@ -13,8 +13,9 @@ LIB = os.path.join(PKG, "libsq.so")
 # the same library with the device-side index checks on (-DSQ_DEBUG_CHECKS): every checked store
 # tests its index against its buffer, skips it when outside and reports SQ_ERR_INDEX
 LIB_DEBUG = os.path.join(PKG, "libsq_debug.so")
-SOURCES = ["sq_api.cu", "sq_quant.cu", "sq_gemm.cu", "sq_svd.cu", "sq_w8a8_quant.cu", "sq_w8a8.cu"]
-HEADERS = ["sq_device.cuh", "sq_ptx.cuh", "sq_kernels.h", "sq_w8a8.cuh", "sq_w8a8_stage.h"]
+SOURCES = ["sq_api.cu", "sq_quant.cu", "sq_gemm.cu", "sq_svd.cu", "sq_w8a8_quant.cu", "sq_w8a8.cu",
+           "sq_fp8_quant.cu", "sq_fp8.cu"]
+HEADERS = ["sq_device.cuh", "sq_ptx.cuh", "sq_kernels.h", "sq_w8a8.cuh", "sq_w8a8_stage.h", "sq_fp8.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -33,7 +34,7 @@ def _stale(lib: str = LIB) -> bool:
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, h) for h in ("sq.h", "sq_w8a8.h")]
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, h) for h in ("sq.h", "sq_w8a8.h", "sq_fp8.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

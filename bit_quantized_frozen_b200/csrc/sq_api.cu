@@ -11,7 +11,9 @@
 
 #include "sq.h"
 #include "sq_w8a8.h"
+#include "sq_fp8.h"
 #include "sq_device.cuh"
+#include "sq_fp8.cuh"
 #include "sq_kernels.h"
 #include "sq_ptx.cuh"
 
@@ -226,6 +228,24 @@ I8Layout i8_layout(bool bwd, int64_t M, int64_t N, int64_t K)
 constexpr int64_t kMaxExperts = 1024;
 constexpr int64_t kMaxSumI8 = int64_t(1) << 17;   // 127 * 128 * 2^17 < 2^31: the 32-bit sums are exact
 
+// block-scaled e4m3 products: header and the row operand (codes, words of scales), twice for the
+// gradients of a gated pair
+struct Fp8Layout {
+    size_t codes = 0, words = 0, total = 0;
+};
+
+Fp8Layout fp8_layout(bool bwd, bool gated, int64_t M, int64_t N, int64_t K)
+{
+    Fp8Layout L;
+    const int64_t len = bwd ? N : K, halves = bwd && gated ? 2 : 1;
+    L.codes = round_up(kHeader, kAlign);
+    L.words = round_up(L.codes + (size_t)halves * (size_t)M * (size_t)len, kAlign);
+    L.total = round_up(L.words + (size_t)halves * (size_t)sq::fp8_groups(len) * (size_t)M * 4, kAlign);
+    return L;
+}
+
+constexpr int64_t kMaxFp8 = int64_t(1) << 20;     // N, K
+
 uint8_t *ws_at(void *ws, size_t off)
 {
     return reinterpret_cast<uint8_t *>(ws) + off;
@@ -353,6 +373,113 @@ sq_status i8_product(bool bwd, int64_t E, const sq_weight *w, const uint16_t *x,
     return SQ_OK;
 }
 
+// What the block-scaled calls have in common: forward (bwd = false) or input gradient of one weight or
+// of a gated pair (w[1], else NULL), dense (E == 0) or grouped.
+struct Fp8Call {
+    bool bwd;
+    int64_t E;
+    const sq_weight *w[2];
+    const uint16_t *x, *g, *u;       // rows; gated backward: what the forward kept
+    const int32_t *offsets;
+    int64_t M;
+    int32_t act;
+    void *y;
+    uint16_t *g_out, *u_out;
+};
+
+sq_status fp8_product(const Fp8Call &c, bool gated, uint32_t flags, void *ws, size_t ws_bytes, void *stream)
+{
+    for (int i = 0; i < (gated ? 2 : 1); ++i) {
+        const sq_weight *w = c.w[i];
+        if (!w || !w->codes || !w->scales)
+            return SQ_ERR_NULL;
+        if (w->fmt != SQ_FMT_FP8_BLOCK || w->g_w || w->lora_up || w->lora_down)
+            return SQ_ERR_ARG;
+        if (w->N <= 0 || w->K <= 0 || w->N % 16 || w->K % 16 || w->N > kMaxFp8 || w->K > kMaxFp8 ||
+            w->N * w->K >= (int64_t(1) << 40) || w->N != c.w[0]->N || w->K != c.w[0]->K)
+            return SQ_ERR_SHAPE;
+        if (!aligned(w->codes, 16))
+            return SQ_ERR_ALIGN;
+    }
+    if ((flags & ~(SQ_OUT_BF16 | SQ_CHECK_FINITE | (c.E > 0 ? SQ_ZERO_UNGROUPED : 0u))) ||
+        (gated && c.act != SQ_ACT_SILU && c.act != SQ_ACT_GELU_TANH))
+        return SQ_ERR_ARG;
+    const int64_t N = c.w[0]->N, K = c.w[0]->K, M = c.M;
+    if (M < 0 || M > kMaxM || (c.E == 0 && M == 0))
+        return SQ_ERR_SHAPE;
+    if (c.E > 0 && !c.offsets)
+        return SQ_ERR_NULL;
+    if (c.E > 0 && M == 0)                            // no rows: nothing to do
+        return SQ_OK;
+    if (!c.x || !c.y || !ws || (gated && c.bwd && (!c.g || !c.u)) || (c.g_out == nullptr) != (c.u_out == nullptr))
+        return SQ_ERR_NULL;
+    if (!aligned(c.x, 16) || !aligned(c.y, 16) || !aligned(c.g, 16) || !aligned(c.u, 16) || !aligned(c.g_out, 16) ||
+        !aligned(c.u_out, 16) || !aligned(c.offsets, 4) || !aligned(ws, 256))
+        return SQ_ERR_ALIGN;
+    const Fp8Layout L = fp8_layout(c.bwd, gated, M, N, K);
+    if (ws_bytes < L.total)
+        return SQ_ERR_WORKSPACE;
+    int sms = 0;
+    sq_status st = check_device(&sms);
+    if (st != SQ_OK)
+        return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    uint32_t *status = reinterpret_cast<uint32_t *>(ws_at(ws, 0));
+    sq::Fp8QuantArgs q;
+    memset(&q, 0, sizeof(q));
+    q.x = c.x;
+    q.g = c.g;
+    q.u = c.u;
+    q.offsets = c.offsets;
+    q.codes = ws_at(ws, L.codes);
+    q.words = reinterpret_cast<uint32_t *>(ws_at(ws, L.words));
+    q.status = status;
+    if (flags & SQ_ZERO_UNGROUPED) {
+        q.zero[0] = reinterpret_cast<uint8_t *>(c.y);
+        q.zero[1] = reinterpret_cast<uint8_t *>(c.g_out);
+        q.zero[2] = reinterpret_cast<uint8_t *>(c.u_out);
+        q.zero_row_bytes[0] = (c.bwd ? K : N) * ((flags & SQ_OUT_BF16) ? 2 : 4);
+        q.zero_row_bytes[1] = q.zero_row_bytes[2] = 2 * N;
+    }
+    q.M = M;
+    q.L = c.bwd ? N : K;
+    q.E = (int)c.E;
+    q.act = c.act;
+    q.finite_check = (flags & SQ_CHECK_FINITE) ? 1 : 0;
+    // the first block of the rounding writes the status word; with a finite check any block may set
+    // it, so it is cleared first
+    if (q.finite_check)
+        SQ_CUDA(cudaMemsetAsync(status, 0, 4, s), "memset");
+    SQ_CUDA(stage_event(SQ_STAGE_ACT_QUANT, 0, s), "event record");
+    SQ_CUDA(sq::launch_fp8_quant(q, sms, s), "e4m3 row rounding");
+    SQ_CUDA(stage_event(SQ_STAGE_ACT_QUANT, 1, s), "event record");
+    sq::Fp8GemmLaunch g;
+    memset(&g, 0, sizeof(g));
+    g.bwd = c.bwd;
+    g.gated = gated;
+    g.E = (int)c.E;
+    g.act = c.act;
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    g.offsets = c.offsets;
+    g.codes = q.codes;
+    g.words = q.words;
+    for (int i = 0; i < (gated ? 2 : 1); ++i) {
+        g.wcodes[i] = c.w[i]->codes;
+        g.wscales[i] = reinterpret_cast<const uint8_t *>(c.w[i]->scales);
+    }
+    g.y = c.y;
+    g.g_out = c.g_out;
+    g.u_out = c.u_out;
+    g.out_bf16 = (flags & SQ_OUT_BF16) ? 1 : 0;
+    g.status = status;
+    SQ_CUDA(stage_event(SQ_STAGE_GEMM, 0, s), "event record");
+    SQ_CUDA(sq::launch_fp8_gemm(g, sms, s), "e4m3 product");
+    SQ_CUDA(stage_event(SQ_STAGE_GEMM, 1, s), "event record");
+    return SQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -432,6 +559,13 @@ size_t sq_workspace_bytes(int op, int64_t M, int64_t N, int64_t K)
         return i8_layout(false, M, N, K).total;
     case SQ_OP_LINEAR_BWD_DX_W8A8:
         return i8_layout(true, M, N, K).total;
+    case SQ_OP_LINEAR_FWD_FP8:
+    case SQ_OP_GATED_FWD_FP8:
+        return fp8_layout(false, false, M, N, K).total;
+    case SQ_OP_LINEAR_BWD_DX_FP8:
+        return fp8_layout(true, false, M, N, K).total;
+    case SQ_OP_GATED_BWD_DX_FP8:
+        return fp8_layout(true, true, M, N, K).total;
     default:
         return 0;
     }
@@ -446,6 +580,13 @@ size_t sq_grouped_workspace_bytes(int op, int64_t E, int64_t M, int64_t N, int64
         return i8_layout(false, M, N, K).total;
     case SQ_OP_GROUPED_BWD_DX_W8A8:
         return i8_layout(true, M, N, K).total;
+    case SQ_OP_GROUPED_FWD_FP8:
+    case SQ_OP_GROUPED_GATED_FWD_FP8:
+        return fp8_layout(false, false, M, N, K).total;
+    case SQ_OP_GROUPED_BWD_DX_FP8:
+        return fp8_layout(true, false, M, N, K).total;
+    case SQ_OP_GROUPED_GATED_BWD_DX_FP8:
+        return fp8_layout(true, true, M, N, K).total;
     default:
         return 0;
     }
@@ -846,6 +987,95 @@ sq_status sq_grouped_bwd_dx_w8a8(const sq_weight *w, int64_t E, const uint16_t *
     if (E < 1 || E > kMaxExperts)
         return SQ_ERR_SHAPE;
     return i8_product(true, E, w, dy, M, offsets, dx, flags, ws, ws_bytes, stream);
+}
+
+sq_status sq_build_fp8(const void *W, int64_t N, int64_t K, uint32_t flags, uint8_t *codes, uint8_t *scales,
+                       void *stream)
+{
+    if (!W || !codes || !scales)
+        return SQ_ERR_NULL;
+    if (flags & ~SQ_IN_BF16)
+        return SQ_ERR_ARG;
+    if (N <= 0 || K <= 0 || N % 16 || K % 16 || N > kMaxFp8 || K > kMaxFp8)
+        return SQ_ERR_SHAPE;
+    if (!aligned(W, 16) || !aligned(codes, 16))
+        return SQ_ERR_ALIGN;
+    int sms = 0;
+    sq_status st = check_device(&sms);
+    if (st != SQ_OK)
+        return st;
+    SQ_CUDA(sq::launch_fp8_build(W, (flags & SQ_IN_BF16) ? 1 : 0, N, K, codes, scales,
+                                 reinterpret_cast<cudaStream_t>(stream)),
+            "e4m3 build");
+    return SQ_OK;
+}
+
+sq_status sq_linear_fwd_fp8(const sq_weight *w, const uint16_t *x, int64_t M, void *y, uint32_t flags, void *ws,
+                            size_t ws_bytes, void *stream)
+{
+    return fp8_product({false, 0, {w, nullptr}, x, nullptr, nullptr, nullptr, M, 0, y, nullptr, nullptr}, false, flags,
+                       ws, ws_bytes, stream);
+}
+
+sq_status sq_linear_bwd_dx_fp8(const sq_weight *w, const uint16_t *dy, int64_t M, void *dx, uint32_t flags, void *ws,
+                               size_t ws_bytes, void *stream)
+{
+    return fp8_product({true, 0, {w, nullptr}, dy, nullptr, nullptr, nullptr, M, 0, dx, nullptr, nullptr}, false, flags,
+                       ws, ws_bytes, stream);
+}
+
+sq_status sq_gated_fwd_fp8(const sq_weight *gate, const sq_weight *up, const uint16_t *x, int64_t M, int32_t act,
+                           void *h, uint16_t *g_out, uint16_t *u_out, uint32_t flags, void *ws, size_t ws_bytes,
+                           void *stream)
+{
+    return fp8_product({false, 0, {gate, up}, x, nullptr, nullptr, nullptr, M, act, h, g_out, u_out}, true, flags, ws,
+                       ws_bytes, stream);
+}
+
+sq_status sq_gated_bwd_dx_fp8(const sq_weight *gate, const sq_weight *up, const uint16_t *dh, const uint16_t *g,
+                              const uint16_t *u, int64_t M, int32_t act, void *dx, uint32_t flags, void *ws,
+                              size_t ws_bytes, void *stream)
+{
+    return fp8_product({true, 0, {gate, up}, dh, g, u, nullptr, M, act, dx, nullptr, nullptr}, true, flags, ws,
+                       ws_bytes, stream);
+}
+
+sq_status sq_grouped_fwd_fp8(const sq_weight *w, int64_t E, const uint16_t *x, int64_t M, const int32_t *offsets,
+                             void *y, uint32_t flags, void *ws, size_t ws_bytes, void *stream)
+{
+    if (E < 1 || E > kMaxExperts)
+        return SQ_ERR_SHAPE;
+    return fp8_product({false, E, {w, nullptr}, x, nullptr, nullptr, offsets, M, 0, y, nullptr, nullptr}, false, flags,
+                       ws, ws_bytes, stream);
+}
+
+sq_status sq_grouped_bwd_dx_fp8(const sq_weight *w, int64_t E, const uint16_t *dy, int64_t M, const int32_t *offsets,
+                                void *dx, uint32_t flags, void *ws, size_t ws_bytes, void *stream)
+{
+    if (E < 1 || E > kMaxExperts)
+        return SQ_ERR_SHAPE;
+    return fp8_product({true, E, {w, nullptr}, dy, nullptr, nullptr, offsets, M, 0, dx, nullptr, nullptr}, false, flags,
+                       ws, ws_bytes, stream);
+}
+
+sq_status sq_grouped_gated_fwd_fp8(const sq_weight *gate, const sq_weight *up, int64_t E, const uint16_t *x, int64_t M,
+                                   const int32_t *offsets, int32_t act, void *h, uint16_t *g_out, uint16_t *u_out,
+                                   uint32_t flags, void *ws, size_t ws_bytes, void *stream)
+{
+    if (E < 1 || E > kMaxExperts)
+        return SQ_ERR_SHAPE;
+    return fp8_product({false, E, {gate, up}, x, nullptr, nullptr, offsets, M, act, h, g_out, u_out}, true, flags, ws,
+                       ws_bytes, stream);
+}
+
+sq_status sq_grouped_gated_bwd_dx_fp8(const sq_weight *gate, const sq_weight *up, int64_t E, const uint16_t *dh,
+                                      const uint16_t *g, const uint16_t *u, int64_t M, const int32_t *offsets,
+                                      int32_t act, void *dx, uint32_t flags, void *ws, size_t ws_bytes, void *stream)
+{
+    if (E < 1 || E > kMaxExperts)
+        return SQ_ERR_SHAPE;
+    return fp8_product({true, E, {gate, up}, dh, g, u, offsets, M, act, dx, nullptr, nullptr}, true, flags, ws,
+                       ws_bytes, stream);
 }
 
 sq_status sq_set_stage_events(int32_t stage, void *start_event, void *stop_event)

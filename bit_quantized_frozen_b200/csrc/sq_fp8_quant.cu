@@ -1,0 +1,320 @@
+// sq_fp8_quant.cu -- e4m3 codes with one power-of-two scale for each block of 128: of the rows
+// that the block-scaled product (sq_fp8.cu) multiplies, and of a weight (128 x 128 blocks).
+//
+//   s = the least power of two >= 2^-127 with max|r| <= 448 s,   code = e4m3(r / s)
+//
+// max|r| = 2^E (1.m): s = 2^(E - 8), or the next one where 1.m > 1.75 (448 = 1.75 * 2^8), straight
+// from the maximum's bits; r / s = r 2^-e is exact in fp32, so the code is one rounding of r.
+//
+// Rows: r = x, or the two gradients of a gated pair, formed here from dh, g and u:
+//   dg = (dh u) act'(g),  du = dh act(g)            (fp32)
+//
+// A block with a NaN or an infinity gets NaN codes, so that the whole row's sums are NaN.
+#include <cuda.h>
+
+#include "sq_fp8.cuh"
+#include "sq_kernels.h"
+#include "sq_ptx.cuh"
+
+namespace sq {
+
+constexpr uint32_t kInf = 0x7F800000u;
+constexpr uint32_t kNanCodes = 0x7F7F7F7Fu;
+constexpr int kQuantThreads = 128;
+
+// e8m0 byte of a block from the bits of its largest |r| (finite)
+__device__ __forceinline__ uint32_t fp8_scale_byte(uint32_t amax_bits)
+{
+    const int e = (int)(amax_bits >> 23) - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return e < 0 ? 0u : (uint32_t)e;
+}
+
+// 2^-e as a float (the byte is at most 247)
+__device__ __forceinline__ float fp8_inverse(uint32_t byte)
+{
+    return __uint_as_float((254u - byte) << 23);
+}
+
+__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
+
+__device__ __forceinline__ void widen8(const uint4 &w, float (&v)[16], int at)
+{
+    const uint32_t p[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[at + 2 * i] = __uint_as_float(p[i] << 16);
+        v[at + 2 * i + 1] = __uint_as_float(p[i] & 0xFFFF0000u);
+    }
+}
+
+// A lane's 16 neighbouring values of a row (8 lanes a block): their codes, and the block's byte.
+__device__ __forceinline__ uint4 quantise16(const float (&v)[16], uint32_t &byte, bool &bad)
+{
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int x = 1; x <= 4; x <<= 1)
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
+    if (top >= kInf) {
+        bad = true;
+        byte = 127u;
+        return make_uint4(kNanCodes, kNanCodes, kNanCodes, kNanCodes);
+    }
+    byte = fp8_scale_byte(top);
+    const float inv = fp8_inverse(byte);
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        c[i] = to_e4m3x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+    return make_uint4(c[0], c[1], c[2], c[3]);
+}
+
+// a block's byte to the word of its four blocks: lanes 0, 8, 16, 24 hold them
+__device__ __forceinline__ uint32_t scale_word(uint32_t byte, int lane)
+{
+    uint32_t w = byte << (8 * (lane >> 3));
+    w |= __shfl_xor_sync(0xffffffffu, w, 8);
+    w |= __shfl_xor_sync(0xffffffffu, w, 16);
+    return w;
+}
+
+// what the first block does for the whole call: the status word
+__device__ __forceinline__ void fp8_begin_call(const Fp8QuantArgs &a)
+{
+    bool bad = false;
+    if (a.E > 0) {
+        for (int i = threadIdx.x; i <= a.E; i += blockDim.x) {
+            const int32_t o = a.offsets[i];
+            bad |= o < 0 || o > a.M || (i > 0 && o < a.offsets[i - 1]);
+        }
+        bad = __syncthreads_or(bad);
+    }
+    if (threadIdx.x == 0) {
+        if (a.finite_check) {                     // (the word was cleared before the launch)
+            if (bad)
+                atomicOr(a.status, kStatusIndex);
+        } else {
+            *a.status = bad ? kStatusIndex : 0u;
+        }
+    }
+}
+
+// GATED 0: rows of x; 1, 2: the gradients of a gated pair with silu, gelu.  A warp takes ROWS rows x
+// 512 columns at a time, a lane 16 neighbouring values of each row.
+template <int GATED, int ROWS>
+__global__ void __launch_bounds__(kQuantThreads) fp8_quant_kernel(const Fp8QuantArgs a)
+{
+    const int lane = threadIdx.x & 31;
+    grid_dep_wait();                              // x, and the workspace of the call before
+    grid_dep_launch();                            // the product may fetch its first weights
+    if (blockIdx.x == 0)
+        fp8_begin_call(a);
+    // rows of no expert are not looked at
+    int64_t lo = 0, hi = a.M;
+    if (a.E > 0) {
+        const int64_t first = __ldg(a.offsets), last = __ldg(a.offsets + a.E);
+        lo = first < 0 ? 0 : first > a.M ? a.M : first;
+        hi = last < lo ? lo : last > a.M ? a.M : last;
+    }
+    const int64_t groups = fp8_groups(a.L);
+    const int64_t units = (hi - lo + ROWS - 1) / ROWS * groups;
+    const int64_t warps = (int64_t)gridDim.x * (kQuantThreads / 32);
+    bool bad = false;
+    for (int64_t unit = (int64_t)blockIdx.x * (kQuantThreads / 32) + (threadIdx.x >> 5); unit < units; unit += warps) {
+        const int64_t grp = unit % groups, row0 = lo + unit / groups * ROWS;
+        const int64_t col = grp * (kFp8Block * kFp8Group) + 16 * lane;
+        constexpr int OPS = GATED ? 3 : 1;
+        uint4 w[OPS][ROWS][2];
+#pragma unroll
+        for (int o = 0; o < OPS; ++o) {
+            const uint16_t *src = o == 0 ? a.x : o == 1 ? a.g : a.u;
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                const bool live = row0 + r < hi && col < a.L;
+                const uint4 *p = reinterpret_cast<const uint4 *>(src + (row0 + r) * a.L + col);
+                w[o][r][0] = live ? __ldg(p) : make_uint4(0u, 0u, 0u, 0u);
+                w[o][r][1] = live ? __ldg(p + 1) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+        uint32_t words[GATED ? 2 : 1] = {};
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            float v[16];
+            widen8(w[0][r][0], v, 0);
+            widen8(w[0][r][1], v, 8);
+            float second[GATED ? 16 : 1];
+            if constexpr (GATED != 0) {
+                float g[16], u[16];
+                widen8(w[1][r][0], g, 0);
+                widen8(w[1][r][1], g, 8);
+                widen8(w[2][r][0], u, 0);
+                widen8(w[2][r][1], u, 8);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float act, slope;
+                    act_grad<GATED - 1>(g[i], act, slope);
+                    second[i] = v[i] * act;
+                    v[i] = v[i] * u[i] * slope;
+                }
+            }
+            const bool live = row0 + r < hi && col < a.L;
+            uint32_t byte;
+            const uint4 c = quantise16(v, byte, bad);
+            const uint32_t word = scale_word(byte, lane);
+            if (lane == r)
+                words[0] = word;
+            if (live && SQ_DCHECK(row0 + r < a.M, a.status))
+                *reinterpret_cast<uint4 *>(a.codes + (row0 + r) * a.L + col) = c;
+            if constexpr (GATED != 0) {
+                const uint4 d = quantise16(second, byte, bad);
+                const uint32_t word2 = scale_word(byte, lane);
+                if (lane == r)
+                    words[1] = word2;
+                if (live)
+                    *reinterpret_cast<uint4 *>(a.codes + (a.M + row0 + r) * a.L + col) = d;
+            }
+        }
+        if (lane < ROWS && row0 + lane < hi) {
+            a.words[grp * a.M + row0 + lane] = words[0];
+            if constexpr (GATED != 0)
+                a.words[(groups + grp) * a.M + row0 + lane] = words[1];
+        }
+    }
+    if (a.finite_check && bad)
+        atomicOr(a.status, kStatusNonfinite);
+    // rows of no expert: 0
+    if (a.E > 0) {
+        for (int k = 0; k < 3; ++k) {
+            if (!a.zero[k])
+                continue;
+            const int64_t n16 = a.zero_row_bytes[k] / 16, rows = lo + a.M - hi;
+            for (int64_t i = blockIdx.x; i < rows; i += gridDim.x) {
+                const int64_t m = i < lo ? i : hi + (i - lo);
+                uint4 *row = reinterpret_cast<uint4 *>(a.zero[k] + m * a.zero_row_bytes[k]);
+                for (int64_t c = threadIdx.x; c < n16; c += kQuantThreads)
+                    if (SQ_DCHECK(m < a.M, a.status))
+                        row[c] = make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+    }
+}
+
+template <int GATED, int ROWS>
+static cudaError_t launch_quant(const Fp8QuantArgs &a, int sms, cudaStream_t s)
+{
+    const int64_t units = (a.M + ROWS - 1) / ROWS * fp8_groups(a.L);
+    const int64_t blocks = (units + kQuantThreads / 32 - 1) / (kQuantThreads / 32), most = (int64_t)sms * 16;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks < most ? blocks : most));
+    cfg.blockDim = dim3(kQuantThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fp8_quant_kernel<GATED, ROWS>, a);
+}
+
+cudaError_t launch_fp8_quant(const Fp8QuantArgs &a, int sms, cudaStream_t s)
+{
+    if (!a.g)
+        return launch_quant<0, 4>(a, sms, s);
+    return a.act == 0 ? launch_quant<1, 2>(a, sms, s) : launch_quant<2, 2>(a, sms, s);
+}
+
+// ---------------------------------------------------------------------------
+// the weight: a CTA a block of 128 x 128, 8 lanes a row of 128
+// ---------------------------------------------------------------------------
+template <bool BF16>
+__global__ void __launch_bounds__(256) fp8_build_kernel(const void *__restrict__ W, int64_t N, int64_t K,
+                                                        uint8_t *__restrict__ codes, uint8_t *__restrict__ scales)
+{
+    __shared__ uint32_t warp_top[8];
+    const int64_t kbs = (K + kFp8Block - 1) / kFp8Block;
+    const int64_t kb = (int64_t)blockIdx.x % kbs, nb = (int64_t)blockIdx.x / kbs;
+    const int64_t col = kb * kFp8Block + 16 * (threadIdx.x & 7);
+    const int64_t row = nb * kFp8Block + (threadIdx.x >> 3);          // and 32, 64, 96 further
+    float v[4][16];
+    uint32_t top = 0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int64_t n = row + 32 * r;
+        if (n < N && col < K) {
+            if (BF16) {
+                const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(W) + n * K + col);
+                widen8(__ldg(p), v[r], 0);
+                widen8(__ldg(p + 1), v[r], 8);
+            } else {
+                const float4 *p = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(W) + n * K + col);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 f = __ldg(p + i);
+                    v[r][4 * i] = f.x;
+                    v[r][4 * i + 1] = f.y;
+                    v[r][4 * i + 2] = f.z;
+                    v[r][4 * i + 3] = f.w;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                v[r][i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t b = __float_as_uint(v[r][i]) & 0x7FFFFFFFu;
+            top = max(top, b < kInf ? b : 0u);
+        }
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if ((threadIdx.x & 31) == 0)
+        warp_top[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        top = max(top, warp_top[i]);
+    const uint32_t byte = fp8_scale_byte(top);
+    const float inv = fp8_inverse(byte);
+    if (threadIdx.x == 0)
+        scales[nb * kbs + kb] = (uint8_t)byte;
+    auto code = [&](float f) {                    // (the conversion would clamp an infinity)
+        return (__float_as_uint(f) & 0x7FFFFFFFu) >= kInf ? __uint_as_float(0x7FFFFFFFu) : f * inv;
+    };
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int64_t n = row + 32 * r;
+        if (n < N && col < K) {
+            uint32_t c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                c[i] = to_e4m3x4(code(v[r][4 * i]), code(v[r][4 * i + 1]), code(v[r][4 * i + 2]),
+                                 code(v[r][4 * i + 3]));
+            *reinterpret_cast<uint4 *>(codes + n * K + col) = make_uint4(c[0], c[1], c[2], c[3]);
+        }
+    }
+}
+
+cudaError_t launch_fp8_build(const void *W, int bf16, int64_t N, int64_t K, uint8_t *codes, uint8_t *scales,
+                             cudaStream_t s)
+{
+    const int64_t blocks = (N + kFp8Block - 1) / kFp8Block * ((K + kFp8Block - 1) / kFp8Block);
+    if (bf16)
+        fp8_build_kernel<true><<<(unsigned)blocks, 256, 0, s>>>(W, N, K, codes, scales);
+    else
+        fp8_build_kernel<false><<<(unsigned)blocks, 256, 0, s>>>(W, N, K, codes, scales);
+    return cudaGetLastError();
+}
+
+}  // namespace sq

@@ -133,6 +133,45 @@ struct I8GemmLaunch {
 };
 cudaError_t launch_i8_gemm(const I8GemmLaunch &g, int sms, cudaStream_t stream);
 
+// ---- block-scaled e4m3 products (sq_fp8_quant.cu, sq_fp8.cu) ---------------------
+// The row operand: rows of L values become e4m3 codes and one e8m0 scale for each block of 128.
+struct Fp8QuantArgs {
+    const uint16_t *x;          // [M, L] bf16; gated backward: dh
+    const uint16_t *g, *u;      // gated backward: [M, L] bf16, else NULL
+    const int32_t *offsets;     // [E + 1], E > 0
+    uint8_t *codes;             // [M, L]; gated backward: [2, M, L], dg's and du's
+    uint32_t *words;            // [fp8_groups(L), M] scales of four blocks each (gated backward: twice)
+    uint32_t *status;
+    uint8_t *zero[3];           // outputs whose rows outside every expert become 0, or NULL
+    int64_t zero_row_bytes[3];
+    int64_t M, L;               // L % 16 == 0
+    int E;                      // experts, 0: one layer
+    int act;                    // gated backward
+    int finite_check;           // 1: a NaN or an infinity sets kStatusNonfinite
+};
+cudaError_t launch_fp8_quant(const Fp8QuantArgs &a, int sms, cudaStream_t s);
+cudaError_t launch_fp8_build(const void *W, int bf16, int64_t N, int64_t K, uint8_t *codes, uint8_t *scales,
+                             cudaStream_t s);
+
+// The product.  Forward: y[m, n] = sum_k x[m, k] W[n, k], gated: h = act(g) u of two weights;
+// backward: dx[m, k] = sum_n dy[m, n] W[n, k], gated: the sum over both weights.
+struct Fp8GemmLaunch {
+    bool bwd, gated;
+    int E;                      // experts, 0: one layer
+    int act;
+    int64_t M, N, K;
+    const int32_t *offsets;     // [E + 1] (device), E > 0
+    const uint8_t *codes;       // row operand (Fp8QuantArgs)
+    const uint32_t *words;
+    const uint8_t *wcodes[2];   // [max(E, 1), N, K]; gated: gate, up
+    const uint8_t *wscales[2];  // [max(E, 1), ceil(N / 128), ceil(K / 128)]
+    void *y;                    // [M, N] (backward [M, K]) fp32 or bf16
+    uint16_t *g_out, *u_out;    // gated forward: [M, N] bf16, or NULL
+    int out_bf16;
+    uint32_t *status;
+};
+cudaError_t launch_fp8_gemm(const Fp8GemmLaunch &g, int sms, cudaStream_t stream);
+
 // ID of the current CUDA context (unique for the life of the process; a context created
 // after cudaDeviceReset gets a new one), 0 if it cannot be read.  Per-device caches of
 // symbol addresses and function attributes are keyed on it: a new context loads the
