@@ -450,9 +450,11 @@ sq_status fp8_product(const Fp8Call &c, bool gated, uint32_t flags, void *ws, si
     // it, so it is cleared first
     if (q.finite_check)
         SQ_CUDA(cudaMemsetAsync(status, 0, 4, s), "memset");
-    SQ_CUDA(stage_event(SQ_STAGE_ACT_QUANT, 0, s), "event record");
-    SQ_CUDA(sq::launch_fp8_quant(q, sms, s), "e4m3 row rounding");
-    SQ_CUDA(stage_event(SQ_STAGE_ACT_QUANT, 1, s), "event record");
+    if (!sq::fp8_rounds_rows((int)c.E, M)) {
+        SQ_CUDA(stage_event(SQ_STAGE_ACT_QUANT, 0, s), "event record");
+        SQ_CUDA(sq::launch_fp8_quant(q, sms, s), "e4m3 row rounding");
+        SQ_CUDA(stage_event(SQ_STAGE_ACT_QUANT, 1, s), "event record");
+    }
     sq::Fp8GemmLaunch g;
     memset(&g, 0, sizeof(g));
     g.bwd = c.bwd;
@@ -475,7 +477,7 @@ sq_status fp8_product(const Fp8Call &c, bool gated, uint32_t flags, void *ws, si
     g.out_bf16 = (flags & SQ_OUT_BF16) ? 1 : 0;
     g.status = status;
     SQ_CUDA(stage_event(SQ_STAGE_GEMM, 0, s), "event record");
-    SQ_CUDA(sq::launch_fp8_gemm(g, sms, s), "e4m3 product");
+    SQ_CUDA(sq::launch_fp8_gemm(g, q, sms, s), "e4m3 product");
     SQ_CUDA(stage_event(SQ_STAGE_GEMM, 1, s), "event record");
     return SQ_OK;
 }

@@ -12,18 +12,24 @@
 // memory; backward the summed axis simply runs through both weights.
 //
 // Scales.  The tensor cores take one e8m0 byte for each row of A and of B and 32 values; a block of
-// 128 is four of them with the same byte.  A word holds the bytes of four neighbouring blocks, the
-// instruction names the one to use, so that a row's scales for 512 values are one 32-bit word in
-// tensor memory.  The scale warps lay the words of a tile out in shared memory (rows r, r + 32,
-// r + 64, r + 96 of 128 in one 16-byte line), the issuing thread copies them into tensor memory in
-// front of the products that need them.
+// 128 is four of them with the same byte.  A word holds the bytes of a group of four neighbouring
+// blocks, the instruction names the one to use, so that a row's scales for 512 values are one 32-bit
+// word in tensor memory.  Sets of four feeder warps, one for each 32 lanes, write the words there, up
+// to four groups ahead of the products.  (Copied by the issuing thread from shared memory instead,
+// tcgen05.cp, each group held the tensor pipe up by some 600 cycles.)
 //
-// CTA (CG = 1, tiles of 128 tokens x up to 128 columns) or CTA pair (CG = 2, 256 x 256) per SM,
-// persistent: 8 epilogue warps, TMA producers, scale warps and an issuer that also allocates tensor
-// memory.  Two accumulators, 256 columns wide at columns 0 and 224: they share 32 columns, which the
-// epilogue reads first, so that the scales find room behind them (480 .. 511) and the next tile's
-// products still start almost at once.
+// Few rows (at most kFuseRows): the feeders round the rows themselves, straight into the operand's
+// shared-memory layout, and the call is one kernel.
+//
+// CTA (CG = 1, tiles of 128 tokens x up to 128 columns) or CTA pair (CG = 2, 256 x up to 256) per SM,
+// persistent: 8 epilogue warps, TMA producers, feeders, and an issuer that also allocates tensor
+// memory.
+//
+// Few tiles (CG = 1): a cluster of CTAs shares a tile, each with some of the groups, and joins the
+// partial sums over distributed shared memory, in the order of the CTAs' ranks.
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "sq_fp8.cuh"
 #include "sq_kernels.h"
@@ -35,27 +41,33 @@ namespace sq {
 enum Fp8Mode { kFp8Fwd = 0, kFp8Gated = 1, kFp8Bwd = 2 };
 
 constexpr int kFChunk = 128;                      // summed values (bytes) of a shared-memory row
-constexpr uint32_t kFSlot1 = 224;                 // second accumulator
-constexpr uint32_t kFScaleCol = 480;              // two buffers of 16 columns: 8 for B, 4 for A
+// Tensor memory: two accumulators from columns 0 and 224 on (0 and 192 where a tile has 256 columns:
+// they share 64), then four buffers of 16 columns with a group's scales, 8 for B and 4 for A.  Fewer
+// buffers would not do: from the end of a group's products to the next scales in its buffer of both
+// CTAs it takes some 2500 cycles, more than a group's products (4480 x 16384 x 6144: 405 us with two,
+// 337 with four).
+constexpr int kFBufs = 4;
+constexpr uint32_t kFScaleCol = 448;
 constexpr uint32_t kFTmemCols = 512;
-constexpr int kFEpiWarps = 8;
 constexpr int kFPatchBytes = 32 * 64;             // a warp's 32 rows x 64 bytes on their way out
-constexpr int kFSfSlots = 4;                      // shared-memory copies of the scale words
-constexpr int kFSfBytes = 512 + 1024;             // of A's 128 rows and of B's 256
+constexpr int kFuseRows = 16;
+constexpr int kFMaxSplit = 8;
 
-template <int CG, int MODE>
+template <int CG, int MODE, bool FUSE>
 struct Fp8Cfg {
-    static constexpr int kProducers = CG == 2 ? 1 : 2;
-    static constexpr int kScaleWarps = CG == 2 ? 2 : 4;
-    static constexpr int kThreads = 32 * (kFEpiWarps + kProducers + kScaleWarps + 1);
+    static constexpr int kEpi = FUSE ? 4 : 8;     // epilogue warps
+    static constexpr int kProducersPerKind = CG == 2 ? 1 : 2;
+    static constexpr int kProducers = (FUSE ? 1 : 2) * kProducersPerKind;     // of the weight, of the rows
+    static constexpr int kSets = FUSE ? 2 : 1;    // of four feeder warps
+    static constexpr int kThreads = 32 * (kEpi + kProducers + 4 * kSets + 1);
     static constexpr int kRing = 192 * 1024;
-    static constexpr int kMaxStages = CG == 2 ? 6 : 24;
+    static constexpr int kMaxStages = CG == 2 ? 12 : 24;
     static constexpr int kPatchOff = kRing;       // (CG = 1: the MMA reads 128 rows of A, up to 16 KB behind the last stage)
-    static constexpr int kSfOff = kPatchOff + kFEpiWarps * kFPatchBytes;
-    static constexpr int kPlanOff = kSfOff + kFSfSlots * kFSfBytes;
-    static constexpr int kBarOff = kPlanOff + (2 * kMaxExperts + 4) * 4;
-    // full, empty, sf_full, sf_empty, acc_full[2], acc_empty, drain
-    static constexpr int kNumBars = 2 * kMaxStages + 2 * kFSfSlots + 4;
+    static constexpr int kPlanOff = kPatchOff + 8 * kFPatchBytes;
+    static constexpr int kFeedOff = kPlanOff + (2 * kMaxExperts + 4) * 4;     // [sets][2][32] words (FUSE)
+    static constexpr int kBarOff = kFeedOff + kSets * 2 * 32 * 4;
+    // full, empty, sf_full, sf_empty, acc_full[2], acc_empty[2], drain, peers, parts
+    static constexpr int kNumBars = 2 * kMaxStages + 2 * kFBufs + 7;
     static constexpr int kSmemBytes = kBarOff + 8 * kNumBars + 16 + 1024;
     // e4m3 x e4m3, e8m0 scales; B N-major backward; 128 CG rows (columns / 8 << 17 comes at run time)
     static constexpr uint32_t kIdesc = (1u << 23) | (MODE == kFp8Bwd ? 1u << 16 : 0u) | ((uint32_t)(8 * CG) << 24);
@@ -65,33 +77,32 @@ struct Fp8Cfg {
 struct Fp8Args {
     const int32_t *offsets;
     const uint32_t *words;    // row scales, [halves * groups, M]
+    const uint16_t *x, *g, *u;   // FUSE: the rows themselves
     const uint8_t *ws[2];     // weight scales, [E, nbs, kbs]
     void *y;
     uint16_t *g_out, *u_out;
     uint32_t *status;
+    uint8_t *zero[3];         // FUSE: outputs whose rows outside every expert become 0
+    int64_t zero_row_bytes[3];
     int64_t M, width;         // rows, and columns of y
-    int E, act, out_bf16;
-    int N;                    // weight rows of an expert (coordinates of TMA boxes)
+    int64_t L;                // length of the summed axis (of one weight)
+    int E, act, out_bf16, finite_check;
     int nbs, kbs;             // blocks of a weight along N and K
     int blocks;               // blocks of the summed axis (of one weight)
     int halves;               // weights that the sum runs through
     int tile;                 // output channels of a tile
-    int a_rows;               // rows of A that a stage reserves (CG = 1)
+    int a_rows;               // rows of A that a stage (FUSE: a group) reserves
+    int box;                  // rows of a copy (CG = 1)
     int per;                  // chunks of a stage: 1, 2 or 4
     int stages;
+    int split;                // CTAs of a cluster that share a tile (CG = 1)
+    int slot1;                // column of the second accumulator
 };
 
 template <int CG>
 __device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag, uint32_t *status)
 {
     return CG == 2 ? mbar_wait_cluster(bar, parity, abort_flag, status) : mbar_wait(bar, parity, abort_flag, status);
-}
-
-// bounded wait with acquire at cluster scope
-__device__ __forceinline__ bool fp8_wait_acquire(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag,
-                                                 uint32_t *status)
-{
-    return mbar_wait_cluster(bar, parity, abort_flag, status) && mbar_try_wait_acquire_cluster(bar, parity);
 }
 
 // warp-uniform bounded wait: lane 0 polls, the verdict is broadcast
@@ -132,68 +143,103 @@ __device__ __forceinline__ void store_rows64(const uint32_t (&v)[16], uint8_t *p
     __syncwarp();
 }
 
-// 32 columns of y from fp32 values, as bf16 or fp32; `cols` of them exist
+// 32 columns of y from fp32 values, as bf16 or fp32; `cols` of them exist.  FEW: few rows, whose lanes
+// write theirs directly.
+template <bool FEW>
 __device__ __forceinline__ void store_cols32(const float (&o)[32], uint8_t *patch, int lane, void *y, int64_t row,
                                              int64_t col, int64_t width, int rows, int cols, bool bf16)
 {
     uint32_t v[16];
+    auto out = [&](int64_t size, int from, int bytes) {                // 64 bytes a row
+        uint8_t *dst = reinterpret_cast<uint8_t *>(y) + size * (row * width + col + from);
+        if (FEW) {
+            if (lane < rows)
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+                    if (16 * p < bytes)
+                        *reinterpret_cast<uint4 *>(dst + lane * size * width + 16 * p) =
+                            make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
+        } else {
+            store_rows64(v, patch, lane, dst, size * width, rows, bytes);
+        }
+    };
     if (bf16) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             v[i] = f32x2_to_bf16x2_bits(o[2 * i], o[2 * i + 1]);
-        store_rows64(v, patch, lane, reinterpret_cast<uint8_t *>(y) + 2 * (row * width + col), 2 * width, rows, 2 * cols);
+        out(2, 0, 2 * cols);
     } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 v[i] = __float_as_uint(o[16 * h + i]);
-            store_rows64(v, patch, lane, reinterpret_cast<uint8_t *>(y) + 4 * (row * width + col + 16 * h), 4 * width,
-                         rows, 4 * (cols - 16 * h));
+            out(4, 16 * h, 4 * (cols - 16 * h));
         }
     }
 }
 
-template <int CG, int MODE>
-__global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(Fp8Cfg<CG, MODE>::kThreads, 1)
+// What a group of four blocks is: number g2 of the tile's, of weight `half`.
+struct Fp8Walk {
+    int groups, blocks;       // of one weight
+    int lo, hi;               // the CTA's groups of a tile
+
+    __device__ __forceinline__ void at(int g2, int &half, int &grp, int &live) const
+    {
+        half = g2 >= groups ? 1 : 0;
+        grp = g2 - half * groups;
+        live = min(kFp8Group, blocks - kFp8Group * grp);
+    }
+};
+
+template <int CG, int MODE, bool FUSE>
+__global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
     sq_fp8_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                   const __grid_constant__ CUtensorMap tmW2, const Fp8Args args)
 {
-    using Cfg = Fp8Cfg<CG, MODE>;
+    using Cfg = Fp8Cfg<CG, MODE, FUSE>;
     constexpr bool BWD = MODE == kFp8Bwd, GATED = MODE == kFp8Gated;
+    static_assert(!FUSE || CG == 1, "few rows take tiles of one CTA");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     int32_t *plan_mem = reinterpret_cast<int32_t *>(smem + Cfg::kPlanOff);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kBarOff);
     const uint32_t bar_full = smem_u32(bars);                          // leader: both CTAs' stage ready
     const uint32_t bar_empty = bar_full + 8 * Cfg::kMaxStages;         // each CTA: its stage may be refilled
-    const uint32_t bar_sf_full = bar_empty + 8 * Cfg::kMaxStages;      // leader: both CTAs' scale words ready
-    const uint32_t bar_sf_empty = bar_sf_full + 8 * kFSfSlots;         // each CTA: they have been copied
-    const uint32_t bar_acc_full = bar_sf_empty + 8 * kFSfSlots;        // each CTA: accumulator ready
-    const uint32_t bar_acc_empty = bar_acc_full + 16;                  // leader: the shared columns have been read
-    const uint32_t bar_drain = bar_acc_empty + 8;                      // leader: every MMA finished
+    const uint32_t bar_sf_full = bar_empty + 8 * Cfg::kMaxStages;      // leader: a group's scales (FUSE: and rows) ready
+    const uint32_t bar_sf_empty = bar_sf_full + 8 * kFBufs;            // each CTA: the group's products are done
+    const uint32_t bar_acc_full = bar_sf_empty + 8 * kFBufs;           // each CTA: accumulator ready
+    const uint32_t bar_acc_empty = bar_acc_full + 16;                  // leader: accumulator read
+    const uint32_t bar_drain = bar_acc_empty + 16;                     // leader: every MMA finished
+    const uint32_t bar_peers = bar_drain + 8;                          // split: the other CTAs' rings may be written
+    const uint32_t bar_parts = bar_peers + 8;                          // split: bytes of their sums
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + Cfg::kNumBars);
     volatile uint32_t *abort_flag = tmem_holder + 1;
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
+    const int split = CG == 1 ? args.split : 1;
+    const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;            // in the pair
+    const int part = split > 1 ? (int)cluster_ctarank() : 0;           // of the tile's groups
     const bool leader = rank == 0;
-    constexpr int kProducer = kFEpiWarps, kScale = kProducer + Cfg::kProducers, kIssuer = kScale + Cfg::kScaleWarps;
+    constexpr int kProducer = Cfg::kEpi, kFeeder = kProducer + Cfg::kProducers, kIssuer = kFeeder + 4 * Cfg::kSets;
 
     if (threadIdx.x == 0) {
         for (int st = 0; st < Cfg::kMaxStages; ++st) {
             mbar_init(bar_full + 8 * st, 1);
             mbar_init(bar_empty + 8 * st, 1);
         }
-        for (int i = 0; i < kFSfSlots; ++i) {
-            mbar_init(bar_sf_full + 8 * i, CG);
+        for (int i = 0; i < kFBufs; ++i) {
+            mbar_init(bar_sf_full + 8 * i, 4 * CG);
             mbar_init(bar_sf_empty + 8 * i, 1);
         }
-        mbar_init(bar_acc_full, 1);
-        mbar_init(bar_acc_full + 8, 1);
-        mbar_init(bar_acc_empty, CG * kFEpiWarps);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar_acc_full + 8 * i, 1);
+            mbar_init(bar_acc_empty + 8 * i, CG * Cfg::kEpi);
+        }
         mbar_init(bar_drain, 1);
+        mbar_init(bar_peers, max(split - 1, 1));
+        mbar_init(bar_parts, 1);
         *abort_flag = 0u;
         fence_mbar_init();
     }
@@ -207,123 +253,165 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(Fp8Cfg<CG, MODE>::k
         }
     }
     if (warp == kProducer && lane == 0) {
-        prefetch_tmap(&tmX);
+        if (!FUSE)
+            prefetch_tmap(&tmX);
         prefetch_tmap(&tmW);
         prefetch_tmap(&tmW2);
     }
-    grid_dep_launch();                            // the next call's rounding may be set up
-    // the offsets are an input of the call: they are there before the kernel in front starts
+    // The kernel in front: without FUSE it is this call's rounding, which lets this one start after its
+    // own wait, so that the offsets and the weight are there; with FUSE it can be any.
+    if (FUSE && args.E > 0)
+        grid_dep_wait();
+    grid_dep_launch();                            // the next call may be set up
     I8Plan plan;
     plan.E = args.E > 0 ? args.E : 1;
     plan.start = plan_mem;
     plan.prefix = plan_mem + kMaxExperts + 1;
     plan.wts = (int)((args.width + args.tile - 1) / args.tile);
     plan.tok_tile = 128 * CG;
-    plan.build(args.E > 0 ? args.offsets : nullptr, args.M, threadIdx.x, Cfg::kThreads);
+    if (args.E > 0) {
+        plan.build(args.offsets, args.M, threadIdx.x, Cfg::kThreads);
+    } else if (threadIdx.x == 0) {
+        plan.start[0] = plan.prefix[0] = 0;
+        plan.start[1] = (int32_t)args.M;
+        plan.prefix[1] = (int32_t)((args.M + plan.tok_tile - 1) / plan.tok_tile);
+    }
     tc_fence_before();
-    if (CG == 2)
-        cluster_sync();                           // barriers of both CTAs initialised, TMEM allocated
+    if (CG == 2 || split > 1)
+        cluster_sync();                           // barriers of every CTA initialised, TMEM allocated
     else
         __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
 
     const int tiles = plan.tiles();
-    const int unit = (int)blockIdx.x / CG;
-    const int units = (int)gridDim.x / CG;
+    const int unit = (int)blockIdx.x / (CG * split);
+    const int units = (int)gridDim.x / (CG * split);
     const int per = args.per;
     const int T = args.tile;
-    const int b_rows = GATED ? (CG == 2 ? T : 2 * T) : T / CG;         // rows of B (columns) that this CTA loads
+    const int b_rows = GATED ? (CG == 2 ? T : 2 * T) : T / CG;         // rows (backward: columns) of B in this CTA
     const int cols = GATED ? 2 * T : T;                                // columns of the accumulator
-    const int a_bytes = (CG == 2 ? 128 : args.a_rows) * kFChunk;
-    const int chunk_bytes = a_bytes + (BWD ? 128 : b_rows) * kFChunk;
+    const int a_bytes = args.a_rows * kFChunk;                         // of a chunk
+    const int b_bytes = (BWD ? 128 : b_rows) * kFChunk;
+    const int chunk_bytes = (FUSE ? 0 : a_bytes) + b_bytes;
     const int stage_bytes = per * chunk_bytes;
     const int stages = args.stages;
-    const int half_steps = (args.blocks + per - 1) / per;
-    const int steps = half_steps * args.halves;
-    const int groups = (args.blocks + kFp8Group - 1) / kFp8Group;      // scale words of one weight's summed axis
+    const uint32_t slot1 = (uint32_t)args.slot1;
+    const int shared_chunks = max(cols - (int)slot1, 0) / 32;          // columns that the accumulators share
+    const int ring0 = FUSE ? kFBufs * kFp8Group * a_bytes : 0;         // FUSE: the rows of four groups, then the stages
+    Fp8Walk walk;
+    walk.blocks = args.blocks;
+    walk.groups = (args.blocks + kFp8Group - 1) / kFp8Group;
+    walk.lo = walk.groups * args.halves * part / split;
+    walk.hi = walk.groups * args.halves * (part + 1) / split;
 
-    if (warp >= kProducer && warp < kScale) {
+    if (warp >= kProducer && warp < kFeeder) {
         // ------------------------------------------------------------ producers (every CTA)
-        // Producer p fills stages p, p + P, ... with every P-th step of the unit's work.
-        constexpr int P = Cfg::kProducers;
-        const int p = warp - kProducer;
+        // One warp brings the weight, another the rows (a copy takes a thread some 100 cycles to issue);
+        // with several of a kind each takes every P-th stage.
+        constexpr int P = Cfg::kProducersPerKind;
+        const bool rows_kind = !FUSE && ((warp - kProducer) & 1);
+        const int p = FUSE ? warp - kProducer : (warp - kProducer) >> 1;
         const bool issue = one_lane();
-        const uint32_t s0 = smem_u32(smem);
-        auto boxes_of = [&](const I8Tile &t) { return CG == 2 ? 4 : (t.rows + 31) / 32; };   // of 32 rows
-        auto load_w = [&](int stage, const I8Tile &t, int step) {
-            const uint32_t fb = bar_full + 8 * stage;
-            const int half = step >= half_steps ? 1 : 0;
-            const int x0 = (step - half * half_steps) * per * kFChunk;
-            if (leader)
-                mbar_arrive_expect_tx(fb, CG * per * (boxes_of(t) * 32 + (BWD ? 128 : b_rows)) * kFChunk);
+        const uint32_t s0 = smem_u32(smem) + ring0;
+        // chunks of weight `half` from block `block` on, of tile t
+        auto weight_box = [&](const I8Tile &t, int half, int x, auto &&copy) {
             const int n0 = t.wt * T;
-            for (int u = 0; u < per; ++u) {
-                const uint32_t sB = s0 + stage * stage_bytes + u * chunk_bytes + a_bytes;
-                const int x = x0 + u * kFChunk;
-                if (BWD) {
-                    tma_load_3d<CG>(sB, half ? &tmW2 : &tmW, n0 + (int)rank * 128, x, t.e, fb);
-                } else if (GATED && CG == 1) {
-                    tma_load_3d<CG>(sB, &tmW, x, n0, t.e, fb);
-                    tma_load_3d<CG>(sB + T * kFChunk, &tmW2, x, n0, t.e, fb);
-                } else if (GATED) {
-                    tma_load_3d<CG>(sB, rank ? &tmW2 : &tmW, x, n0, t.e, fb);
-                } else {
-                    tma_load_3d<CG>(sB, &tmW, x, n0 + (int)rank * b_rows, t.e, fb);
-                }
+            if (BWD) {
+                copy(half ? &tmW2 : &tmW, 0, n0 + (int)rank * b_rows, x);
+            } else if (GATED && CG == 1) {
+                copy(&tmW, 0, x, n0);
+                copy(&tmW2, T * kFChunk, x, n0);
+            } else if (GATED) {
+                copy(rank ? &tmW2 : &tmW, 0, x, n0);
+            } else {
+                copy(&tmW, 0, x, n0 + (int)rank * b_rows);
             }
         };
-        auto load_x = [&](int stage, const I8Tile &t, int step) {
-            const uint32_t fb = bar_full + 8 * stage;
-            const int half = step >= half_steps ? 1 : 0;
-            const int x0 = (step - half * half_steps) * per * kFChunk;
-            const int row = t.row0 + half * (int)args.M + (int)rank * 128;
-            const int boxes = boxes_of(t);
-            for (int u = 0; u < per; ++u) {
-                const uint32_t sA = s0 + stage * stage_bytes + u * chunk_bytes;
+        auto load_w = [&](uint32_t dst, uint32_t fb, const I8Tile &t, uint32_t bytes, int half, int block, int chunks) {
+            if (leader)
+                mbar_arrive_expect_tx(fb, chunks * bytes);
+            for (int u = 0; u < chunks; ++u)
+                weight_box(t, half, (block + u) * kFChunk, [&](const CUtensorMap *m, int at, int x, int y) {
+                    tma_load_3d<CG>(dst + u * chunk_bytes + at, m, x, y, t.e, fb);
+                });
+        };
+        auto load_x = [&](uint32_t dst, uint32_t fb, int row, int boxes, int block, int chunks) {
+            for (int u = 0; u < chunks; ++u) {
                 if (CG == 2)
-                    tma_load_2d_pair(sA, &tmX, x0 + u * kFChunk, row, fb);
+                    tma_load_2d_pair(dst + u * chunk_bytes, &tmX, (block + u) * kFChunk, row, fb);
                 else
                     for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(sA + b * 32 * kFChunk, &tmX, x0 + u * kFChunk, row + 32 * b, fb);
+                        tma_load_2d(dst + u * chunk_bytes + b * args.box * kFChunk, &tmX, (block + u) * kFChunk,
+                                    row + b * args.box, fb);
             }
         };
-        int e = 0, early = 0;                     // steps of the first tile whose weight is on its way
-        if (unit < tiles) {
+        // a stage's bytes, of one chunk: both CTAs'
+        auto boxes_of = [&](const I8Tile &t) { return CG == 2 ? 1 : (t.rows + args.box - 1) / args.box; };
+        auto bytes_of = [&](const I8Tile &t) {
+            return (uint32_t)(CG * ((FUSE ? 0 : boxes_of(t) * args.box * kFChunk) + b_bytes));
+        };
+        const uint32_t dst0 = s0 + (FUSE || rows_kind ? 0 : a_bytes);
+        int e = 0, early = 0;                     // stages of the first tile whose weight is on its way
+        if (!rows_kind && unit < tiles && !(FUSE && args.E > 0)) {
             const I8Tile t = plan.find(unit, e);
-            early = min(steps, stages);
-            if (issue)
-                for (int i = p; i < early; i += P)
-                    load_w(i, t, i);
-        }
-        grid_dep_wait();                          // codes and scales of the rows
-        e = 0;
-        int stage = p;
-        uint32_t phase = 0;
-        bool ok = true;
-        int skip = p;                             // steps of the others before this producer's next one
-        for (int tile = unit; ok && tile < tiles; tile += units) {
-            const I8Tile t = plan.find(tile, e);
-            int c = skip;
-            for (; c < steps; c += P) {
-                const bool fresh = early <= p;
-                if (fresh && !mbar_wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag, args.status)) {
-                    ok = false;
-                    break;
-                }
-                early -= P;
-                if (issue) {
-                    if (fresh)
-                        load_w(stage, t, c);
-                    load_x(stage, t, c);
-                }
-                stage += P;
-                if (stage >= stages) {
-                    stage = p;
-                    phase ^= 1u;
+            int n = 0;
+            for (int g2 = walk.lo; g2 < walk.hi && n < stages; ++g2) {
+                int half, grp, live;
+                walk.at(g2, half, grp, live);
+                for (int u = 0; u < live && n < stages; u += per, ++n) {
+                    const int block = kFp8Group * grp + u, chunks = min(per, live - u);
+                    if (!issue || n % P != p)
+                        continue;
+                    if (FUSE)                     // (into L2: the kernel in front may have written the weight)
+                        for (int v = 0; v < chunks; ++v)
+                            weight_box(t, half, (block + v) * kFChunk,
+                                       [&](const CUtensorMap *m, int, int x, int y) { tma_prefetch_3d(m, x, y, t.e); });
+                    else
+                        load_w(dst0 + n * stage_bytes, bar_full + 8 * n, t, bytes_of(t), half, block, chunks);
                 }
             }
-            skip = c - steps;
+            early = FUSE ? 0 : n;
+        }
+        if (!(FUSE && args.E > 0))
+            grid_dep_wait();                      // codes and scales of the rows
+        e = 0;
+        int stage = p, turn = p;                  // turn: stages of the others before this warp's next one
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int tile = unit; ok && tile < tiles; tile += units) {
+            const I8Tile t = plan.find(tile, e);
+            const uint32_t bytes = bytes_of(t);
+            const int boxes = boxes_of(t);
+            for (int g2 = walk.lo; ok && g2 < walk.hi; ++g2) {
+                int half, grp, live;
+                walk.at(g2, half, grp, live);
+                const int row = t.row0 + half * (int)args.M + (int)rank * 128;
+                for (int u = 0; u < live; u += per) {
+                    if (P > 1 && turn-- != 0)
+                        continue;
+                    turn = P - 1;
+                    const int block = kFp8Group * grp + u, chunks = min(per, live - u);
+                    const uint32_t dst = dst0 + stage * stage_bytes, fb = bar_full + 8 * stage;
+                    if (early > p) {
+                        early -= P;
+                    } else {
+                        if (!mbar_wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag, args.status)) {
+                            ok = false;
+                            break;
+                        }
+                        if (issue && !rows_kind)
+                            load_w(dst, fb, t, bytes, half, block, chunks);
+                    }
+                    if (issue && rows_kind)
+                        load_x(dst, fb, row, boxes, block, chunks);
+                    stage += P;
+                    if (stage >= stages) {
+                        stage = p;
+                        phase ^= 1u;
+                    }
+                }
+            }
         }
         // let every load that was issued land (and be consumed) before the CTA exits
         for (int st = p; st < stages; st += P) {
@@ -335,161 +423,297 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(Fp8Cfg<CG, MODE>::k
             }
         }
         __syncwarp();
-    } else if (warp >= kScale && warp < kIssuer) {
-        // ------------------------------------------------------------ scale warps (every CTA)
-        // Warp s takes every S-th group of four blocks.  Its words: this CTA's rows of A, all of B's.
-        constexpr int S = Cfg::kScaleWarps;
-        const int s = warp - kScale;
+    } else if (warp >= kFeeder && warp < kIssuer) {
+        // ------------------------------------------------------------ feeders (every CTA)
+        // Warp q of a set writes lanes 32 q .. + 31 of tensor memory, which hold the same words in each
+        // quarter: column j of A line l is row 32 j + l.  Set s takes every S-th group.
+        constexpr int S = Cfg::kSets;
+        const int set = (warp - kFeeder) >> 2, q = warp & 3;
+        const int wq = (warp - kFeeder) & 3;                           // (which of the set's four)
         const uint32_t full_leader = CG == 2 ? mapa_shared(bar_sf_full, 0) : bar_sf_full;
+        const uint32_t sf_lanes = tmem_base + ((uint32_t)(32 * q) << 16) + kFScaleCol;
         const int64_t expert_blocks = (int64_t)args.nbs * args.kbs;
-        grid_dep_wait();
-        int e = 0, next = s, count = 0;           // groups so far
-        bool ok = true;
-        for (int tile = unit; ok && tile < tiles; tile += units) {
-            const I8Tile t = plan.find(tile, e);
-            const int mine = min(max(t.rows - (int)rank * 128, 0), 128);
-            const int n0 = t.wt * T, nb0 = n0 / kFp8Block;
-            for (int g2 = 0; g2 < groups * args.halves; ++g2, ++count) {
-                if (count != next)
-                    continue;
-                next += S;
-                const int half = g2 >= groups ? 1 : 0, grp = g2 - half * groups;
-                const int slot = count % kFSfSlots;
-                uint32_t aw[4], bw[8];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int r = 32 * j + lane;
-                    aw[j] = r < mine ? __ldg(args.words + (int64_t)g2 * args.M + t.row0 + (int)rank * 128 + r) : 0u;
-                }
-                // bytes of the (at most three) blocks that the tile's channels lie in, four along the
-                // sum: lanes 4 b + i; gated: the up projection's at 16 + 4 b + i
-                uint32_t v = 0;
-                {
-                    const int b = (lane >> 2) & 3, ch = nb0 + b, kb = kFp8Group * grp + (lane & 3);
-                    const bool second = GATED ? lane >= 16 : half != 0;
-                    const int nb = BWD ? kb : ch, kk = BWD ? ch : kb;
-                    if (nb < args.nbs && kk < args.kbs)
-                        v = __ldg((second ? args.ws[1] : args.ws[0]) + t.e * expert_blocks + (int64_t)nb * args.kbs + kk);
-                    v <<= 8 * (lane & 3);
-                    v |= __shfl_xor_sync(0xffffffffu, v, 1);
-                    v |= __shfl_xor_sync(0xffffffffu, v, 2);
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int r = 32 * j + lane;
-                    const bool second = GATED && r >= T;
-                    const int ch = n0 + (second ? r - T : r);
-                    bw[j] = __shfl_sync(0xffffffffu, v, 4 * ((ch / kFp8Block - nb0) & 3) + (second ? 16 : 0));
-                }
-                if (!fp8_warp_wait<CG>(bar_sf_empty + 8 * slot, ((uint32_t)(count / kFSfSlots) & 1u) ^ 1u, abort_flag,
-                                       args.status, lane)) {
-                    ok = false;
-                    break;
-                }
-                uint4 *line = reinterpret_cast<uint4 *>(smem + Cfg::kSfOff + slot * kFSfBytes) + lane;
-                line[0] = make_uint4(aw[0], aw[1], aw[2], aw[3]);
-                line[32] = make_uint4(bw[0], bw[1], bw[2], bw[3]);
-                if (CG == 2)
-                    line[64] = make_uint4(bw[4], bw[5], bw[6], bw[7]);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    if (CG == 2)
-                        mbar_arrive_release_cluster(full_leader + 8 * slot);
-                    else
-                        mbar_arrive(full_leader + 8 * slot);
-                }
+        uint32_t *const feeds = reinterpret_cast<uint32_t *>(smem + Cfg::kFeedOff) + 64 * set;
+        if (!(FUSE && args.E > 0))
+            grid_dep_wait();
+        struct Item {
+            I8Tile t;
+            int tile, g2, number, e;
+        };
+        // this set's first or next group
+        auto advance = [&](Item &it, int by) {
+            it.number += by;
+            it.g2 += by;
+            while (it.g2 >= walk.hi) {
+                it.tile += units;
+                if (it.tile >= tiles)
+                    return false;
+                it.t = plan.find(it.tile, it.e);
+                it.g2 -= walk.hi - walk.lo;
             }
+            return true;
+        };
+        constexpr int R = FUSE ? kFuseRows / 4 : 1;                    // rows of a warp fetched in advance
+        struct Raw {
+            uint32_t aw[FUSE ? 1 : 4], v;
+            uint4 x[FUSE ? R : 1][2];
+        };
+        const bool pair_grad = FUSE && BWD && args.g != nullptr;       // the rows: gradients of a gated pair
+        // a lane's 16 values of row r of the item's rows, 0 behind their end
+        auto load16 = [&](const uint16_t *src, const Item &it, int64_t col, int r, uint4 (&a)[2]) {
+            const bool live = r < it.t.rows && col < args.L;
+            const uint4 *ptr = reinterpret_cast<const uint4 *>(src + ((int64_t)it.t.row0 + r) * args.L + col);
+            a[0] = live ? __ldg(ptr) : make_uint4(0u, 0u, 0u, 0u);
+            a[1] = live ? __ldg(ptr + 1) : make_uint4(0u, 0u, 0u, 0u);
+        };
+        auto fetch = [&](const Item &it, Raw &r) {
+            int half, grp, live;
+            walk.at(it.g2, half, grp, live);
+            if constexpr (FUSE) {
+                if (!pair_grad)
+#pragma unroll
+                    for (int i = 0; i < R; ++i)
+                        load16(args.x, it, (int64_t)grp * (kFp8Block * kFp8Group) + 16 * lane, wq + 4 * i, r.x[i]);
+            } else {
+                const int mine = min(max(it.t.rows - (int)rank * 128, 0), 128);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    r.aw[j] = 32 * j + lane < mine ? __ldg(args.words + (int64_t)it.g2 * args.M + it.t.row0 +
+                                                           (int)rank * 128 + 32 * j + lane)
+                                                   : 0u;
+            }
+            // bytes of the (at most three) blocks that the tile's channels lie in, four along the sum:
+            // lanes 4 b + i; gated: the up projection's at 16 + 4 b + i
+            const int ch = it.t.wt * T / kFp8Block + ((lane >> 2) & 3), kb = kFp8Group * grp + (lane & 3);
+            const bool second = GATED ? lane >= 16 : half != 0;
+            const int nb = BWD ? kb : ch, kk = BWD ? ch : kb;
+            r.v = nb < args.nbs && kk < args.kbs
+                      ? (uint32_t)__ldg((second ? args.ws[1] : args.ws[0]) + it.t.e * expert_blocks +
+                                        (int64_t)nb * args.kbs + kk)
+                      : 0u;
+        };
+        bool bad = false;
+        // writes group `cur` to tensor memory (FUSE: and its rows to shared memory); false: gave up
+        auto put = [&](const Item &cur, const Raw &raw) {
+            const int buf = cur.number & (kFBufs - 1);
+            if (!fp8_warp_wait<CG>(bar_sf_empty + 8 * buf, ((uint32_t)(cur.number / kFBufs) & 1u) ^ 1u, abort_flag,
+                                   args.status, lane))
+                return false;
+            uint32_t aw[4] = {0u, 0u, 0u, 0u}, bw[8];
+            if constexpr (FUSE) {
+                // rows wq, wq + 4, ... of the tile, rounded into the operand's layout: rows of 128 bytes,
+                // 16-byte piece i of row r at i ^ (r % 8); a lane has one piece
+                int half, grp, live;
+                walk.at(cur.g2, half, grp, live);
+                const int64_t col = (int64_t)grp * (kFp8Block * kFp8Group) + 16 * lane;
+                uint8_t *dst = smem + buf * (kFp8Group * a_bytes) + (lane >> 3) * a_bytes;
+                const int n = cur.t.rows;
+                // (two in turn: the barrier of the next group lies between a read and the next write)
+                uint32_t *feed = feeds + 32 * ((cur.number / S) & 1);
+                auto round_row = [&](int r, const float (&v)[16]) {
+                    uint32_t byte;
+                    const uint4 c = quantise16(v, byte, bad);
+                    *reinterpret_cast<uint4 *>(dst + r * kFChunk + (((lane & 7) ^ (r & 7)) << 4)) = c;
+                    const uint32_t word = scale_word(byte, lane);
+                    if (lane == 0)
+                        feed[r] = word;
+                };
+                if (pair_grad) {
+                    for (int r = wq; r < n; r += 4) {
+                        uint4 a[3][2];
+                        load16(args.x, cur, col, r, a[0]);
+                        load16(args.g, cur, col, r, a[1]);
+                        load16(args.u, cur, col, r, a[2]);
+                        float v[16], g[16], u[16];
+                        widen8(a[0][0], v, 0);
+                        widen8(a[0][1], v, 8);
+                        widen8(a[1][0], g, 0);
+                        widen8(a[1][1], g, 8);
+                        widen8(a[2][0], u, 0);
+                        widen8(a[2][1], u, 8);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float act, slope;
+                            if (args.act == 0)
+                                act_grad<0>(g[i], act, slope);
+                            else
+                                act_grad<1>(g[i], act, slope);
+                            v[i] = half ? v[i] * act : v[i] * u[i] * slope;
+                        }
+                        round_row(r, v);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < R; ++i)
+                        if (wq + 4 * i < n) {
+                            float v[16];
+                            widen8(raw.x[i][0], v, 0);
+                            widen8(raw.x[i][1], v, 8);
+                            round_row(wq + 4 * i, v);
+                        }
+                    for (int r = wq + 4 * R; r < n; r += 4) {
+                        uint4 a[2];
+                        load16(args.x, cur, col, r, a);
+                        float v[16];
+                        widen8(a[0], v, 0);
+                        widen8(a[1], v, 8);
+                        round_row(r, v);
+                    }
+                }
+                fence_proxy_async_smem();
+                named_barrier_sync(2 + set, 128);          // the set's words and rows are there
+                aw[0] = lane < n ? feed[lane] : 0u;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    aw[j] = raw.aw[j];
+            }
+            uint32_t v = raw.v << (8 * (lane & 3));
+            v |= __shfl_xor_sync(0xffffffffu, v, 1);
+            v |= __shfl_xor_sync(0xffffffffu, v, 2);
+            const int n0 = cur.t.wt * T;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int r = 32 * j + lane;
+                const bool second = GATED && r >= T;
+                const int ch = n0 + (second ? r - T : r);
+                bw[j] = __shfl_sync(0xffffffffu, v, 4 * ((ch / kFp8Block - n0 / kFp8Block) & 3) + (second ? 16 : 0));
+            }
+            tc_fence_after();
+            tmem_st_8cols(sf_lanes + 16 * buf, bw);
+            tmem_st_4cols(sf_lanes + 16 * buf + 8, aw);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 2)
+                    mbar_arrive_cluster(full_leader + 8 * buf);
+                else
+                    mbar_arrive(full_leader + 8 * buf);
+            }
+            return true;
+        };
+        // two groups in turn: the next one's values are on their way while one is written
+        Item one, two;
+        one.tile = unit;
+        one.e = 0;
+        one.g2 = walk.lo;
+        one.number = 0;
+        Raw r1 = {}, r2 = {};
+        bool more = unit < tiles && walk.lo < walk.hi;
+        if (more) {
+            one.t = plan.find(unit, one.e);
+            more = advance(one, set);
         }
+        if (more)
+            fetch(one, r1);
+        while (more) {
+            two = one;
+            more = advance(two, S);
+            if (more)
+                fetch(two, r2);
+            if (!put(one, r1) || !more)
+                break;
+            one = two;
+            more = advance(one, S);
+            if (more)
+                fetch(one, r1);
+            if (!put(two, r2))
+                break;
+        }
+        if (FUSE && args.finite_check && bad)
+            atomicOr(args.status, kStatusNonfinite);
         __syncwarp();
     } else if (warp == kIssuer) {
         // ------------------------------------------------------------ MMA issuer (leader)
         if (leader) {
             const bool issue = one_lane();
-            const uint32_t s0 = smem_u32(smem);
-            const uint64_t dA0 = sdesc_sw128(s0), dB0 = sdesc_sw128(s0 + a_bytes);
-            const uint64_t dS0 = sdesc_sf(s0 + Cfg::kSfOff);
-            const uint32_t stage16 = stage_bytes >> 4, chunk16 = chunk_bytes >> 4;
+            const uint32_t s0 = smem_u32(smem) + ring0;
+            const uint64_t dA = FUSE ? sdesc_sw128(smem_u32(smem)) : sdesc_sw128(s0);
+            const uint32_t dA0 = (uint32_t)dA, dB0 = (uint32_t)sdesc_sw128(s0 + (FUSE ? 0 : a_bytes));
+            const uint32_t desc_hi = (uint32_t)(dA >> 32);
+            const uint32_t stage16 = stage_bytes >> 4, chunk16 = chunk_bytes >> 4, a16 = a_bytes >> 4;
             const uint32_t idesc0 = Cfg::kIdesc | (uint32_t)(cols >> 3) << 17;
-            int stage = 0;
-            uint32_t phase = 0;
-            uint64_t dA = dA0, dB = dB0;
-            int count = 0, group = 0;
-            bool ok = true;
-            for (int tile = unit; ok && tile < tiles; tile += units, ++count) {
-                const uint32_t acc = tmem_base + ((count & 1) ? kFSlot1 : 0u);
-                // the columns that the previous tile's accumulator shares with this one have been read
-                // (and all of the one before it)
-                if (count >= 1 && !fp8_wait<CG>(bar_acc_empty, (uint32_t)((count - 1) & 1), abort_flag, args.status))
-                    break;
-                tc_fence_after();
-                for (int c = 0; c < steps && ok; ++c) {
-                    const int kb0 = (c >= half_steps ? c - half_steps : c) * per;
-                    if (!fp8_wait<CG>(bar_full + 8 * stage, phase, abort_flag, args.status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    for (int u = 0; u < per && kb0 + u < args.blocks; ++u) {
-                        const int kb = kb0 + u;
-                        if ((kb & 3) == 0) {               // the next four blocks' scales
-                            const int slot = group % kFSfSlots;
-                            const uint32_t parity = (uint32_t)(group / kFSfSlots) & 1u;
-                            if (!(CG == 2 ? fp8_wait_acquire(bar_sf_full + 8 * slot, parity, abort_flag, args.status)
-                                          : mbar_wait(bar_sf_full + 8 * slot, parity, abort_flag, args.status))) {
-                                ok = false;
+            auto commit = [&](uint32_t bar) {
+                if (CG == 2)
+                    tc_commit2_both(bar);
+                else
+                    tc_commit(bar);
+            };
+            // One thread issues, the warp runs the loops on uniform values.  What lies between two stages'
+            // products is time in which the tensor pipe runs dry (it takes few products in advance), so a
+            // whole group is unrolled, for each number of chunks that a stage can have.
+            auto run = [&](auto chunks) {
+                constexpr int PER = decltype(chunks)::value;
+                int stage = 0;
+                uint32_t phase = 0, off = 0;               // off: the stage's, in 16 bytes
+                uint32_t buf = 0, buf_phase = 0;
+                int count = 0;
+                for (int tile = unit; tile < tiles; tile += units, ++count) {
+                    const uint32_t acc = tmem_base + ((count & 1) ? slot1 : 0u);
+                    // the tile before last (same accumulator) has left tensor memory; where the accumulators
+                    // overlap, the last one's shared columns have (and all of the one before)
+                    const int last = count - (shared_chunks > 0 ? 1 : 2);
+                    if (last >= 0 && !fp8_wait<CG>(bar_acc_empty + 8 * (last & 1), (uint32_t)((last >> 1) & 1),
+                                                   abort_flag, args.status))
+                        return;
+                    uint32_t sum = 0;
+                    int left = walk.blocks - kFp8Group * (walk.lo >= walk.groups ? walk.lo - walk.groups : walk.lo);
+                    for (int g2 = walk.lo; g2 < walk.hi; ++g2) {
+                        if (!fp8_wait<CG>(bar_sf_full + 8 * buf, buf_phase, abort_flag, args.status))
+                            return;
+                        const uint32_t sf = tmem_base + kFScaleCol + 16 * buf;
+#pragma unroll
+                        for (int u0 = 0; u0 < kFp8Group; u0 += PER) {
+                            if (u0 > 0 && u0 >= left)
                                 break;
-                            }
+                            if (!fp8_wait<CG>(bar_full + 8 * stage, phase, abort_flag, args.status))
+                                return;
                             tc_fence_after();
                             if (issue) {
-                                const uint32_t sf = tmem_base + kFScaleCol + 16 * (group & 1);
-                                const uint64_t d = dS0 + (uint32_t)(slot * kFSfBytes >> 4);
-                                if (CG == 2) {
-                                    tmem_cp2_32x128b_x4(sf + 8, d);
-                                    tmem_cp2_32x128b_x4(sf, d + 32);
-                                    tmem_cp2_32x128b_x4(sf + 4, d + 64);
-                                    tc_commit2_both(bar_sf_empty + 8 * slot);
-                                } else {
-                                    tmem_cp_32x128b_x4(sf + 8, d);
-                                    tmem_cp_32x128b_x4(sf, d + 32);
-                                    tc_commit(bar_sf_empty + 8 * slot);
-                                }
-                            }
-                            ++group;
-                        }
-                        if (issue) {
-                            const uint32_t sf = tmem_base + kFScaleCol + 16 * ((group - 1) & 1);
-                            const uint32_t idesc = idesc0 | (uint32_t)(kb & 3) << 4 | (uint32_t)(kb & 3) << 29;
 #pragma unroll
-                            for (int k = 0; k < kFChunk / 32; ++k)
-                                mma_fp8<CG>(acc, dA + u * chunk16 + 2 * k, dB + u * chunk16 + Cfg::kBStep16 * k, idesc,
-                                            sf + 8, sf, (c > 0 || u > 0 || k > 0) ? 1u : 0u);
+                                for (int u = 0; u < PER; ++u) {
+                                    if (u > 0 && u0 + u >= left)
+                                        break;
+                                    const uint32_t idesc = idesc0 | (uint32_t)(u0 + u) << 4 | (uint32_t)(u0 + u) << 29;
+                                    const uint32_t a = FUSE ? dA0 + (buf * kFp8Group + u0 + u) * a16
+                                                            : dA0 + off + u * chunk16;
+                                    const uint32_t b = dB0 + off + u * chunk16;
+#pragma unroll
+                                    for (int k = 0; k < kFChunk / 32; ++k)
+                                        mma_fp8<CG>(acc, a + 2 * k, b + Cfg::kBStep16 * k, desc_hi, idesc, sf + 8, sf,
+                                                    u0 + u + k > 0 ? 1u : sum);
+                                }
+                                commit(bar_empty + 8 * stage);
+                            }
+                            off += stage16;
+                            if (++stage == stages) {
+                                stage = 0;
+                                off = 0;
+                                phase ^= 1u;
+                            }
                         }
+                        if (issue)
+                            commit(bar_sf_empty + 8 * buf);
+                        sum = 1u;
+                        if (++buf == (uint32_t)kFBufs) {
+                            buf = 0;
+                            buf_phase ^= 1u;
+                        }
+                        left -= kFp8Group;
+                        if (left <= 0)
+                            left = walk.blocks;            // the second weight's
                     }
-                    if (!ok)
-                        break;
-                    if (issue) {
-                        if (CG == 2)
-                            tc_commit2_both(bar_empty + 8 * stage);
-                        else
-                            tc_commit(bar_empty + 8 * stage);
-                    }
-                    dA += stage16;
-                    dB += stage16;
-                    if (++stage == stages) {
-                        stage = 0;
-                        dA = dA0;
-                        dB = dB0;
-                        phase ^= 1u;
-                    }
+                    if (issue)
+                        commit(bar_acc_full + 8 * (count & 1));
                 }
-                if (ok && issue) {
-                    if (CG == 2)
-                        tc_commit2_both(bar_acc_full + 8 * (count & 1));
-                    else
-                        tc_commit(bar_acc_full + 8 * (count & 1));
-                }
-            }
+            };
+            if (per == 1)
+                run(std::integral_constant<int, 1>());
+            else if (per == 2)
+                run(std::integral_constant<int, 2>());
+            else
+                run(std::integral_constant<int, 4>());
             // all issued MMAs must finish before tensor memory is released
             if (issue) {
                 if (CG == 2)
@@ -503,95 +727,189 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(Fp8Cfg<CG, MODE>::k
     } else {
         // ------------------------------------------------------------ epilogue (every CTA)
         // Warp w: lanes 32 (w % 4) .. + 31, the first (w < 4) or second half of the tile's channels, 32
-        // at a time, from the end that the other accumulator shares.
-        const int wq = warp & 3, wh = warp >> 2;
+        // at a time.
+        const int wq = warp & 3, wh = warp >> 2;          // (four epilogue warps: all of the channels)
         const uint32_t acc_empty_leader = CG == 2 ? mapa_shared(bar_acc_empty, 0) : bar_acc_empty;
         uint8_t *patch = smem + Cfg::kPatchOff + warp * kFPatchBytes;
         const bool ybf = args.out_bf16 != 0;
-        const int chunks = (T + 31) / 32, c_first = wh ? (chunks + 1) / 2 : 0;
-        const int own = wh ? chunks - c_first : (chunks + 1) / 2;
-        int count = 0, e = 0;
-        grid_dep_wait();
-        for (int tile = unit; tile < tiles; tile += units, ++count) {
-            const I8Tile t = plan.find(tile, e);
-            const int slot = count & 1;
-            if (!fp8_warp_wait<CG>(bar_acc_full + 8 * slot, (uint32_t)((count >> 1) & 1), abort_flag, args.status, lane))
-                break;
-            tc_fence_after();
-            const uint32_t acc = tmem_base + ((uint32_t)(32 * wq) << 16) + (slot ? kFSlot1 : 0u);
-            const int first_row = (int)rank * 128 + 32 * wq;
-            const int rows = min(t.rows - first_row, 32);              // (may be negative)
-            const int64_t row = (int64_t)t.row0 + first_row;
-            auto release = [&]() {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (CG == 2)
-                        mbar_arrive_cluster(acc_empty_leader);
-                    else
-                        mbar_arrive(acc_empty_leader);
-                }
-            };
-            if (own == 0)
-                release();
-            for (int i = 0; i < own; ++i) {
-                const int c = 32 * (c_first + (slot ? i : own - 1 - i));
-                const int64_t col = (int64_t)t.wt * T + c;
-                const int64_t left = args.width - col;
-                const int live = (int)min((int64_t)min(T - c, 32), left);
+        const int chunks = (T + 31) / 32, half_chunks = Cfg::kEpi == 4 ? chunks : (chunks + 1) / 2;
+        const int c_first = wh * half_chunks, own = wh ? chunks - half_chunks : half_chunks;
+        // a chunk's 32 columns from fp32 sums (gated: q the up projection's)
+        auto finish = [&](const I8Tile &t, int c, int rows, int64_t row, const float (&r)[32], const float (&q)[GATED ? 32 : 1]) {
+            const int64_t col = (int64_t)t.wt * T + c;
+            const int live = (int)min((int64_t)min(T - c, 32), args.width - col);
+            if (rows <= 0 || live <= 0 || !SQ_DCHECK(row + rows <= args.M && col + live <= args.width, args.status))
+                return;
+            if constexpr (GATED) {
                 float o[32];
-                uint32_t r[32];
-                __syncwarp();
-                if constexpr (GATED) {
-                    uint32_t q[32];
-                    tmem_ld_32cols(acc + c, r);
-                    tmem_ld_32cols(acc + T + c, q);
-                    tmem_wait_ld();
-                    if (i == 0)
-                        release();
-                    if (rows <= 0 || live <= 0)
-                        continue;
-                    if (args.act == 0) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            o[j] = act_value<0>(__uint_as_float(r[j])) * __uint_as_float(q[j]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            o[j] = act_value<1>(__uint_as_float(r[j])) * __uint_as_float(q[j]);
-                    }
-                    if (args.g_out) {
-                        float f[32];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            f[j] = __uint_as_float(r[j]);
-                        store_cols32(f, patch, lane, args.g_out, row, col, args.width, rows, live, true);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            f[j] = __uint_as_float(q[j]);
-                        store_cols32(f, patch, lane, args.u_out, row, col, args.width, rows, live, true);
-                    }
-                } else {
-                    tmem_ld_32cols(acc + c, r);
-                    tmem_wait_ld();
-                    if (i == 0)
-                        release();
-                    if (rows <= 0 || live <= 0)
-                        continue;
+                if (args.act == 0) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        o[j] = __uint_as_float(r[j]);
+                        o[j] = act_value<0>(r[j]) * q[j];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        o[j] = act_value<1>(r[j]) * q[j];
                 }
-                if (SQ_DCHECK(row + rows <= args.M && col + live <= args.width, args.status))
-                    store_cols32(o, patch, lane, args.y, row, col, args.width, rows, live, ybf);
+                if (args.g_out) {
+                    store_cols32<FUSE>(r, patch, lane, args.g_out, row, col, args.width, rows, live, true);
+                    store_cols32<FUSE>(q, patch, lane, args.u_out, row, col, args.width, rows, live, true);
+                }
+                store_cols32<FUSE>(o, patch, lane, args.y, row, col, args.width, rows, live, ybf);
+            } else {
+                store_cols32<FUSE>(r, patch, lane, args.y, row, col, args.width, rows, live, ybf);
             }
+        };
+        auto load_chunk = [&](uint32_t acc, int c, float (&r)[32], float (&q)[GATED ? 32 : 1]) {
+            uint32_t a[32];
+            __syncwarp();
+            tmem_ld_32cols(acc + c, a);
+            if constexpr (GATED) {
+                uint32_t b[32];
+                tmem_ld_32cols(acc + T + c, b);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    q[j] = __uint_as_float(b[j]);
+            } else {
+                tmem_wait_ld();
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                r[j] = __uint_as_float(a[j]);
+        };
+        int count = 0, e = 0;
+        if (!(FUSE && args.E > 0))
+            grid_dep_wait();
+        if (FUSE) {
+            if (blockIdx.x == 0)
+                fp8_begin_call(args.offsets, args.E, args.M, args.finite_check, args.status, threadIdx.x);
+            if (args.E > 0)                                            // rows of no expert: 0
+                for (int k = 0; k < 3; ++k) {
+                    if (!args.zero[k])
+                        continue;
+                    const int64_t n16 = args.zero_row_bytes[k] / 16, lo = plan.start[0], hi = plan.start[args.E];
+                    for (int64_t m = 0; m < args.M; ++m)
+                        if (m < lo || m >= hi)
+                            for (int64_t c = (int64_t)blockIdx.x * (32 * Cfg::kEpi) + threadIdx.x; c < n16;
+                                 c += (int64_t)gridDim.x * (32 * Cfg::kEpi))
+                                *reinterpret_cast<uint4 *>(args.zero[k] + m * args.zero_row_bytes[k] + 16 * c) =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                }
+        }
+        if (split == 1) {
+            for (int tile = unit; tile < tiles; tile += units, ++count) {
+                const I8Tile t = plan.find(tile, e);
+                const int slot = count & 1;
+                if (!fp8_warp_wait<CG>(bar_acc_full + 8 * slot, (uint32_t)((count >> 1) & 1), abort_flag, args.status, lane))
+                    break;
+                tc_fence_after();
+                const uint32_t acc = tmem_base + ((uint32_t)(32 * wq) << 16) + (slot ? slot1 : 0u);
+                const int first_row = (int)rank * 128 + 32 * wq;
+                const int rows = min(t.rows - first_row, 32);          // (may be negative)
+                auto release = [&]() {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (CG == 2)
+                            mbar_arrive_cluster(acc_empty_leader + 8 * slot);
+                        else
+                            mbar_arrive(acc_empty_leader + 8 * slot);
+                    }
+                };
+                // overlapping accumulators: the chunks that they share first (the last of the one at column
+                // 0, the first of the other), then the next tile may start
+                const int held = rows <= 0 ? 0 : shared_chunks > 0 ? min(shared_chunks, own) : own;
+                if (held == 0)
+                    release();
+                if (rows > 0)
+                    for (int i = 0; i < own; ++i) {
+                        const int c = 32 * (c_first + (slot ? i : own - 1 - i));
+                        float r[32], q[GATED ? 32 : 1];
+                        load_chunk(acc, c, r, q);
+                        if (i == held - 1)
+                            release();
+                        finish(t, c, rows, (int64_t)t.row0 + first_row, r, q);
+                    }
+            }
+        } else if (fp8_warp_wait<CG>(bar_acc_full, 0, abort_flag, args.status, lane)) {
+            // One tile a cluster.  Chunk c of its columns is finished by CTA c % split, to which the others
+            // send theirs, into the ring: a CTA whose products are done tells the others that its ring is
+            // free.
+            constexpr int kParts = GATED ? 2 : 1;
+            tc_fence_after();
+            const I8Tile t = plan.find(unit, e);
+            const uint32_t acc = tmem_base + ((uint32_t)(32 * wq) << 16);
+            const int rows = min(t.rows - 32 * wq, 32);
+            const int mine = (chunks - part + split - 1) / split;      // chunks that this CTA finishes
+            if (warp == 0) {
+                if (lane < split && lane != part)
+                    mbar_arrive_cluster(mapa_shared(bar_peers, lane));
+                if (lane == 0)
+                    mbar_arrive_expect_tx(bar_parts, mine * (split - 1) * t.rows * 128 * kParts);
+            }
+            // place of a chunk's part from CTA `from`: [chunk / split][from][gate, up][quarter][8][32 lanes] float4
+            auto place = [&](int c, int from, int which) {
+                return (uint32_t)(((((c / split) * split + from) * kParts + which) * 4 + wq) * 8 * 32 + lane) * 16u;
+            };
+            const uint32_t s0 = smem_u32(smem);
+            bool ok = fp8_warp_wait<2>(bar_peers, 0, abort_flag, args.status, lane);
+            if (ok && rows > 0)
+                for (int i = 0; i < own; ++i) {
+                    const int c = c_first + i, to = c % split;
+                    if (to == part)
+                        continue;
+                    float r[32], q[GATED ? 32 : 1];
+                    load_chunk(acc, 32 * c, r, q);
+                    const uint32_t dst = mapa_shared(s0, to), bar = mapa_shared(bar_parts, to);
+                    if (lane < rows)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            st_async_v4(dst + place(c, part, 0) + j * 512, r + 4 * j, bar);
+                            if constexpr (GATED)
+                                st_async_v4(dst + place(c, part, 1) + j * 512, q + 4 * j, bar);
+                        }
+                }
+            __syncwarp();
+            ok = ok && fp8_warp_wait<2>(bar_parts, 0, abort_flag, args.status, lane);
+            if (ok && rows > 0)
+                for (int i = 0; i < own; ++i) {
+                    const int c = c_first + i;
+                    if (c % split != part)
+                        continue;
+                    float r[32], q[GATED ? 32 : 1];
+                    load_chunk(acc, 32 * c, r, q);
+                    auto join = [&](float *v, int which, int j) {      // four columns: the parts in order
+                        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        for (int from = 0; from < split; ++from) {
+                            const float4 w = from == part ? make_float4(v[0], v[1], v[2], v[3])
+                                                          : *reinterpret_cast<const float4 *>(
+                                                                smem + place(c, from, which) + j * 512);
+                            sum.x += w.x;
+                            sum.y += w.y;
+                            sum.z += w.z;
+                            sum.w += w.w;
+                        }
+                        v[0] = sum.x;
+                        v[1] = sum.y;
+                        v[2] = sum.z;
+                        v[3] = sum.w;
+                    };
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        join(r + 4 * j, 0, j);
+                        if constexpr (GATED)
+                            join(q + 4 * j, 1, j);
+                    }
+                    finish(t, 32 * c, rows, (int64_t)t.row0 + 32 * wq, r, q);
+                }
         }
         __syncwarp();
     }
 
     tc_fence_before();
-    if (CG == 2)
-        cluster_meet();                               // no CTA leaves while its peer may still signal it
+    if (CG == 2 || split > 1)
+        cluster_meet();                               // no CTA leaves while another may still signal it
     else
         __syncthreads();
     tc_fence_after();
@@ -634,118 +952,243 @@ bool byte_map(CUtensorMap *m, const void *base, int64_t inner, int64_t rows, int
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int CG, int MODE>
-cudaError_t launch_fp8(const Fp8GemmLaunch &g, int tile, int sms, cudaStream_t stream)
+// A tile and its split: how a call's tiles are cut (see pick).
+struct Fp8Shape {
+    int cg, tile, split;
+};
+
+// what runs on the device at once: clusters of `split` one-CTA tiles, and CTA pairs
+struct Fp8Room {
+    unsigned long long ctx = 0;
+    int clusters[kFMaxSplit + 1] = {};
+    int pairs = 0;
+};
+constexpr int kMaxDev = 64;
+
+void cluster_attr(cudaLaunchAttribute &at, int size)
 {
-    using Cfg = Fp8Cfg<CG, MODE>;
-    constexpr bool BWD = MODE == kFp8Bwd, GATED = MODE == kFp8Gated;
-    constexpr int kMaxDev = 64;
-    static unsigned long long ctx_seen[kMaxDev];
-    static int resident_units[kMaxDev];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev)
-        return cudaErrorInvalidDevice;
-    const unsigned long long ctx = current_context_id();
-    if (ctx == 0 || ctx_seen[dev] != ctx) {
-        cudaError_t e = cudaFuncSetAttribute(sq_fp8_kernel<CG, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             Cfg::kSmemBytes);
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)size;
+    at.val.clusterDim.y = 1;
+    at.val.clusterDim.z = 1;
+}
+
+template <int CG, int MODE, bool FUSE>
+cudaError_t allow_smem(int dev, unsigned long long ctx)
+{
+    static unsigned long long seen[kMaxDev];
+    if (ctx != 0 && seen[dev] == ctx)
+        return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(sq_fp8_kernel<CG, MODE, FUSE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               Fp8Cfg<CG, MODE, FUSE>::kSmemBytes);
+    if (e == cudaSuccess)
+        seen[dev] = ctx;
+    return e;
+}
+
+// (not every SM finds its partners inside its GPC)
+template <int CG, int MODE>
+int resident_clusters(int size, int sms)
+{
+    using Cfg = Fp8Cfg<CG, MODE, false>;
+    cudaLaunchConfig_t o = {};
+    cudaLaunchAttribute at[1];
+    cluster_attr(at[0], size);
+    o.gridDim = dim3((unsigned)(sms / size * size));
+    o.blockDim = dim3(Cfg::kThreads);
+    o.dynamicSmemBytes = Cfg::kSmemBytes;
+    o.attrs = at;
+    o.numAttrs = 1;
+    int n = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, sq_fp8_kernel<CG, MODE, false>, &o);
+    (void)cudaGetLastError();
+    return e == cudaSuccess && n > 0 && n < sms / size ? n : sms / size;
+}
+
+cudaError_t room_of(int dev, unsigned long long ctx, int sms, const Fp8Room **out)
+{
+    static Fp8Room rooms[kMaxDev];
+    Fp8Room &r = rooms[dev];
+    if (ctx == 0 || r.ctx != ctx) {
+        cudaError_t e = allow_smem<2, kFp8Fwd, false>(dev, ctx);
+        if (e == cudaSuccess)
+            e = allow_smem<1, kFp8Fwd, false>(dev, ctx);
         if (e != cudaSuccess)
             return e;
-        int units = sms / CG;
-        if (CG == 2) {                            // not every SM can pair up inside its GPC
-            cudaLaunchConfig_t q = {};
-            q.gridDim = dim3(2 * units);
-            q.blockDim = dim3(Cfg::kThreads);
-            q.dynamicSmemBytes = Cfg::kSmemBytes;
-            int resident = 0;
-            e = cudaOccupancyMaxActiveClusters(&resident, sq_fp8_kernel<CG, MODE>, &q);
-            (void)cudaGetLastError();
-            if (e == cudaSuccess && resident > 0 && resident < units)
-                units = resident;
-        }
-        resident_units[dev] = units;
-        ctx_seen[dev] = ctx;
+        r.pairs = resident_clusters<2, kFp8Fwd>(2, sms);
+        r.clusters[1] = sms;
+        for (int n = 2; n <= kFMaxSplit; ++n)
+            r.clusters[n] = resident_clusters<1, kFp8Fwd>(n, sms);
+        r.ctx = ctx;
     }
+    *out = &r;
+    return cudaSuccess;
+}
+
+template <int CG, int MODE, bool FUSE>
+cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8Shape &sh, int dev,
+                       unsigned long long ctx, int most_units, cudaStream_t stream)
+{
+    using Cfg = Fp8Cfg<CG, MODE, FUSE>;
+    constexpr bool BWD = MODE == kFp8Bwd, GATED = MODE == kFp8Gated;
+    if (cudaError_t e = allow_smem<CG, MODE, FUSE>(dev, ctx); e != cudaSuccess)
+        return e;
+    const int tile = sh.tile;
     const int64_t Em = g.E > 0 ? g.E : 1;
     const int64_t summed = BWD ? g.N : g.K;
     const int halves = BWD && g.gated ? 2 : 1;
     const int b_rows = BWD ? 128 : GATED ? (CG == 2 ? tile : 2 * tile) : tile / CG;
-    CUtensorMap tmX, tmW, tmW2;
-    const int w_rows = BWD ? 128 : GATED ? tile : tile / CG;
-    bool ok = byte_map(&tmX, g.codes, summed, halves * g.M, 0, CG == 2 ? 128 : 32) &&
-              byte_map(&tmW, g.wcodes[0], g.K, g.N, Em, w_rows);
-    tmW2 = tmW;
-    if (g.gated)
-        ok = ok && byte_map(&tmW2, g.wcodes[1], g.K, g.N, Em, w_rows);
-    if (!ok)
-        return cudaErrorInvalidValue;
     Fp8Args a;
     a.offsets = g.offsets;
     a.words = g.words;
+    a.x = q.x;
+    a.g = q.g;
+    a.u = q.u;
     a.ws[0] = g.wscales[0];
     a.ws[1] = g.gated ? g.wscales[1] : g.wscales[0];
     a.y = g.y;
     a.g_out = g.g_out;
     a.u_out = g.u_out;
     a.status = g.status;
+    for (int i = 0; i < 3; ++i) {
+        a.zero[i] = q.zero[i];
+        a.zero_row_bytes[i] = q.zero_row_bytes[i];
+    }
     a.M = g.M;
     a.width = BWD ? g.K : g.N;
+    a.L = summed;
     a.E = g.E;
     a.act = g.act;
     a.out_bf16 = g.out_bf16;
-    a.N = (int)g.N;
+    a.finite_check = q.finite_check;
     a.nbs = (int)((g.N + kFp8Block - 1) / kFp8Block);
     a.kbs = (int)((g.K + kFp8Block - 1) / kFp8Block);
     a.blocks = (int)((summed + kFp8Block - 1) / kFp8Block);
     a.halves = halves;
     a.tile = tile;
-    a.a_rows = CG == 2 || g.M >= 128 ? 128 : (int)((g.M + 31) / 32 * 32);
-    a.per = 1;
-    const int chunk = (a.a_rows + b_rows) * kFChunk;
+    a.a_rows = FUSE ? (int)((g.M + 7) / 8 * 8) : CG == 2 || g.M >= 128 ? 128 : (int)((g.M + 31) / 32 * 32);
+    const int cols = GATED ? 2 * tile : tile;
+    a.slot1 = cols > 224 ? 192 : 224;
+    // one copy a chunk, but for experts with few rows
+    a.box = CG == 2 || g.E <= 1 || g.M / g.E > 64 ? a.a_rows : 32;
+    a.split = sh.split;
+    CUtensorMap tmX, tmW, tmW2;
+    const int w_rows = BWD ? 128 : GATED ? tile : tile / CG;
+    bool ok = byte_map(&tmW, g.wcodes[0], g.K, g.N, Em, w_rows);
+    tmX = tmW2 = tmW;
+    if (!FUSE)
+        ok = ok && byte_map(&tmX, g.codes, summed, halves * g.M, 0, a.box);
+    if (g.gated)
+        ok = ok && byte_map(&tmW2, g.wcodes[1], g.K, g.N, Em, w_rows);
+    if (!ok)
+        return cudaErrorInvalidValue;
+    // the stages: as many chunks as leave four of them
+    const int ring = Cfg::kRing - (FUSE ? kFBufs * kFp8Group * a.a_rows * kFChunk : 0);
+    const int chunk = ((FUSE ? 0 : a.a_rows) + b_rows) * kFChunk;
+    a.per = CG;               // (a pair: with one chunk a stage the tensor pipe is 78 % active, with two 90 %)
     if (CG == 1)
-        while (a.per < 4 && 2 * a.per * chunk * 4 <= Cfg::kRing)
+        while (a.per < 4 && 2 * a.per * chunk * 4 <= ring)
             a.per *= 2;
-    a.stages = Cfg::kRing / (a.per * chunk);
+    a.stages = ring / (a.per * chunk);
     if (a.stages > Cfg::kMaxStages)
         a.stages = Cfg::kMaxStages;
-    a.stages = a.stages / Cfg::kProducers * Cfg::kProducers;
+    a.stages = a.stages / Cfg::kProducersPerKind * Cfg::kProducersPerKind;
+    if (a.stages < Cfg::kProducersPerKind)
+        return cudaErrorInvalidValue;
     // dependent launch: set-up and the first weight tiles overlap the rounding in front
-    int64_t work = (a.width + tile - 1) / tile * ((g.M + 128 * CG - 1) / (128 * CG) + (g.E > 0 ? g.E : 0));
-    const int units = (int)(work < resident_units[dev] ? work : resident_units[dev]);
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cluster_attr(at[1], CG * sh.split);
+    const int64_t work = (a.width + tile - 1) / tile * ((g.M + 128 * CG - 1) / (128 * CG) + (g.E > 0 ? g.E : 0));
+    const int units = (int)(work < most_units ? work : most_units);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * CG));
+    cfg.gridDim = dim3((unsigned)(units * CG * sh.split));
     cfg.blockDim = dim3(Cfg::kThreads);
     cfg.dynamicSmemBytes = Cfg::kSmemBytes;
     cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, sq_fp8_kernel<CG, MODE>, tmX, tmW, tmW2, a);
+    cfg.numAttrs = CG * sh.split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, sq_fp8_kernel<CG, MODE, FUSE>, tmX, tmW, tmW2, a);
+}
+
+// How a call's tiles are cut: the candidate with the least time by a simple count of cycles.  A chunk
+// of 128 summed values takes the longer of its products (2 cycles a column) and its copies (about 66
+// bytes a cycle and SM); between overlapping accumulators the products pause; a tile's groups may be shared by a cluster where all tiles run at once.
+Fp8Shape pick(const Fp8GemmLaunch &g, bool fuse, const Fp8Room &room)
+{
+    const int64_t width = g.bwd ? g.K : g.N, summed = g.bwd ? g.N : g.K;
+    const int weights = g.gated && !g.bwd ? 2 : 1;             // columns of B for an output channel
+    const int64_t groups = fp8_groups(summed) * (g.gated && g.bwd ? 2 : 1);
+    Fp8Shape best = {1, 128 / weights, 1};
+    int64_t best_cost = INT64_MAX;
+    auto offer = [&](int cg, int cols, int split) {
+        const int tile = cols / weights;
+        const int64_t tiles = (g.M + 128 * cg - 1) / (128 * cg) * ((width + tile - 1) / tile);
+        const int64_t units = cg == 2 ? room.pairs : room.clusters[split];
+        const int64_t rounds = (tiles + units - 1) / units;
+        if (split > 1 && rounds > 1)
+            return;
+        const int64_t a = fuse ? 0 : cg == 2 || g.M >= 128 ? 128 : (g.M + 31) / 32 * 32;
+        const int64_t b = g.bwd ? 128 : cols / cg;
+        const int64_t mma = 2 * (cols < 64 ? 64 : cols), copy = (a + b) * kFChunk / 66;
+        const int64_t chunk = mma > copy ? mma : copy;
+        const int64_t cost = rounds * ((groups + split - 1) / split * kFp8Group * chunk + (cols > 224 ? 2500 : 500)) +
+                             (split > 1 ? 1500 : 0);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = {cg, tile, split};
+        }
+    };
+    const int64_t rows = g.E > 1 ? (g.M + g.E - 1) / g.E : g.M;        // (experts: the mean)
+    if (g.E > 0) {
+        if (rows <= 128 || fuse)
+            return {1, 128 / weights, 1};
+        return {2, (g.bwd ? 256 : 224) / weights, 1};
+    }
+    if (!fuse)
+        for (int cols = 256; cols >= 64; cols -= 32)
+            offer(2, cols, 1);
+    const int most = weights == 2 ? 6 : kFMaxSplit;            // (what the ring holds of the others' sums)
+    for (int cols = 128; cols >= (g.bwd ? 128 : 32); cols -= 16 * weights)
+        for (int split = 1; split <= most && split <= groups; ++split)
+            offer(1, cols, split);
+    return best;
+}
+
+template <int CG, bool FUSE>
+cudaError_t launch_mode(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8Shape &sh, int dev,
+                        unsigned long long ctx, int units, cudaStream_t stream)
+{
+    if (g.bwd)
+        return launch_fp8<CG, kFp8Bwd, FUSE>(g, q, sh, dev, ctx, units, stream);
+    return g.gated ? launch_fp8<CG, kFp8Gated, FUSE>(g, q, sh, dev, ctx, units, stream)
+                   : launch_fp8<CG, kFp8Fwd, FUSE>(g, q, sh, dev, ctx, units, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_fp8_gemm(const Fp8GemmLaunch &g, int sms, cudaStream_t stream)
+bool fp8_rounds_rows(int E, int64_t M)
 {
-    const int64_t rows = g.E > 1 ? (g.M + g.E - 1) / g.E : g.M;        // (experts: the mean)
-    const int64_t width = g.bwd ? g.K : g.N;
-    if (rows > 128) {
-        if (g.bwd)
-            return launch_fp8<2, kFp8Bwd>(g, 256, sms, stream);
-        return g.gated ? launch_fp8<2, kFp8Gated>(g, 128, sms, stream) : launch_fp8<2, kFp8Fwd>(g, 256, sms, stream);
-    }
-    if (g.bwd)
-        return launch_fp8<1, kFp8Bwd>(g, 128, sms, stream);
-    // one CTA: an equal share of the channels for every SM
-    const int most = g.gated ? 64 : 128;
-    int64_t tile = (width + sms - 1) / sms;
-    tile = (tile + 15) / 16 * 16;
-    if (tile > most || g.E > 0)
-        tile = most;
-    return g.gated ? launch_fp8<1, kFp8Gated>(g, (int)tile, sms, stream)
-                   : launch_fp8<1, kFp8Fwd>(g, (int)tile, sms, stream);
+    return M <= (E > 0 ? 32 : kFuseRows);
+}
+
+cudaError_t launch_fp8_gemm(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, int sms, cudaStream_t stream)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev)
+        return cudaErrorInvalidDevice;
+    const unsigned long long ctx = current_context_id();
+    const Fp8Room *room = nullptr;
+    if (cudaError_t e = room_of(dev, ctx, sms, &room); e != cudaSuccess)
+        return e;
+    const bool fuse = fp8_rounds_rows(g.E, g.M);
+    const Fp8Shape sh = pick(g, fuse, *room);
+    if (sh.cg == 2)
+        return launch_mode<2, false>(g, q, sh, dev, ctx, room->pairs, stream);
+    const int units = room->clusters[sh.split];
+    return fuse ? launch_mode<1, true>(g, q, sh, dev, ctx, units, stream)
+                : launch_mode<1, false>(g, q, sh, dev, ctx, units, stream);
 }
 
 }  // namespace sq

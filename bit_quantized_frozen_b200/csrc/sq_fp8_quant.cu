@@ -18,97 +18,7 @@
 
 namespace sq {
 
-constexpr uint32_t kInf = 0x7F800000u;
-constexpr uint32_t kNanCodes = 0x7F7F7F7Fu;
 constexpr int kQuantThreads = 128;
-
-// e8m0 byte of a block from the bits of its largest |r| (finite)
-__device__ __forceinline__ uint32_t fp8_scale_byte(uint32_t amax_bits)
-{
-    const int e = (int)(amax_bits >> 23) - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    return e < 0 ? 0u : (uint32_t)e;
-}
-
-// 2^-e as a float (the byte is at most 247)
-__device__ __forceinline__ float fp8_inverse(uint32_t byte)
-{
-    return __uint_as_float((254u - byte) << 23);
-}
-
-__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d)
-{
-    uint32_t r;
-    asm("{\n\t.reg .b16 lo, hi;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
-        "mov.b32 %0, {lo, hi};\n\t}"
-        : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
-    return r;
-}
-
-__device__ __forceinline__ void widen8(const uint4 &w, float (&v)[16], int at)
-{
-    const uint32_t p[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[at + 2 * i] = __uint_as_float(p[i] << 16);
-        v[at + 2 * i + 1] = __uint_as_float(p[i] & 0xFFFF0000u);
-    }
-}
-
-// A lane's 16 neighbouring values of a row (8 lanes a block): their codes, and the block's byte.
-__device__ __forceinline__ uint4 quantise16(const float (&v)[16], uint32_t &byte, bool &bad)
-{
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-#pragma unroll
-    for (int x = 1; x <= 4; x <<= 1)
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
-    if (top >= kInf) {
-        bad = true;
-        byte = 127u;
-        return make_uint4(kNanCodes, kNanCodes, kNanCodes, kNanCodes);
-    }
-    byte = fp8_scale_byte(top);
-    const float inv = fp8_inverse(byte);
-    uint32_t c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        c[i] = to_e4m3x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
-    return make_uint4(c[0], c[1], c[2], c[3]);
-}
-
-// a block's byte to the word of its four blocks: lanes 0, 8, 16, 24 hold them
-__device__ __forceinline__ uint32_t scale_word(uint32_t byte, int lane)
-{
-    uint32_t w = byte << (8 * (lane >> 3));
-    w |= __shfl_xor_sync(0xffffffffu, w, 8);
-    w |= __shfl_xor_sync(0xffffffffu, w, 16);
-    return w;
-}
-
-// what the first block does for the whole call: the status word
-__device__ __forceinline__ void fp8_begin_call(const Fp8QuantArgs &a)
-{
-    bool bad = false;
-    if (a.E > 0) {
-        for (int i = threadIdx.x; i <= a.E; i += blockDim.x) {
-            const int32_t o = a.offsets[i];
-            bad |= o < 0 || o > a.M || (i > 0 && o < a.offsets[i - 1]);
-        }
-        bad = __syncthreads_or(bad);
-    }
-    if (threadIdx.x == 0) {
-        if (a.finite_check) {                     // (the word was cleared before the launch)
-            if (bad)
-                atomicOr(a.status, kStatusIndex);
-        } else {
-            *a.status = bad ? kStatusIndex : 0u;
-        }
-    }
-}
 
 // GATED 0: rows of x; 1, 2: the gradients of a gated pair with silu, gelu.  A warp takes ROWS rows x
 // 512 columns at a time, a lane 16 neighbouring values of each row.
@@ -119,7 +29,7 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quant_kernel(const Fp8Quant
     grid_dep_wait();                              // x, and the workspace of the call before
     grid_dep_launch();                            // the product may fetch its first weights
     if (blockIdx.x == 0)
-        fp8_begin_call(a);
+        fp8_begin_call(a.offsets, a.E, a.M, a.finite_check, a.status, threadIdx.x);
     // rows of no expert are not looked at
     int64_t lo = 0, hi = a.M;
     if (a.E > 0) {
@@ -275,7 +185,7 @@ __global__ void __launch_bounds__(256) fp8_build_kernel(const void *__restrict__
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const uint32_t b = __float_as_uint(v[r][i]) & 0x7FFFFFFFu;
-            top = max(top, b < kInf ? b : 0u);
+            top = max(top, b < kFp8Inf ? b : 0u);
         }
     }
     top = __reduce_max_sync(0xffffffffu, top);
@@ -290,7 +200,7 @@ __global__ void __launch_bounds__(256) fp8_build_kernel(const void *__restrict__
     if (threadIdx.x == 0)
         scales[nb * kbs + kb] = (uint8_t)byte;
     auto code = [&](float f) {                    // (the conversion would clamp an infinity)
-        return (__float_as_uint(f) & 0x7FFFFFFFu) >= kInf ? __uint_as_float(0x7FFFFFFFu) : f * inv;
+        return (__float_as_uint(f) & 0x7FFFFFFFu) >= kFp8Inf ? __uint_as_float(0x7FFFFFFFu) : f * inv;
     };
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
