@@ -473,102 +473,125 @@ _FP8 = {}                                # entry point by name, looked up once
 _FP8_ACTS = {"silu": SQ_ACT_SILU, "gelu": SQ_ACT_GELU_TANH}
 
 
-def _fp8_refuse(fn, weights, rows, outs, offsets, ws):
-    """Names what is wrong with the tensors of a block-scaled call (outs: (tensor, name, dtype, shape))."""
-    w = weights[0]
+def _fp8_refuse(fn, weights, rows, outs, offsets, flags, ws):
+    """Names what is wrong with the tensors of a block-scaled call."""
+    w, x = weights[0], rows[0]
     N, K, E = w.N, w.K, getattr(w, "E", None)
-    lead, dev = (() if E is None else (E,)), rows[0][0].get_device()
-    blocks = ((N + 127) // 128, (K + 127) // 128)
+    back, gated = "bwd" in fn, len(weights) == 2
+    lead, dev = (() if E is None else (E,)), x.get_device()
+    names = ("dh", "gate", "up") if gated and back else ("dy",) if back else ("x",)
+    onames = ("dx",) if back else ("h", "g", "u") if gated else ("y",)
     want = [(t, name, dtype, shape) for v in weights
-            for t, name, dtype, shape in ((v.codes, "codes", _E4M3, (*lead, N, K)), (v.scales, "scales", _E8M0, (*lead, *blocks)))]
-    want += rows + outs
-    if offsets is not None:
+            for t, name, dtype, shape in ((v.codes, "codes", _E4M3, (*lead, N, K)),
+                                          (v.scales, "scales", _E8M0, (*lead, (N + 127) // 128, (K + 127) // 128)))]
+    want += [(t, name, _BF16, tuple(x.shape)) for t, name in zip(rows, names)]
+    if E is not None:
+        if not isinstance(offsets, torch.Tensor):
+            raise ValueError(f"{fn}: offsets must be an int32 tensor of {E + 1} values")
         want.append((offsets, "offsets", torch.int32, (E + 1,)))
-    want.append((ws, "ws", None, None))
+    want += [(t, name, _F32 if i == 0 and not flags & SQ_OUT_BF16 else _BF16, (x.shape[0], K if back else N))
+             for i, (t, name) in enumerate(zip(outs, onames)) if i == 0 or t is not None]
+    if ws is not None:
+        want.append((ws, "ws", None, None))
     for t, name, dtype, shape in want:
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{fn}: {name} must be a tensor")
         if dtype is not None and (t.dtype is not dtype or t.shape != shape):
             raise ValueError(f"{fn}: {name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
         if t.get_device() != dev:
-            raise ValueError(f"{fn}: {name} is on {t.device}, {rows[0][1]} on {rows[0][0].device}")
+            raise ValueError(f"{fn}: {name} is on {t.device}, {names[0]} on {x.device}")
         if not t.is_contiguous():
             raise ValueError(f"{fn}: expected a contiguous tensor for {name}")
 
 
-def _fp8(fn, op, weights, rows, offsets, act, outs, flags, ws, stream):
+def _fp8(fn, weights, rows, offsets, act, outs, flags, ws, stream, fresh=False):
     """Checks and call of the block-scaled products.  weights: one Weight or GroupedWeight, or a gated pair;
-    rows: x, dy, or (dh, gate, up); outs: y, dx, or (h, g, u); None among the outs: not wanted."""
+    rows: x, dy, or (dh, gate, up); outs: y, dx, or (h, g, u), None: not wanted.  fresh: outs and ws were
+    made for this call on the rows' device, as the call needs them."""
     w, x = weights[0], rows[0]
     N, K, E = w.N, w.K, getattr(w, "E", None)
-    gated, bwd = len(weights) == 2, "bwd" in fn
+    back = "bwd" in fn
     for v in weights:
         if v.fmt != SQ_FMT_FP8_BLOCK:
             raise ValueError(f"{fn}: the weight must be SQ_FMT_FP8_BLOCK")
         if v.lora_up is not None or v.lora_down is not None:
             raise ValueError(f"{fn}: a block-scaled weight has no low-rank branch")
-    if ("grouped" in fn) != (E is not None):
+        if v.N != N or v.K != K or getattr(v, "E", None) != E:
+            raise ValueError(f"{fn}: the two weights differ in their sizes")
+    if (E is not None) != ("grouped" in fn):
         raise ValueError(f"{fn}: the weight is a {type(w).__name__}")
-    if gated and (weights[1].N != N or weights[1].K != K or getattr(weights[1], "E", None) != E):
-        raise ValueError(f"{fn}: the two weights differ in their sizes")
-    wide, out = (N, K) if bwd else (K, N)
+    wide = N if back else K
     shape = x.shape
     if len(shape) != 2 or shape[1] != wide or x.dtype is not _BF16:
-        raise ValueError(f"{fn}: {('dh' if gated else 'dy') if bwd else 'x'} must be bfloat16 [M, {wide}], "
+        raise ValueError(f"{fn}: {('dh' if len(weights) == 2 else 'dy') if back else 'x'} must be bfloat16 [M, {wide}], "
                          f"got {x.dtype} {list(x.shape)}")
     M, dev = shape[0], x.get_device()
-    lead = () if E is None else (E,)
-    codes, blocks = (*lead, N, K), (*lead, (N + 127) // 128, (K + 127) // 128)
-    ydt, yshape = (_BF16 if flags & SQ_OUT_BF16 else _F32), (M, out)
     # every tensor: its type and shape, on one device, contiguous.  One pass for the usual call; the
     # loop in _fp8_refuse names what is wrong.
-    ok = x.is_contiguous()
-    for v in weights:
-        c, s = v.codes, v.scales
-        ok = (ok and c.dtype is _E4M3 and c.shape == codes and c.get_device() == dev and c.is_contiguous()
-              and s.dtype is _E8M0 and s.shape == blocks and s.get_device() == dev and s.is_contiguous())
-    for t in rows[1:]:
-        ok = ok and t.dtype is _BF16 and t.shape == shape and t.get_device() == dev and t.is_contiguous()
-    y = outs[0]
-    ok = (ok and y is not None and y.dtype is ydt and y.shape == yshape and y.get_device() == dev and y.is_contiguous()
-          and ws is not None and ws.get_device() == dev and ws.is_contiguous())
-    for t in outs[1:]:
-        ok = ok and (t is None or t.dtype is _BF16 and t.shape == yshape and t.get_device() == dev and t.is_contiguous())
-    if E is not None:
-        ok = (ok and isinstance(offsets, torch.Tensor) and offsets.dtype is torch.int32 and offsets.shape == (E + 1,)
-              and offsets.get_device() == dev and offsets.is_contiguous())
+    if E is None:
+        codes, blocks = (N, K), (N + 127 >> 7, K + 127 >> 7)
+    else:
+        codes, blocks = (E, N, K), (E, N + 127 >> 7, K + 127 >> 7)
+    try:
+        ok = x.is_contiguous()
+        args = []
+        for v in weights:
+            c, s = v.codes, v.scales
+            ok = (ok and c.dtype is _E4M3 and c.shape == codes and c.get_device() == dev and c.is_contiguous()
+                  and s.dtype is _E8M0 and s.shape == blocks and s.get_device() == dev and s.is_contiguous())
+            args.append(ctypes.byref(sq_weight(SQ_FMT_FP8_BLOCK, N, K, c.data_ptr(), s.data_ptr())))
+        if E is not None:
+            args.append(E)
+        args.append(x.data_ptr())
+        for t in rows[1:]:
+            ok = ok and t.dtype is _BF16 and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+            args.append(t.data_ptr())
+        args.append(M)
+        if E is not None:
+            ok = (ok and isinstance(offsets, torch.Tensor) and offsets.dtype is torch.int32 and offsets.shape == (E + 1,)
+                  and offsets.get_device() == dev and offsets.is_contiguous())
+        if not fresh:
+            ok = ok and _fp8_outs_fit(outs, (M, K if back else N), flags, ws, dev)
+    except AttributeError:                   # something else than a tensor
+        ok = False
     if not ok:
-        if E is not None and not isinstance(offsets, torch.Tensor):
-            raise ValueError(f"{fn}: offsets must be an int32 tensor of {E + 1} values")
-        names = ("dh", "gate", "up") if gated and bwd else ("dy",) if bwd else ("x",)
-        onames = ("dx",) if bwd else ("h", "g", "u") if gated else ("y",)
-        _fp8_refuse(fn, weights, [(t, n, _BF16, tuple(shape)) for t, n in zip(rows, names)],
-                    [(t, n, ydt if i == 0 else _BF16, yshape) for i, (t, n) in enumerate(zip(outs, onames))
-                     if i == 0 or t is not None], offsets, ws)
+        _fp8_refuse(fn, weights, rows, outs, offsets, flags, ws)
     if dev < 0:
         raise ValueError(f"{fn}: expected a CUDA tensor")
     if dev != torch.cuda.current_device():
         raise ValueError(f"{fn}: the tensors are on {x.device}, the current device is {torch.cuda.current_device()}")
-    if M == 0 and E is not None:
-        return
-    stream = _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
+    if E is not None:
+        if M == 0:
+            return
+        args.append(offsets.data_ptr())
+    if len(weights) == 2:
+        args.append(act)
+    for t in outs:
+        args.append(None if t is None else t.data_ptr())
     f = _FP8.get(fn)
     if f is None:
         f = _FP8[fn] = getattr(lib(), fn)
-    args = [ctypes.byref(sq_weight(SQ_FMT_FP8_BLOCK, N, K, v.codes.data_ptr(), v.scales.data_ptr(), None, None, None))
-            for v in weights]
-    if E is not None:
-        args.append(E)
-    args += [t.data_ptr() for t in rows]
-    args.append(M)
-    if E is not None:
-        args.append(offsets.data_ptr())
-    if gated:
-        args.append(act)
-    args += [None if t is None else t.data_ptr() for t in outs]
-    st = f(*args, flags, ws.data_ptr(), ws.nbytes, stream)
+    stream = _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
+    if ws is None:
+        st = f(*args, flags, None, 0, stream)
+    else:
+        st = f(*args, flags, ws.data_ptr(), ws.nbytes, stream)
     if st != SQ_OK:
         _check(fn, st)
+
+
+def _fp8_outs_fit(outs, shape, flags, ws, dev):
+    """Whether the caller's outputs and workspace are what the call takes (a missing workspace is the library's
+    to judge: few rows need none)."""
+    dtype = _BF16 if flags & SQ_OUT_BF16 else _F32
+    for t in outs:
+        if t is None:
+            if t is outs[0]:
+                return False
+        elif t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+            return False
+        dtype = _BF16
+    return ws is None or ws.get_device() == dev and ws.is_contiguous()
 
 
 def _fp8_act(fn, act):
@@ -591,44 +614,44 @@ def sq_build_fp8(W, codes, scales, stream=None):
 
 
 def sq_linear_fwd_fp8(w: "Weight", x, y, flags: int = 0, ws=None, stream=None):
-    _fp8("sq_linear_fwd_fp8", SQ_OP_LINEAR_FWD_FP8, (w,), (x,), None, 0, (y,), flags, ws, stream)
+    _fp8("sq_linear_fwd_fp8", (w,), (x,), None, 0, (y,), flags, ws, stream)
 
 
 def sq_linear_bwd_dx_fp8(w: "Weight", dy, dx, flags: int = 0, ws=None, stream=None):
-    _fp8("sq_linear_bwd_dx_fp8", SQ_OP_LINEAR_BWD_DX_FP8, (w,), (dy,), None, 0, (dx,), flags, ws, stream)
+    _fp8("sq_linear_bwd_dx_fp8", (w,), (dy,), None, 0, (dx,), flags, ws, stream)
 
 
 def sq_gated_fwd_fp8(w_gate: "Weight", w_up: "Weight", x, h, g=None, u=None, act: str = "silu", flags: int = 0,
                      ws=None, stream=None):
     fn = "sq_gated_fwd_fp8"
-    _fp8(fn, SQ_OP_GATED_FWD_FP8, (w_gate, w_up), (x,), None, _fp8_act(fn, act), (h, g, u), flags, ws, stream)
+    _fp8(fn, (w_gate, w_up), (x,), None, _fp8_act(fn, act), (h, g, u), flags, ws, stream)
 
 
 def sq_gated_bwd_dx_fp8(w_gate: "Weight", w_up: "Weight", dh, g, u, dx, act: str = "silu", flags: int = 0, ws=None,
                         stream=None):
     fn = "sq_gated_bwd_dx_fp8"
-    _fp8(fn, SQ_OP_GATED_BWD_DX_FP8, (w_gate, w_up), (dh, g, u), None, _fp8_act(fn, act), (dx,), flags, ws, stream)
+    _fp8(fn, (w_gate, w_up), (dh, g, u), None, _fp8_act(fn, act), (dx,), flags, ws, stream)
 
 
 def sq_grouped_fwd_fp8(w: "GroupedWeight", x, offsets, y, flags: int = 0, ws=None, stream=None):
-    _fp8("sq_grouped_fwd_fp8", SQ_OP_GROUPED_FWD_FP8, (w,), (x,), offsets, 0, (y,), flags, ws, stream)
+    _fp8("sq_grouped_fwd_fp8", (w,), (x,), offsets, 0, (y,), flags, ws, stream)
 
 
 def sq_grouped_bwd_dx_fp8(w: "GroupedWeight", dy, offsets, dx, flags: int = 0, ws=None, stream=None):
-    _fp8("sq_grouped_bwd_dx_fp8", SQ_OP_GROUPED_BWD_DX_FP8, (w,), (dy,), offsets, 0, (dx,), flags, ws, stream)
+    _fp8("sq_grouped_bwd_dx_fp8", (w,), (dy,), offsets, 0, (dx,), flags, ws, stream)
 
 
 def sq_grouped_gated_fwd_fp8(w_gate: "GroupedWeight", w_up: "GroupedWeight", x, offsets, h, g=None, u=None,
                              act: str = "silu", flags: int = 0, ws=None, stream=None):
     fn = "sq_grouped_gated_fwd_fp8"
-    _fp8(fn, SQ_OP_GROUPED_GATED_FWD_FP8, (w_gate, w_up), (x,), offsets, _fp8_act(fn, act), (h, g, u), flags, ws,
+    _fp8(fn, (w_gate, w_up), (x,), offsets, _fp8_act(fn, act), (h, g, u), flags, ws,
          stream)
 
 
 def sq_grouped_gated_bwd_dx_fp8(w_gate: "GroupedWeight", w_up: "GroupedWeight", dh, g, u, offsets, dx,
                                 act: str = "silu", flags: int = 0, ws=None, stream=None):
     fn = "sq_grouped_gated_bwd_dx_fp8"
-    _fp8(fn, SQ_OP_GROUPED_GATED_BWD_DX_FP8, (w_gate, w_up), (dh, g, u), offsets, _fp8_act(fn, act), (dx,), flags, ws,
+    _fp8(fn, (w_gate, w_up), (dh, g, u), offsets, _fp8_act(fn, act), (dx,), flags, ws,
          stream)
 
 
@@ -899,15 +922,19 @@ def _fp8_out_here(fn, op, weights, rows, offsets, act, save, ws, flags, out_bf16
     M, E = x.shape[0], getattr(w, "E", None)
     width = w.K if "bwd" in fn else w.N
     y = x.new_empty(M, width, dtype=_BF16 if flags & SQ_OUT_BF16 else _F32)
-    if ws is None:
-        ws = x.new_empty(_w8a8_bytes(op, E, M, w.N, w.K), dtype=torch.uint8)
+    fresh = ws is None
+    if fresh:
+        n = _w8a8_bytes(op, E, M, w.N, w.K)
+        if n:
+            ws = x.new_empty(n, dtype=torch.uint8)
     if E is not None:
         flags |= SQ_ZERO_UNGROUPED
-    if act is None:
-        _fp8(fn, op, weights, rows, offsets, 0, (y,), flags, ws, stream)
-        return y
-    outs = (y,) if "bwd" in fn else (y, *((x.new_empty(M, width), x.new_empty(M, width)) if save else (None, None)))
-    _fp8(fn, op, weights, rows, offsets, _fp8_act(fn, act), outs, flags, ws, stream)
+    outs = (y,)
+    if act is not None:
+        act = _fp8_act(fn, act)
+        if "fwd" in fn:
+            outs = (y, x.new_empty(M, width), x.new_empty(M, width)) if save else (y, None, None)
+    _fp8(fn, weights, rows, offsets, act, outs, flags, ws, stream, fresh)
     return outs if save else y
 
 

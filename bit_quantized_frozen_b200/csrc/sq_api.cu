@@ -411,28 +411,29 @@ sq_status fp8_product(const Fp8Call &c, bool gated, uint32_t flags, void *ws, si
         return SQ_ERR_NULL;
     if (c.E > 0 && M == 0)                            // no rows: nothing to do
         return SQ_OK;
-    if (!c.x || !c.y || !ws || (gated && c.bwd && (!c.g || !c.u)) || (c.g_out == nullptr) != (c.u_out == nullptr))
+    const bool fused = sq::fp8_rounds_rows((int)c.E, M);      // (needs no workspace)
+    if (!c.x || !c.y || (!ws && !fused) || (gated && c.bwd && (!c.g || !c.u)) || (c.g_out == nullptr) != (c.u_out == nullptr))
         return SQ_ERR_NULL;
     if (!aligned(c.x, 16) || !aligned(c.y, 16) || !aligned(c.g, 16) || !aligned(c.u, 16) || !aligned(c.g_out, 16) ||
         !aligned(c.u_out, 16) || !aligned(c.offsets, 4) || !aligned(ws, 256))
         return SQ_ERR_ALIGN;
     const Fp8Layout L = fp8_layout(c.bwd, gated, M, N, K);
-    if (ws_bytes < L.total)
+    if (ws && ws_bytes < (fused ? kHeader : L.total))
         return SQ_ERR_WORKSPACE;
     int sms = 0;
     sq_status st = check_device(&sms);
     if (st != SQ_OK)
         return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    uint32_t *status = reinterpret_cast<uint32_t *>(ws_at(ws, 0));
+    uint32_t *status = reinterpret_cast<uint32_t *>(ws);      // NULL: the library's own word
     sq::Fp8QuantArgs q;
     memset(&q, 0, sizeof(q));
     q.x = c.x;
     q.g = c.g;
     q.u = c.u;
     q.offsets = c.offsets;
-    q.codes = ws_at(ws, L.codes);
-    q.words = reinterpret_cast<uint32_t *>(ws_at(ws, L.words));
+    q.codes = fused ? nullptr : ws_at(ws, L.codes);
+    q.words = fused ? nullptr : reinterpret_cast<uint32_t *>(ws_at(ws, L.words));
     q.status = status;
     if (flags & SQ_ZERO_UNGROUPED) {
         q.zero[0] = reinterpret_cast<uint8_t *>(c.y);
@@ -446,11 +447,12 @@ sq_status fp8_product(const Fp8Call &c, bool gated, uint32_t flags, void *ws, si
     q.E = (int)c.E;
     q.act = c.act;
     q.finite_check = (flags & SQ_CHECK_FINITE) ? 1 : 0;
-    // the first block of the rounding writes the status word; with a finite check any block may set
-    // it, so it is cleared first
-    if (q.finite_check)
+    // the first block of the rounding writes the workspace's status word; with a finite check any block
+    // may set it, so it is cleared first.  (The library's word is shared: calls only add to it.)
+    q.keep_status = q.finite_check || !status;
+    if (q.finite_check && status)
         SQ_CUDA(cudaMemsetAsync(status, 0, 4, s), "memset");
-    if (!sq::fp8_rounds_rows((int)c.E, M)) {
+    if (!fused) {
         SQ_CUDA(stage_event(SQ_STAGE_ACT_QUANT, 0, s), "event record");
         SQ_CUDA(sq::launch_fp8_quant(q, sms, s), "e4m3 row rounding");
         SQ_CUDA(stage_event(SQ_STAGE_ACT_QUANT, 1, s), "event record");
@@ -563,11 +565,11 @@ size_t sq_workspace_bytes(int op, int64_t M, int64_t N, int64_t K)
         return i8_layout(true, M, N, K).total;
     case SQ_OP_LINEAR_FWD_FP8:
     case SQ_OP_GATED_FWD_FP8:
-        return fp8_layout(false, false, M, N, K).total;
+        return sq::fp8_rounds_rows(0, M) ? 0 : fp8_layout(false, false, M, N, K).total;
     case SQ_OP_LINEAR_BWD_DX_FP8:
-        return fp8_layout(true, false, M, N, K).total;
+        return sq::fp8_rounds_rows(0, M) ? 0 : fp8_layout(true, false, M, N, K).total;
     case SQ_OP_GATED_BWD_DX_FP8:
-        return fp8_layout(true, true, M, N, K).total;
+        return sq::fp8_rounds_rows(0, M) ? 0 : fp8_layout(true, true, M, N, K).total;
     default:
         return 0;
     }
@@ -584,11 +586,11 @@ size_t sq_grouped_workspace_bytes(int op, int64_t E, int64_t M, int64_t N, int64
         return i8_layout(true, M, N, K).total;
     case SQ_OP_GROUPED_FWD_FP8:
     case SQ_OP_GROUPED_GATED_FWD_FP8:
-        return fp8_layout(false, false, M, N, K).total;
+        return sq::fp8_rounds_rows((int)E, M) ? 0 : fp8_layout(false, false, M, N, K).total;
     case SQ_OP_GROUPED_BWD_DX_FP8:
-        return fp8_layout(true, false, M, N, K).total;
+        return sq::fp8_rounds_rows((int)E, M) ? 0 : fp8_layout(true, false, M, N, K).total;
     case SQ_OP_GROUPED_GATED_BWD_DX_FP8:
-        return fp8_layout(true, true, M, N, K).total;
+        return sq::fp8_rounds_rows((int)E, M) ? 0 : fp8_layout(true, true, M, N, K).total;
     default:
         return 0;
     }

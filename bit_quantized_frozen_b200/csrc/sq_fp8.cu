@@ -55,15 +55,17 @@ constexpr int kFMaxSplit = 8;
 
 template <int CG, int MODE, bool FUSE>
 struct Fp8Cfg {
-    static constexpr int kEpi = FUSE ? 4 : 8;     // epilogue warps
-    static constexpr int kProducersPerKind = CG == 2 ? 1 : 2;
-    static constexpr int kProducers = (FUSE ? 1 : 2) * kProducersPerKind;     // of the weight, of the rows
+    static constexpr int kEpi = FUSE ? 2 : 8;     // epilogue warps
+    static constexpr int kProducers = CG == 2 || FUSE ? 2 : 3;
     static constexpr int kSets = FUSE ? 2 : 1;    // of four feeder warps
     static constexpr int kThreads = 32 * (kEpi + kProducers + 4 * kSets + 1);
-    static constexpr int kRing = 192 * 1024;
+    static constexpr int kRing = (FUSE ? 184 : 192) * 1024;
+    // behind the ring (CG = 1: the MMA reads 128 rows of A, up to 16 KB behind the last stage): patches
+    // of the stores; FUSE: a split tile's sums from the other CTAs
+    static constexpr int kPatchBytes = FUSE ? 24 * 1024 : 8 * kFPatchBytes;
     static constexpr int kMaxStages = CG == 2 ? 12 : 24;
-    static constexpr int kPatchOff = kRing;       // (CG = 1: the MMA reads 128 rows of A, up to 16 KB behind the last stage)
-    static constexpr int kPlanOff = kPatchOff + 8 * kFPatchBytes;
+    static constexpr int kPatchOff = kRing;
+    static constexpr int kPlanOff = kPatchOff + kPatchBytes;
     static constexpr int kFeedOff = kPlanOff + (2 * kMaxExperts + 4) * 4;     // [sets][2][32] words (FUSE)
     static constexpr int kBarOff = kFeedOff + kSets * 2 * 32 * 4;
     // full, empty, sf_full, sf_empty, acc_full[2], acc_empty[2], drain, peers, parts
@@ -86,7 +88,7 @@ struct Fp8Args {
     int64_t zero_row_bytes[3];
     int64_t M, width;         // rows, and columns of y
     int64_t L;                // length of the summed axis (of one weight)
-    int E, act, out_bf16, finite_check;
+    int E, act, out_bf16, finite_check, keep_status;
     int nbs, kbs;             // blocks of a weight along N and K
     int blocks;               // blocks of the summed axis (of one weight)
     int halves;               // weights that the sum runs through
@@ -222,7 +224,12 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
     const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;            // in the pair
     const int part = split > 1 ? (int)cluster_ctarank() : 0;           // of the tile's groups
     const bool leader = rank == 0;
-    constexpr int kProducer = Cfg::kEpi, kFeeder = kProducer + Cfg::kProducers, kIssuer = kFeeder + 4 * Cfg::kSets;
+    // Roles.  A warp reaches the 32 lanes of tensor memory that its number modulo 4 gives: a set of
+    // feeders needs all four, and few rows lie in lanes 0 .. 31 alone.
+    constexpr int kIssuer = FUSE ? 11 : Cfg::kEpi + Cfg::kProducers + 4 * Cfg::kSets;
+    constexpr int kProducer = FUSE ? 9 : Cfg::kEpi, kFeeder = FUSE ? 0 : kProducer + Cfg::kProducers;
+    const bool producer = warp >= kProducer && warp < kProducer + Cfg::kProducers;
+    const bool feeder = warp >= kFeeder && warp < kFeeder + 4 * Cfg::kSets;
 
     if (threadIdx.x == 0) {
         for (int st = 0; st < Cfg::kMaxStages; ++st) {
@@ -305,13 +312,12 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
     walk.lo = walk.groups * args.halves * part / split;
     walk.hi = walk.groups * args.halves * (part + 1) / split;
 
-    if (warp >= kProducer && warp < kFeeder) {
+    if (producer) {
         // ------------------------------------------------------------ producers (every CTA)
-        // One warp brings the weight, another the rows (a copy takes a thread some 100 cycles to issue);
-        // with several of a kind each takes every P-th stage.
-        constexpr int P = Cfg::kProducersPerKind;
-        const bool rows_kind = !FUSE && ((warp - kProducer) & 1);
-        const int p = FUSE ? warp - kProducer : (warp - kProducer) >> 1;
+        // Producer p takes every P-th stage of the unit's work (a copy takes a thread some 100 cycles to
+        // issue, a stage's waiting and counting more).
+        constexpr int P = Cfg::kProducers;
+        const int p = warp - kProducer;
         const bool issue = one_lane();
         const uint32_t s0 = smem_u32(smem) + ring0;
         // chunks of weight `half` from block `block` on, of tile t
@@ -351,9 +357,9 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
         auto bytes_of = [&](const I8Tile &t) {
             return (uint32_t)(CG * ((FUSE ? 0 : boxes_of(t) * args.box * kFChunk) + b_bytes));
         };
-        const uint32_t dst0 = s0 + (FUSE || rows_kind ? 0 : a_bytes);
+        const uint32_t w_off = FUSE ? 0 : a_bytes;
         int e = 0, early = 0;                     // stages of the first tile whose weight is on its way
-        if (!rows_kind && unit < tiles && !(FUSE && args.E > 0)) {
+        if (unit < tiles && !(FUSE && args.E > 0)) {
             const I8Tile t = plan.find(unit, e);
             int n = 0;
             for (int g2 = walk.lo; g2 < walk.hi && n < stages; ++g2) {
@@ -368,7 +374,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                             weight_box(t, half, (block + v) * kFChunk,
                                        [&](const CUtensorMap *m, int, int x, int y) { tma_prefetch_3d(m, x, y, t.e); });
                     else
-                        load_w(dst0 + n * stage_bytes, bar_full + 8 * n, t, bytes_of(t), half, block, chunks);
+                        load_w(s0 + w_off + n * stage_bytes, bar_full + 8 * n, t, bytes_of(t), half, block, chunks);
                 }
             }
             early = FUSE ? 0 : n;
@@ -376,7 +382,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
         if (!(FUSE && args.E > 0))
             grid_dep_wait();                      // codes and scales of the rows
         e = 0;
-        int stage = p, turn = p;                  // turn: stages of the others before this warp's next one
+        int stage = 0, turn = p;                  // turn: stages of the others before this warp's next one
         uint32_t phase = 0;
         bool ok = true;
         for (int tile = unit; ok && tile < tiles; tile += units) {
@@ -388,42 +394,40 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                 walk.at(g2, half, grp, live);
                 const int row = t.row0 + half * (int)args.M + (int)rank * 128;
                 for (int u = 0; u < live; u += per) {
-                    if (P > 1 && turn-- != 0)
-                        continue;
-                    turn = P - 1;
-                    const int block = kFp8Group * grp + u, chunks = min(per, live - u);
-                    const uint32_t dst = dst0 + stage * stage_bytes, fb = bar_full + 8 * stage;
-                    if (early > p) {
-                        early -= P;
-                    } else {
-                        if (!mbar_wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag, args.status)) {
+                    if (--turn < 0) {
+                        turn = P - 1;
+                        const int block = kFp8Group * grp + u, chunks = min(per, live - u);
+                        const uint32_t dst = s0 + stage * stage_bytes, fb = bar_full + 8 * stage;
+                        const bool fresh = early <= 0;
+                        if (fresh && !mbar_wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag, args.status)) {
                             ok = false;
                             break;
                         }
-                        if (issue && !rows_kind)
-                            load_w(dst, fb, t, bytes, half, block, chunks);
+                        if (issue) {
+                            if (fresh)
+                                load_w(dst + w_off, fb, t, bytes, half, block, chunks);
+                            if (!FUSE)
+                                load_x(dst, fb, row, boxes, block, chunks);
+                        }
                     }
-                    if (issue && rows_kind)
-                        load_x(dst, fb, row, boxes, block, chunks);
-                    stage += P;
-                    if (stage >= stages) {
-                        stage = p;
+                    --early;
+                    if (++stage == stages) {
+                        stage = 0;
                         phase ^= 1u;
                     }
                 }
             }
         }
         // let every load that was issued land (and be consumed) before the CTA exits
-        for (int st = p; st < stages; st += P) {
+        for (int st = 0; st < stages; ++st) {
             (void)mbar_wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag, args.status);
-            stage += P;
-            if (stage >= stages) {
-                stage = p;
+            if (++stage == stages) {
+                stage = 0;
                 phase ^= 1u;
             }
         }
         __syncwarp();
-    } else if (warp >= kFeeder && warp < kIssuer) {
+    } else if (feeder) {
         // ------------------------------------------------------------ feeders (every CTA)
         // Warp q of a set writes lanes 32 q .. + 31 of tensor memory, which hold the same words in each
         // quarter: column j of A line l is row 32 j + l.  Set s takes every S-th group.
@@ -728,12 +732,14 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
         // ------------------------------------------------------------ epilogue (every CTA)
         // Warp w: lanes 32 (w % 4) .. + 31, the first (w < 4) or second half of the tile's channels, 32
         // at a time.
-        const int wq = warp & 3, wh = warp >> 2;          // (four epilogue warps: all of the channels)
+        // (FUSE: lanes 0 .. 31, every other chunk.)
+        const int wq = FUSE ? 0 : warp & 3, wh = FUSE ? (warp == 8 ? 0 : 1) : warp >> 2;
         const uint32_t acc_empty_leader = CG == 2 ? mapa_shared(bar_acc_empty, 0) : bar_acc_empty;
         uint8_t *patch = smem + Cfg::kPatchOff + warp * kFPatchBytes;
         const bool ybf = args.out_bf16 != 0;
-        const int chunks = (T + 31) / 32, half_chunks = Cfg::kEpi == 4 ? chunks : (chunks + 1) / 2;
-        const int c_first = wh * half_chunks, own = wh ? chunks - half_chunks : half_chunks;
+        const int chunks = (T + 31) / 32;
+        const int own = (chunks + 1 - wh) / 2;
+        auto chunk_of = [&](int i) { return FUSE ? wh + 2 * i : wh * ((chunks + 1) / 2) + i; };
         // a chunk's 32 columns from fp32 sums (gated: q the up projection's)
         auto finish = [&](const I8Tile &t, int c, int rows, int64_t row, const float (&r)[32], const float (&q)[GATED ? 32 : 1]) {
             const int64_t col = (int64_t)t.wt * T + c;
@@ -782,8 +788,8 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
         if (!(FUSE && args.E > 0))
             grid_dep_wait();
         if (FUSE) {
-            if (blockIdx.x == 0)
-                fp8_begin_call(args.offsets, args.E, args.M, args.finite_check, args.status, threadIdx.x);
+            if (blockIdx.x == 0 && wh == 0)
+                fp8_begin_call(args.offsets, args.E, args.M, args.keep_status, args.status, lane);
             if (args.E > 0)                                            // rows of no expert: 0
                 for (int k = 0; k < 3; ++k) {
                     if (!args.zero[k])
@@ -791,8 +797,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                     const int64_t n16 = args.zero_row_bytes[k] / 16, lo = plan.start[0], hi = plan.start[args.E];
                     for (int64_t m = 0; m < args.M; ++m)
                         if (m < lo || m >= hi)
-                            for (int64_t c = (int64_t)blockIdx.x * (32 * Cfg::kEpi) + threadIdx.x; c < n16;
-                                 c += (int64_t)gridDim.x * (32 * Cfg::kEpi))
+                            for (int64_t c = (int64_t)(2 * blockIdx.x + wh) * 32 + lane; c < n16; c += 64 * (int64_t)gridDim.x)
                                 *reinterpret_cast<uint4 *>(args.zero[k] + m * args.zero_row_bytes[k] + 16 * c) =
                                     make_uint4(0u, 0u, 0u, 0u);
                 }
@@ -824,7 +829,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                     release();
                 if (rows > 0)
                     for (int i = 0; i < own; ++i) {
-                        const int c = 32 * (c_first + (slot ? i : own - 1 - i));
+                        const int c = 32 * chunk_of(slot ? i : own - 1 - i);
                         float r[32], q[GATED ? 32 : 1];
                         load_chunk(acc, c, r, q);
                         if (i == held - 1)
@@ -834,29 +839,32 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
             }
         } else if (fp8_warp_wait<CG>(bar_acc_full, 0, abort_flag, args.status, lane)) {
             // One tile a cluster.  Chunk c of its columns is finished by CTA c % split, to which the others
-            // send theirs, into the ring: a CTA whose products are done tells the others that its ring is
-            // free.
+            // send theirs: few rows into a place of its own, else into the ring, once a CTA whose products
+            // are done has told the others that its ring is free.
             constexpr int kParts = GATED ? 2 : 1;
             tc_fence_after();
             const I8Tile t = plan.find(unit, e);
             const uint32_t acc = tmem_base + ((uint32_t)(32 * wq) << 16);
             const int rows = min(t.rows - 32 * wq, 32);
             const int mine = (chunks - part + split - 1) / split;      // chunks that this CTA finishes
-            if (warp == 0) {
-                if (lane < split && lane != part)
+            if (wq == 0 && wh == 0) {
+                if (!FUSE && lane < split && lane != part)
                     mbar_arrive_cluster(mapa_shared(bar_peers, lane));
                 if (lane == 0)
                     mbar_arrive_expect_tx(bar_parts, mine * (split - 1) * t.rows * 128 * kParts);
             }
-            // place of a chunk's part from CTA `from`: [chunk / split][from][gate, up][quarter][8][32 lanes] float4
+            // place of a chunk's part from CTA `from`: [chunk / split][from][gate, up][quarter][8][lanes] float4
+            constexpr int kLanes = FUSE ? kFuseRows : 32;
+            uint8_t *parts = smem + (FUSE ? Cfg::kPatchOff : 0);
             auto place = [&](int c, int from, int which) {
-                return (uint32_t)(((((c / split) * split + from) * kParts + which) * 4 + wq) * 8 * 32 + lane) * 16u;
+                return (uint32_t)(((((c / split) * split + from) * kParts + which) * (FUSE ? 1 : 4) + wq) * 8 * kLanes + lane) *
+                       16u;
             };
-            const uint32_t s0 = smem_u32(smem);
-            bool ok = fp8_warp_wait<2>(bar_peers, 0, abort_flag, args.status, lane);
+            const uint32_t s0 = smem_u32(parts);
+            bool ok = FUSE || fp8_warp_wait<2>(bar_peers, 0, abort_flag, args.status, lane);
             if (ok && rows > 0)
                 for (int i = 0; i < own; ++i) {
-                    const int c = c_first + i, to = c % split;
+                    const int c = chunk_of(i), to = c % split;
                     if (to == part)
                         continue;
                     float r[32], q[GATED ? 32 : 1];
@@ -865,16 +873,16 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                     if (lane < rows)
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            st_async_v4(dst + place(c, part, 0) + j * 512, r + 4 * j, bar);
+                            st_async_v4(dst + place(c, part, 0) + j * 16 * kLanes, r + 4 * j, bar);
                             if constexpr (GATED)
-                                st_async_v4(dst + place(c, part, 1) + j * 512, q + 4 * j, bar);
+                                st_async_v4(dst + place(c, part, 1) + j * 16 * kLanes, q + 4 * j, bar);
                         }
                 }
             __syncwarp();
             ok = ok && fp8_warp_wait<2>(bar_parts, 0, abort_flag, args.status, lane);
             if (ok && rows > 0)
                 for (int i = 0; i < own; ++i) {
-                    const int c = c_first + i;
+                    const int c = chunk_of(i);
                     if (c % split != part)
                         continue;
                     float r[32], q[GATED ? 32 : 1];
@@ -882,9 +890,9 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                     auto join = [&](float *v, int which, int j) {      // four columns: the parts in order
                         float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                         for (int from = 0; from < split; ++from) {
-                            const float4 w = from == part ? make_float4(v[0], v[1], v[2], v[3])
+                            const float4 w = from == part || lane >= rows ? make_float4(v[0], v[1], v[2], v[3])
                                                           : *reinterpret_cast<const float4 *>(
-                                                                smem + place(c, from, which) + j * 512);
+                                                                parts + place(c, from, which) + j * 16 * kLanes);
                             sum.x += w.x;
                             sum.y += w.y;
                             sum.z += w.z;
@@ -962,6 +970,7 @@ struct Fp8Room {
     unsigned long long ctx = 0;
     int clusters[kFMaxSplit + 1] = {};
     int pairs = 0;
+    uint32_t *status = nullptr;                   // the library's word
 };
 constexpr int kMaxDev = 64;
 
@@ -1013,6 +1022,8 @@ cudaError_t room_of(int dev, unsigned long long ctx, int sms, const Fp8Room **ou
         cudaError_t e = allow_smem<2, kFp8Fwd, false>(dev, ctx);
         if (e == cudaSuccess)
             e = allow_smem<1, kFp8Fwd, false>(dev, ctx);
+        if (e == cudaSuccess)
+            e = library_status_word(&r.status);
         if (e != cudaSuccess)
             return e;
         r.pairs = resident_clusters<2, kFp8Fwd>(2, sms);
@@ -1026,12 +1037,12 @@ cudaError_t room_of(int dev, unsigned long long ctx, int sms, const Fp8Room **ou
 }
 
 template <int CG, int MODE, bool FUSE>
-cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8Shape &sh, int dev,
-                       unsigned long long ctx, int most_units, cudaStream_t stream)
+cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8Shape &sh, int dev, const Fp8Room &room,
+                       cudaStream_t stream)
 {
     using Cfg = Fp8Cfg<CG, MODE, FUSE>;
     constexpr bool BWD = MODE == kFp8Bwd, GATED = MODE == kFp8Gated;
-    if (cudaError_t e = allow_smem<CG, MODE, FUSE>(dev, ctx); e != cudaSuccess)
+    if (cudaError_t e = allow_smem<CG, MODE, FUSE>(dev, room.ctx); e != cudaSuccess)
         return e;
     const int tile = sh.tile;
     const int64_t Em = g.E > 0 ? g.E : 1;
@@ -1049,7 +1060,7 @@ cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8S
     a.y = g.y;
     a.g_out = g.g_out;
     a.u_out = g.u_out;
-    a.status = g.status;
+    a.status = g.status ? g.status : room.status;
     for (int i = 0; i < 3; ++i) {
         a.zero[i] = q.zero[i];
         a.zero_row_bytes[i] = q.zero_row_bytes[i];
@@ -1061,6 +1072,7 @@ cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8S
     a.act = g.act;
     a.out_bf16 = g.out_bf16;
     a.finite_check = q.finite_check;
+    a.keep_status = q.keep_status;
     a.nbs = (int)((g.N + kFp8Block - 1) / kFp8Block);
     a.kbs = (int)((g.K + kFp8Block - 1) / kFp8Block);
     a.blocks = (int)((summed + kFp8Block - 1) / kFp8Block);
@@ -1092,8 +1104,7 @@ cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8S
     a.stages = ring / (a.per * chunk);
     if (a.stages > Cfg::kMaxStages)
         a.stages = Cfg::kMaxStages;
-    a.stages = a.stages / Cfg::kProducersPerKind * Cfg::kProducersPerKind;
-    if (a.stages < Cfg::kProducersPerKind)
+    if (a.stages < 2)
         return cudaErrorInvalidValue;
     // dependent launch: set-up and the first weight tiles overlap the rounding in front
     cudaLaunchAttribute at[2];
@@ -1101,7 +1112,8 @@ cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8S
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cluster_attr(at[1], CG * sh.split);
     const int64_t work = (a.width + tile - 1) / tile * ((g.M + 128 * CG - 1) / (128 * CG) + (g.E > 0 ? g.E : 0));
-    const int units = (int)(work < most_units ? work : most_units);
+    const int64_t most = CG == 2 ? room.pairs : room.clusters[sh.split];
+    const int units = (int)(work < most ? work : most);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * CG * sh.split));
     cfg.blockDim = dim3(Cfg::kThreads);
@@ -1113,7 +1125,7 @@ cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8S
 }
 
 // How a call's tiles are cut: the candidate with the least time by a simple count of cycles.  A chunk
-// of 128 summed values takes the longer of its products (2 cycles a column) and its copies (about 66
+// of 128 summed values takes the longer of its products (2 cycles a column; one CTA: 140 more) and its copies (about 66
 // bytes a cycle and SM); between overlapping accumulators the products pause; a tile's groups may be shared by a cluster where all tiles run at once.
 Fp8Shape pick(const Fp8GemmLaunch &g, bool fuse, const Fp8Room &room)
 {
@@ -1131,10 +1143,10 @@ Fp8Shape pick(const Fp8GemmLaunch &g, bool fuse, const Fp8Room &room)
             return;
         const int64_t a = fuse ? 0 : cg == 2 || g.M >= 128 ? 128 : (g.M + 31) / 32 * 32;
         const int64_t b = g.bwd ? 128 : cols / cg;
-        const int64_t mma = 2 * (cols < 64 ? 64 : cols), copy = (a + b) * kFChunk / 66;
+        const int64_t mma = cg == 2 ? 2 * cols : 140 + 2 * cols, copy = (a + b) * kFChunk / 66;
         const int64_t chunk = mma > copy ? mma : copy;
         const int64_t cost = rounds * ((groups + split - 1) / split * kFp8Group * chunk + (cols > 224 ? 2500 : 500)) +
-                             (split > 1 ? 1500 : 0);
+                             (split == 1 ? 0 : fuse ? 2000 : 5000);
         if (cost < best_cost) {
             best_cost = cost;
             best = {cg, tile, split};
@@ -1158,12 +1170,12 @@ Fp8Shape pick(const Fp8GemmLaunch &g, bool fuse, const Fp8Room &room)
 
 template <int CG, bool FUSE>
 cudaError_t launch_mode(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8Shape &sh, int dev,
-                        unsigned long long ctx, int units, cudaStream_t stream)
+                        const Fp8Room &room, cudaStream_t stream)
 {
     if (g.bwd)
-        return launch_fp8<CG, kFp8Bwd, FUSE>(g, q, sh, dev, ctx, units, stream);
-    return g.gated ? launch_fp8<CG, kFp8Gated, FUSE>(g, q, sh, dev, ctx, units, stream)
-                   : launch_fp8<CG, kFp8Fwd, FUSE>(g, q, sh, dev, ctx, units, stream);
+        return launch_fp8<CG, kFp8Bwd, FUSE>(g, q, sh, dev, room, stream);
+    return g.gated ? launch_fp8<CG, kFp8Gated, FUSE>(g, q, sh, dev, room, stream)
+                   : launch_fp8<CG, kFp8Fwd, FUSE>(g, q, sh, dev, room, stream);
 }
 
 }  // namespace
@@ -1185,10 +1197,8 @@ cudaError_t launch_fp8_gemm(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, int s
     const bool fuse = fp8_rounds_rows(g.E, g.M);
     const Fp8Shape sh = pick(g, fuse, *room);
     if (sh.cg == 2)
-        return launch_mode<2, false>(g, q, sh, dev, ctx, room->pairs, stream);
-    const int units = room->clusters[sh.split];
-    return fuse ? launch_mode<1, true>(g, q, sh, dev, ctx, units, stream)
-                : launch_mode<1, false>(g, q, sh, dev, ctx, units, stream);
+        return launch_mode<2, false>(g, q, sh, dev, *room, stream);
+    return fuse ? launch_mode<1, true>(g, q, sh, dev, *room, stream) : launch_mode<1, false>(g, q, sh, dev, *room, stream);
 }
 
 }  // namespace sq

@@ -126,27 +126,22 @@ __device__ __forceinline__ uint32_t scale_word(uint32_t byte, int lane)
     return w;
 }
 
-// What one block does for the whole call: the status word (its first warp).
-// With a finite check the word was cleared before the launch.
-__device__ __forceinline__ void fp8_begin_call(const int32_t *offsets, int E, int64_t M, int finite_check,
-                                               uint32_t *status, int tid)
+// What one warp does for the whole call: the status word (with `keep` it is only added to).
+__device__ __forceinline__ void fp8_begin_call(const int32_t *offsets, int E, int64_t M, int keep, uint32_t *status,
+                                               int lane)
 {
     bool bad = false;
-    if (tid < 32) {
-        if (E > 0)
-            for (int i = tid; i <= E; i += 32) {
-                const int32_t o = offsets[i];
-                bad |= o < 0 || o > M || (i > 0 && o < offsets[i - 1]);
-            }
-        bad = __any_sync(0xffffffffu, bad);
-        if (tid == 0) {
-            if (finite_check) {
-                if (bad)
-                    atomicOr(status, kStatusIndex);
-            } else {
-                *status = bad ? kStatusIndex : 0u;
-            }
+    if (E > 0)
+        for (int i = lane; i <= E; i += 32) {
+            const int32_t o = offsets[i];
+            bad |= o < 0 || o > M || (i > 0 && o < offsets[i - 1]);
         }
+    bad = __any_sync(0xffffffffu, bad);
+    if (lane == 0) {
+        if (!keep)
+            *status = bad ? kStatusIndex : 0u;
+        else if (bad)
+            atomicOr(status, kStatusIndex);
     }
 }
 

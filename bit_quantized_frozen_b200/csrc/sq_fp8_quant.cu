@@ -28,8 +28,8 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quant_kernel(const Fp8Quant
     const int lane = threadIdx.x & 31;
     grid_dep_wait();                              // x, and the workspace of the call before
     grid_dep_launch();                            // the product may fetch its first weights
-    if (blockIdx.x == 0)
-        fp8_begin_call(a.offsets, a.E, a.M, a.finite_check, a.status, threadIdx.x);
+    if (blockIdx.x == 0 && threadIdx.x < 32)
+        fp8_begin_call(a.offsets, a.E, a.M, a.keep_status, a.status, lane);
     // rows of no expert are not looked at
     int64_t lo = 0, hi = a.M;
     if (a.E > 0) {

@@ -148,6 +148,7 @@ struct Fp8QuantArgs {
     int E;                      // experts, 0: one layer
     int act;                    // gated backward
     int finite_check;           // 1: a NaN or an infinity sets kStatusNonfinite
+    int keep_status;            // 1: the call only adds to the status word
 };
 cudaError_t launch_fp8_quant(const Fp8QuantArgs &a, int sms, cudaStream_t s);
 cudaError_t launch_fp8_build(const void *W, int bf16, int64_t N, int64_t K, uint8_t *codes, uint8_t *scales,
@@ -168,7 +169,7 @@ struct Fp8GemmLaunch {
     void *y;                    // [M, N] (backward [M, K]) fp32 or bf16
     uint16_t *g_out, *u_out;    // gated forward: [M, N] bf16, or NULL
     int out_bf16;
-    uint32_t *status;
+    uint32_t *status;           // NULL (few rows): the library's own word
 };
 cudaError_t launch_fp8_gemm(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, int sms, cudaStream_t stream);
 // whether that kernel rounds the rows itself (few rows: launch_fp8_quant is not called)

@@ -55,6 +55,7 @@ def call(fn, weights, operands, offsets=None, act="silu", bf16=False, flags=0, s
         outs += [Out(M, width, torch.bfloat16, fill) for _ in range(2)]
     op = getattr(sq, "SQ_OP_" + fn[3:].upper())
     n = sq.sq_grouped_workspace_bytes(op, w.E, M, w.N, w.K) if offsets is not None else sq.sq_workspace_bytes(op, M, w.N, w.K)
+    n = max(n, 256)
     ws = guarded(n)
     kw = dict(act=act) if two else {}
     getattr(sq, fn)(*weights, *operands, *(() if offsets is None else (offsets,)), *(o.t for o in outs),
