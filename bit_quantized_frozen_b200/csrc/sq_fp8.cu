@@ -47,11 +47,10 @@ constexpr int kFChunk = 128;                      // summed values (bytes) of a 
 // CTAs it takes some 2500 cycles, more than a group's products (4480 x 16384 x 6144: 405 us with two,
 // 337 with four).
 constexpr int kFBufs = 4;
-constexpr uint32_t kFScaleCol = 448;
-constexpr uint32_t kFTmemCols = 512;
 constexpr int kFPatchBytes = 32 * 64;             // a warp's 32 rows x 64 bytes on their way out
 constexpr int kFuseRows = 16;
 constexpr int kFMaxSplit = 8;
+constexpr int kPrefetchBytes = 64 * 1024;
 
 template <int CG, int MODE, bool FUSE>
 struct Fp8Cfg {
@@ -59,18 +58,20 @@ struct Fp8Cfg {
     static constexpr int kProducers = CG == 2 || FUSE ? 2 : 3;
     static constexpr int kSets = FUSE ? 2 : 1;    // of four feeder warps
     static constexpr int kThreads = 32 * (kEpi + kProducers + 4 * kSets + 1);
-    static constexpr int kRing = (FUSE ? 184 : 192) * 1024;
-    // behind the ring (CG = 1: the MMA reads 128 rows of A, up to 16 KB behind the last stage): patches
-    // of the stores; FUSE: a split tile's sums from the other CTAs
-    static constexpr int kPatchBytes = FUSE ? 24 * 1024 : 8 * kFPatchBytes;
+    static constexpr uint32_t kTmemCols = 512, kScaleCol = 448;
     static constexpr int kMaxStages = CG == 2 ? 12 : 24;
-    static constexpr int kPatchOff = kRing;
-    static constexpr int kPlanOff = kPatchOff + kPatchBytes;
+    // shared memory: the ring, then
+    //   patches of the stores; FUSE: a split tile's sums from the other CTAs.  (CG = 1: the MMA reads
+    //   128 rows of A, up to 16 KB behind the last stage.)
+    static constexpr int kPatchBytes = FUSE ? 12 * 1024 : 8 * kFPatchBytes;
+    static constexpr int kPlanOff = kPatchBytes;
     static constexpr int kFeedOff = kPlanOff + (2 * kMaxExperts + 4) * 4;     // [sets][2][32] words (FUSE)
     static constexpr int kBarOff = kFeedOff + kSets * 2 * 32 * 4;
     // full, empty, sf_full, sf_empty, acc_full[2], acc_empty[2], drain, peers, parts
     static constexpr int kNumBars = 2 * kMaxStages + 2 * kFBufs + 7;
-    static constexpr int kSmemBytes = kBarOff + 8 * kNumBars + 16 + 1024;
+    static constexpr int kRestBytes = kBarOff + 8 * kNumBars + 16;
+    static constexpr int kRing = 192 * 1024;
+    static constexpr int kSmemBytes = kRing + kRestBytes + 1024;
     // e4m3 x e4m3, e8m0 scales; B N-major backward; 128 CG rows (columns / 8 << 17 comes at run time)
     static constexpr uint32_t kIdesc = (1u << 23) | (MODE == kFp8Bwd ? 1u << 16 : 0u) | ((uint32_t)(8 * CG) << 24);
     static constexpr uint32_t kBStep16 = MODE == kFp8Bwd ? (32u * 128u) >> 4 : 2u;   // B descriptor step per MMA
@@ -94,9 +95,10 @@ struct Fp8Args {
     int halves;               // weights that the sum runs through
     int tile;                 // output channels of a tile
     int a_rows;               // rows of A that a stage (FUSE: a group) reserves
-    int box;                  // rows of a copy (CG = 1)
+    int boxed_rows;           // up to so many rows come in boxes of 32
     int per;                  // chunks of a stage: 1, 2 or 4
     int stages;
+    int prefetch;             // FUSE: chunks of a tile fetched into L2 before the kernel in front has ended
     int split;                // CTAs of a cluster that share a tile (CG = 1)
     int slot1;                // column of the second accumulator
 };
@@ -145,38 +147,45 @@ __device__ __forceinline__ void store_rows64(const uint32_t (&v)[16], uint8_t *p
     __syncwarp();
 }
 
-// 32 columns of y from fp32 values, as bf16 or fp32; `cols` of them exist.  FEW: few rows, whose lanes
-// write theirs directly.
-template <bool FEW>
-__device__ __forceinline__ void store_cols32(const float (&o)[32], uint8_t *patch, int lane, void *y, int64_t row,
-                                             int64_t col, int64_t width, int rows, int cols, bool bf16)
+// C neighbouring columns of y from fp32 values, as bf16 or fp32; the first `cols` of them and `rows`
+// rows exist.  32 columns leave through the patch; 16 (few rows) are written by their lanes directly.
+template <int C>
+__device__ __forceinline__ void store_cols(const float (&o)[C], uint8_t *patch, int lane, void *y, int64_t row,
+                                           int64_t col, int64_t width, int rows, int cols, bool bf16)
 {
-    uint32_t v[16];
-    auto out = [&](int64_t size, int from, int bytes) {                // 64 bytes a row
-        uint8_t *dst = reinterpret_cast<uint8_t *>(y) + size * (row * width + col + from);
-        if (FEW) {
-            if (lane < rows)
+    uint8_t *dst = reinterpret_cast<uint8_t *>(y) + (bf16 ? 2 : 4) * (row * width + col);
+    if constexpr (C == 16) {
+        if (lane >= rows)
+            return;
+        dst += (bf16 ? 2 : 4) * width * lane;
+        if (bf16) {
 #pragma unroll
-                for (int p = 0; p < 4; ++p)
-                    if (16 * p < bytes)
-                        *reinterpret_cast<uint4 *>(dst + lane * size * width + 16 * p) =
-                            make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
+            for (int p = 0; p < 2; ++p)
+                if (8 * p < cols)
+                    *reinterpret_cast<uint4 *>(dst + 16 * p) =
+                        make_uint4(f32x2_to_bf16x2_bits(o[8 * p], o[8 * p + 1]), f32x2_to_bf16x2_bits(o[8 * p + 2], o[8 * p + 3]),
+                                   f32x2_to_bf16x2_bits(o[8 * p + 4], o[8 * p + 5]), f32x2_to_bf16x2_bits(o[8 * p + 6], o[8 * p + 7]));
         } else {
-            store_rows64(v, patch, lane, dst, size * width, rows, bytes);
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                if (4 * p < cols)
+                    *reinterpret_cast<float4 *>(dst + 16 * p) = make_float4(o[4 * p], o[4 * p + 1], o[4 * p + 2], o[4 * p + 3]);
         }
-    };
-    if (bf16) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            v[i] = f32x2_to_bf16x2_bits(o[2 * i], o[2 * i + 1]);
-        out(2, 0, 2 * cols);
     } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        uint32_t v[16];
+        if (bf16) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                v[i] = __float_as_uint(o[16 * h + i]);
-            out(4, 16 * h, 4 * (cols - 16 * h));
+                v[i] = f32x2_to_bf16x2_bits(o[2 * i], o[2 * i + 1]);
+            store_rows64(v, patch, lane, dst, 2 * width, rows, 2 * cols);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    v[i] = __float_as_uint(o[16 * h + i]);
+                store_rows64(v, patch, lane, dst + 64 * h, 4 * width, rows, 4 * (cols - 16 * h));
+            }
         }
     }
 }
@@ -196,16 +205,17 @@ struct Fp8Walk {
 
 template <int CG, int MODE, bool FUSE>
 __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
-    sq_fp8_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-                  const __grid_constant__ CUtensorMap tmW2, const Fp8Args args)
+    sq_fp8_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmX32,
+                  const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmW2, const Fp8Args args)
 {
     using Cfg = Fp8Cfg<CG, MODE, FUSE>;
     constexpr bool BWD = MODE == kFp8Bwd, GATED = MODE == kFp8Gated;
     static_assert(!FUSE || CG == 1, "few rows take tiles of one CTA");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    int32_t *plan_mem = reinterpret_cast<int32_t *>(smem + Cfg::kPlanOff);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kBarOff);
+    uint8_t *rest = smem + Cfg::kRing;
+    int32_t *plan_mem = reinterpret_cast<int32_t *>(rest + Cfg::kPlanOff);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(rest + Cfg::kBarOff);
     const uint32_t bar_full = smem_u32(bars);                          // leader: both CTAs' stage ready
     const uint32_t bar_empty = bar_full + 8 * Cfg::kMaxStages;         // each CTA: its stage may be refilled
     const uint32_t bar_sf_full = bar_empty + 8 * Cfg::kMaxStages;      // leader: a group's scales (FUSE: and rows) ready
@@ -252,10 +262,10 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
     }
     if (warp == kIssuer) {
         if (CG == 2) {
-            tmem_alloc2(smem_u32(tmem_holder), kFTmemCols);
+            tmem_alloc2(smem_u32(tmem_holder), Cfg::kTmemCols);
             tmem_relinquish2();
         } else {
-            tmem_alloc(smem_u32(tmem_holder), kFTmemCols);
+            tmem_alloc(smem_u32(tmem_holder), Cfg::kTmemCols);
             tmem_relinquish();
         }
     }
@@ -304,7 +314,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
     const int stage_bytes = per * chunk_bytes;
     const int stages = args.stages;
     const uint32_t slot1 = (uint32_t)args.slot1;
-    const int shared_chunks = max(cols - (int)slot1, 0) / 32;          // columns that the accumulators share
+    const int shared_cols = max(cols - (int)slot1, 0);                 // that the accumulators share
     const int ring0 = FUSE ? kFBufs * kFp8Group * a_bytes : 0;         // FUSE: the rows of four groups, then the stages
     Fp8Walk walk;
     walk.blocks = args.blocks;
@@ -342,30 +352,39 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                     tma_load_3d<CG>(dst + u * chunk_bytes + at, m, x, y, t.e, fb);
                 });
         };
-        auto load_x = [&](uint32_t dst, uint32_t fb, int row, int boxes, int block, int chunks) {
-            for (int u = 0; u < chunks; ++u) {
-                if (CG == 2)
-                    tma_load_2d_pair(dst + u * chunk_bytes, &tmX, (block + u) * kFChunk, row, fb);
-                else
-                    for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(dst + u * chunk_bytes + b * args.box * kFChunk, &tmX, (block + u) * kFChunk,
-                                    row + b * args.box, fb);
-            }
+        // Rows of CTA r of the pair: of one expert at most t.rows.  Up to 96 come in boxes of 32, since an
+        // expert's few rows would otherwise bring as many of the next ones' (and what is not brought is
+        // multiplied all the same: the lanes behind the tile's rows are not looked at).
+        auto live_of = [&](const I8Tile &t, int r) { return min(max(t.rows - 128 * r, 0), 128); };
+        auto rows_brought = [&](int live) { return live > args.boxed_rows ? args.a_rows : (live + 31) / 32 * 32; };
+        auto load_x = [&](uint32_t dst, uint32_t fb, int row, int live, int block, int chunks) {
+            const bool whole = live > args.boxed_rows;
+            for (int u = 0; u < chunks; ++u)
+                for (int b = 0; b < live; b += whole ? 128 : 32) {
+                    const CUtensorMap *m = whole ? &tmX : &tmX32;
+                    if (CG == 2)
+                        tma_load_2d_pair(dst + u * chunk_bytes + b * kFChunk, m, (block + u) * kFChunk, row + b, fb);
+                    else
+                        tma_load_2d(dst + u * chunk_bytes + b * kFChunk, m, (block + u) * kFChunk, row + b, fb);
+                }
         };
         // a stage's bytes, of one chunk: both CTAs'
-        auto boxes_of = [&](const I8Tile &t) { return CG == 2 ? 1 : (t.rows + args.box - 1) / args.box; };
         auto bytes_of = [&](const I8Tile &t) {
-            return (uint32_t)(CG * ((FUSE ? 0 : boxes_of(t) * args.box * kFChunk) + b_bytes));
+            int rows = 0;
+            for (int r = 0; !FUSE && r < CG; ++r)
+                rows += rows_brought(live_of(t, r));
+            return (uint32_t)(rows * kFChunk + CG * b_bytes);
         };
         const uint32_t w_off = FUSE ? 0 : a_bytes;
         int e = 0, early = 0;                     // stages of the first tile whose weight is on its way
         if (unit < tiles && !(FUSE && args.E > 0)) {
             const I8Tile t = plan.find(unit, e);
+            const int most = FUSE ? args.prefetch / per : stages;
             int n = 0;
-            for (int g2 = walk.lo; g2 < walk.hi && n < stages; ++g2) {
+            for (int g2 = walk.lo; g2 < walk.hi && n < most; ++g2) {
                 int half, grp, live;
                 walk.at(g2, half, grp, live);
-                for (int u = 0; u < live && n < stages; u += per, ++n) {
+                for (int u = 0; u < live && n < most; u += per, ++n) {
                     const int block = kFp8Group * grp + u, chunks = min(per, live - u);
                     if (!issue || n % P != p)
                         continue;
@@ -388,7 +407,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
         for (int tile = unit; ok && tile < tiles; tile += units) {
             const I8Tile t = plan.find(tile, e);
             const uint32_t bytes = bytes_of(t);
-            const int boxes = boxes_of(t);
+            const int live_rows = live_of(t, (int)rank);
             for (int g2 = walk.lo; ok && g2 < walk.hi; ++g2) {
                 int half, grp, live;
                 walk.at(g2, half, grp, live);
@@ -407,7 +426,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                             if (fresh)
                                 load_w(dst + w_off, fb, t, bytes, half, block, chunks);
                             if (!FUSE)
-                                load_x(dst, fb, row, boxes, block, chunks);
+                                load_x(dst, fb, row, live_rows, block, chunks);
                         }
                     }
                     --early;
@@ -435,9 +454,9 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
         const int set = (warp - kFeeder) >> 2, q = warp & 3;
         const int wq = (warp - kFeeder) & 3;                           // (which of the set's four)
         const uint32_t full_leader = CG == 2 ? mapa_shared(bar_sf_full, 0) : bar_sf_full;
-        const uint32_t sf_lanes = tmem_base + ((uint32_t)(32 * q) << 16) + kFScaleCol;
+        const uint32_t sf_lanes = tmem_base + ((uint32_t)(32 * q) << 16) + Cfg::kScaleCol;
         const int64_t expert_blocks = (int64_t)args.nbs * args.kbs;
-        uint32_t *const feeds = reinterpret_cast<uint32_t *>(smem + Cfg::kFeedOff) + 64 * set;
+        uint32_t *const feeds = reinterpret_cast<uint32_t *>(rest + Cfg::kFeedOff) + 64 * set;
         if (!(FUSE && args.E > 0))
             grid_dep_wait();
         struct Item {
@@ -457,7 +476,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
             }
             return true;
         };
-        constexpr int R = FUSE ? kFuseRows / 4 : 1;                    // rows of a warp fetched in advance
+        constexpr int R = FUSE ? 2 : 1;                    // rows of a warp fetched in advance
         struct Raw {
             uint32_t aw[FUSE ? 1 : 4], v;
             uint4 x[FUSE ? R : 1][2];
@@ -514,7 +533,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                 const int n = cur.t.rows;
                 // (two in turn: the barrier of the next group lies between a read and the next write)
                 uint32_t *feed = feeds + 32 * ((cur.number / S) & 1);
-                auto round_row = [&](int r, const float (&v)[16]) {
+                auto round_row = [&](int r, const auto &v) {
                     uint32_t byte;
                     const uint4 c = quantise16(v, byte, bad);
                     *reinterpret_cast<uint4 *>(dst + r * kFChunk + (((lane & 7) ^ (r & 7)) << 4)) = c;
@@ -528,21 +547,20 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                         load16(args.x, cur, col, r, a[0]);
                         load16(args.g, cur, col, r, a[1]);
                         load16(args.u, cur, col, r, a[2]);
-                        float v[16], g[16], u[16];
-                        widen8(a[0][0], v, 0);
-                        widen8(a[0][1], v, 8);
-                        widen8(a[1][0], g, 0);
-                        widen8(a[1][1], g, 8);
-                        widen8(a[2][0], u, 0);
-                        widen8(a[2][1], u, 8);
+                        float v[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
+                        for (int i = 0; i < 16; ++i) {             // (bf16 pairs: value i in half i & 1)
+                            auto pick = [&](const uint4 (&w)[2]) {
+                                const uint4 &h = w[i >> 3];
+                                const uint32_t b = (i >> 1 & 3) == 0 ? h.x : (i >> 1 & 3) == 1 ? h.y : (i >> 1 & 3) == 2 ? h.z : h.w;
+                                return __uint_as_float(i & 1 ? b & 0xFFFF0000u : b << 16);
+                            };
                             float act, slope;
                             if (args.act == 0)
-                                act_grad<0>(g[i], act, slope);
+                                act_grad<0>(pick(a[1]), act, slope);
                             else
-                                act_grad<1>(g[i], act, slope);
-                            v[i] = half ? v[i] * act : v[i] * u[i] * slope;
+                                act_grad<1>(pick(a[1]), act, slope);
+                            v[i] = half ? pick(a[0]) * act : pick(a[0]) * pick(a[2]) * slope;
                         }
                         round_row(r, v);
                     }
@@ -550,18 +568,12 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < R; ++i)
                         if (wq + 4 * i < n) {
-                            float v[16];
-                            widen8(raw.x[i][0], v, 0);
-                            widen8(raw.x[i][1], v, 8);
-                            round_row(wq + 4 * i, v);
+                            round_row(wq + 4 * i, raw.x[i]);
                         }
                     for (int r = wq + 4 * R; r < n; r += 4) {
                         uint4 a[2];
                         load16(args.x, cur, col, r, a);
-                        float v[16];
-                        widen8(a[0], v, 0);
-                        widen8(a[1], v, 8);
-                        round_row(r, v);
+                        round_row(r, a);
                     }
                 }
                 fence_proxy_async_smem();
@@ -597,33 +609,45 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
             }
             return true;
         };
-        // two groups in turn: the next one's values are on their way while one is written
-        Item one, two;
-        one.tile = unit;
-        one.e = 0;
-        one.g2 = walk.lo;
-        one.number = 0;
-        Raw r1 = {}, r2 = {};
+        // kAhead groups in turn: the next ones' values are on their way while one is written (a load takes
+        // 2 us and more while the weights stream)
+        constexpr int kAhead = 3;
+        Item items[kAhead];
+        Raw raws[kAhead];
+        Item next;                                // the last one fetched
+        next.tile = unit;
+        next.e = 0;
+        next.g2 = walk.lo;
+        next.number = 0;
         bool more = unit < tiles && walk.lo < walk.hi;
         if (more) {
-            one.t = plan.find(unit, one.e);
-            more = advance(one, set);
+            next.t = plan.find(unit, next.e);
+            more = advance(next, set);
         }
-        if (more)
-            fetch(one, r1);
-        while (more) {
-            two = one;
-            more = advance(two, S);
-            if (more)
-                fetch(two, r2);
-            if (!put(one, r1) || !more)
-                break;
-            one = two;
-            more = advance(one, S);
-            if (more)
-                fetch(one, r1);
-            if (!put(two, r2))
-                break;
+        int held = 0;                             // fetched, not yet written
+#pragma unroll
+        for (int d = 0; d < kAhead - 1; ++d)
+            if (more) {
+                items[d] = next;
+                fetch(next, raws[d]);
+                ++held;
+                more = advance(next, S);
+            }
+        bool ok = true;
+        while (ok && held > 0) {
+#pragma unroll
+            for (int d = 0; d < kAhead; ++d) {
+                if (!ok || held == 0)
+                    break;
+                if (more) {
+                    items[(d + kAhead - 1) % kAhead] = next;
+                    fetch(next, raws[(d + kAhead - 1) % kAhead]);
+                    ++held;
+                    more = advance(next, S);
+                }
+                ok = put(items[d], raws[d]);
+                --held;
+            }
         }
         if (FUSE && args.finite_check && bad)
             atomicOr(args.status, kStatusNonfinite);
@@ -657,7 +681,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                     const uint32_t acc = tmem_base + ((count & 1) ? slot1 : 0u);
                     // the tile before last (same accumulator) has left tensor memory; where the accumulators
                     // overlap, the last one's shared columns have (and all of the one before)
-                    const int last = count - (shared_chunks > 0 ? 1 : 2);
+                    const int last = count - (shared_cols > 0 ? 1 : 2);
                     if (last >= 0 && !fp8_wait<CG>(bar_acc_empty + 8 * (last & 1), (uint32_t)((last >> 1) & 1),
                                                    abort_flag, args.status))
                         return;
@@ -666,7 +690,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                     for (int g2 = walk.lo; g2 < walk.hi; ++g2) {
                         if (!fp8_wait<CG>(bar_sf_full + 8 * buf, buf_phase, abort_flag, args.status))
                             return;
-                        const uint32_t sf = tmem_base + kFScaleCol + 16 * buf;
+                        const uint32_t sf = tmem_base + Cfg::kScaleCol + 16 * buf;
 #pragma unroll
                         for (int u0 = 0; u0 < kFp8Group; u0 += PER) {
                             if (u0 > 0 && u0 >= left)
@@ -730,58 +754,59 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
         __syncwarp();
     } else {
         // ------------------------------------------------------------ epilogue (every CTA)
-        // Warp w: lanes 32 (w % 4) .. + 31, the first (w < 4) or second half of the tile's channels, 32
-        // at a time.
+        // Warp w: lanes 32 (w % 4) .. + 31, the first (w < 4) or second half of the tile's channels, C at a
+        // time.
         // (FUSE: lanes 0 .. 31, every other chunk.)
         const int wq = FUSE ? 0 : warp & 3, wh = FUSE ? (warp == 8 ? 0 : 1) : warp >> 2;
         const uint32_t acc_empty_leader = CG == 2 ? mapa_shared(bar_acc_empty, 0) : bar_acc_empty;
-        uint8_t *patch = smem + Cfg::kPatchOff + warp * kFPatchBytes;
+        uint8_t *patch = rest + warp * kFPatchBytes;
         const bool ybf = args.out_bf16 != 0;
-        const int chunks = (T + 31) / 32;
+        constexpr int C = FUSE ? 16 : 32;
+        const int chunks = (T + C - 1) / C;
         const int own = (chunks + 1 - wh) / 2;
         auto chunk_of = [&](int i) { return FUSE ? wh + 2 * i : wh * ((chunks + 1) / 2) + i; };
-        // a chunk's 32 columns from fp32 sums (gated: q the up projection's)
-        auto finish = [&](const I8Tile &t, int c, int rows, int64_t row, const float (&r)[32], const float (&q)[GATED ? 32 : 1]) {
+        // a chunk's columns from fp32 sums (gated: q the up projection's)
+        auto finish = [&](const I8Tile &t, int c, int rows, int64_t row, const float (&r)[C], const float (&q)[GATED ? C : 1]) {
             const int64_t col = (int64_t)t.wt * T + c;
-            const int live = (int)min((int64_t)min(T - c, 32), args.width - col);
+            const int live = (int)min((int64_t)min(T - c, C), args.width - col);
             if (rows <= 0 || live <= 0 || !SQ_DCHECK(row + rows <= args.M && col + live <= args.width, args.status))
                 return;
             if constexpr (GATED) {
-                float o[32];
+                float o[C];
                 if (args.act == 0) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
+                    for (int j = 0; j < C; ++j)
                         o[j] = act_value<0>(r[j]) * q[j];
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
+                    for (int j = 0; j < C; ++j)
                         o[j] = act_value<1>(r[j]) * q[j];
                 }
                 if (args.g_out) {
-                    store_cols32<FUSE>(r, patch, lane, args.g_out, row, col, args.width, rows, live, true);
-                    store_cols32<FUSE>(q, patch, lane, args.u_out, row, col, args.width, rows, live, true);
+                    store_cols<C>(r, patch, lane, args.g_out, row, col, args.width, rows, live, true);
+                    store_cols<C>(q, patch, lane, args.u_out, row, col, args.width, rows, live, true);
                 }
-                store_cols32<FUSE>(o, patch, lane, args.y, row, col, args.width, rows, live, ybf);
+                store_cols<C>(o, patch, lane, args.y, row, col, args.width, rows, live, ybf);
             } else {
-                store_cols32<FUSE>(r, patch, lane, args.y, row, col, args.width, rows, live, ybf);
+                store_cols<C>(r, patch, lane, args.y, row, col, args.width, rows, live, ybf);
             }
         };
-        auto load_chunk = [&](uint32_t acc, int c, float (&r)[32], float (&q)[GATED ? 32 : 1]) {
-            uint32_t a[32];
+        auto load_chunk = [&](uint32_t acc, int c, float (&r)[C], float (&q)[GATED ? C : 1]) {
+            uint32_t a[C];
             __syncwarp();
-            tmem_ld_32cols(acc + c, a);
+            tmem_ld_cols(acc + c, a);
             if constexpr (GATED) {
-                uint32_t b[32];
-                tmem_ld_32cols(acc + T + c, b);
+                uint32_t b[C];
+                tmem_ld_cols(acc + T + c, b);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
+                for (int j = 0; j < C; ++j)
                     q[j] = __uint_as_float(b[j]);
             } else {
                 tmem_wait_ld();
             }
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
+            for (int j = 0; j < C; ++j)
                 r[j] = __uint_as_float(a[j]);
         };
         int count = 0, e = 0;
@@ -824,13 +849,13 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                 };
                 // overlapping accumulators: the chunks that they share first (the last of the one at column
                 // 0, the first of the other), then the next tile may start
-                const int held = rows <= 0 ? 0 : shared_chunks > 0 ? min(shared_chunks, own) : own;
+                const int held = rows <= 0 ? 0 : shared_cols > 0 ? min(shared_cols / C, own) : own;
                 if (held == 0)
                     release();
                 if (rows > 0)
                     for (int i = 0; i < own; ++i) {
-                        const int c = 32 * chunk_of(slot ? i : own - 1 - i);
-                        float r[32], q[GATED ? 32 : 1];
+                        const int c = C * chunk_of(slot ? i : own - 1 - i);
+                        float r[C], q[GATED ? C : 1];
                         load_chunk(acc, c, r, q);
                         if (i == held - 1)
                             release();
@@ -851,13 +876,13 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                 if (!FUSE && lane < split && lane != part)
                     mbar_arrive_cluster(mapa_shared(bar_peers, lane));
                 if (lane == 0)
-                    mbar_arrive_expect_tx(bar_parts, mine * (split - 1) * t.rows * 128 * kParts);
+                    mbar_arrive_expect_tx(bar_parts, mine * (split - 1) * t.rows * (4 * C) * kParts);
             }
-            // place of a chunk's part from CTA `from`: [chunk / split][from][gate, up][quarter][8][lanes] float4
+            // place of a chunk's part from CTA `from`: [chunk / split][from][gate, up][quarter][C / 4][lanes] float4
             constexpr int kLanes = FUSE ? kFuseRows : 32;
-            uint8_t *parts = smem + (FUSE ? Cfg::kPatchOff : 0);
+            uint8_t *parts = FUSE ? rest : smem;
             auto place = [&](int c, int from, int which) {
-                return (uint32_t)(((((c / split) * split + from) * kParts + which) * (FUSE ? 1 : 4) + wq) * 8 * kLanes + lane) *
+                return (uint32_t)(((((c / split) * split + from) * kParts + which) * (FUSE ? 1 : 4) + wq) * (C / 4) * kLanes + lane) *
                        16u;
             };
             const uint32_t s0 = smem_u32(parts);
@@ -867,12 +892,12 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                     const int c = chunk_of(i), to = c % split;
                     if (to == part)
                         continue;
-                    float r[32], q[GATED ? 32 : 1];
-                    load_chunk(acc, 32 * c, r, q);
+                    float r[C], q[GATED ? C : 1];
+                    load_chunk(acc, C * c, r, q);
                     const uint32_t dst = mapa_shared(s0, to), bar = mapa_shared(bar_parts, to);
                     if (lane < rows)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
+                        for (int j = 0; j < C / 4; ++j) {
                             st_async_v4(dst + place(c, part, 0) + j * 16 * kLanes, r + 4 * j, bar);
                             if constexpr (GATED)
                                 st_async_v4(dst + place(c, part, 1) + j * 16 * kLanes, q + 4 * j, bar);
@@ -885,8 +910,8 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                     const int c = chunk_of(i);
                     if (c % split != part)
                         continue;
-                    float r[32], q[GATED ? 32 : 1];
-                    load_chunk(acc, 32 * c, r, q);
+                    float r[C], q[GATED ? C : 1];
+                    load_chunk(acc, C * c, r, q);
                     auto join = [&](float *v, int which, int j) {      // four columns: the parts in order
                         float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                         for (int from = 0; from < split; ++from) {
@@ -904,12 +929,12 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                         v[3] = sum.w;
                     };
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
+                    for (int j = 0; j < C / 4; ++j) {
                         join(r + 4 * j, 0, j);
                         if constexpr (GATED)
                             join(q + 4 * j, 1, j);
                     }
-                    finish(t, 32 * c, rows, (int64_t)t.row0 + 32 * wq, r, q);
+                    finish(t, C * c, rows, (int64_t)t.row0 + 32 * wq, r, q);
                 }
         }
         __syncwarp();
@@ -923,9 +948,9 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
     tc_fence_after();
     if (warp == kIssuer) {
         if (CG == 2)
-            tmem_dealloc2(tmem_base, kFTmemCols);
+            tmem_dealloc2(tmem_base, Cfg::kTmemCols);
         else
-            tmem_dealloc(tmem_base, kFTmemCols);
+            tmem_dealloc(tmem_base, Cfg::kTmemCols);
     }
 }
 
@@ -1081,15 +1106,16 @@ cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8S
     a.a_rows = FUSE ? (int)((g.M + 7) / 8 * 8) : CG == 2 || g.M >= 128 ? 128 : (int)((g.M + 31) / 32 * 32);
     const int cols = GATED ? 2 * tile : tile;
     a.slot1 = cols > 224 ? 192 : 224;
-    // one copy a chunk, but for experts with few rows
-    a.box = CG == 2 || g.E <= 1 || g.M / g.E > 64 ? a.a_rows : 32;
+    a.boxed_rows = g.E > 0 ? (a.a_rows - 1) / 32 * 32 : 0;
     a.split = sh.split;
-    CUtensorMap tmX, tmW, tmW2;
+    CUtensorMap tmX, tmX32, tmW, tmW2;
     const int w_rows = BWD ? 128 : GATED ? tile : tile / CG;
     bool ok = byte_map(&tmW, g.wcodes[0], g.K, g.N, Em, w_rows);
-    tmX = tmW2 = tmW;
+    tmX = tmX32 = tmW2 = tmW;
     if (!FUSE)
-        ok = ok && byte_map(&tmX, g.codes, summed, halves * g.M, 0, a.box);
+        ok = ok && byte_map(&tmX, g.codes, summed, halves * g.M, 0, a.a_rows);
+    if (!FUSE && a.boxed_rows > 0)
+        ok = ok && byte_map(&tmX32, g.codes, summed, halves * g.M, 0, 32);
     if (g.gated)
         ok = ok && byte_map(&tmW2, g.wcodes[1], g.K, g.N, Em, w_rows);
     if (!ok)
@@ -1097,6 +1123,7 @@ cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8S
     // the stages: as many chunks as leave four of them
     const int ring = Cfg::kRing - (FUSE ? kFBufs * kFp8Group * a.a_rows * kFChunk : 0);
     const int chunk = ((FUSE ? 0 : a.a_rows) + b_rows) * kFChunk;
+    a.prefetch = kPrefetchBytes / chunk;
     a.per = CG;               // (a pair: with one chunk a stage the tensor pipe is 78 % active, with two 90 %)
     if (CG == 1)
         while (a.per < 4 && 2 * a.per * chunk * 4 <= ring)
@@ -1121,7 +1148,7 @@ cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8S
     cfg.stream = stream;
     cfg.attrs = at;
     cfg.numAttrs = CG * sh.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, sq_fp8_kernel<CG, MODE, FUSE>, tmX, tmW, tmW2, a);
+    return cudaLaunchKernelEx(&cfg, sq_fp8_kernel<CG, MODE, FUSE>, tmX, tmX32, tmW, tmW2, a);
 }
 
 // How a call's tiles are cut: the candidate with the least time by a simple count of cycles.  A chunk
@@ -1145,8 +1172,8 @@ Fp8Shape pick(const Fp8GemmLaunch &g, bool fuse, const Fp8Room &room)
         const int64_t b = g.bwd ? 128 : cols / cg;
         const int64_t mma = cg == 2 ? 2 * cols : 140 + 2 * cols, copy = (a + b) * kFChunk / 66;
         const int64_t chunk = mma > copy ? mma : copy;
-        const int64_t cost = rounds * ((groups + split - 1) / split * kFp8Group * chunk + (cols > 224 ? 2500 : 500)) +
-                             (split == 1 ? 0 : fuse ? 2000 : 5000);
+        const int64_t cost = rounds * ((groups + split - 1) / split * kFp8Group * chunk + (cols > 224 ? 2500 : 500)) + 10 * cols +
+                             (split == 1 ? 0 : 8000);
         if (cost < best_cost) {
             best_cost = cost;
             best = {cg, tile, split};
@@ -1161,8 +1188,9 @@ Fp8Shape pick(const Fp8GemmLaunch &g, bool fuse, const Fp8Room &room)
     if (!fuse)
         for (int cols = 256; cols >= 64; cols -= 32)
             offer(2, cols, 1);
-    const int most = weights == 2 ? 6 : kFMaxSplit;            // (what the ring holds of the others' sums)
-    for (int cols = 128; cols >= (g.bwd ? 128 : 32); cols -= 16 * weights)
+    // (what shared memory holds of the others' sums)
+    const int most = fuse ? (weights == 2 ? 3 : 4) : weights == 2 ? 6 : kFMaxSplit;
+    for (int cols = 128; cols >= (g.bwd ? 128 : 32); cols -= 16)
         for (int split = 1; split <= most && split <= groups; ++split)
             offer(1, cols, split);
     return best;

@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include "sq_device.cuh"
+#include "sq_ptx.cuh"
 
 namespace sq {
 
@@ -18,26 +19,35 @@ __host__ __device__ __forceinline__ int64_t fp8_groups(int64_t len)
     return (len + kFp8Block * kFp8Group - 1) / (kFp8Block * kFp8Group);
 }
 
-// sigmoid(v) and sigmoid(-v), both without cancellation: t = e^-|v| <= 1
-__device__ __forceinline__ void sigmoid2(float v, float &s, float &other)
+// sigmoid(x ln 2) and its complement, both without cancellation: t = 2^-|x| <= 1 (a NaN stays one)
+__device__ __forceinline__ void sigmoid2(float x, float &s, float &other)
 {
-    const float t = __expf(-fabsf(v));
-    const float big = __fdividef(1.0f, 1.0f + t), small = t * big;
-    s = v < 0.0f ? small : big;
-    other = v < 0.0f ? big : small;
-    if (v != v)
-        s = other = v;
+    float t, big;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(-fabsf(x)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(big) : "f"(1.0f + t));
+    const float small = t * big;
+    s = x < 0.0f ? small : big;
+    other = x < 0.0f ? big : small;
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGelu2C = 1.5957691216057308f;    // 2 sqrt(2 / pi)
 constexpr float kGeluCube = 0.044715f;
 
-// act(g); gelu: (1 + tanh z) / 2 = sigmoid(2 z)
+// act's argument of the sigmoid, in units of ln 2; gelu: (1 + tanh z) / 2 = sigmoid(2 z).  g2: g^2,
+// kept finite, so that what it multiplies may be 0
+template <int ACT>
+__device__ __forceinline__ float act_arg(float g, float g2)
+{
+    return ACT == 0 ? kLog2e * g : g * (kLog2e * kGelu2C + kLog2e * kGelu2C * kGeluCube * g2);
+}
+
+// act(g)
 template <int ACT>
 __device__ __forceinline__ float act_value(float g)
 {
     float s, o;
-    sigmoid2(ACT == 0 ? g : kGelu2C * (g + kGeluCube * g * g * g), s, o);
+    sigmoid2(act_arg<ACT>(g, fminf(g * g, 1e30f)), s, o);
     return g * s;
 }
 
@@ -46,13 +56,11 @@ template <int ACT>
 __device__ __forceinline__ void act_grad(float g, float &a, float &slope)
 {
     float s, o;
-    sigmoid2(ACT == 0 ? g : kGelu2C * (g + kGeluCube * g * g * g), s, o);
+    const float g2 = fminf(g * g, 1e30f);
+    sigmoid2(act_arg<ACT>(g, g2), s, o);
     a = g * s;
-    const float w = s * o;                        // sigmoid'; where it is 0, so is its term, whatever g^2 comes to
-    if (ACT == 0)
-        slope = s + (w == 0.0f ? 0.0f : g * w);
-    else
-        slope = s + (w == 0.0f ? 0.0f : g * w * (kGelu2C + 3.0f * kGelu2C * kGeluCube * g * g));
+    const float w = a * o;                        // g sigmoid'
+    slope = ACT == 0 ? s + w : s + w * (kGelu2C + 3.0f * kGelu2C * kGeluCube * g2);
 }
 
 // ---- rounding to e4m3 --------------------------------------------------------------
@@ -93,16 +101,31 @@ __device__ __forceinline__ void widen8(const uint4 &w, float (&v)[16], int at)
     }
 }
 
-// A lane's 16 neighbouring values of a row (8 lanes a block): their codes, and the block's byte.
-__device__ __forceinline__ uint4 quantise16(const float (&v)[16], uint32_t &byte, bool &bad)
+// max(a, |b|, |c|), NaN if any is
+__device__ __forceinline__ float fp8_absmax3(float a, float b, float c)
 {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+    return r;
+}
+
+// the largest |r| of a block from its eight lanes' (bits: NaN above infinity above all others)
+__device__ __forceinline__ uint32_t block_top(uint32_t top)
+{
 #pragma unroll
     for (int x = 1; x <= 4; x <<= 1)
         top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
+    return top;
+}
+
+// A lane's 16 neighbouring values of a row (8 lanes a block): their codes, and the block's byte.
+__device__ __forceinline__ uint4 quantise16(const float (&v)[16], uint32_t &byte, bool &bad)
+{
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; i += 2)
+        m = fp8_absmax3(m, v[i], v[i + 1]);
+    const uint32_t top = block_top(__float_as_uint(m) & 0x7FFFFFFFu);
     if (top >= kFp8Inf) {
         bad = true;
         byte = 127u;
@@ -114,6 +137,35 @@ __device__ __forceinline__ uint4 quantise16(const float (&v)[16], uint32_t &byte
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         c[i] = to_e4m3x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+    return make_uint4(c[0], c[1], c[2], c[3]);
+}
+
+// The same of 16 bf16 values, two at a time as long as that is exact (the maximum, and the product with
+// a power of two: what it loses below bf16's range rounds to 0 all the same).
+__device__ __forceinline__ uint4 quantise16(const uint4 (&w)[2], uint32_t &byte, bool &bad)
+{
+    const uint32_t p[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(p[i] & 0x7FFF7FFFu));
+    const uint32_t top = block_top(max(m << 16, m & 0xFFFF0000u) & 0x7FFFFFFFu);
+    if (top >= kFp8Inf) {
+        bad = true;
+        byte = 127u;
+        return make_uint4(kFp8NanCodes, kFp8NanCodes, kFp8NanCodes, kFp8NanCodes);
+    }
+    byte = fp8_scale_byte(top);
+    const uint32_t inv = __float_as_uint(fp8_inverse(byte)), inv2 = inv | inv >> 16;
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t a, b;
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(p[2 * i]), "r"(inv2));
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(p[2 * i + 1]), "r"(inv2));
+        c[i] = to_e4m3x4(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u), __uint_as_float(b << 16),
+                         __uint_as_float(b & 0xFFFF0000u));
+    }
     return make_uint4(c[0], c[1], c[2], c[3]);
 }
 
@@ -190,6 +242,28 @@ __device__ __forceinline__ void tma_prefetch_3d(const void *tmap, int32_t x, int
 {
     asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];"
                  ::"l"((uint64_t)tmap), "r"(x), "r"(y), "r"(z) : "memory");
+}
+
+// each thread of the warp reads 16 consecutive 32-bit columns of its lane
+__device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                   "=r"(r[15])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16])
+{
+    tmem_ld_16cols(taddr, r);
+}
+
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[32])
+{
+    tmem_ld_32cols(taddr, r);
 }
 
 // 16 bytes into another CTA's shared memory, counted on its barrier

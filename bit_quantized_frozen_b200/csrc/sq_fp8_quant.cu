@@ -19,11 +19,17 @@
 namespace sq {
 
 constexpr int kQuantThreads = 128;
+// CTAs an SM holds at once: the grid is no larger, since what waits for a second turn would make the
+// last CTAs of the first wait too
+constexpr int quant_ctas(int gated)
+{
+    return gated ? 9 : 8;
+}
 
 // GATED 0: rows of x; 1, 2: the gradients of a gated pair with silu, gelu.  A warp takes ROWS rows x
 // 512 columns at a time, a lane 16 neighbouring values of each row.
 template <int GATED, int ROWS>
-__global__ void __launch_bounds__(kQuantThreads) fp8_quant_kernel(const Fp8QuantArgs a)
+__global__ void __launch_bounds__(kQuantThreads, quant_ctas(GATED)) fp8_quant_kernel(const Fp8QuantArgs a)
 {
     const int lane = threadIdx.x & 31;
     grid_dep_wait();                              // x, and the workspace of the call before
@@ -37,13 +43,24 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quant_kernel(const Fp8Quant
         lo = first < 0 ? 0 : first > a.M ? a.M : first;
         hi = last < lo ? lo : last > a.M ? a.M : last;
     }
-    const int64_t groups = fp8_groups(a.L);
-    const int64_t units = (hi - lo + ROWS - 1) / ROWS * groups;
-    const int64_t warps = (int64_t)gridDim.x * (kQuantThreads / 32);
+    // the warps take (rows, group) pairs in turn, the group changing fastest; the next pair is found without
+    // a division (two of 64 bits cost more than a pair's values)
+    const int groups = (int)fp8_groups(a.L);
+    const unsigned warps = gridDim.x * (kQuantThreads / 32), me = blockIdx.x * (kQuantThreads / 32) + (threadIdx.x >> 5);
+    const int step_grp = (int)(warps % (unsigned)groups);
+    const int64_t step_row = (int64_t)(warps / (unsigned)groups) * ROWS;
+    int grp = (int)(me % (unsigned)groups);
+    int64_t row0 = lo + (int64_t)(me / (unsigned)groups) * ROWS;
+    auto settle = [&]() {                         // past the last group: the next rows
+        if (grp >= groups) {
+            grp -= groups;
+            row0 += ROWS;
+        }
+    };
     bool bad = false;
-    for (int64_t unit = (int64_t)blockIdx.x * (kQuantThreads / 32) + (threadIdx.x >> 5); unit < units; unit += warps) {
-        const int64_t grp = unit % groups, row0 = lo + unit / groups * ROWS;
-        const int64_t col = grp * (kFp8Block * kFp8Group) + 16 * lane;
+    while (row0 < hi) {
+        const int64_t row = row0, col = (int64_t)grp * (kFp8Block * kFp8Group) + 16 * lane;
+        const int g512 = grp;
         constexpr int OPS = GATED ? 3 : 1;
         uint4 w[OPS][ROWS][2];
 #pragma unroll
@@ -51,21 +68,27 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quant_kernel(const Fp8Quant
             const uint16_t *src = o == 0 ? a.x : o == 1 ? a.g : a.u;
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) {
-                const bool live = row0 + r < hi && col < a.L;
-                const uint4 *p = reinterpret_cast<const uint4 *>(src + (row0 + r) * a.L + col);
+                const bool live = row + r < hi && col < a.L;
+                const uint4 *p = reinterpret_cast<const uint4 *>(src + (row + r) * a.L + col);
                 w[o][r][0] = live ? __ldg(p) : make_uint4(0u, 0u, 0u, 0u);
                 w[o][r][1] = live ? __ldg(p + 1) : make_uint4(0u, 0u, 0u, 0u);
             }
         }
+        row0 += step_row;
+        grp += step_grp;
+        settle();
         uint32_t words[GATED ? 2 : 1] = {};
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-            float v[16];
-            widen8(w[0][r][0], v, 0);
-            widen8(w[0][r][1], v, 8);
-            float second[GATED ? 16 : 1];
-            if constexpr (GATED != 0) {
-                float g[16], u[16];
+            const bool live = row + r < hi && col < a.L;
+            uint32_t byte;
+            uint4 c;
+            if constexpr (GATED == 0) {
+                c = quantise16(w[0][r], byte, bad);
+            } else {
+                float v[16], g[16], u[16], second[16];
+                widen8(w[0][r][0], v, 0);
+                widen8(w[0][r][1], v, 8);
                 widen8(w[1][r][0], g, 0);
                 widen8(w[1][r][1], g, 8);
                 widen8(w[2][r][0], u, 0);
@@ -77,28 +100,24 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quant_kernel(const Fp8Quant
                     second[i] = v[i] * act;
                     v[i] = v[i] * u[i] * slope;
                 }
+                c = quantise16(second, byte, bad);
+                const uint32_t word = scale_word(byte, lane);
+                if (lane == r)
+                    words[1] = word;
+                if (live && SQ_DCHECK(row + r < a.M, a.status))
+                    *reinterpret_cast<uint4 *>(a.codes + (a.M + row + r) * a.L + col) = c;
+                c = quantise16(v, byte, bad);
             }
-            const bool live = row0 + r < hi && col < a.L;
-            uint32_t byte;
-            const uint4 c = quantise16(v, byte, bad);
             const uint32_t word = scale_word(byte, lane);
             if (lane == r)
                 words[0] = word;
-            if (live && SQ_DCHECK(row0 + r < a.M, a.status))
-                *reinterpret_cast<uint4 *>(a.codes + (row0 + r) * a.L + col) = c;
-            if constexpr (GATED != 0) {
-                const uint4 d = quantise16(second, byte, bad);
-                const uint32_t word2 = scale_word(byte, lane);
-                if (lane == r)
-                    words[1] = word2;
-                if (live)
-                    *reinterpret_cast<uint4 *>(a.codes + (a.M + row0 + r) * a.L + col) = d;
-            }
+            if (live && SQ_DCHECK(row + r < a.M, a.status))
+                *reinterpret_cast<uint4 *>(a.codes + (row + r) * a.L + col) = c;
         }
-        if (lane < ROWS && row0 + lane < hi) {
-            a.words[grp * a.M + row0 + lane] = words[0];
+        if (lane < ROWS && row + lane < hi) {
+            a.words[(int64_t)g512 * a.M + row + lane] = words[0];
             if constexpr (GATED != 0)
-                a.words[(groups + grp) * a.M + row0 + lane] = words[1];
+                a.words[(int64_t)(groups + g512) * a.M + row + lane] = words[1];
         }
     }
     if (a.finite_check && bad)
@@ -124,7 +143,8 @@ template <int GATED, int ROWS>
 static cudaError_t launch_quant(const Fp8QuantArgs &a, int sms, cudaStream_t s)
 {
     const int64_t units = (a.M + ROWS - 1) / ROWS * fp8_groups(a.L);
-    const int64_t blocks = (units + kQuantThreads / 32 - 1) / (kQuantThreads / 32), most = (int64_t)sms * 16;
+    const int64_t blocks = (units + kQuantThreads / 32 - 1) / (kQuantThreads / 32);
+    const int64_t most = (int64_t)sms * quant_ctas(GATED);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(blocks < most ? blocks : most));
     cfg.blockDim = dim3(kQuantThreads);
@@ -141,7 +161,7 @@ cudaError_t launch_fp8_quant(const Fp8QuantArgs &a, int sms, cudaStream_t s)
 {
     if (!a.g)
         return launch_quant<0, 4>(a, sms, s);
-    return a.act == 0 ? launch_quant<1, 2>(a, sms, s) : launch_quant<2, 2>(a, sms, s);
+    return a.act == 0 ? launch_quant<1, 1>(a, sms, s) : launch_quant<2, 1>(a, sms, s);
 }
 
 // ---------------------------------------------------------------------------
