@@ -63,14 +63,15 @@ struct Fp8Cfg {
     // shared memory: the ring, then
     //   patches of the stores; FUSE: a split tile's sums from the other CTAs.  (CG = 1: the MMA reads
     //   128 rows of A, up to 16 KB behind the last stage.)
-    static constexpr int kPatchBytes = FUSE ? 12 * 1024 : 8 * kFPatchBytes;
+    static constexpr int kPatches = CG == 2 && MODE != kFp8Bwd ? 2 : 1;       // of an epilogue warp
+    static constexpr int kPatchBytes = FUSE ? 12 * 1024 : 8 * kPatches * kFPatchBytes;
     static constexpr int kPlanOff = kPatchBytes;
     static constexpr int kFeedOff = kPlanOff + (2 * kMaxExperts + 4) * 4;     // [sets][2][32] words (FUSE)
     static constexpr int kBarOff = kFeedOff + kSets * 2 * 32 * 4;
     // full, empty, sf_full, sf_empty, acc_full[2], acc_empty[2], drain, peers, parts
     static constexpr int kNumBars = 2 * kMaxStages + 2 * kFBufs + 7;
     static constexpr int kRestBytes = kBarOff + 8 * kNumBars + 16;
-    static constexpr int kRing = 192 * 1024;
+    static constexpr int kRing = (kPatches == 2 ? 180 : 192) * 1024;
     static constexpr int kSmemBytes = kRing + kRestBytes + 1024;
     // e4m3 x e4m3, e8m0 scales; B N-major backward; 128 CG rows (columns / 8 << 17 comes at run time)
     static constexpr uint32_t kIdesc = (1u << 23) | (MODE == kFp8Bwd ? 1u << 16 : 0u) | ((uint32_t)(8 * CG) << 24);
@@ -127,32 +128,60 @@ __device__ __forceinline__ bool one_lane()
     return p != 0;
 }
 
-// One warp's 32 rows x 64 bytes to y: through the patch, so that a row's 64 bytes leave in one run.
+// A warp's place for 32 rows x 64 bytes on their way out, or two in turn.
+struct Fp8Patch {
+    uint8_t *mem;
+    int lane, turn;
+};
+
+// One warp's 32 rows x 64 bytes to y through its patch: by TMA (map, box of 64 bytes x 32 rows at x, y),
+// or where not all of them exist (map NULL) row by row, so that a row's 64 bytes leave in one run.
 // dst: row 0's first byte; the first `rows` rows and `bytes` bytes (a multiple of 16) of each exist.
-__device__ __forceinline__ void store_rows64(const uint32_t (&v)[16], uint8_t *patch, int lane, uint8_t *dst,
-                                             int64_t row_bytes, int rows, int bytes)
+template <int PATCHES>
+__device__ __forceinline__ void store_rows64(const uint32_t (&v)[16], Fp8Patch &out, const CUtensorMap *map, int x,
+                                             int y, uint8_t *dst, int64_t row_bytes, int rows, int bytes)
 {
-#pragma unroll
-    for (int p = 0; p < 4; ++p)
-        *reinterpret_cast<uint4 *>(patch + lane * 64 + ((p ^ ((lane >> 1) & 3)) << 4)) =
-            make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = 8 * i + (lane >> 2), p = lane & 3;
-        const uint4 w = *reinterpret_cast<const uint4 *>(patch + row * 64 + ((p ^ ((row >> 1) & 3)) << 4));
-        if (row < rows && 16 * p < bytes)
-            *reinterpret_cast<uint4 *>(dst + row * row_bytes + 16 * p) = w;
+    const int lane = out.lane;
+    uint8_t *patch = out.mem + (PATCHES == 2 ? out.turn * kFPatchBytes : 0);
+    out.turn ^= 1;
+    if (lane == 0) {                              // what was in it has left
+        if (PATCHES == 2)
+            bulk_wait_group_read1();
+        else
+            bulk_wait_group_read0();
     }
     __syncwarp();
+#pragma unroll
+    for (int p = 0; p < 4; ++p)                   // (the order that the 64-byte swizzle of the map has)
+        *reinterpret_cast<uint4 *>(patch + lane * 64 + ((p ^ ((lane >> 1) & 3)) << 4)) =
+            make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
+    if (map) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+            tma_store_2d(map, smem_u32(patch), x, y);
+    } else {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = 8 * i + (lane >> 2), p = lane & 3;
+            const uint4 w = *reinterpret_cast<const uint4 *>(patch + row * 64 + ((p ^ ((row >> 1) & 3)) << 4));
+            if (row < rows && 16 * p < bytes)
+                *reinterpret_cast<uint4 *>(dst + row * row_bytes + 16 * p) = w;
+        }
+        __syncwarp();
+    }
+    if (lane == 0)
+        bulk_commit_group();                      // (empty without a map: the patches are counted in groups)
 }
 
 // C neighbouring columns of y from fp32 values, as bf16 or fp32; the first `cols` of them and `rows`
 // rows exist.  32 columns leave through the patch; 16 (few rows) are written by their lanes directly.
-template <int C>
-__device__ __forceinline__ void store_cols(const float (&o)[C], uint8_t *patch, int lane, void *y, int64_t row,
-                                           int64_t col, int64_t width, int rows, int cols, bool bf16)
+template <int C, int PATCHES>
+__device__ __forceinline__ void store_cols(const float (&o)[C], Fp8Patch &out, const CUtensorMap *map, void *y,
+                                           int64_t row, int64_t col, int64_t width, int rows, int cols, bool bf16)
 {
+    const int lane = out.lane;
     uint8_t *dst = reinterpret_cast<uint8_t *>(y) + (bf16 ? 2 : 4) * (row * width + col);
     if constexpr (C == 16) {
         if (lane >= rows)
@@ -177,14 +206,14 @@ __device__ __forceinline__ void store_cols(const float (&o)[C], uint8_t *patch, 
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 v[i] = f32x2_to_bf16x2_bits(o[2 * i], o[2 * i + 1]);
-            store_rows64(v, patch, lane, dst, 2 * width, rows, 2 * cols);
+            store_rows64<PATCHES>(v, out, map, (int)col, (int)row, dst, 2 * width, rows, 2 * cols);
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     v[i] = __float_as_uint(o[16 * h + i]);
-                store_rows64(v, patch, lane, dst + 64 * h, 4 * width, rows, 4 * (cols - 16 * h));
+                store_rows64<PATCHES>(v, out, map, (int)col + 16 * h, (int)row, dst + 64 * h, 4 * width, rows, 4 * (cols - 16 * h));
             }
         }
     }
@@ -206,7 +235,9 @@ struct Fp8Walk {
 template <int CG, int MODE, bool FUSE>
 __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
     sq_fp8_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmX32,
-                  const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmW2, const Fp8Args args)
+                  const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmW2,
+                  const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmG,
+                  const __grid_constant__ CUtensorMap tmU, const Fp8Args args)
 {
     using Cfg = Fp8Cfg<CG, MODE, FUSE>;
     constexpr bool BWD = MODE == kFp8Bwd, GATED = MODE == kFp8Gated;
@@ -759,7 +790,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
         // (FUSE: lanes 0 .. 31, every other chunk.)
         const int wq = FUSE ? 0 : warp & 3, wh = FUSE ? (warp == 8 ? 0 : 1) : warp >> 2;
         const uint32_t acc_empty_leader = CG == 2 ? mapa_shared(bar_acc_empty, 0) : bar_acc_empty;
-        uint8_t *patch = rest + warp * kFPatchBytes;
+        Fp8Patch out = {rest + warp * (Cfg::kPatches * kFPatchBytes), lane, 0};
         const bool ybf = args.out_bf16 != 0;
         constexpr int C = FUSE ? 16 : 32;
         const int chunks = (T + C - 1) / C;
@@ -771,7 +802,16 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
             const int live = (int)min((int64_t)min(T - c, C), args.width - col);
             if (rows <= 0 || live <= 0 || !SQ_DCHECK(row + rows <= args.M && col + live <= args.width, args.status))
                 return;
+            // all 32 rows and C columns are the tile's, or lie behind the matrix's end
+            const bool whole = (rows == 32 || args.E == 0) && (live == C || col + live == args.width);
+            auto put_out = [&](const float (&o)[C], const CUtensorMap &m, void *to, bool bf16) {
+                store_cols<C, Cfg::kPatches>(o, out, whole ? &m : nullptr, to, row, col, args.width, rows, live, bf16);
+            };
             if constexpr (GATED) {
+                if (args.g_out) {
+                    put_out(r, tmG, args.g_out, true);
+                    put_out(q, tmU, args.u_out, true);
+                }
                 float o[C];
                 if (args.act == 0) {
 #pragma unroll
@@ -782,13 +822,9 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                     for (int j = 0; j < C; ++j)
                         o[j] = act_value<1>(r[j]) * q[j];
                 }
-                if (args.g_out) {
-                    store_cols<C>(r, patch, lane, args.g_out, row, col, args.width, rows, live, true);
-                    store_cols<C>(q, patch, lane, args.u_out, row, col, args.width, rows, live, true);
-                }
-                store_cols<C>(o, patch, lane, args.y, row, col, args.width, rows, live, ybf);
+                put_out(o, tmY, args.y, ybf);
             } else {
-                store_cols<C>(r, patch, lane, args.y, row, col, args.width, rows, live, ybf);
+                put_out(r, tmY, args.y, ybf);
             }
         };
         auto load_chunk = [&](uint32_t acc, int c, float (&r)[C], float (&q)[GATED ? C : 1]) {
@@ -937,6 +973,8 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                     finish(t, C * c, rows, (int64_t)t.row0 + 32 * wq, r, q);
                 }
         }
+        if (!FUSE && lane == 0)
+            bulk_wait_group_all();
         __syncwarp();
     }
 
@@ -963,9 +1001,7 @@ typedef CUresult (*PFN_encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, v
                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// byte matrices [outer, rows, inner] in a row, boxes of box_rows x 128; what lies outside one of them
-// reads as 0 (a box that ends behind an expert's last row does not see the next expert's)
-bool byte_map(CUtensorMap *m, const void *base, int64_t inner, int64_t rows, int64_t outer, int box_rows)
+PFN_encode encode_fn()
 {
     static PFN_encode fn = nullptr;
     if (!fn) {
@@ -973,9 +1009,19 @@ bool byte_map(CUtensorMap *m, const void *base, int64_t inner, int64_t rows, int
         cudaDriverEntryPointQueryResult q;
         if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
             q != cudaDriverEntryPointSuccess)
-            return false;
+            return nullptr;
         fn = reinterpret_cast<PFN_encode>(p);
     }
+    return fn;
+}
+
+// byte matrices [outer, rows, inner] in a row, boxes of box_rows x 128; what lies outside one of them
+// reads as 0 (a box that ends behind an expert's last row does not see the next expert's)
+bool byte_map(CUtensorMap *m, const void *base, int64_t inner, int64_t rows, int64_t outer, int box_rows)
+{
+    const PFN_encode fn = encode_fn();
+    if (!fn)
+        return false;
     const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)outer};
     const cuuint64_t strides[2] = {(cuuint64_t)inner, (cuuint64_t)(inner * rows)};
     const cuuint32_t box[3] = {kFChunk, (cuuint32_t)box_rows, 1};
@@ -1005,6 +1051,22 @@ void cluster_attr(cudaLaunchAttribute &at, int size)
     at.val.clusterDim.x = (unsigned)size;
     at.val.clusterDim.y = 1;
     at.val.clusterDim.z = 1;
+}
+
+// an output [rows, width], boxes of 32 rows x 64 bytes
+bool out_map(CUtensorMap *m, const void *base, int64_t width, int64_t rows, bool bf16)
+{
+    const PFN_encode fn = encode_fn();
+    if (!fn)
+        return false;
+    const int size = bf16 ? 2 : 4;
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(width * size)};
+    const cuuint32_t box[2] = {(cuuint32_t)(64 / size), 32};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void *>(base),
+              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int CG, int MODE, bool FUSE>
@@ -1108,23 +1170,29 @@ cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8S
     a.slot1 = cols > 224 ? 192 : 224;
     a.boxed_rows = g.E > 0 ? (a.a_rows - 1) / 32 * 32 : 0;
     a.split = sh.split;
-    CUtensorMap tmX, tmX32, tmW, tmW2;
+    CUtensorMap tmX, tmX32, tmW, tmW2, tmY, tmG, tmU;
     const int w_rows = BWD ? 128 : GATED ? tile : tile / CG;
     bool ok = byte_map(&tmW, g.wcodes[0], g.K, g.N, Em, w_rows);
-    tmX = tmX32 = tmW2 = tmW;
+    tmX = tmX32 = tmW2 = tmY = tmG = tmU = tmW;
     if (!FUSE)
         ok = ok && byte_map(&tmX, g.codes, summed, halves * g.M, 0, a.a_rows);
     if (!FUSE && a.boxed_rows > 0)
         ok = ok && byte_map(&tmX32, g.codes, summed, halves * g.M, 0, 32);
     if (g.gated)
         ok = ok && byte_map(&tmW2, g.wcodes[1], g.K, g.N, Em, w_rows);
+    if (!FUSE)
+        ok = ok && out_map(&tmY, g.y, a.width, g.M, g.out_bf16 != 0);
+    if (!FUSE && g.g_out)
+        ok = ok && out_map(&tmG, g.g_out, a.width, g.M, true) && out_map(&tmU, g.u_out, a.width, g.M, true);
     if (!ok)
         return cudaErrorInvalidValue;
     // the stages: as many chunks as leave four of them
     const int ring = Cfg::kRing - (FUSE ? kFBufs * kFp8Group * a.a_rows * kFChunk : 0);
     const int chunk = ((FUSE ? 0 : a.a_rows) + b_rows) * kFChunk;
     a.prefetch = kPrefetchBytes / chunk;
-    a.per = CG;               // (a pair: with one chunk a stage the tensor pipe is 78 % active, with two 90 %)
+    a.per = 1;                // a pair: two where that leaves three stages (4480 x 16384 x 6144: 295 us, with one 328)
+    if (CG == 2 && 6 * chunk <= ring)
+        a.per = 2;
     if (CG == 1)
         while (a.per < 4 && 2 * a.per * chunk * 4 <= ring)
             a.per *= 2;
@@ -1148,7 +1216,7 @@ cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8S
     cfg.stream = stream;
     cfg.attrs = at;
     cfg.numAttrs = CG * sh.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, sq_fp8_kernel<CG, MODE, FUSE>, tmX, tmX32, tmW, tmW2, a);
+    return cudaLaunchKernelEx(&cfg, sq_fp8_kernel<CG, MODE, FUSE>, tmX, tmX32, tmW, tmW2, tmY, tmG, tmU, a);
 }
 
 // How a call's tiles are cut: the candidate with the least time by a simple count of cycles.  A chunk

@@ -42,12 +42,13 @@ __device__ __forceinline__ float act_arg(float g, float g2)
     return ACT == 0 ? kLog2e * g : g * (kLog2e * kGelu2C + kLog2e * kGelu2C * kGeluCube * g2);
 }
 
-// act(g)
+// act(g) = g / (1 + 2^-x): where the power leaves fp32's range, the quotient is 0
 template <int ACT>
 __device__ __forceinline__ float act_value(float g)
 {
-    float s, o;
-    sigmoid2(act_arg<ACT>(g, fminf(g * g, 1e30f)), s, o);
+    float t, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(-act_arg<ACT>(g, fminf(g * g, 1e30f))));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + t));
     return g * s;
 }
 
