@@ -19,8 +19,9 @@
  * the call, in blocks of 128 along the summed axis:
  *   s = the least power of two >= 2^-127 with max|r| <= 448 s,   code = e4m3(r / s),
  * r / s is exact, the conversion rounds to nearest even.  The products of codes and
- * scales are exact in the tensor cores and summed there in fp32.  A row with a NaN or
- * an infinity gives a row of NaN; other rows are not affected.
+ * scales are exact in the tensor cores and summed there in fp32 (a sum whose parts
+ * pass fp32's range is infinite or NaN).  A row with a NaN or an infinity gives a row
+ * of NaN; other rows are not affected.
  *
  * Few rows (M <= 16, grouped M <= 32) are rounded by the product itself.  Such a call
  * needs no workspace: its size is 0 and ws may be NULL; the status word is then the
