@@ -340,7 +340,8 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
     const int b_rows = GATED ? (CG == 2 ? T : 2 * T) : T / CG;         // rows (backward: columns) of B in this CTA
     const int cols = GATED ? 2 * T : T;                                // columns of the accumulator
     const int a_bytes = args.a_rows * kFChunk;                         // of a chunk
-    const int b_bytes = (BWD ? 128 : b_rows) * kFChunk;
+    const int boxes = BWD ? (b_rows + 127) / 128 : 1;                  // of 128 columns (backward)
+    const int b_bytes = (BWD ? 128 * boxes : b_rows) * kFChunk;
     const int chunk_bytes = (FUSE ? 0 : a_bytes) + b_bytes;
     const int stage_bytes = per * chunk_bytes;
     const int stages = args.stages;
@@ -365,7 +366,8 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
         auto weight_box = [&](const I8Tile &t, int half, int x, auto &&copy) {
             const int n0 = t.wt * T;
             if (BWD) {
-                copy(half ? &tmW2 : &tmW, 0, n0 + (int)rank * b_rows, x);
+                for (int b = 0; b < boxes; ++b)
+                    copy(half ? &tmW2 : &tmW, b * 128 * kFChunk, n0 + (int)rank * b_rows + 128 * b, x);
             } else if (GATED && CG == 1) {
                 copy(&tmW, 0, x, n0);
                 copy(&tmW2, T * kFChunk, x, n0);
@@ -689,7 +691,9 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
             const bool issue = one_lane();
             const uint32_t s0 = smem_u32(smem) + ring0;
             const uint64_t dA = FUSE ? sdesc_sw128(smem_u32(smem)) : sdesc_sw128(s0);
-            const uint32_t dA0 = (uint32_t)dA, dB0 = (uint32_t)sdesc_sw128(s0 + (FUSE ? 0 : a_bytes));
+            // (backward: from 128 columns of B to the next 128 it is 16 KB)
+            const uint32_t dA0 = (uint32_t)dA, dB0 = ((uint32_t)sdesc_sw128(s0 + (FUSE ? 0 : a_bytes)) & 0xFFFFu) |
+                                                     (BWD ? (128u * kFChunk >> 4) << 16 : 1u << 16);
             const uint32_t desc_hi = (uint32_t)(dA >> 32);
             const uint32_t stage16 = stage_bytes >> 4, chunk16 = chunk_bytes >> 4, a16 = a_bytes >> 4;
             const uint32_t idesc0 = Cfg::kIdesc | (uint32_t)(cols >> 3) << 17;
@@ -898,7 +902,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                         finish(t, c, rows, (int64_t)t.row0 + first_row, r, q);
                     }
             }
-        } else if (fp8_warp_wait<CG>(bar_acc_full, 0, abort_flag, args.status, lane)) {
+        } else if (unit < tiles && fp8_warp_wait<CG>(bar_acc_full, 0, abort_flag, args.status, lane)) {
             // One tile a cluster.  Chunk c of its columns is finished by CTA c % split, to which the others
             // send theirs: few rows into a place of its own, else into the ring, once a CTA whose products
             // are done has told the others that its ring is free.
@@ -1135,7 +1139,7 @@ cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8S
     const int64_t Em = g.E > 0 ? g.E : 1;
     const int64_t summed = BWD ? g.N : g.K;
     const int halves = BWD && g.gated ? 2 : 1;
-    const int b_rows = BWD ? 128 : GATED ? (CG == 2 ? tile : 2 * tile) : tile / CG;
+    const int b_rows = BWD ? (tile / CG + 127) / 128 * 128 : GATED ? (CG == 2 ? tile : 2 * tile) : tile / CG;
     Fp8Args a;
     a.offsets = g.offsets;
     a.words = g.words;
@@ -1206,7 +1210,8 @@ cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8S
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cluster_attr(at[1], CG * sh.split);
-    const int64_t work = (a.width + tile - 1) / tile * ((g.M + 128 * CG - 1) / (128 * CG) + (g.E > 0 ? g.E : 0));
+    const int64_t some = g.E > 0 ? (g.E < g.M ? g.E : g.M) : 0;                  // experts: the most row tiles
+    const int64_t work = (a.width + tile - 1) / tile * (g.E > 0 ? some + g.M / (128 * CG) : (g.M + 128 * CG - 1) / (128 * CG));
     const int64_t most = CG == 2 ? room.pairs : room.clusters[sh.split];
     const int units = (int)(work < most ? work : most);
     cudaLaunchConfig_t cfg = {};
@@ -1220,46 +1225,57 @@ cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8S
 }
 
 // How a call's tiles are cut: the candidate with the least time by a simple count of cycles.  A chunk
-// of 128 summed values takes the longer of its products (2 cycles a column; one CTA: 140 more) and its copies (about 66
-// bytes a cycle and SM); between overlapping accumulators the products pause; a tile's groups may be shared by a cluster where all tiles run at once.
+// of 128 summed values takes the longer of its products (2 cycles a column; one CTA: 140 more) and its
+// copies (about 66 bytes a cycle and SM); between overlapping accumulators the products pause; a tile's
+// groups may be shared by a cluster where all tiles run at once, which costs some 8000 cycles.
+//
+// Experts: the host does not see the offsets.  It counts a row tile for each expert that can have rows,
+// or half of one and the whole ones that all rows make; no more than one and the whole ones each.
+// Measured, us a call, one CTA 128 and 224 columns wide (backward 256), pair 224 (256): 8192 rows of 61
+// experts, gated, 2 x 1408 x 2048: 95, 86, 95; 8192 of 64, backward, 2816 x 2048: 97, 89, 104; 8192 of 8,
+// 4096 x 2048: 90, 77, 74; 1500 of 64, 2816 x 2048: 70, 71, 90.  So pairs from 512 rows an expert on, and
+// tiles of 128 columns at most up to 32 (bound by the weights' bytes).
 Fp8Shape pick(const Fp8GemmLaunch &g, bool fuse, const Fp8Room &room)
 {
     const int64_t width = g.bwd ? g.K : g.N, summed = g.bwd ? g.N : g.K;
     const int weights = g.gated && !g.bwd ? 2 : 1;             // columns of B for an output channel
     const int64_t groups = fp8_groups(summed) * (g.gated && g.bwd ? 2 : 1);
+    const int64_t experts = g.E > 0 ? (g.E < g.M ? g.E : g.M) : 1, mean = g.M / experts;
     Fp8Shape best = {1, 128 / weights, 1};
     int64_t best_cost = INT64_MAX;
     auto offer = [&](int cg, int cols, int split) {
         const int tile = cols / weights;
-        const int64_t tiles = (g.M + 128 * cg - 1) / (128 * cg) * ((width + tile - 1) / tile);
+        const int64_t whole = g.M / (128 * cg), col_tiles = (width + tile - 1) / tile;
+        int64_t rows = (g.M + 128 * cg - 1) / (128 * cg), most_rows = rows;
+        if (g.E > 0) {
+            rows = experts / 2 + whole > experts ? experts / 2 + whole : experts;
+            most_rows = experts + whole;
+        }
         const int64_t units = cg == 2 ? room.pairs : room.clusters[split];
-        const int64_t rounds = (tiles + units - 1) / units;
-        if (split > 1 && rounds > 1)
+        if (split > 1 && most_rows * col_tiles > units)
             return;
-        const int64_t a = fuse ? 0 : cg == 2 || g.M >= 128 ? 128 : (g.M + 31) / 32 * 32;
-        const int64_t b = g.bwd ? 128 : cols / cg;
+        const int64_t tiles = rows * col_tiles;
+        // (in eighths; many rounds of tiles that are only an estimate: half of one for the last)
+        const int64_t rounds8 = g.E > 0 && tiles > 2 * units ? tiles * 8 / units + 4 : (tiles + units - 1) / units * 8;
+        const int64_t a = fuse ? 0 : cg == 2 || mean >= 96 ? 128 : (mean + 31) / 32 * 32;
+        const int64_t b = g.bwd ? (cols / cg + 127) / 128 * 128 : cols / cg;
         const int64_t mma = cg == 2 ? 2 * cols : 140 + 2 * cols, copy = (a + b) * kFChunk / 66;
         const int64_t chunk = mma > copy ? mma : copy;
-        const int64_t cost = rounds * ((groups + split - 1) / split * kFp8Group * chunk + (cols > 224 ? 2500 : 500)) + 10 * cols +
-                             (split == 1 ? 0 : 8000);
+        const int64_t cost = rounds8 * ((groups + split - 1) / split * kFp8Group * chunk + (cols > 224 ? 2500 : 500)) / 8 +
+                             10 * cols + (split == 1 ? 0 : 8000);
         if (cost < best_cost) {
             best_cost = cost;
             best = {cg, tile, split};
         }
     };
-    const int64_t rows = g.E > 1 ? (g.M + g.E - 1) / g.E : g.M;        // (experts: the mean)
-    if (g.E > 0) {
-        if (rows <= 128 || fuse)
-            return {1, 128 / weights, 1};
-        return {2, (g.bwd ? 256 : 224) / weights, 1};
-    }
-    if (!fuse)
+    if (!fuse && (g.E == 0 || mean >= 512))
         for (int cols = 256; cols >= 64; cols -= 32)
             offer(2, cols, 1);
     // (what shared memory holds of the others' sums)
     const int most = fuse ? (weights == 2 ? 3 : 4) : weights == 2 ? 6 : kFMaxSplit;
-    for (int cols = 128; cols >= (g.bwd ? 128 : 32); cols -= 16)
-        for (int split = 1; split <= most && split <= groups; ++split)
+    const int widest = g.E > 0 && mean > 32 ? (g.bwd ? 256 : 224) : 128;
+    for (int cols = widest; cols >= (g.bwd ? 128 : 32); cols -= g.bwd ? 128 : 16)
+        for (int split = 1; split <= most && split <= groups && (split == 1 || cols <= 128); ++split)
             offer(1, cols, split);
     return best;
 }
