@@ -469,18 +469,32 @@ def sq_grouped_workspace_bytes(op: int, E: int, M: int, N: int, K: int) -> int:
 
 
 _E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
-_FP8 = {}                                # entry point by name, looked up once
+_FP8 = {}                                # _fp8_entry's
+_byref = ctypes.byref
 _FP8_ACTS = {"silu": SQ_ACT_SILU, "gelu": SQ_ACT_GELU_TANH}
 
 
 def _fp8_refuse(fn, weights, rows, outs, offsets, flags, ws):
-    """Names what is wrong with the tensors of a block-scaled call."""
+    """Names what is wrong with the arguments of a block-scaled call (returns if nothing is)."""
     w, x = weights[0], rows[0]
     N, K, E = w.N, w.K, getattr(w, "E", None)
     back, gated = "bwd" in fn, len(weights) == 2
-    lead, dev = (() if E is None else (E,)), x.get_device()
+    for v in weights:
+        if v.fmt != SQ_FMT_FP8_BLOCK:
+            raise ValueError(f"{fn}: the weight must be SQ_FMT_FP8_BLOCK")
+        if v.lora_up is not None or v.lora_down is not None:
+            raise ValueError(f"{fn}: a block-scaled weight has no low-rank branch")
+        if v.N != N or v.K != K or getattr(v, "E", None) != E:
+            raise ValueError(f"{fn}: the two weights differ in their sizes")
+    if (E is not None) != ("grouped" in fn):
+        raise ValueError(f"{fn}: the weight is a {type(w).__name__}")
     names = ("dh", "gate", "up") if gated and back else ("dy",) if back else ("x",)
     onames = ("dx",) if back else ("h", "g", "u") if gated else ("y",)
+    wide = N if back else K
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] != wide or x.dtype is not _BF16:
+        got = f"{x.dtype} {list(x.shape)}" if isinstance(x, torch.Tensor) else type(x).__name__
+        raise ValueError(f"{fn}: {names[0]} must be bfloat16 [M, {wide}], got {got}")
+    lead, dev = (() if E is None else (E,)), x.get_device()
     want = [(t, name, dtype, shape) for v in weights
             for t, name, dtype, shape in ((v.codes, "codes", _E4M3, (*lead, N, K)),
                                           (v.scales, "scales", _E8M0, (*lead, (N + 127) // 128, (K + 127) // 128)))]
@@ -502,82 +516,75 @@ def _fp8_refuse(fn, weights, rows, outs, offsets, flags, ws):
             raise ValueError(f"{fn}: {name} is on {t.device}, {names[0]} on {x.device}")
         if not t.is_contiguous():
             raise ValueError(f"{fn}: expected a contiguous tensor for {name}")
+    if dev < 0:
+        raise ValueError(f"{fn}: expected a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{fn}: the tensors are on {x.device}, the current device is {torch.cuda.current_device()}")
+
+
+def _fp8_weight(v, N, K, codes, blocks, dev):
+    """The C handle of a block-scaled weight of these sizes, None if it is none."""
+    c, s = v.codes, v.scales
+    if (v.fmt == SQ_FMT_FP8_BLOCK and v.lora_up is None and v.lora_down is None and v.N == N and v.K == K
+            and c.dtype is _E4M3 and s.dtype is _E8M0 and c.shape == codes and s.shape == blocks
+            and c.get_device() == dev and s.get_device() == dev and c.is_contiguous() and s.is_contiguous()):
+        return _byref(sq_weight(SQ_FMT_FP8_BLOCK, N, K, c.data_ptr(), s.data_ptr()))
+    return None
 
 
 def _fp8(fn, weights, rows, offsets, act, outs, flags, ws, stream, fresh=False):
     """Checks and call of the block-scaled products.  weights: one Weight or GroupedWeight, or a gated pair;
     rows: x, dy, or (dh, gate, up); outs: y, dx, or (h, g, u), None: not wanted.  fresh: outs and ws were
-    made for this call on the rows' device, as the call needs them."""
+    made for this call on the rows' device, as the call needs them.
+
+    One pass checks every tensor's type and shape, that it is contiguous and on the current device; what
+    does not pass is named by _fp8_refuse."""
     w, x = weights[0], rows[0]
-    N, K, E = w.N, w.K, getattr(w, "E", None)
-    back = "bwd" in fn
-    for v in weights:
-        if v.fmt != SQ_FMT_FP8_BLOCK:
-            raise ValueError(f"{fn}: the weight must be SQ_FMT_FP8_BLOCK")
-        if v.lora_up is not None or v.lora_down is not None:
-            raise ValueError(f"{fn}: a block-scaled weight has no low-rank branch")
-        if v.N != N or v.K != K or getattr(v, "E", None) != E:
-            raise ValueError(f"{fn}: the two weights differ in their sizes")
-    if (E is not None) != ("grouped" in fn):
-        raise ValueError(f"{fn}: the weight is a {type(w).__name__}")
-    wide = N if back else K
-    shape = x.shape
-    if len(shape) != 2 or shape[1] != wide or x.dtype is not _BF16:
-        raise ValueError(f"{fn}: {('dh' if len(weights) == 2 else 'dy') if back else 'x'} must be bfloat16 [M, {wide}], "
-                         f"got {x.dtype} {list(x.shape)}")
-    M, dev = shape[0], x.get_device()
-    # every tensor: its type and shape, on one device, contiguous.  One pass for the usual call; the
-    # loop in _fp8_refuse names what is wrong.
-    if E is None:
-        codes, blocks = (N, K), (N + 127 >> 7, K + 127 >> 7)
-    else:
-        codes, blocks = (E, N, K), (E, N + 127 >> 7, K + 127 >> 7)
+    f, back, grouped = _FP8.get(fn) or _fp8_entry(fn)
+    N, K = w.N, w.K
+    args = ok = None
     try:
-        ok = x.is_contiguous()
-        args = []
-        for v in weights:
-            c, s = v.codes, v.scales
-            ok = (ok and c.dtype is _E4M3 and c.shape == codes and c.get_device() == dev and c.is_contiguous()
-                  and s.dtype is _E8M0 and s.shape == blocks and s.get_device() == dev and s.is_contiguous())
-            args.append(ctypes.byref(sq_weight(SQ_FMT_FP8_BLOCK, N, K, c.data_ptr(), s.data_ptr())))
-        if E is not None:
+        shape, dev = x.shape, x.get_device()
+        M, wide = shape
+        E = w.E if grouped else None
+        codes, blocks = ((E, N, K), (E, N + 127 >> 7, K + 127 >> 7)) if grouped else ((N, K), (N + 127 >> 7, K + 127 >> 7))
+        args = [_fp8_weight(v, N, K, codes, blocks, dev) for v in weights]
+        ok = (None not in args and wide == (N if back else K) and x.dtype is _BF16 and x.is_contiguous()
+              and dev >= 0 and dev == torch.cuda.current_device())
+        if grouped:
             args.append(E)
         args.append(x.data_ptr())
         for t in rows[1:]:
             ok = ok and t.dtype is _BF16 and t.shape == shape and t.get_device() == dev and t.is_contiguous()
             args.append(t.data_ptr())
         args.append(M)
-        if E is not None:
-            ok = (ok and isinstance(offsets, torch.Tensor) and offsets.dtype is torch.int32 and offsets.shape == (E + 1,)
-                  and offsets.get_device() == dev and offsets.is_contiguous())
+        if grouped:
+            ok = (ok and weights[-1].E == E and isinstance(offsets, torch.Tensor) and offsets.dtype is torch.int32
+                  and offsets.shape == (E + 1,) and offsets.get_device() == dev and offsets.is_contiguous())
+            args.append(offsets.data_ptr())
         if not fresh:
             ok = ok and _fp8_outs_fit(outs, (M, K if back else N), flags, ws, dev)
-    except AttributeError:                   # something else than a tensor
+        if len(weights) == 2:
+            args.append(act)
+        for t in outs:
+            args.append(None if t is None else t.data_ptr())
+    except (AttributeError, TypeError, ValueError):          # something else than a tensor, or than two dimensions
         ok = False
     if not ok:
         _fp8_refuse(fn, weights, rows, outs, offsets, flags, ws)
-    if dev < 0:
-        raise ValueError(f"{fn}: expected a CUDA tensor")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{fn}: the tensors are on {x.device}, the current device is {torch.cuda.current_device()}")
-    if E is not None:
-        if M == 0:
-            return
-        args.append(offsets.data_ptr())
-    if len(weights) == 2:
-        args.append(act)
-    for t in outs:
-        args.append(None if t is None else t.data_ptr())
-    f = _FP8.get(fn)
-    if f is None:
-        f = _FP8[fn] = getattr(lib(), fn)
+        raise ValueError(f"{fn}: the tensors do not fit the call")
+    if grouped and M == 0:
+        return
     stream = _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
-    if ws is None:
-        st = f(*args, flags, None, 0, stream)
-    else:
-        st = f(*args, flags, ws.data_ptr(), ws.nbytes, stream)
+    st = f(*args, flags, None, 0, stream) if ws is None else f(*args, flags, ws.data_ptr(), ws.nbytes, stream)
     if st != SQ_OK:
         _check(fn, st)
+
+
+def _fp8_entry(fn):
+    """(entry point, backward, grouped) by name, looked up once."""
+    e = _FP8[fn] = (getattr(lib(), fn), "bwd" in fn, "grouped" in fn)
+    return e
 
 
 def _fp8_outs_fit(outs, shape, flags, ws, dev):
@@ -916,23 +923,24 @@ def _fp8_out(fn, op, weights, rows, offsets, act, save, ws, flags, out_bf16, str
 
 
 def _fp8_out_here(fn, op, weights, rows, offsets, act, save, ws, flags, out_bf16, stream):
+    w, x = weights[0], rows[0]
     if out_bf16:
         flags |= SQ_OUT_BF16
-    w, x = weights[0], rows[0]
-    M, E = x.shape[0], getattr(w, "E", None)
-    width = w.K if "bwd" in fn else w.N
+    M, N, K, E = x.shape[0], w.N, w.K, None
+    if offsets is not None:
+        E = getattr(w, "E", None)
+        flags |= SQ_ZERO_UNGROUPED
+    width = K if op & 1 == 0 else N                          # (the backward operations are the even ones)
     y = x.new_empty(M, width, dtype=_BF16 if flags & SQ_OUT_BF16 else _F32)
     fresh = ws is None
     if fresh:
-        n = _w8a8_bytes(op, E, M, w.N, w.K)
+        n = _w8a8_bytes(op, E, M, N, K)
         if n:
             ws = x.new_empty(n, dtype=torch.uint8)
-    if E is not None:
-        flags |= SQ_ZERO_UNGROUPED
     outs = (y,)
     if act is not None:
         act = _fp8_act(fn, act)
-        if "fwd" in fn:
+        if op & 1:
             outs = (y, x.new_empty(M, width), x.new_empty(M, width)) if save else (y, None, None)
     _fp8(fn, weights, rows, offsets, act, outs, flags, ws, stream, fresh)
     return outs if save else y

@@ -1273,7 +1273,7 @@ Fp8Shape pick(const Fp8GemmLaunch &g, bool fuse, const Fp8Room &room)
             offer(2, cols, 1);
     // (what shared memory holds of the others' sums)
     const int most = fuse ? (weights == 2 ? 3 : 4) : weights == 2 ? 6 : kFMaxSplit;
-    const int widest = g.E > 0 && mean > 32 ? (g.bwd ? 256 : 224) : 128;
+    const int widest = mean > 32 ? (g.bwd ? 256 : 224) : 128;
     for (int cols = widest; cols >= (g.bwd ? 128 : 32); cols -= g.bwd ? 128 : 16)
         for (int split = 1; split <= most && split <= groups && (split == 1 || cols <= 128); ++split)
             offer(1, cols, split);
