@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
         };
         // kAhead groups in turn: the next ones' values are on their way while one is written (a load takes
         // 2 us and more while the weights stream)
-        constexpr int kAhead = 3;
+        constexpr int kAhead = FUSE ? 1 : 3;
         Item items[kAhead];
         Raw raws[kAhead];
         Item next;                                // the last one fetched
@@ -657,29 +657,38 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
             next.t = plan.find(unit, next.e);
             more = advance(next, set);
         }
-        int held = 0;                             // fetched, not yet written
-#pragma unroll
-        for (int d = 0; d < kAhead - 1; ++d)
-            if (more) {
-                items[d] = next;
-                fetch(next, raws[d]);
-                ++held;
+        if constexpr (kAhead == 1) {
+            while (more) {
+                fetch(next, raws[0]);
+                if (!put(next, raws[0]))
+                    break;
                 more = advance(next, S);
             }
-        bool ok = true;
-        while (ok && held > 0) {
+        } else {
+            int held = 0;                         // fetched, not yet written
 #pragma unroll
-            for (int d = 0; d < kAhead; ++d) {
-                if (!ok || held == 0)
-                    break;
+            for (int d = 0; d < kAhead - 1; ++d)
                 if (more) {
-                    items[(d + kAhead - 1) % kAhead] = next;
-                    fetch(next, raws[(d + kAhead - 1) % kAhead]);
+                    items[d] = next;
+                    fetch(next, raws[d]);
                     ++held;
                     more = advance(next, S);
                 }
-                ok = put(items[d], raws[d]);
-                --held;
+            bool ok = true;
+            while (ok && held > 0) {
+#pragma unroll
+                for (int d = 0; d < kAhead; ++d) {
+                    if (!ok || held == 0)
+                        break;
+                    if (more) {
+                        items[(d + kAhead - 1) % kAhead] = next;
+                        fetch(next, raws[(d + kAhead - 1) % kAhead]);
+                        ++held;
+                        more = advance(next, S);
+                    }
+                    ok = put(items[d], raws[d]);
+                    --held;
+                }
             }
         }
         if (FUSE && args.finite_check && bad)
