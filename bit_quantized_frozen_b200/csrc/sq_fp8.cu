@@ -158,7 +158,7 @@ __device__ __forceinline__ void store_rows64(const uint32_t (&v)[16], Fp8Patch &
     if (map) {
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0)
+        if (lane == 0 && rows > 0)
             tma_store_2d(map, smem_u32(patch), x, y);
     } else {
         __syncwarp();
@@ -184,20 +184,21 @@ __device__ __forceinline__ void store_cols(const float (&o)[C], Fp8Patch &out, c
     const int lane = out.lane;
     uint8_t *dst = reinterpret_cast<uint8_t *>(y) + (bf16 ? 2 : 4) * (row * width + col);
     if constexpr (C == 16) {
-        if (lane >= rows)
-            return;
         dst += (bf16 ? 2 : 4) * width * lane;
         if (bf16) {
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
-                if (8 * p < cols)
-                    *reinterpret_cast<uint4 *>(dst + 16 * p) =
-                        make_uint4(f32x2_to_bf16x2_bits(o[8 * p], o[8 * p + 1]), f32x2_to_bf16x2_bits(o[8 * p + 2], o[8 * p + 3]),
-                                   f32x2_to_bf16x2_bits(o[8 * p + 4], o[8 * p + 5]), f32x2_to_bf16x2_bits(o[8 * p + 6], o[8 * p + 7]));
+            for (int p = 0; p < 2; ++p) {
+                const uint4 v = make_uint4(f32x2_to_bf16x2_bits(o[8 * p], o[8 * p + 1]),
+                                           f32x2_to_bf16x2_bits(o[8 * p + 2], o[8 * p + 3]),
+                                           f32x2_to_bf16x2_bits(o[8 * p + 4], o[8 * p + 5]),
+                                           f32x2_to_bf16x2_bits(o[8 * p + 6], o[8 * p + 7]));
+                if (lane < rows && 8 * p < cols)
+                    *reinterpret_cast<uint4 *>(dst + 16 * p) = v;
+            }
         } else {
 #pragma unroll
             for (int p = 0; p < 4; ++p)
-                if (4 * p < cols)
+                if (lane < rows && 4 * p < cols)
                     *reinterpret_cast<float4 *>(dst + 16 * p) = make_float4(o[4 * p], o[4 * p + 1], o[4 * p + 2], o[4 * p + 3]);
         }
     } else {
@@ -658,6 +659,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
             more = advance(next, set);
         }
         if constexpr (kAhead == 1) {
+#pragma unroll 1
             while (more) {
                 fetch(next, raws[0]);
                 if (!put(next, raws[0]))
@@ -813,7 +815,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
         auto finish = [&](const I8Tile &t, int c, int rows, int64_t row, const float (&r)[C], const float (&q)[GATED ? C : 1]) {
             const int64_t col = (int64_t)t.wt * T + c;
             const int live = (int)min((int64_t)min(T - c, C), args.width - col);
-            if (rows <= 0 || live <= 0 || !SQ_DCHECK(row + rows <= args.M && col + live <= args.width, args.status))
+            if (live <= 0 || !SQ_DCHECK(rows <= 0 || (row + rows <= args.M && col + live <= args.width), args.status))
                 return;
             // all 32 rows and C columns are the tile's, or lie behind the matrix's end
             const bool whole = (rows == 32 || args.E == 0) && (live == C || col + live == args.width);
@@ -876,11 +878,17 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                                     make_uint4(0u, 0u, 0u, 0u);
                 }
         }
+        // Few rows: the first turn is a dry one, while the products run.  It reads what tensor memory happens
+        // to hold and writes nothing, so that the code is there when it is needed (a split tile's sums came
+        // together 4 us after its products without, 1.5 us with it).
+        bool dry = FUSE;
         if (split == 1) {
-            for (int tile = unit; tile < tiles; tile += units, ++count) {
+#pragma unroll 1
+            for (int tile = unit; tile < tiles;) {
                 const I8Tile t = plan.find(tile, e);
                 const int slot = count & 1;
-                if (!fp8_warp_wait<CG>(bar_acc_full + 8 * slot, (uint32_t)((count >> 1) & 1), abort_flag, args.status, lane))
+                if (!dry && !fp8_warp_wait<CG>(bar_acc_full + 8 * slot, (uint32_t)((count >> 1) & 1), abort_flag,
+                                               args.status, lane))
                     break;
                 tc_fence_after();
                 const uint32_t acc = tmem_base + ((uint32_t)(32 * wq) << 16) + (slot ? slot1 : 0u);
@@ -889,7 +897,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                 auto release = [&]() {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) {
+                    if (lane == 0 && !dry) {
                         if (CG == 2)
                             mbar_arrive_cluster(acc_empty_leader + 8 * slot);
                         else
@@ -902,43 +910,59 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                 if (held == 0)
                     release();
                 if (rows > 0)
-                    for (int i = 0; i < own; ++i) {
+                    for (int i = 0; i < (dry ? min(own, 1) : own); ++i) {
                         const int c = C * chunk_of(slot ? i : own - 1 - i);
                         float r[C], q[GATED ? C : 1];
                         load_chunk(acc, c, r, q);
                         if (i == held - 1)
                             release();
-                        finish(t, c, rows, (int64_t)t.row0 + first_row, r, q);
+                        finish(t, c, dry ? 0 : rows, (int64_t)t.row0 + first_row, r, q);
                     }
+                if (!dry) {
+                    tile += units;
+                    ++count;
+                }
+                dry = false;
             }
-        } else if (unit < tiles && fp8_warp_wait<CG>(bar_acc_full, 0, abort_flag, args.status, lane)) {
-            // One tile a cluster.  Chunk c of its columns is finished by CTA c % split, to which the others
+        }
+#pragma unroll 1
+        for (int turn = FUSE ? 0 : 1; split > 1 && unit < tiles && turn < 2; ++turn) {
+            dry = turn == 0;
+            if (!dry && !fp8_warp_wait<CG>(bar_acc_full, 0, abort_flag, args.status, lane))
+                break;
+            // One tile a cluster.  Each chunk of its columns is finished by one CTA, owner(c), to which the others
             // send theirs: few rows into a place of its own, else into the ring, once a CTA whose products
             // are done has told the others that its ring is free.
             constexpr int kParts = GATED ? 2 : 1;
             tc_fence_after();
             const I8Tile t = plan.find(unit, e);
             const uint32_t acc = tmem_base + ((uint32_t)(32 * wq) << 16);
-            const int rows = min(t.rows - 32 * wq, 32);
-            const int mine = (chunks - part + split - 1) / split;      // chunks that this CTA finishes
-            if (wq == 0 && wh == 0) {
+            const int rows = dry ? 0 : min(t.rows - 32 * wq, 32);
+            const bool some_rows = t.rows > 32 * wq;
+            // (FUSE: a warp has every other chunk)
+            auto owner = [&](int c) { return (FUSE ? c >> 1 : c) % split; };
+            auto place_of = [&](int c) { return FUSE ? (c >> 1) / split * 2 + (c & 1) : c / split; };
+            int mine = 0;                                              // chunks that this CTA finishes
+            for (int c = 0; c < chunks; ++c)
+                mine += owner(c) == part ? 1 : 0;
+            if (wq == 0 && wh == 0 && !dry) {
                 if (!FUSE && lane < split && lane != part)
                     mbar_arrive_cluster(mapa_shared(bar_peers, lane));
                 if (lane == 0)
                     mbar_arrive_expect_tx(bar_parts, mine * (split - 1) * t.rows * (4 * C) * kParts);
             }
-            // place of a chunk's part from CTA `from`: [chunk / split][from][gate, up][quarter][C / 4][lanes] float4
+            // place of a chunk's part from CTA `from`: [place_of(c)][from][gate, up][quarter][C / 4][lanes] float4
             constexpr int kLanes = FUSE ? kFuseRows : 32;
             uint8_t *parts = FUSE ? rest : smem;
             auto place = [&](int c, int from, int which) {
-                return (uint32_t)(((((c / split) * split + from) * kParts + which) * (FUSE ? 1 : 4) + wq) * (C / 4) * kLanes + lane) *
+                return (uint32_t)((((place_of(c) * split + from) * kParts + which) * (FUSE ? 1 : 4) + wq) * (C / 4) * kLanes + lane) *
                        16u;
             };
             const uint32_t s0 = smem_u32(parts);
-            bool ok = FUSE || fp8_warp_wait<2>(bar_peers, 0, abort_flag, args.status, lane);
-            if (ok && rows > 0)
+            bool ok = FUSE || dry || fp8_warp_wait<2>(bar_peers, 0, abort_flag, args.status, lane);
+            if (ok && some_rows)
                 for (int i = 0; i < own; ++i) {
-                    const int c = chunk_of(i), to = c % split;
+                    const int c = chunk_of(i), to = owner(c);
                     if (to == part)
                         continue;
                     float r[C], q[GATED ? C : 1];
@@ -953,11 +977,11 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                         }
                 }
             __syncwarp();
-            ok = ok && fp8_warp_wait<2>(bar_parts, 0, abort_flag, args.status, lane);
-            if (ok && rows > 0)
+            ok = ok && (dry || fp8_warp_wait<2>(bar_parts, 0, abort_flag, args.status, lane));
+            if (ok && some_rows)
                 for (int i = 0; i < own; ++i) {
                     const int c = chunk_of(i);
-                    if (c % split != part)
+                    if (owner(c) != part)
                         continue;
                     float r[C], q[GATED ? C : 1];
                     load_chunk(acc, C * c, r, q);
