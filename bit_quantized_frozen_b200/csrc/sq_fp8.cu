@@ -64,7 +64,7 @@ struct Fp8Cfg {
     //   patches of the stores; FUSE: a split tile's sums from the other CTAs.  (CG = 1: the MMA reads
     //   128 rows of A, up to 16 KB behind the last stage.)
     static constexpr int kPatches = CG == 2 && MODE != kFp8Bwd ? 2 : 1;       // of an epilogue warp
-    static constexpr int kPatchBytes = FUSE ? 12 * 1024 : 8 * kPatches * kFPatchBytes;
+    static constexpr int kPatchBytes = FUSE ? 24 * 1024 : 8 * kPatches * kFPatchBytes;
     static constexpr int kPlanOff = kPatchBytes;
     static constexpr int kFeedOff = kPlanOff + (2 * kMaxExperts + 4) * 4;     // [sets][2][32] words (FUSE)
     static constexpr int kBarOff = kFeedOff + kSets * 2 * 32 * 4;
@@ -951,12 +951,10 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                 if (lane == 0)
                     mbar_arrive_expect_tx(bar_parts, mine * (split - 1) * t.rows * (4 * C) * kParts);
             }
-            // place of a chunk's part from CTA `from`: [place_of(c)][from][gate, up][quarter][C / 4][lanes] float4
-            constexpr int kLanes = FUSE ? kFuseRows : 32;
+            // place of a chunk's part from CTA `from`: [place_of(c)][from][gate, up][quarter][C / 4][lane] float4
             uint8_t *parts = FUSE ? rest : smem;
             auto place = [&](int c, int from, int which) {
-                return (uint32_t)((((place_of(c) * split + from) * kParts + which) * (FUSE ? 1 : 4) + wq) * (C / 4) * kLanes + lane) *
-                       16u;
+                return (uint32_t)((((place_of(c) * split + from) * kParts + which) * (FUSE ? 1 : 4) + wq) * (C / 4) * 32 + lane) * 16u;
             };
             const uint32_t s0 = smem_u32(parts);
             bool ok = FUSE || dry || fp8_warp_wait<2>(bar_peers, 0, abort_flag, args.status, lane);
@@ -971,9 +969,9 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                     if (lane < rows)
 #pragma unroll
                         for (int j = 0; j < C / 4; ++j) {
-                            st_async_v4(dst + place(c, part, 0) + j * 16 * kLanes, r + 4 * j, bar);
+                            st_async_v4(dst + place(c, part, 0) + j * 512, r + 4 * j, bar);
                             if constexpr (GATED)
-                                st_async_v4(dst + place(c, part, 1) + j * 16 * kLanes, q + 4 * j, bar);
+                                st_async_v4(dst + place(c, part, 1) + j * 512, q + 4 * j, bar);
                         }
                 }
             __syncwarp();
@@ -990,7 +988,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                         for (int from = 0; from < split; ++from) {
                             const float4 w = from == part || lane >= rows ? make_float4(v[0], v[1], v[2], v[3])
                                                           : *reinterpret_cast<const float4 *>(
-                                                                parts + place(c, from, which) + j * 16 * kLanes);
+                                                                parts + place(c, from, which) + j * 512);
                             sum.x += w.x;
                             sum.y += w.y;
                             sum.z += w.z;

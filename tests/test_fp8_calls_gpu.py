@@ -547,3 +547,31 @@ def test_few_and_many_rows_of_many_experts(E, M):
         W = ref.dequant(q[e], s[e])
         ref.check(y[a], *ref.forward(x[a], W), False)
         ref.check(dx[a], *ref.backward(dy[a], W), False)
+
+
+@pytest.mark.parametrize("off", [[0, 31], [0, 18, 32], [0, 0, 32], [2, 24, 24]])
+@pytest.mark.parametrize("long", [2064, 16384])
+def test_few_rows_of_few_experts_on_shared_tiles(off, long):
+    # one or two experts with more than 16 rows, few columns and a long sum: a cluster shares each tile
+    E, M, short = len(off) - 1, off[-1], 96
+    rng = np.random.default_rng([M, E, long])
+    offd = dev(np.array(off, np.int32))
+    rows_of = [(e, slice(off[e], off[e + 1])) for e in range(E) if off[e + 1] > off[e]]
+    q, s = layer(rng, short, long, E)
+    q2, s2 = layer(rng, short, long, E)
+    x = rand(rng, M, long)
+    y = f32(sq.grouped_fwd_fp8(weight(q, s), dev(x, BF), offd))
+    h = f32(sq.grouped_gated_fwd_fp8(weight(q, s), weight(q2, s2), dev(x, BF), offd))
+    for e, a in rows_of:
+        W, W2 = ref.dequant(q[e], s[e]), ref.dequant(q2[e], s2[e])
+        ref.check(y[a], *ref.forward(x[a], W), False)
+        ref.check(h[a], *ref.gated_forward(x[a], W, W2, "silu")[0], False)
+    q, s = layer(rng, long, short, E)
+    q2, s2 = layer(rng, long, short, E)
+    dy, g, u = rand(rng, M, long), rand(rng, M, long), rand(rng, M, long)
+    dx = f32(sq.grouped_bwd_dx_fp8(weight(q, s), dev(dy, BF), offd))
+    dx2 = f32(sq.grouped_gated_bwd_dx_fp8(weight(q, s), weight(q2, s2), dev(dy, BF), dev(g, BF), dev(u, BF), offd))
+    for e, a in rows_of:
+        W, W2 = ref.dequant(q[e], s[e]), ref.dequant(q2[e], s2[e])
+        ref.check(dx[a], *ref.backward(dy[a], W), False)
+        ref.check(dx2[a], *ref.gated_backward(dy[a], g[a], u[a], W, W2, "silu"), False)
