@@ -616,6 +616,9 @@ def sq_build_fp8(W, codes, scales, stream=None):
         raise ValueError(f"{fn}: W must be float32 or bfloat16, got {W.dtype}")
     _need(fn, "codes", codes, N * K)
     _need(fn, "scales", scales, (N + 127) // 128 * ((K + 127) // 128))
+    for t, name in ((W, "W"), (codes, "codes"), (scales, "scales")):
+        if isinstance(t, torch.Tensor) and t.get_device() >= 0 and t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"{fn}: {name} is on {t.device}, the current device is {torch.cuda.current_device()}")
     _check(fn, lib().sq_build_fp8(_ptr(W), N, K, SQ_IN_BF16 if W.dtype is _BF16 else 0, _ptr(codes), _ptr(scales),
                                   _stream(stream)))
 

@@ -575,3 +575,20 @@ def test_few_rows_of_few_experts_on_shared_tiles(off, long):
         W, W2 = ref.dequant(q[e], s[e]), ref.dequant(q2[e], s2[e])
         ref.check(dx[a], *ref.backward(dy[a], W), False)
         ref.check(dx2[a], *ref.gated_backward(dy[a], g[a], u[a], W, W2, "silu"), False)
+
+
+def test_device_checks(monkeypatch):
+    w = weight(*layer(np.random.default_rng(0), 128, 256))
+    W, x, dy = torch.zeros(128, 256, device="cuda"), torch.zeros(4, 256, dtype=BF, device="cuda"), torch.zeros(40, 128, dtype=BF, device="cuda")
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    with monkeypatch.context() as m:
+        m.setattr(torch.cuda, "current_device", lambda: 1)
+        for f in (lambda: sq.build_fp8(W), lambda: sq.linear_fwd_fp8(w, x), lambda: sq.linear_bwd_dx_fp8(w, dy, ws=ws),
+                  lambda: sq.gated_fwd_fp8(w, w, x, save=True)):
+            with pytest.raises(ValueError, match="current device"):
+                f()
+    with pytest.raises(ValueError, match="ws is on cpu"):
+        sq.linear_bwd_dx_fp8(w, dy, ws=ws.cpu())
+    w.scales = w.scales.cpu()
+    with pytest.raises(ValueError, match="scales is on cpu"):
+        sq.linear_fwd_fp8(w, x)
