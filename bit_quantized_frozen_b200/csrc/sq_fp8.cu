@@ -18,7 +18,7 @@
 // to four groups ahead of the products.  (Copied by the issuing thread from shared memory instead,
 // tcgen05.cp, each group held the tensor pipe up by some 600 cycles.)
 //
-// Few rows (at most kFuseRows): the feeders round the rows themselves, straight into the operand's
+// Few rows (fp8_rounds_rows): the feeders round the rows themselves, straight into the operand's
 // shared-memory layout, and the call is one kernel.
 //
 // CTA (CG = 1, tiles of 128 tokens x up to 128 columns) or CTA pair (CG = 2, 256 x up to 256) per SM,
@@ -1257,7 +1257,7 @@ cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8S
 
 // How a call's tiles are cut: the candidate with the least time by a simple count of cycles.  A chunk
 // of 128 summed values takes the longer of its products (2 cycles a column; one CTA: 140 more) and its
-// copies (about 66 bytes a cycle and SM); between overlapping accumulators the products pause; a tile's
+// copies (about 66 bytes a cycle and SM), few rows at least their rounding; between overlapping accumulators the products pause; a tile's
 // groups may be shared by a cluster where all tiles run at once, which costs some 8000 cycles.
 //
 // Experts: the host does not see the offsets.  It counts a row tile for each expert that can have rows,
@@ -1291,8 +1291,8 @@ Fp8Shape pick(const Fp8GemmLaunch &g, bool fuse, const Fp8Room &room)
         const int64_t a = fuse ? 0 : cg == 2 || mean >= 96 ? 128 : (mean + 31) / 32 * 32;
         const int64_t b = g.bwd ? (cols / cg + 127) / 128 * 128 : cols / cg;
         const int64_t mma = cg == 2 ? 2 * cols : 140 + 2 * cols, copy = (a + b) * kFChunk / 66;
-        const int64_t chunk = mma > copy ? mma : copy;
-        const int64_t cost = rounds8 * ((groups + split - 1) / split * kFp8Group * chunk + (cols > 224 ? 2500 : 500)) / 8 +
+        const int64_t group = kFp8Group * (mma > copy ? mma : copy), rounding = fuse ? 250 + 450 * ((mean + 3) / 4) : 0;
+        const int64_t cost = rounds8 * ((groups + split - 1) / split * (group > rounding ? group : rounding) + (cols > 224 ? 2500 : 500)) / 8 +
                              10 * cols + (split == 1 ? 0 : 8000);
         if (cost < best_cost) {
             best_cost = cost;
@@ -1323,9 +1323,15 @@ cudaError_t launch_mode(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8
 
 }  // namespace
 
-bool fp8_rounds_rows(int E, int64_t M)
+// Every CTA rounds the rows for itself: that saves a launch (some 3 us), and costs more with each row, most
+// for a gated pair's gradients.  Measured, us a call, one kernel and two: 8 x 5696 x 1872 6.9, 10.2; gradient
+// of 16 x 1536 11.1, 11.4; gated gradients of 3 x 1568 x 3712 11.4, 12.6, 6 x 544 x 7936 11.6, 9.4 and
+// 16 x 6912 x 14592 116, 38.  Of experts a tile has only some of the rows.
+bool fp8_rounds_rows(int E, int64_t M, bool gated_bwd)
 {
-    return M <= (E > 0 ? 32 : kFuseRows);
+    if (gated_bwd)
+        return M <= (E > 1 ? 8 : 4);
+    return M <= (E > 1 ? 2 * kFuseRows : kFuseRows);
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, int sms, cudaStream_t stream)
@@ -1337,7 +1343,7 @@ cudaError_t launch_fp8_gemm(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, int s
     const Fp8Room *room = nullptr;
     if (cudaError_t e = room_of(dev, ctx, sms, &room); e != cudaSuccess)
         return e;
-    const bool fuse = fp8_rounds_rows(g.E, g.M);
+    const bool fuse = fp8_rounds_rows(g.E, g.M, g.bwd && g.gated);
     const Fp8Shape sh = pick(g, fuse, *room);
     if (sh.cg == 2)
         return launch_mode<2, false>(g, q, sh, dev, *room, stream);

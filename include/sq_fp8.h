@@ -23,10 +23,11 @@
  * pass fp32's range is infinite or NaN).  A row with a NaN or an infinity gives a row
  * of NaN; other rows are not affected.
  *
- * Few rows (M <= 16, grouped M <= 32) are rounded by the product itself.  Such a call
- * needs no workspace: its size is 0 and ws may be NULL; the status word is then the
- * library's own (sq_check_device_status(NULL, stream)), to which calls only add.  A
- * workspace given all the same holds at least 256 bytes.
+ * Few rows are rounded by the product itself: M <= 16, for E > 1 experts M <= 32; the
+ * gradient of a gated pair M <= 4, for E > 1 experts M <= 8.  Such a call needs no
+ * workspace: its size is 0 and ws may be NULL; the status word is then the library's
+ * own (sq_check_device_status(NULL, stream)), to which calls only add.  A workspace
+ * given all the same holds at least 256 bytes.
  */
 #ifndef SQ_FP8_H
 #define SQ_FP8_H

@@ -54,6 +54,11 @@ def size(fn, op, M, N, K, E=4):
     return sq.sq_grouped_workspace_bytes(op, E, M, N, K) if "grouped" in fn else sq.sq_workspace_bytes(op, M, N, K)
 
 
+def few_rows(fn, e):
+    """Rows that the product rounds itself: calls that need no workspace."""
+    return (4 if "gated_bwd" in fn else 16) * (2 if "grouped" in fn and e > 1 else 1)
+
+
 @pytest.mark.parametrize("call,fn,op", CALLS)
 def test_refusals(call, fn, op):
     two = "gated" in fn
@@ -75,7 +80,7 @@ def test_refusals(call, fn, op):
     assert call(fn, M=-1) == SHAPE and call(fn, M=(1 << 24) + 1) == SHAPE
     for flags in (sq.SQ_ACT_STATIC_SCALE, sq.SQ_RECON_RESIDUAL_ONLY, sq.SQ_RECON_TRANSPOSED, sq.SQ_IN_BF16, 0x80):
         assert call(fn, flags=flags) == ARG
-    few = 32 if "grouped" in fn else 16                                     # rows that need no workspace
+    few = few_rows(fn, E)
     assert call(fn, M=few, nb=255) == WORKSPACE and call(fn, M=few + 1, ws=None) == NULL
     n = size(fn, op, 40, 256, 512)
     assert n > 40 * 256 and call(fn, nb=n - 1) == WORKSPACE and call(fn, nb=0) == WORKSPACE
@@ -195,7 +200,7 @@ def test_workspace_covers_its_parts():
             wide = n if back else k
             need = 256 + halves * m * (wide + 4 * ((wide + 511) // 512))
             for e in (1, 64, 1024):
-                if m <= (32 if "grouped" in fn else 16):               # few rows are rounded by the product
+                if m <= few_rows(fn, e):
                     assert size(fn, op, m, n, k, e) == 0
                 else:
                     assert need <= size(fn, op, m, n, k, e) <= need + 4 * 1024
