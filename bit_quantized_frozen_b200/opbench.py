@@ -19,6 +19,10 @@ Operations:
   fwd_int8             sq_linear_fwd, int8 per-row weight (rank-16 low-rank branch)
   fwd_w8a8             sq_linear_fwd_w8a8, int8 per-row weight, 8-bit integer product
   bwd_dx_w8a8          sq_linear_bwd_dx_w8a8 on the same weight
+  fwd_fp8 / bwd_dx_fp8 sq_linear_fwd_fp8, sq_linear_bwd_dx_fp8, block-scaled e4m3 weight, bf16 result
+  gated_fwd_fp8        sq_gated_fwd_fp8 (silu) on two such weights, g and u kept
+  gated_bwd_dx_fp8     sq_gated_bwd_dx_fp8 on the same, bf16 result
+  build_fp8            sq_build_fp8
   build_nvfp4          sq_build_nvfp4
   build_int4           sq_build_int4, group 32
   build_int4_g64       sq_build_int4, group 64
@@ -66,10 +70,10 @@ import synth_inputs as si  # noqa: E402
 
 FLUSH_BYTES = 256 << 20
 
-OPS = ["act_quant", "act_quant_nolowrank", "fwd_nvfp4", "fwd_int4", "fwd_int8", "fwd_w8a8", "build_nvfp4", "build_int4",
-       "build_int4_g64", "build_int8", "recon_nvfp4", "recon_int4", "recon_int4_g64", "recon_int8",
+OPS = ["act_quant", "act_quant_nolowrank", "fwd_nvfp4", "fwd_int4", "fwd_int8", "fwd_w8a8", "fwd_fp8", "gated_fwd_fp8", "build_nvfp4",
+       "build_int4", "build_int4_g64", "build_int8", "build_fp8", "recon_nvfp4", "recon_int4", "recon_int4_g64", "recon_int8",
        "recon_nvfp4_resid", "recon_int4_resid", "recon_int8_resid", "recon_nvfp4_t", "gemm_nvfp4", "gemm_int4",
-       "bwd_dx_nvfp4", "bwd_dx_w8a8", "gemm_bwd_dx", "svd_init"]
+       "bwd_dx_nvfp4", "bwd_dx_w8a8", "bwd_dx_fp8", "gated_bwd_dx_fp8", "gemm_bwd_dx", "svd_init"]
 SVD_ITERS = 8
 
 
@@ -80,6 +84,8 @@ def work(op, M, N, K):
         return "GB/s", MK * (2 + 0.5 + 1 / 16) + (M * 32 * 4 if op == "act_quant" else 0)
     if op == "svd_init":   # fp32 FMA work: two products with W per round, then the residual's chain
         return "TFLOP/s", (4.0 * SVD_ITERS + 2.0) * N * K * 32
+    if op.startswith("gated"):
+        return "TFLOP/s", 4.0 * M * N * K
     if op.startswith("fwd") or op.startswith("gemm") or op.startswith("bwd"):
         return "TFLOP/s", 2.0 * M * N * K
     if op == "build_nvfp4":
@@ -90,6 +96,8 @@ def work(op, M, N, K):
         return "GB/s", NK * (4 + 0.5 + 3 / 64)
     if op == "build_int8":
         return "GB/s", NK * (4 + 1) + N * 5
+    if op == "build_fp8":
+        return "GB/s", NK * (4 + 1 + 2.0 ** -14)
     if op.startswith("recon_int8"):
         return "GB/s", NK * (1 + 2) + N * 4
     scale = {"nvfp4": 1 / 16, "int4": 2 / 32, "int4_g64": 2 / 64}[
@@ -212,10 +220,20 @@ def main():
     ws_8 = sq.workspace(sq.SQ_OP_LINEAR_FWD_INT8, M, N, K, dev)
     ws_q = sq.workspace(sq.SQ_OP_LINEAR_FWD_W8A8, M, N, K, dev)
     ws_qb = sq.workspace(sq.SQ_OP_LINEAR_BWD_DX_W8A8, M, N, K, dev)
+    if any("fp8" in op for op in args.op):
+        w_f, w_f2 = sq.build_fp8(R), sq.build_fp8(R.flip(0))
+        ws_f = sq.workspace(sq.SQ_OP_LINEAR_FWD_FP8, M, N, K, dev)
+        ws_fb = sq.workspace(sq.SQ_OP_GATED_BWD_DX_FP8, M, N, K, dev)
+        h_f, g_f, u_f = (torch.empty((M, N), dtype=torch.bfloat16, device=dev) for _ in range(3))
+        dx_f = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        cf, sf_f = torch.empty_like(w_f.codes), torch.empty_like(w_f.scales)
+        sq.sq_gated_fwd_fp8(w_f, w_f2, x, h_f, g_f, u_f, flags=sq.SQ_OUT_BF16, ws=ws_f)
     ws_b = sq.workspace(sq.SQ_OP_BUILD_NVFP4, 0, N, K, dev)
     ws_a = sq.workspace(sq.SQ_OP_ACT_QUANT_NVFP4, M, 0, K, dev)
     ws_n = sq.workspace(sq.SQ_OP_LINEAR_FWD_NVFP4, M, N, K, dev)
     ws_i = sq.workspace(sq.SQ_OP_LINEAR_FWD_INT4, M, N, K, dev)
+    for ws in (ws_n, ws_i):               # (no status yet, should no selected operation use them)
+        ws[:4].zero_()
     xc = torch.empty((M, K // 2), dtype=torch.uint8, device=dev)
     xsf = torch.empty(sq.sq_sf_bytes(M, K), dtype=torch.uint8, device=dev)
     gx = torch.empty(1, dtype=torch.float32, device=dev)
@@ -247,6 +265,11 @@ def main():
         "fwd_int8": lambda: sq.sq_linear_fwd(w8, x, y, ws=ws_8),
         "fwd_w8a8": lambda: sq.sq_linear_fwd_w8a8(w8, x, y, ws=ws_q),
         "bwd_dx_w8a8": lambda: sq.sq_linear_bwd_dx_w8a8(w8, dy, dx, ws=ws_qb),
+        "fwd_fp8": lambda: sq.sq_linear_fwd_fp8(w_f, x, h_f, sq.SQ_OUT_BF16, ws_f),
+        "bwd_dx_fp8": lambda: sq.sq_linear_bwd_dx_fp8(w_f, dy, dx_f, sq.SQ_OUT_BF16, ws_fb),
+        "gated_fwd_fp8": lambda: sq.sq_gated_fwd_fp8(w_f, w_f2, x, h_f, g_f, u_f, flags=sq.SQ_OUT_BF16, ws=ws_f),
+        "gated_bwd_dx_fp8": lambda: sq.sq_gated_bwd_dx_fp8(w_f, w_f2, dy, g_f, u_f, dx_f, flags=sq.SQ_OUT_BF16, ws=ws_fb),
+        "build_fp8": lambda: sq.sq_build_fp8(R, cf, sf_f),
         "build_int8": lambda: sq.sq_build_int8(R, c8, s8, f8),
         "recon_int8": lambda: sq.sq_reconstruct_bf16(w8, W),
         "recon_int8_resid": lambda: sq.sq_reconstruct_bf16(w8, W, RES),
@@ -302,6 +325,10 @@ def main():
         print(json.dumps(line), flush=True)
     sq.sq_check_device_status(ws_n)
     sq.sq_check_device_status(ws_i)
+    if any("fp8" in op for op in args.op):
+        sq.sq_check_device_status(ws_f)
+        if any("bwd_dx_fp8" in op for op in args.op):
+            sq.sq_check_device_status(ws_fb)
 
 
 if __name__ == "__main__":
