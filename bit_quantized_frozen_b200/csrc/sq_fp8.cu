@@ -581,22 +581,15 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                         load16(args.x, cur, col, r, a[0]);
                         load16(args.g, cur, col, r, a[1]);
                         load16(args.u, cur, col, r, a[2]);
-                        float v[16];
+                        uint64_t dg[8], du[8];
+                        if (args.act == 0)
+                            pair_gradients<0>(a[0], a[1], a[2], dg, du);
+                        else
+                            pair_gradients<1>(a[0], a[1], a[2], dg, du);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {             // (bf16 pairs: value i in half i & 1)
-                            auto pick = [&](const uint4 (&w)[2]) {
-                                const uint4 &h = w[i >> 3];
-                                const uint32_t b = (i >> 1 & 3) == 0 ? h.x : (i >> 1 & 3) == 1 ? h.y : (i >> 1 & 3) == 2 ? h.z : h.w;
-                                return __uint_as_float(i & 1 ? b & 0xFFFF0000u : b << 16);
-                            };
-                            float act, slope;
-                            if (args.act == 0)
-                                act_grad<0>(pick(a[1]), act, slope);
-                            else
-                                act_grad<1>(pick(a[1]), act, slope);
-                            v[i] = half ? pick(a[0]) * act : pick(a[0]) * pick(a[2]) * slope;
-                        }
-                        round_row(r, v);
+                        for (int i = 0; i < 8; ++i)
+                            dg[i] = half ? du[i] : dg[i];
+                        round_row(r, dg);
                     }
                 } else {
 #pragma unroll
@@ -830,12 +823,12 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                 float o[C];
                 if (args.act == 0) {
 #pragma unroll
-                    for (int j = 0; j < C; ++j)
-                        o[j] = act_value<0>(r[j]) * q[j];
+                    for (int j = 0; j < C; j += 2)
+                        f2_unpack(f2_mul(act_value<0>(f2_pack(r[j], r[j + 1])), f2_pack(q[j], q[j + 1])), o[j], o[j + 1]);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < C; ++j)
-                        o[j] = act_value<1>(r[j]) * q[j];
+                    for (int j = 0; j < C; j += 2)
+                        f2_unpack(f2_mul(act_value<1>(f2_pack(r[j], r[j + 1])), f2_pack(q[j], q[j + 1])), o[j], o[j + 1]);
                 }
                 put_out(o, tmY, args.y, ybf);
             } else {

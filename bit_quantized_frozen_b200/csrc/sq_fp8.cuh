@@ -19,49 +19,68 @@ __host__ __device__ __forceinline__ int64_t fp8_groups(int64_t len)
     return (len + kFp8Block * kFp8Group - 1) / (kFp8Block * kFp8Group);
 }
 
-// sigmoid(x ln 2) and its complement, both without cancellation: t = 2^-|x| <= 1 (a NaN stays one)
-__device__ __forceinline__ void sigmoid2(float x, float &s, float &other)
-{
-    float t, big;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(-fabsf(x)));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(big) : "f"(1.0f + t));
-    const float small = t * big;
-    s = x < 0.0f ? small : big;
-    other = x < 0.0f ? big : small;
-}
-
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGelu2C = 1.5957691216057308f;    // 2 sqrt(2 / pi)
 constexpr float kGeluCube = 0.044715f;
 
-// act's argument of the sigmoid, in units of ln 2; gelu: (1 + tanh z) / 2 = sigmoid(2 z).  g2: g^2,
-// kept finite, so that what it multiplies may be 0
-template <int ACT>
-__device__ __forceinline__ float act_arg(float g, float g2)
+__device__ __forceinline__ uint64_t f2_both(float v)
 {
-    return ACT == 0 ? kLog2e * g : g * (kLog2e * kGelu2C + kLog2e * kGelu2C * kGeluCube * g2);
+    return f2_pack(v, v);
 }
 
-// act(g) = g / (1 + 2^-x): where the power leaves fp32's range, the quotient is 0
-template <int ACT>
-__device__ __forceinline__ float act_value(float g)
+// t = 2^x and 1 / (1 + t), two at a time (an infinite t gives 0)
+__device__ __forceinline__ void power_and_share(uint64_t x, float (&t)[2], uint64_t &share)
 {
-    float t, s;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(-act_arg<ACT>(g, fminf(g * g, 1e30f))));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + t));
-    return g * s;
+    float v[2], d[2], s[2];
+    f2_unpack(x, v[0], v[1]);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t[0]) : "f"(v[0]));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t[1]) : "f"(v[1]));
+    f2_unpack(f2_add(f2_pack(t[0], t[1]), f2_both(1.0f)), d[0], d[1]);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s[0]) : "f"(d[0]));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s[1]) : "f"(d[1]));
+    share = f2_pack(s[0], s[1]);
 }
 
-// act(g) and act'(g)
-template <int ACT>
-__device__ __forceinline__ void act_grad(float g, float &a, float &slope)
+// g^2, kept finite, so that what it multiplies may be 0
+__device__ __forceinline__ uint64_t finite_square(uint64_t g)
 {
-    float s, o;
-    const float g2 = fminf(g * g, 1e30f);
-    sigmoid2(act_arg<ACT>(g, g2), s, o);
-    a = g * s;
-    const float w = a * o;                        // g sigmoid'
-    slope = ACT == 0 ? s + w : s + w * (kGelu2C + 3.0f * kGelu2C * kGeluCube * g2);
+    float a, b;
+    f2_unpack(f2_mul(g, g), a, b);
+    return f2_pack(fminf(a, 1e30f), fminf(b, 1e30f));
+}
+
+// minus act's argument of the sigmoid, in units of ln 2; gelu: (1 + tanh z) / 2 = sigmoid(2 z)
+template <int ACT>
+__device__ __forceinline__ uint64_t act_arg(uint64_t g, uint64_t g2)
+{
+    return ACT == 0 ? f2_mul(g, f2_both(-kLog2e))
+                    : f2_mul(g, f2_fma(g2, f2_both(-kLog2e * kGelu2C * kGeluCube), f2_both(-kLog2e * kGelu2C)));
+}
+
+// act(g) = g / (1 + 2^-x) of two: where the power leaves fp32's range, the quotient is 0
+template <int ACT>
+__device__ __forceinline__ uint64_t act_value(uint64_t g)
+{
+    float t[2];
+    uint64_t s;
+    power_and_share(act_arg<ACT>(g, ACT == 0 ? 0 : finite_square(g)), t, s);
+    return f2_mul(g, s);
+}
+
+// act(g) and act'(g) of two.  1 - sigmoid = 2^-x sigmoid, without cancellation; a power out of range
+// meets a sigmoid of 0, so that it may be cut to a finite one
+template <int ACT>
+__device__ __forceinline__ void act_grad(uint64_t g, uint64_t &a, uint64_t &slope)
+{
+    float t[2];
+    uint64_t s;
+    const uint64_t g2 = ACT == 0 ? 0 : finite_square(g);
+    power_and_share(act_arg<ACT>(g, g2), t, s);
+    const uint64_t o = f2_mul(f2_pack(fminf(t[0], 1e38f), fminf(t[1], 1e38f)), s);
+    a = f2_mul(g, s);
+    const uint64_t w = f2_mul(a, o);              // g sigmoid'
+    slope = ACT == 0 ? f2_add(s, w)
+                     : f2_fma(w, f2_fma(g2, f2_both(3.0f * kGelu2C * kGeluCube), f2_both(kGelu2C)), s);
 }
 
 // ---- rounding to e4m3 --------------------------------------------------------------
@@ -119,13 +138,22 @@ __device__ __forceinline__ uint32_t block_top(uint32_t top)
     return top;
 }
 
-// A lane's 16 neighbouring values of a row (8 lanes a block): their codes, and the block's byte.
-__device__ __forceinline__ uint4 quantise16(const float (&v)[16], uint32_t &byte, bool &bad)
+// the bf16 pair in a word as two fp32 values
+__device__ __forceinline__ uint64_t widen2(uint32_t w)
+{
+    return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// A lane's 16 neighbouring values of a row (8 lanes a block), in pairs: their codes, and the block's byte.
+__device__ __forceinline__ uint4 quantise16(const uint64_t (&v)[8], uint32_t &byte, bool &bad)
 {
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; i += 2)
-        m = fp8_absmax3(m, v[i], v[i + 1]);
+    for (int i = 0; i < 8; ++i) {
+        float a, b;
+        f2_unpack(v[i], a, b);
+        m = fp8_absmax3(m, a, b);
+    }
     const uint32_t top = block_top(__float_as_uint(m) & 0x7FFFFFFFu);
     if (top >= kFp8Inf) {
         bad = true;
@@ -133,12 +161,36 @@ __device__ __forceinline__ uint4 quantise16(const float (&v)[16], uint32_t &byte
         return make_uint4(kFp8NanCodes, kFp8NanCodes, kFp8NanCodes, kFp8NanCodes);
     }
     byte = fp8_scale_byte(top);
-    const float inv = fp8_inverse(byte);
+    const uint64_t inv = f2_both(fp8_inverse(byte));
     uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        c[i] = to_e4m3x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+    for (int i = 0; i < 4; ++i) {
+        float r[4];
+        f2_unpack(f2_mul(v[2 * i], inv), r[0], r[1]);
+        f2_unpack(f2_mul(v[2 * i + 1], inv), r[2], r[3]);
+        c[i] = to_e4m3x4(r[0], r[1], r[2], r[3]);
+    }
     return make_uint4(c[0], c[1], c[2], c[3]);
+}
+
+// Eight bf16 pairs of dh, g and u: the gradients dg = (dh u) act'(g) and du = dh act(g).
+template <int ACT>
+__device__ __forceinline__ void pair_gradients(const uint4 (&dh)[2], const uint4 (&g)[2], const uint4 (&u)[2],
+                                               uint64_t (&dg)[8], uint64_t (&du)[8])
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t d[4] = {dh[h].x, dh[h].y, dh[h].z, dh[h].w}, a[4] = {g[h].x, g[h].y, g[h].z, g[h].w},
+                       b[4] = {u[h].x, u[h].y, u[h].z, u[h].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint64_t act, slope;
+            act_grad<ACT>(widen2(a[i]), act, slope);
+            const uint64_t v = widen2(d[i]);
+            du[4 * h + i] = f2_mul(v, act);
+            dg[4 * h + i] = f2_mul(f2_mul(v, widen2(b[i])), slope);
+        }
+    }
 }
 
 // The same of 16 bf16 values, two at a time as long as that is exact (the maximum, and the product with

@@ -10,6 +10,11 @@
 //   dg = (dh u) act'(g),  du = dh act(g)            (fp32)
 //
 // A block with a NaN or an infinity gets NaN codes, so that the whole row's sums are NaN.
+//
+// One read of the rows, one write of the codes: bound by DRAM, and where they are formed from a gated pair by
+// instructions too (two powers, two quotients, some 30 others for two values: packed arithmetic took the 2049 x
+// 8192 pair from 30.1 us to 26 with gelu).  Alone: 4480 x 6144 14 us (5.9 TB/s), 4480 x 16384 30 us (7.3 TB/s, the
+// codes staying in L2), gated pair of 2049 x 8192 24 us with silu, 26 with gelu (5.2 TB/s).
 #include <cuda.h>
 
 #include "sq_fp8.cuh"
@@ -19,11 +24,14 @@
 namespace sq {
 
 constexpr int kQuantThreads = 128;
-// CTAs an SM holds at once: the grid is no larger, since what waits for a second turn would make the
-// last CTAs of the first wait too
+// CTAs of an SM.  The grid is no larger, since what waits for a second turn would make the last CTAs of the
+// first wait too.  Fewer CTAs have more registers each (92 instead of 56 hold a gated pair's operands without
+// spills) and end closer together: a call of 2049 rows, gated gradient, 8192 x 4096, takes 133.8, 132.5, 132.0,
+// 130.4, 131.3 us with 9, 7, 6, 5, 4 of them; 777 x 4240 x 2832, forward, 22.4, 21.0, 21.1, 21.1 us with 8, 6,
+// 5, 4; 4480 x 16384 x 6144 334, 334, 336, 337.
 constexpr int quant_ctas(int gated)
 {
-    return gated ? 9 : 8;
+    return gated ? 5 : 6;
 }
 
 // GATED 0: rows of x; 1, 2: the gradients of a gated pair with silu, gelu.  A warp takes ROWS rows x
@@ -86,20 +94,8 @@ __global__ void __launch_bounds__(kQuantThreads, quant_ctas(GATED)) fp8_quant_ke
             if constexpr (GATED == 0) {
                 c = quantise16(w[0][r], byte, bad);
             } else {
-                float v[16], g[16], u[16], second[16];
-                widen8(w[0][r][0], v, 0);
-                widen8(w[0][r][1], v, 8);
-                widen8(w[1][r][0], g, 0);
-                widen8(w[1][r][1], g, 8);
-                widen8(w[2][r][0], u, 0);
-                widen8(w[2][r][1], u, 8);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float act, slope;
-                    act_grad<GATED - 1>(g[i], act, slope);
-                    second[i] = v[i] * act;
-                    v[i] = v[i] * u[i] * slope;
-                }
+                uint64_t v[8], second[8];
+                pair_gradients<GATED - 1>(w[0][r], w[1][r], w[2][r], v, second);
                 c = quantise16(second, byte, bad);
                 const uint32_t word = scale_word(byte, lane);
                 if (lane == r)
