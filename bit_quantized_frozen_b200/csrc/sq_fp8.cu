@@ -21,12 +21,15 @@
 // Few rows (fp8_rounds_rows): the feeders round the rows themselves, straight into the operand's
 // shared-memory layout, and the call is one kernel.
 //
-// CTA (CG = 1, tiles of 128 tokens x up to 128 columns) or CTA pair (CG = 2, 256 x up to 256) per SM,
-// persistent: 8 epilogue warps, TMA producers, feeders, and an issuer that also allocates tensor
-// memory.
+// CTA (CG = 1, tiles of 128 tokens x up to 224 columns, backward 256) or CTA pair (CG = 2, 256 x up to
+// 256), one CTA per SM, persistent: 8 epilogue warps (few rows: 2), TMA producers, feeders (few rows: two
+// sets), and an issuer that also allocates tensor memory.  Outputs leave by TMA where a warp's 32 rows
+// are all the tile's.
 //
 // Few tiles (CG = 1): a cluster of CTAs shares a tile, each with some of the groups, and joins the
 // partial sums over distributed shared memory, in the order of the CTAs' ranks.
+//
+// (figures)
 #include <cuda.h>
 
 #include <type_traits>
@@ -50,32 +53,34 @@ constexpr int kFBufs = 4;
 constexpr int kFPatchBytes = 32 * 64;             // a warp's 32 rows x 64 bytes on their way out
 constexpr int kFuseRows = 16;
 constexpr int kFMaxSplit = 8;
-constexpr int kPrefetchBytes = 64 * 1024;
+constexpr int kFPartBytes = 24 * 1024;            // FUSE: places for the other CTAs' sums
+constexpr int kFUpRow = 64;                       // FUSE, gated: lane of the up projection's first channel
+constexpr int kPrefetchBytes = 64 * 1024;         // of weight into L2 before the kernel in front has ended, each CTA
 
 template <int CG, int MODE, bool FUSE>
 struct Fp8Cfg {
-    static constexpr int kEpi = FUSE ? 2 : 8;     // epilogue warps
+    static constexpr int kEpi = FUSE ? 4 : 8;     // epilogue warps
     static constexpr int kProducers = CG == 2 || FUSE ? 2 : 3;
     static constexpr int kSets = FUSE ? 2 : 1;    // of four feeder warps
     static constexpr int kThreads = 32 * (kEpi + kProducers + 4 * kSets + 1);
     static constexpr uint32_t kTmemCols = 512, kScaleCol = 448;
     static constexpr int kMaxStages = CG == 2 ? 12 : 24;
     // shared memory: the ring, then
-    //   patches of the stores; FUSE: a split tile's sums from the other CTAs.  (CG = 1: the MMA reads
-    //   128 rows of A, up to 16 KB behind the last stage.)
+    //   patches of the stores; FUSE: a split tile's sums from the other CTAs, and the up projection's of
+    //   four warps.  (CG = 1: the MMA reads 128 rows of A, up to 16 KB behind the last stage.)
     static constexpr int kPatches = CG == 2 && MODE != kFp8Bwd ? 2 : 1;       // of an epilogue warp
-    static constexpr int kPatchBytes = FUSE ? 24 * 1024 : 8 * kPatches * kFPatchBytes;
+    static constexpr int kPatchBytes = FUSE ? kFPartBytes + 4096 : 8 * kPatches * kFPatchBytes;
     static constexpr int kPlanOff = kPatchBytes;
     static constexpr int kFeedOff = kPlanOff + (2 * kMaxExperts + 4) * 4;     // [sets][2][32] words (FUSE)
     static constexpr int kBarOff = kFeedOff + kSets * 2 * 32 * 4;
     // full, empty, sf_full, sf_empty, acc_full[2], acc_empty[2], drain, peers, parts
     static constexpr int kNumBars = 2 * kMaxStages + 2 * kFBufs + 7;
     static constexpr int kRestBytes = kBarOff + 8 * kNumBars + 16;
-    static constexpr int kRing = (kPatches == 2 ? 180 : 192) * 1024;
+    static constexpr int kRing = (FUSE ? 184 : kPatches == 2 ? 180 : 192) * 1024;
     static constexpr int kSmemBytes = kRing + kRestBytes + 1024;
-    // e4m3 x e4m3, e8m0 scales; B N-major backward; 128 CG rows (columns / 8 << 17 comes at run time)
-    static constexpr uint32_t kIdesc = (1u << 23) | (MODE == kFp8Bwd ? 1u << 16 : 0u) | ((uint32_t)(8 * CG) << 24);
-    static constexpr uint32_t kBStep16 = MODE == kFp8Bwd ? (32u * 128u) >> 4 : 2u;   // B descriptor step per MMA
+    // e4m3 x e4m3, e8m0 scales; the weight N-major backward; 128 CG rows (columns / 8 << 17 comes at run time)
+    static constexpr uint32_t kIdesc = (1u << 23) | (MODE == kFp8Bwd ? 1u << (FUSE ? 15 : 16) : 0u) | ((uint32_t)(8 * CG) << 24);
+    static constexpr uint32_t kWStep16 = MODE == kFp8Bwd ? (32u * 128u) >> 4 : 2u;   // the weight's descriptor step per MMA
 };
 
 struct Fp8Args {
@@ -95,7 +100,7 @@ struct Fp8Args {
     int blocks;               // blocks of the summed axis (of one weight)
     int halves;               // weights that the sum runs through
     int tile;                 // output channels of a tile
-    int a_rows;               // rows of A that a stage (FUSE: a group) reserves
+    int a_rows;               // rows that a stage (FUSE: a group) reserves
     int boxed_rows;           // up to so many rows come in boxes of 32
     int per;                  // chunks of a stage: 1, 2 or 4
     int stages;
@@ -175,47 +180,26 @@ __device__ __forceinline__ void store_rows64(const uint32_t (&v)[16], Fp8Patch &
         bulk_commit_group();                      // (empty without a map: the patches are counted in groups)
 }
 
-// C neighbouring columns of y from fp32 values, as bf16 or fp32; the first `cols` of them and `rows`
-// rows exist.  32 columns leave through the patch; 16 (few rows) are written by their lanes directly.
-template <int C, int PATCHES>
-__device__ __forceinline__ void store_cols(const float (&o)[C], Fp8Patch &out, const CUtensorMap *map, void *y,
+// 32 neighbouring columns of y from fp32 values, as bf16 or fp32, through the patch; the first `cols` of them
+// and `rows` rows exist.
+template <int PATCHES>
+__device__ __forceinline__ void store_cols(const float (&o)[32], Fp8Patch &out, const CUtensorMap *map, void *y,
                                            int64_t row, int64_t col, int64_t width, int rows, int cols, bool bf16)
 {
-    const int lane = out.lane;
     uint8_t *dst = reinterpret_cast<uint8_t *>(y) + (bf16 ? 2 : 4) * (row * width + col);
-    if constexpr (C == 16) {
-        dst += (bf16 ? 2 : 4) * width * lane;
-        if (bf16) {
+    uint32_t v[16];
+    if (bf16) {
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const uint4 v = make_uint4(f32x2_to_bf16x2_bits(o[8 * p], o[8 * p + 1]),
-                                           f32x2_to_bf16x2_bits(o[8 * p + 2], o[8 * p + 3]),
-                                           f32x2_to_bf16x2_bits(o[8 * p + 4], o[8 * p + 5]),
-                                           f32x2_to_bf16x2_bits(o[8 * p + 6], o[8 * p + 7]));
-                if (lane < rows && 8 * p < cols)
-                    *reinterpret_cast<uint4 *>(dst + 16 * p) = v;
-            }
-        } else {
-#pragma unroll
-            for (int p = 0; p < 4; ++p)
-                if (lane < rows && 4 * p < cols)
-                    *reinterpret_cast<float4 *>(dst + 16 * p) = make_float4(o[4 * p], o[4 * p + 1], o[4 * p + 2], o[4 * p + 3]);
-        }
+        for (int i = 0; i < 16; ++i)
+            v[i] = f32x2_to_bf16x2_bits(o[2 * i], o[2 * i + 1]);
+        store_rows64<PATCHES>(v, out, map, (int)col, (int)row, dst, 2 * width, rows, 2 * cols);
     } else {
-        uint32_t v[16];
-        if (bf16) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                v[i] = f32x2_to_bf16x2_bits(o[2 * i], o[2 * i + 1]);
-            store_rows64<PATCHES>(v, out, map, (int)col, (int)row, dst, 2 * width, rows, 2 * cols);
-        } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    v[i] = __float_as_uint(o[16 * h + i]);
-                store_rows64<PATCHES>(v, out, map, (int)col + 16 * h, (int)row, dst + 64 * h, 4 * width, rows, 4 * (cols - 16 * h));
-            }
+                v[i] = __float_as_uint(o[16 * h + i]);
+            store_rows64<PATCHES>(v, out, map, (int)col + 16 * h, (int)row, dst + 64 * h, 4 * width, rows, 4 * (cols - 16 * h));
         }
     }
 }
@@ -266,10 +250,10 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
     const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;            // in the pair
     const int part = split > 1 ? (int)cluster_ctarank() : 0;           // of the tile's groups
     const bool leader = rank == 0;
-    // Roles.  A warp reaches the 32 lanes of tensor memory that its number modulo 4 gives: a set of
-    // feeders needs all four, and few rows lie in lanes 0 .. 31 alone.
-    constexpr int kIssuer = FUSE ? 11 : Cfg::kEpi + Cfg::kProducers + 4 * Cfg::kSets;
-    constexpr int kProducer = FUSE ? 9 : Cfg::kEpi, kFeeder = FUSE ? 0 : kProducer + Cfg::kProducers;
+    // Roles: epilogue, producers, feeders, issuer.  A warp reaches the 32 lanes of tensor memory that its
+    // number modulo 4 gives: the epilogue and a set of feeders need all four.
+    constexpr int kIssuer = Cfg::kEpi + Cfg::kProducers + 4 * Cfg::kSets;
+    constexpr int kProducer = Cfg::kEpi, kFeeder = kProducer + Cfg::kProducers;
     const bool producer = warp >= kProducer && warp < kProducer + Cfg::kProducers;
     const bool feeder = warp >= kFeeder && warp < kFeeder + 4 * Cfg::kSets;
 
@@ -343,7 +327,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
     const int a_bytes = args.a_rows * kFChunk;                         // of a chunk
     const int boxes = BWD ? (b_rows + 127) / 128 : 1;                  // of 128 columns (backward)
     const int b_bytes = (BWD ? 128 * boxes : b_rows) * kFChunk;
-    const int chunk_bytes = (FUSE ? 0 : a_bytes) + b_bytes;
+    const int chunk_bytes = FUSE ? (GATED ? (kFUpRow + T) * kFChunk : b_bytes) : a_bytes + b_bytes;
     const int stage_bytes = per * chunk_bytes;
     const int stages = args.stages;
     const uint32_t slot1 = (uint32_t)args.slot1;
@@ -371,7 +355,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                     copy(half ? &tmW2 : &tmW, b * 128 * kFChunk, n0 + (int)rank * b_rows + 128 * b, x);
             } else if (GATED && CG == 1) {
                 copy(&tmW, 0, x, n0);
-                copy(&tmW2, T * kFChunk, x, n0);
+                copy(&tmW2, (FUSE ? kFUpRow : T) * kFChunk, x, n0);
             } else if (GATED) {
                 copy(rank ? &tmW2 : &tmW, 0, x, n0);
             } else {
@@ -483,7 +467,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
     } else if (feeder) {
         // ------------------------------------------------------------ feeders (every CTA)
         // Warp q of a set writes lanes 32 q .. + 31 of tensor memory, which hold the same words in each
-        // quarter: column j of A line l is row 32 j + l.  Set s takes every S-th group.
+        // quarter: line l of column j is row 32 j + l.  Set s takes every S-th group.
         constexpr int S = Cfg::kSets;
         const int set = (warp - kFeeder) >> 2, q = warp & 3;
         const int wq = (warp - kFeeder) & 3;                           // (which of the set's four)
@@ -512,7 +496,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
         };
         constexpr int R = FUSE ? 2 : 1;                    // rows of a warp fetched in advance
         struct Raw {
-            uint32_t aw[FUSE ? 1 : 4], v;
+            uint32_t rw[FUSE ? 1 : 4], v;
             uint4 x[FUSE ? R : 1][2];
         };
         const bool pair_grad = FUSE && BWD && args.g != nullptr;       // the rows: gradients of a gated pair
@@ -535,7 +519,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                 const int mine = min(max(it.t.rows - (int)rank * 128, 0), 128);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    r.aw[j] = 32 * j + lane < mine ? __ldg(args.words + (int64_t)it.g2 * args.M + it.t.row0 +
+                    r.rw[j] = 32 * j + lane < mine ? __ldg(args.words + (int64_t)it.g2 * args.M + it.t.row0 +
                                                            (int)rank * 128 + 32 * j + lane)
                                                    : 0u;
             }
@@ -553,10 +537,12 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
         // writes group `cur` to tensor memory (FUSE: and its rows to shared memory); false: gave up
         auto put = [&](const Item &cur, const Raw &raw) {
             const int buf = cur.number & (kFBufs - 1);
+            // (few rows: a warp that gave up goes on, since the others of its set may wait for it)
             if (!fp8_warp_wait<CG>(bar_sf_empty + 8 * buf, ((uint32_t)(cur.number / kFBufs) & 1u) ^ 1u, abort_flag,
-                                   args.status, lane))
+                                   args.status, lane) &&
+                !FUSE)
                 return false;
-            uint32_t aw[4] = {0u, 0u, 0u, 0u}, bw[8];
+            uint32_t rw[4] = {0u, 0u, 0u, 0u}, ww[FUSE ? 4 : 8];     // words of the rows and of the weight
             if constexpr (FUSE) {
                 // rows wq, wq + 4, ... of the tile, rounded into the operand's layout: rows of 128 bytes,
                 // 16-byte piece i of row r at i ^ (r % 8); a lane has one piece
@@ -605,26 +591,31 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                 }
                 fence_proxy_async_smem();
                 named_barrier_sync(2 + set, 128);          // the set's words and rows are there
-                aw[0] = lane < n ? feed[lane] : 0u;
+                rw[0] = lane < n ? feed[lane] : 0u;
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    aw[j] = raw.aw[j];
+                    rw[j] = raw.rw[j];
             }
             uint32_t v = raw.v << (8 * (lane & 3));
             v |= __shfl_xor_sync(0xffffffffu, v, 1);
             v |= __shfl_xor_sync(0xffffffffu, v, 2);
             const int n0 = cur.t.wt * T;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int r = 32 * j + lane;
-                const bool second = GATED && r >= T;
-                const int ch = n0 + (second ? r - T : r);
-                bw[j] = __shfl_sync(0xffffffffu, v, 4 * ((ch / kFp8Block - n0 / kFp8Block) & 3) + (second ? 16 : 0));
+            for (int j = 0; j < (FUSE ? 4 : 8); ++j) {
+                const int r = 32 * j + lane, up = FUSE ? kFUpRow : T;
+                const bool second = GATED && r >= up;
+                const int ch = n0 + (second ? r - up : r);
+                ww[j] = __shfl_sync(0xffffffffu, v, 4 * ((ch / kFp8Block - n0 / kFp8Block) & 3) + (second ? 16 : 0));
             }
             tc_fence_after();
-            tmem_st_8cols(sf_lanes + 16 * buf, bw);
-            tmem_st_4cols(sf_lanes + 16 * buf + 8, aw);
+            if constexpr (FUSE) {
+                tmem_st_4cols(sf_lanes + 16 * buf, rw);
+                tmem_st_4cols(sf_lanes + 16 * buf + 8, ww);
+            } else {
+                tmem_st_8cols(sf_lanes + 16 * buf, ww);
+                tmem_st_4cols(sf_lanes + 16 * buf + 8, rw);
+            }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -637,7 +628,8 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
             return true;
         };
         // kAhead groups in turn: the next ones' values are on their way while one is written (a load takes
-        // 2 us and more while the weights stream)
+        // 2 us and more while the weights stream).  Few rows: none, since two sets take turns anyway and more
+        // code takes longer to fetch in a call that runs it once.
         constexpr int kAhead = FUSE ? 1 : 3;
         Item items[kAhead];
         Raw raws[kAhead];
@@ -694,13 +686,14 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
         if (leader) {
             const bool issue = one_lane();
             const uint32_t s0 = smem_u32(smem) + ring0;
-            const uint64_t dA = FUSE ? sdesc_sw128(smem_u32(smem)) : sdesc_sw128(s0);
-            // (backward: from 128 columns of B to the next 128 it is 16 KB)
-            const uint32_t dA0 = (uint32_t)dA, dB0 = ((uint32_t)sdesc_sw128(s0 + (FUSE ? 0 : a_bytes)) & 0xFFFFu) |
+            // the rows' and the weight's descriptors (backward: from 128 columns of the weight to the next 128 it
+            // is 16 KB)
+            const uint64_t dR = sdesc_sw128(FUSE ? smem_u32(smem) : s0);
+            const uint32_t dR0 = (uint32_t)dR, dW0 = ((uint32_t)sdesc_sw128(s0 + (FUSE ? 0 : a_bytes)) & 0xFFFFu) |
                                                      (BWD ? (128u * kFChunk >> 4) << 16 : 1u << 16);
-            const uint32_t desc_hi = (uint32_t)(dA >> 32);
+            const uint32_t desc_hi = (uint32_t)(dR >> 32);
             const uint32_t stage16 = stage_bytes >> 4, chunk16 = chunk_bytes >> 4, a16 = a_bytes >> 4;
-            const uint32_t idesc0 = Cfg::kIdesc | (uint32_t)(cols >> 3) << 17;
+            const uint32_t idesc0 = Cfg::kIdesc | (uint32_t)((FUSE ? args.a_rows : cols) >> 3) << 17;
             auto commit = [&](uint32_t bar) {
                 if (CG == 2)
                     tc_commit2_both(bar);
@@ -743,13 +736,15 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                                     if (u > 0 && u0 + u >= left)
                                         break;
                                     const uint32_t idesc = idesc0 | (uint32_t)(u0 + u) << 4 | (uint32_t)(u0 + u) << 29;
-                                    const uint32_t a = FUSE ? dA0 + (buf * kFp8Group + u0 + u) * a16
-                                                            : dA0 + off + u * chunk16;
-                                    const uint32_t b = dB0 + off + u * chunk16;
+                                    const uint32_t r = FUSE ? dR0 + (buf * kFp8Group + u0 + u) * a16
+                                                            : dR0 + off + u * chunk16;
+                                    const uint32_t w = dW0 + off + u * chunk16;
 #pragma unroll
-                                    for (int k = 0; k < kFChunk / 32; ++k)
-                                        mma_fp8<CG>(acc, a + 2 * k, b + Cfg::kBStep16 * k, desc_hi, idesc, sf + 8, sf,
+                                    for (int k = 0; k < kFChunk / 32; ++k) {
+                                        const uint32_t rk = r + 2 * k, wk = w + Cfg::kWStep16 * k;
+                                        mma_fp8<CG>(acc, FUSE ? wk : rk, FUSE ? rk : wk, desc_hi, idesc, sf + 8, sf,
                                                     u0 + u + k > 0 ? 1u : sum);
+                                    }
                                 }
                                 commit(bar_empty + 8 * stage);
                             }
@@ -791,19 +786,195 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
             (void)mbar_wait(bar_drain, 0, abort_flag, args.status);
         }
         __syncwarp();
+    } else if constexpr (FUSE) {
+        // ------------------------------------------------------------ epilogue, few rows (every CTA)
+        // A lane of warp q holds channel 32 q + lane of the tile (gated: the up projection's from kFUpRow on), a
+        // column a row, 16 columns at a time.
+        const int q = warp, slots = args.a_rows;
+        const bool second = GATED && 32 * q >= kFUpRow;
+        const int ch = 32 * q + lane - (second ? kFUpRow : 0);
+        const bool ybf = args.out_bf16 != 0;
+        float *const exchange = reinterpret_cast<float *>(rest + kFPartBytes) + (q & 1) * 512 + lane;
+        int count = 0, e = 0;
+        if (args.E == 0)
+            grid_dep_wait();
+        if (blockIdx.x == 0 && q == 0)
+            fp8_begin_call(args.offsets, args.E, args.M, args.keep_status, args.status, lane);
+        if (args.E > 0)                                                // rows of no expert: 0
+            for (int k = 0; k < 3; ++k) {
+                if (!args.zero[k])
+                    continue;
+                const int64_t n16 = args.zero_row_bytes[k] / 16, lo = plan.start[0], hi = plan.start[args.E];
+                for (int64_t m = 0; m < args.M; ++m)
+                    if (m < lo || m >= hi)
+                        for (int64_t c = (int64_t)(4 * blockIdx.x + q) * 32 + lane; c < n16; c += 128 * (int64_t)gridDim.x)
+                            *reinterpret_cast<uint4 *>(args.zero[k] + m * args.zero_row_bytes[k] + 16 * c) =
+                                make_uint4(0u, 0u, 0u, 0u);
+            }
+        // 16 rows' values of the lane's channel, `rows` of them real, to a matrix of the width of y
+        auto put = [&](const float (&v)[16], void *to, bool bf16, int64_t row, int64_t col, int rows) {
+            const int64_t at = row * args.width + col;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                if (bf16) {
+                    uint16_t *dst = reinterpret_cast<uint16_t *>(to) + at + i * args.width;
+                    const uint32_t w = f32x2_to_bf16x2_bits(v[i], v[i + 1]);
+                    if (i < rows)
+                        dst[0] = (uint16_t)w;
+                    if (i + 1 < rows)
+                        dst[args.width] = (uint16_t)(w >> 16);
+                } else {
+                    float *dst = reinterpret_cast<float *>(to) + at + i * args.width;
+                    if (i < rows)
+                        dst[0] = v[i];
+                    if (i + 1 < rows)
+                        dst[args.width] = v[i + 1];
+                }
+            }
+        };
+        // sums of rows b .. b + 15 of tile t: out (gated: the gate's warp gets the up projection's from its fellow)
+        auto finish = [&](const I8Tile &t, int b, float (&v)[16], bool real) {
+            const int64_t col = (int64_t)t.wt * T + ch, row = (int64_t)t.row0 + b;
+            int rows = real && ch < T && col < args.width ? t.rows - b : 0;
+            if (!SQ_DCHECK(rows <= 0 || row + min(rows, 16) <= args.M, args.status))
+                rows = 0;
+            if constexpr (GATED) {
+                if (args.g_out)
+                    put(v, second ? args.u_out : args.g_out, true, row, col, rows);
+                if (second) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        exchange[32 * i] = v[i];
+                }
+                named_barrier_sync(4 + (q & 1), 64);
+                if (!second) {
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        const uint64_t g = f2_pack(v[i], v[i + 1]), u = f2_pack(exchange[32 * i], exchange[32 * i + 32]);
+                        f2_unpack(f2_mul(args.act == 0 ? act_value<0>(g) : act_value<1>(g), u), v[i], v[i + 1]);
+                    }
+                }
+                named_barrier_sync(4 + (q & 1), 64);                   // (what was read may be written again)
+                if (!second)
+                    put(v, args.y, ybf, row, col, rows);
+            } else {
+                put(v, args.y, ybf, row, col, rows);
+            }
+        };
+        auto load = [&](uint32_t taddr, float (&v)[16]) {
+            uint32_t a[16];
+            __syncwarp();
+            tmem_ld_16cols(taddr, a);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                v[i] = __uint_as_float(a[i]);
+        };
+        // The first turn is a dry one, while the products run.  It reads what tensor memory happens to hold and
+        // writes nothing, so that the code is there when it is needed (a split tile's sums came together 4 us
+        // after its products without, 1.5 us with it).
+        bool dry = true;
+        if (split == 1) {
+#pragma unroll 1
+            for (int tile = unit; tile < tiles;) {
+                const I8Tile t = plan.find(tile, e);
+                const int slot = count & 1;
+                // (one that gave up goes on without effect, as its fellow may wait for it)
+                const bool real = !dry && fp8_warp_wait<CG>(bar_acc_full + 8 * slot, (uint32_t)((count >> 1) & 1), abort_flag,
+                                                            args.status, lane);
+                tc_fence_after();
+                const uint32_t acc = tmem_base + ((uint32_t)(32 * q) << 16) + (slot ? slot1 : 0u);
+#pragma unroll 1
+                for (int b = 0; b < slots && (b == 0 || (!dry && b < t.rows)); b += 16) {
+                    float v[16];
+                    load(acc + b, v);
+                    finish(t, b, v, real);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (!dry) {
+                    if (lane == 0)
+                        mbar_arrive(bar_acc_empty + 8 * slot);
+                    tile += units;
+                    ++count;
+                }
+                dry = false;
+            }
+        }
+        // One tile a cluster.  Each warp's channels are finished by one CTA (gated: the gate's and the up
+        // projection's by the same), to which the others send theirs.
+        const int owner = (GATED ? q & 1 : q) % split, place0 = GATED ? q >> 1 : q / split;
+        const uint32_t acc = tmem_base + ((uint32_t)(32 * q) << 16);
+#pragma unroll 1
+        for (int turn = 0; split > 1 && unit < tiles && turn < 2; ++turn) {
+            dry = turn == 0;
+            bool real = !dry && fp8_warp_wait<CG>(bar_acc_full, 0, abort_flag, args.status, lane);
+            tc_fence_after();
+            const I8Tile t = plan.find(unit, e);
+            const int quads = (t.rows + 3) / 4;                        // rows are sent in fours
+            if (q == 0 && lane == 0 && !dry) {
+                int mine = 0;                                          // warps whose channels this CTA finishes
+                for (int w = 0; w < 4; ++w)
+                    mine += (GATED ? w & 1 : w) % split == part ? 1 : 0;
+                mbar_arrive_expect_tx(bar_parts, mine * (split - 1) * quads * 512);
+            }
+            // [place0][from][quad][lane] float4
+            auto place = [&](int from, int quad) {
+                return (uint32_t)(((place0 * split + from) * quads + quad) * 32 + lane) * 16u;
+            };
+            if (owner != part || dry) {
+                const uint32_t dst = mapa_shared(smem_u32(rest), owner), bar = mapa_shared(bar_parts, owner);
+#pragma unroll 1
+                for (int b = 0; b < slots && b < t.rows; b += 16) {
+                    float v[16];
+                    load(acc + b, v);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (real && b / 4 + j < quads)
+                            st_async_v4(dst + place(part, b / 4 + j), v + 4 * j, bar);
+                }
+            }
+            if (owner == part || dry) {
+                real = real && fp8_warp_wait<2>(bar_parts, 0, abort_flag, args.status, lane);
+#pragma unroll 1
+                for (int b = 0; b < slots && b < t.rows; b += 16) {
+                    float v[16];
+                    load(acc + b, v);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (b / 4 + j >= quads)
+                            break;
+                        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        for (int from = 0; from < split; ++from) {     // the parts in order
+                            const float4 w = from == part ? make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3])
+                                                          : *reinterpret_cast<const float4 *>(rest + place(from, b / 4 + j));
+                            sum.x += w.x;
+                            sum.y += w.y;
+                            sum.z += w.z;
+                            sum.w += w.w;
+                        }
+                        v[4 * j] = sum.x;
+                        v[4 * j + 1] = sum.y;
+                        v[4 * j + 2] = sum.z;
+                        v[4 * j + 3] = sum.w;
+                    }
+                    finish(t, b, v, real);
+                }
+            }
+        }
+        __syncwarp();
     } else {
         // ------------------------------------------------------------ epilogue (every CTA)
         // Warp w: lanes 32 (w % 4) .. + 31, the first (w < 4) or second half of the tile's channels, C at a
         // time.
-        // (FUSE: lanes 0 .. 31, every other chunk.)
-        const int wq = FUSE ? 0 : warp & 3, wh = FUSE ? (warp == 8 ? 0 : 1) : warp >> 2;
+        const int wq = warp & 3, wh = warp >> 2;
         const uint32_t acc_empty_leader = CG == 2 ? mapa_shared(bar_acc_empty, 0) : bar_acc_empty;
         Fp8Patch out = {rest + warp * (Cfg::kPatches * kFPatchBytes), lane, 0};
         const bool ybf = args.out_bf16 != 0;
-        constexpr int C = FUSE ? 16 : 32;
+        constexpr int C = 32;
         const int chunks = (T + C - 1) / C;
         const int own = (chunks + 1 - wh) / 2;
-        auto chunk_of = [&](int i) { return FUSE ? wh + 2 * i : wh * ((chunks + 1) / 2) + i; };
+        auto chunk_of = [&](int i) { return wh * ((chunks + 1) / 2) + i; };
         // a chunk's columns from fp32 sums (gated: q the up projection's)
         auto finish = [&](const I8Tile &t, int c, int rows, int64_t row, const float (&r)[C], const float (&q)[GATED ? C : 1]) {
             const int64_t col = (int64_t)t.wt * T + c;
@@ -813,7 +984,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
             // all 32 rows and C columns are the tile's, or lie behind the matrix's end
             const bool whole = (rows == 32 || args.E == 0) && (live == C || col + live == args.width);
             auto put_out = [&](const float (&o)[C], const CUtensorMap &m, void *to, bool bf16) {
-                store_cols<C, Cfg::kPatches>(o, out, whole ? &m : nullptr, to, row, col, args.width, rows, live, bf16);
+                store_cols<Cfg::kPatches>(o, out, whole ? &m : nullptr, to, row, col, args.width, rows, live, bf16);
             };
             if constexpr (GATED) {
                 if (args.g_out) {
@@ -838,10 +1009,10 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
         auto load_chunk = [&](uint32_t acc, int c, float (&r)[C], float (&q)[GATED ? C : 1]) {
             uint32_t a[C];
             __syncwarp();
-            tmem_ld_cols(acc + c, a);
+            tmem_ld_32cols(acc + c, a);
             if constexpr (GATED) {
                 uint32_t b[C];
-                tmem_ld_cols(acc + T + c, b);
+                tmem_ld_32cols(acc + T + c, b);
                 tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < C; ++j)
@@ -854,34 +1025,14 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                 r[j] = __uint_as_float(a[j]);
         };
         int count = 0, e = 0;
-        if (!(FUSE && args.E > 0))
-            grid_dep_wait();
-        if (FUSE) {
-            if (blockIdx.x == 0 && wh == 0)
-                fp8_begin_call(args.offsets, args.E, args.M, args.keep_status, args.status, lane);
-            if (args.E > 0)                                            // rows of no expert: 0
-                for (int k = 0; k < 3; ++k) {
-                    if (!args.zero[k])
-                        continue;
-                    const int64_t n16 = args.zero_row_bytes[k] / 16, lo = plan.start[0], hi = plan.start[args.E];
-                    for (int64_t m = 0; m < args.M; ++m)
-                        if (m < lo || m >= hi)
-                            for (int64_t c = (int64_t)(2 * blockIdx.x + wh) * 32 + lane; c < n16; c += 64 * (int64_t)gridDim.x)
-                                *reinterpret_cast<uint4 *>(args.zero[k] + m * args.zero_row_bytes[k] + 16 * c) =
-                                    make_uint4(0u, 0u, 0u, 0u);
-                }
-        }
-        // Few rows: the first turn is a dry one, while the products run.  It reads what tensor memory happens
-        // to hold and writes nothing, so that the code is there when it is needed (a split tile's sums came
-        // together 4 us after its products without, 1.5 us with it).
-        bool dry = FUSE;
+        grid_dep_wait();
         if (split == 1) {
 #pragma unroll 1
-            for (int tile = unit; tile < tiles;) {
+            for (int tile = unit; tile < tiles; tile += units, ++count) {
                 const I8Tile t = plan.find(tile, e);
                 const int slot = count & 1;
-                if (!dry && !fp8_warp_wait<CG>(bar_acc_full + 8 * slot, (uint32_t)((count >> 1) & 1), abort_flag,
-                                               args.status, lane))
+                if (!fp8_warp_wait<CG>(bar_acc_full + 8 * slot, (uint32_t)((count >> 1) & 1), abort_flag, args.status,
+                                       lane))
                     break;
                 tc_fence_after();
                 const uint32_t acc = tmem_base + ((uint32_t)(32 * wq) << 16) + (slot ? slot1 : 0u);
@@ -890,7 +1041,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                 auto release = [&]() {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0 && !dry) {
+                    if (lane == 0) {
                         if (CG == 2)
                             mbar_arrive_cluster(acc_empty_leader + 8 * slot);
                         else
@@ -903,55 +1054,41 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                 if (held == 0)
                     release();
                 if (rows > 0)
-                    for (int i = 0; i < (dry ? min(own, 1) : own); ++i) {
+                    for (int i = 0; i < own; ++i) {
                         const int c = C * chunk_of(slot ? i : own - 1 - i);
                         float r[C], q[GATED ? C : 1];
                         load_chunk(acc, c, r, q);
                         if (i == held - 1)
                             release();
-                        finish(t, c, dry ? 0 : rows, (int64_t)t.row0 + first_row, r, q);
+                        finish(t, c, rows, (int64_t)t.row0 + first_row, r, q);
                     }
-                if (!dry) {
-                    tile += units;
-                    ++count;
-                }
-                dry = false;
             }
         }
-#pragma unroll 1
-        for (int turn = FUSE ? 0 : 1; split > 1 && unit < tiles && turn < 2; ++turn) {
-            dry = turn == 0;
-            if (!dry && !fp8_warp_wait<CG>(bar_acc_full, 0, abort_flag, args.status, lane))
-                break;
-            // One tile a cluster.  Each chunk of its columns is finished by one CTA, owner(c), to which the others
-            // send theirs: few rows into a place of its own, else into the ring, once a CTA whose products
-            // are done has told the others that its ring is free.
+        // One tile a cluster.  Each chunk of its columns is finished by one CTA, owner(c), to which the others
+        // send theirs, into the ring, once a CTA whose products are done has told the others that it is free.
+        if (split > 1 && unit < tiles && fp8_warp_wait<CG>(bar_acc_full, 0, abort_flag, args.status, lane)) {
             constexpr int kParts = GATED ? 2 : 1;
             tc_fence_after();
             const I8Tile t = plan.find(unit, e);
             const uint32_t acc = tmem_base + ((uint32_t)(32 * wq) << 16);
-            const int rows = dry ? 0 : min(t.rows - 32 * wq, 32);
-            const bool some_rows = t.rows > 32 * wq;
-            // (FUSE: a warp has every other chunk)
-            auto owner = [&](int c) { return (FUSE ? c >> 1 : c) % split; };
-            auto place_of = [&](int c) { return FUSE ? (c >> 1) / split * 2 + (c & 1) : c / split; };
+            const int rows = min(t.rows - 32 * wq, 32);
+            auto owner = [&](int c) { return c % split; };
             int mine = 0;                                              // chunks that this CTA finishes
             for (int c = 0; c < chunks; ++c)
                 mine += owner(c) == part ? 1 : 0;
-            if (wq == 0 && wh == 0 && !dry) {
-                if (!FUSE && lane < split && lane != part)
+            if (wq == 0 && wh == 0) {
+                if (lane < split && lane != part)
                     mbar_arrive_cluster(mapa_shared(bar_peers, lane));
                 if (lane == 0)
                     mbar_arrive_expect_tx(bar_parts, mine * (split - 1) * t.rows * (4 * C) * kParts);
             }
-            // place of a chunk's part from CTA `from`: [place_of(c)][from][gate, up][quarter][C / 4][lane] float4
-            uint8_t *parts = FUSE ? rest : smem;
+            // place of a chunk's part from CTA `from`: [c / split][from][gate, up][quarter][C / 4][lane] float4
             auto place = [&](int c, int from, int which) {
-                return (uint32_t)((((place_of(c) * split + from) * kParts + which) * (FUSE ? 1 : 4) + wq) * (C / 4) * 32 + lane) * 16u;
+                return (uint32_t)((((c / split * split + from) * kParts + which) * 4 + wq) * (C / 4) * 32 + lane) * 16u;
             };
-            const uint32_t s0 = smem_u32(parts);
-            bool ok = FUSE || dry || fp8_warp_wait<2>(bar_peers, 0, abort_flag, args.status, lane);
-            if (ok && some_rows)
+            const uint32_t s0 = smem_u32(smem);
+            bool ok = fp8_warp_wait<2>(bar_peers, 0, abort_flag, args.status, lane);
+            if (ok && rows > 0)
                 for (int i = 0; i < own; ++i) {
                     const int c = chunk_of(i), to = owner(c);
                     if (to == part)
@@ -968,8 +1105,8 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                         }
                 }
             __syncwarp();
-            ok = ok && (dry || fp8_warp_wait<2>(bar_parts, 0, abort_flag, args.status, lane));
-            if (ok && some_rows)
+            ok = ok && fp8_warp_wait<2>(bar_parts, 0, abort_flag, args.status, lane);
+            if (ok && rows > 0)
                 for (int i = 0; i < own; ++i) {
                     const int c = chunk_of(i);
                     if (owner(c) != part)
@@ -981,7 +1118,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                         for (int from = 0; from < split; ++from) {
                             const float4 w = from == part || lane >= rows ? make_float4(v[0], v[1], v[2], v[3])
                                                           : *reinterpret_cast<const float4 *>(
-                                                                parts + place(c, from, which) + j * 512);
+                                                                smem + place(c, from, which) + j * 512);
                             sum.x += w.x;
                             sum.y += w.y;
                             sum.z += w.z;
@@ -1001,7 +1138,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                     finish(t, C * c, rows, (int64_t)t.row0 + 32 * wq, r, q);
                 }
         }
-        if (!FUSE && lane == 0)
+        if (lane == 0)
             bulk_wait_group_all();
         __syncwarp();
     }
@@ -1193,7 +1330,7 @@ cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8S
     a.blocks = (int)((summed + kFp8Block - 1) / kFp8Block);
     a.halves = halves;
     a.tile = tile;
-    a.a_rows = FUSE ? (int)((g.M + 7) / 8 * 8) : CG == 2 || g.M >= 128 ? 128 : (int)((g.M + 31) / 32 * 32);
+    a.a_rows = FUSE ? (int)((g.M + 15) / 16 * 16) : CG == 2 || g.M >= 128 ? 128 : (int)((g.M + 31) / 32 * 32);
     const int cols = GATED ? 2 * tile : tile;
     a.slot1 = cols > 224 ? 192 : 224;
     a.boxed_rows = g.E > 0 ? (a.a_rows - 1) / 32 * 32 : 0;
@@ -1216,7 +1353,7 @@ cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8S
         return cudaErrorInvalidValue;
     // the stages: as many chunks as leave four of them
     const int ring = Cfg::kRing - (FUSE ? kFBufs * kFp8Group * a.a_rows * kFChunk : 0);
-    const int chunk = ((FUSE ? 0 : a.a_rows) + b_rows) * kFChunk;
+    const int chunk = (FUSE ? (GATED ? kFUpRow + tile : b_rows) : a.a_rows + b_rows) * kFChunk;
     a.prefetch = kPrefetchBytes / chunk;
     a.per = 1;                // a pair: two where that leaves three stages (4480 x 16384 x 6144: 295 us, with one 328)
     if (CG == 2 && 6 * chunk <= ring)
@@ -1283,7 +1420,7 @@ Fp8Shape pick(const Fp8GemmLaunch &g, bool fuse, const Fp8Room &room)
         const int64_t rounds8 = g.E > 0 && tiles > 2 * units ? tiles * 8 / units + 4 : (tiles + units - 1) / units * 8;
         const int64_t a = fuse ? 0 : cg == 2 || mean >= 96 ? 128 : (mean + 31) / 32 * 32;
         const int64_t b = g.bwd ? (cols / cg + 127) / 128 * 128 : cols / cg;
-        const int64_t mma = cg == 2 ? 2 * cols : 140 + 2 * cols, copy = (a + b) * kFChunk / 66;
+        const int64_t mma = cg == 2 ? 2 * cols : 140 + 2 * (fuse ? (g.M + 15) / 16 * 16 : cols), copy = (a + b) * kFChunk / 66;
         const int64_t group = kFp8Group * (mma > copy ? mma : copy), rounding = fuse ? 250 + 450 * ((mean + 3) / 4) : 0;
         const int64_t cost = rounds8 * ((groups + split - 1) / split * (group > rounding ? group : rounding) + (cols > 224 ? 2500 : 500)) / 8 +
                              10 * cols + (split == 1 ? 0 : 8000);
@@ -1296,7 +1433,7 @@ Fp8Shape pick(const Fp8GemmLaunch &g, bool fuse, const Fp8Room &room)
         for (int cols = 256; cols >= 64; cols -= 32)
             offer(2, cols, 1);
     // (what shared memory holds of the others' sums)
-    const int most = fuse ? (weights == 2 ? 3 : 4) : weights == 2 ? 6 : kFMaxSplit;
+    const int most = fuse ? (weights == 2 ? (g.M > 16 ? 3 : 6) : g.M > 16 ? 6 : kFMaxSplit) : weights == 2 ? 6 : kFMaxSplit;
     const int widest = mean > 32 ? (g.bwd ? 256 : 224) : 128;
     for (int cols = widest; cols >= (g.bwd ? 128 : 32); cols -= g.bwd ? 128 : 16)
         for (int split = 1; split <= most && split <= groups && (split == 1 || cols <= 128); ++split)

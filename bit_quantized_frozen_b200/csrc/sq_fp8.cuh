@@ -1,6 +1,6 @@
 // sq_fp8.cuh -- what the row rounding (sq_fp8_quant.cu) and the block-scaled e4m3 product
-// (sq_fp8.cu) share: the launch arguments, the activations, and the tcgen05 instructions of
-// kind::mxf8f6f4.
+// (sq_fp8.cu) share: the activations, the rounding to e4m3, and the tcgen05 and copy instructions of the
+// product.
 #pragma once
 
 #include <cstdint>
@@ -13,7 +13,7 @@ namespace sq {
 constexpr int kFp8Block = 128;                    // values of a scale
 constexpr int kFp8Group = 4;                      // blocks whose scales share a 32-bit word
 
-// 32-bit words of row scales along an axis of `len` values (one tcgen05.cp brings a word of each row)
+// 32-bit words of row scales along an axis of `len` values
 __host__ __device__ __forceinline__ int64_t fp8_groups(int64_t len)
 {
     return (len + kFp8Block * kFp8Group - 1) / (kFp8Block * kFp8Group);
@@ -307,16 +307,6 @@ __device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&r)[16]
                    "=r"(r[15])
                  : "r"(taddr)
                  : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16])
-{
-    tmem_ld_16cols(taddr, r);
-}
-
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[32])
-{
-    tmem_ld_32cols(taddr, r);
 }
 
 // 16 bytes into another CTA's shared memory, counted on its barrier

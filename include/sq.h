@@ -72,7 +72,7 @@ typedef enum {
     SQ_FMT_INT8_ROW = 4    /* int8 codes [N, K], fp32 scales [N], rank-16 low rank */
 } sq_format;
 
-/* operations for sq_workspace_bytes() (11 and 12: the products of sq_w8a8.h) */
+/* operations for sq_workspace_bytes() (11 and 12: the products of sq_w8a8.h, 15 to 18: of sq_fp8.h) */
 typedef enum {
     SQ_OP_BUILD_INT4 = 1,
     SQ_OP_BUILD_NVFP4 = 2,
@@ -376,7 +376,7 @@ SQ_API sq_status sq_linear_bwd_dx(const sq_weight *w, const uint16_t *dy, int64_
 
 /*
  * Optional instrumentation for timing the tensor-core GEMM on its own: when
- * both handles are non-NULL, every later sq_linear_fwd, sq_linear_bwd_dx or w8a8 call
+ * both handles are non-NULL, every later sq_linear_fwd, sq_linear_bwd_dx, w8a8 or fp8 call
  * made by this host thread records start_event immediately before and
  * stop_event immediately after its GEMM launch, on the call's stream.  The handles are cudaEvent_t
  * values passed as void*, created and owned by the caller; (NULL, NULL) turns
