@@ -1420,10 +1420,11 @@ Fp8Shape pick(const Fp8GemmLaunch &g, bool fuse, const Fp8Room &room)
         const int64_t rounds8 = g.E > 0 && tiles > 2 * units ? tiles * 8 / units + 4 : (tiles + units - 1) / units * 8;
         const int64_t a = fuse ? 0 : cg == 2 || mean >= 96 ? 128 : (mean + 31) / 32 * 32;
         const int64_t b = g.bwd ? (cols / cg + 127) / 128 * 128 : cols / cg;
-        const int64_t mma = cg == 2 ? 2 * cols : 140 + 2 * (fuse ? (g.M + 15) / 16 * 16 : cols), copy = (a + b) * kFChunk / 66;
-        const int64_t group = kFp8Group * (mma > copy ? mma : copy), rounding = fuse ? 250 + 450 * ((mean + 3) / 4) : 0;
+        const int64_t mma = cg == 2 ? 2 * cols : fuse ? 190 + (g.M + 15) / 16 * 32 : 140 + 2 * cols, copy = (a + b) * kFChunk / (fuse ? 72 : 66);
+        const int64_t group = kFp8Group * (mma > copy ? mma : copy), rounding = fuse ? 250 + (weights < 2 && g.gated ? 1000 : 450) * ((mean + 3) / 4) : 0;
+        const int64_t ctas = (tiles < units ? tiles : units) * split;
         const int64_t cost = rounds8 * ((groups + split - 1) / split * (group > rounding ? group : rounding) + (cols > 224 ? 2500 : 500)) / 8 +
-                             10 * cols + (split == 1 ? 0 : 8000);
+                             (fuse ? 30 * ctas + (split == 1 ? 0 : 1200 + 200 * split) : 10 * cols + (split == 1 ? 0 : 8000));
         if (cost < best_cost) {
             best_cost = cost;
             best = {cg, tile, split};
@@ -1454,14 +1455,13 @@ cudaError_t launch_mode(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8
 }  // namespace
 
 // Every CTA rounds the rows for itself: that saves a launch (some 3 us), and costs more with each row, most
-// for a gated pair's gradients.  Measured, us a call, one kernel and two: 8 x 5696 x 1872 6.9, 10.2; gradient
-// of 16 x 1536 11.1, 11.4; gated gradients of 3 x 1568 x 3712 11.4, 12.6, 6 x 544 x 7936 11.6, 9.4 and
-// 16 x 6912 x 14592 116, 38.  Of experts a tile has only some of the rows.
+// for a gated pair's gradients.  Measured, us a call, one kernel and two: 7 x 4128 x 1536 6.2, 8.5;
+// 16 x 6784 x 880 5.7, 8.7; gradients of 15 x 6784 x 1584 8.5, 13.6, 24 x 8192 x 9216 26.8, 23.4 and
+// 31 x 7680 x 11136 49.8, 21.9; gated gradients of 6 x 1248 x 1248 6.4, 10.5, 7 x 9216 x 4224 24.6, 23.7 and
+// 17 x 3712 x 4560 21.1, 18.0.  Of experts a tile has only some of the rows.
 bool fp8_rounds_rows(int E, int64_t M, bool gated_bwd)
 {
-    if (gated_bwd)
-        return M <= (E > 1 ? 8 : 4);
-    return M <= (E > 1 ? 2 * kFuseRows : kFuseRows);
+    return M <= kFuseRows * (E > 1 ? 2 : 1) / (gated_bwd ? 2 : 1);
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, int sms, cudaStream_t stream)

@@ -24,7 +24,7 @@
  * of NaN; other rows are not affected.
  *
  * Few rows are rounded by the product itself: M <= 16, for E > 1 experts M <= 32; the
- * gradient of a gated pair M <= 4, for E > 1 experts M <= 8.  Such a call needs no
+ * gradient of a gated pair M <= 8, for E > 1 experts M <= 16.  Such a call needs no
  * workspace: its size is 0 and ws may be NULL; the status word is then the library's
  * own (sq_check_device_status(NULL, stream)), to which calls only add.  A workspace
  * given all the same holds at least 256 bytes.

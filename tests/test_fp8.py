@@ -56,7 +56,7 @@ def size(fn, op, M, N, K, E=4):
 
 def few_rows(fn, e):
     """Rows that the product rounds itself: calls that need no workspace."""
-    return (4 if "gated_bwd" in fn else 16) * (2 if "grouped" in fn and e > 1 else 1)
+    return (8 if "gated_bwd" in fn else 16) * (2 if "grouped" in fn and e > 1 else 1)
 
 
 @pytest.mark.parametrize("call,fn,op", CALLS)
