@@ -5,9 +5,9 @@
 //   gated     h[m, n]  = act(g) u,  g and u such sums of two weights
 //   backward  dx[m, k] = sum_n dy[m, n] W[n, k], gated: sum over both weights
 //
-// Tensor-memory lanes hold tokens, columns output channels.  A = the rows' codes (K-major); B =
-// the weight's codes, K-major forward and N-major backward (they are read as they lie, never
-// transposed).  Gated: B is a tile of the gate's rows and the same rows of the up projection, so
+// Tensor-memory lanes hold tokens, columns output channels (few rows: see below).  A = the rows' codes
+// (K-major); B = the weight's codes, K-major forward and N-major backward (they are read as they lie,
+// never transposed).  Gated: B is a tile of the gate's rows and the same rows of the up projection, so
 // that both sums of an output lie in one lane and the activation is applied as they leave tensor
 // memory; backward the summed axis simply runs through both weights.
 //
@@ -18,18 +18,29 @@
 // to four groups ahead of the products.  (Copied by the issuing thread from shared memory instead,
 // tcgen05.cp, each group held the tensor pipe up by some 600 cycles.)
 //
-// Few rows (fp8_rounds_rows): the feeders round the rows themselves, straight into the operand's
-// shared-memory layout, and the call is one kernel.
+// Few rows (FUSE, see fp8_rounds_rows): the feeders round the rows themselves, straight into the operand's
+// shared-memory layout, and the call is one kernel.  There the operands change places: lanes hold up to 128
+// channels (gated: the gate's in lanes 0 .. 63, the up projection's from 64 on), columns 16 or 32 rows.  With
+// the rows as lanes, the tensor cores multiplied 128 of them for the 8 that were there: 8 x 16384 x 6144,
+// gated, took 36 us, and 42 once the power cap had lowered the clocks, instead of 33.5 for as long as it runs.
 //
 // CTA (CG = 1, tiles of 128 tokens x up to 224 columns, backward 256) or CTA pair (CG = 2, 256 x up to
-// 256), one CTA per SM, persistent: 8 epilogue warps (few rows: 2), TMA producers, feeders (few rows: two
+// 256), one CTA per SM, persistent: 8 epilogue warps (few rows: 4), TMA producers, feeders (few rows: two
 // sets), and an issuer that also allocates tensor memory.  Outputs leave by TMA where a warp's 32 rows
 // are all the tile's.
 //
 // Few tiles (CG = 1): a cluster of CTAs shares a tile, each with some of the groups, and joins the
 // partial sums over distributed shared memory, in the order of the CTAs' ranks.
 //
-// (figures)
+// What bounds it, in a stream of calls (us a call with the rounding; many at a stretch in brackets, where the
+// power cap lowers the clocks):
+//   4480 x 16384 x 6144   forward 334 (387), gradient 365 (431), gated 692 (801): tensor pipe 89 to 92 % active
+//                         (forward alone 295 us, 3.06 PFLOP/s), then the power cap
+//   8300 rows of 61 experts, gated 2 x 1408 x 2048   88 (105): 59 % of DRAM, tiles of a few rows more than 128
+//   8 x 16384 x 6144, gated   33.5: the weights' bytes at 6.0 TB/s
+//   32 rows of 27 experts, 2816 x 2048   30.4 (156 MB: 5.1 TB/s): the last tiles
+//   1 x 6144 x 6144       10.0: start, 38 MB from DRAM, the join of two CTAs' sums
+//   777 x 4240 x 2832     21.0: one round of tiles behind the rounding
 #include <cuda.h>
 
 #include <type_traits>
@@ -1387,8 +1398,13 @@ cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8S
 
 // How a call's tiles are cut: the candidate with the least time by a simple count of cycles.  A chunk
 // of 128 summed values takes the longer of its products (2 cycles a column; one CTA: 140 more) and its
-// copies (about 66 bytes a cycle and SM), few rows at least their rounding; between overlapping accumulators the products pause; a tile's
+// copies (about 66 bytes a cycle and SM); between overlapping accumulators the products pause; a tile's
 // groups may be shared by a cluster where all tiles run at once, which costs some 8000 cycles.
+// Few rows: products of 128 channels whatever the tile has, 190 cycles and 2 a row of the operand; a group at
+// least as long as its rounding; 30 for each CTA, which all read the rows; 1200 and 200 a CTA for a shared
+// tile.  Measured, us a call of one token, 6144 x 6144, tiles of 48, 64, 80 channels 12.1, 11.2, 11.8, two CTAs
+// on tiles of 96, 112, 128 channels 10.5, 10.2, 10.0; over 100 calls with sizes at random the choice was 2 %
+// from the fastest candidate on average and 23 % at worst (few of many experts, which the host cannot know).
 //
 // Experts: the host does not see the offsets.  It counts a row tile for each expert that can have rows,
 // or half of one and the whole ones that all rows make; no more than one and the whole ones each.

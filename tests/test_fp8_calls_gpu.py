@@ -592,3 +592,34 @@ def test_device_checks(monkeypatch):
     w.scales = w.scales.cpu()
     with pytest.raises(ValueError, match="scales is on cpu"):
         sq.linear_fwd_fp8(w, x)
+
+
+@pytest.mark.parametrize("M,off", [(5, None), (8, None), (9, None), (16, None), (17, None), (16, [0, 0, 16, 16]), (17, [0, 17, 17, 17]),
+                                   (32, [0, 1, 31, 32]), (33, [0, 33, 33, 33])])
+def test_rows_around_the_border_of_one_kernel(M, off):
+    """The most rows that the product rounds itself and one more, all of one expert among them; tiles that end
+    inside a block, a second weight."""
+    E = None if off is None else len(off) - 1
+    N, K = 336, 1168
+    rng = np.random.default_rng([M, E or 0])
+    p, r = layer(rng, N, K, E), layer(rng, N, K, E)
+    w, w2 = weight(*p), weight(*r)
+    x, dy, g, u = rand(rng, M, K), rand(rng, M, N), rand(rng, M, N), rand(rng, M, N)
+    a = [dev(v, BF) for v in (x, dy, g, u)]
+    if E is None:
+        got = [sq.linear_fwd_fp8(w, a[0]), sq.linear_bwd_dx_fp8(w, a[1]), *sq.gated_fwd_fp8(w, w2, a[0], act="gelu", save=True),
+               sq.gated_bwd_dx_fp8(w, w2, *a[1:], act="gelu")]
+    else:
+        o = dev(np.array(off, np.int32))
+        got = [sq.grouped_fwd_fp8(w, a[0], o), sq.grouped_bwd_dx_fp8(w, a[1], o),
+               *sq.grouped_gated_fwd_fp8(w, w2, a[0], o, act="gelu", save=True),
+               sq.grouped_gated_bwd_dx_fp8(w, w2, *a[1:], o, act="gelu")]
+    for e in range(E or 1):
+        s = slice(None) if E is None else slice(off[e], off[e + 1])
+        if E is not None and off[e] == off[e + 1]:
+            continue
+        W, W2 = (ref.dequant(*v) if E is None else ref.dequant(v[0][e], v[1][e]) for v in (p, r))
+        want = [ref.forward(x[s], W), ref.backward(dy[s], W), *ref.gated_forward(x[s], W, W2, "gelu"),
+                ref.gated_backward(dy[s], g[s], u[s], W, W2, "gelu")]
+        for i, (y, v) in enumerate(zip(got, want)):
+            ref.check(f32(y[s]), *v, i in (3, 4))
