@@ -1399,7 +1399,11 @@ cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8S
 // How a call's tiles are cut: the candidate with the least time by a simple count of cycles.  A chunk
 // of 128 summed values takes the longer of its products (2 cycles a column; one CTA: 140 more) and its
 // copies (about 66 bytes a cycle and SM); between overlapping accumulators the products pause; a tile's
-// groups may be shared by a cluster where all tiles run at once, which costs some 8000 cycles.
+// groups may be shared by a cluster where all tiles run at once, which costs some 8000 cycles (of clusters
+// larger than two, some room is left: the last one waited for SMs that other kernels still held, 262 x 1616 x
+// 14080 in 45 clusters of three of 45 that fit took 31.6 us, with 39 of them 24.1).  A pair's start takes 700
+// more.  Backward a CTA's columns start at 32-byte sectors (4480 x 16384 x 6144, pairs of 192, 224 and 256
+// columns: 423, 450, 361 us).
 // Few rows: products of 128 channels whatever the tile has, 190 cycles and 2 a row of the operand; a group at
 // least as long as its rounding; 30 for each CTA, which all read the rows; 1200 and 200 a CTA for a shared
 // tile.  Measured, us a call of one token, 6144 x 6144, tiles of 48, 64, 80 channels 12.1, 11.2, 11.8, two CTAs
@@ -1429,7 +1433,7 @@ Fp8Shape pick(const Fp8GemmLaunch &g, bool fuse, const Fp8Room &room)
             most_rows = experts + whole;
         }
         const int64_t units = cg == 2 ? room.pairs : room.clusters[split];
-        if (split > 1 && most_rows * col_tiles > units)
+        if (split > 1 && most_rows * col_tiles > (split > 2 ? units * 15 / 16 : units))
             return;
         const int64_t tiles = rows * col_tiles;
         // (in eighths; many rounds of tiles that are only an estimate: half of one for the last)
@@ -1440,14 +1444,15 @@ Fp8Shape pick(const Fp8GemmLaunch &g, bool fuse, const Fp8Room &room)
         const int64_t group = kFp8Group * (mma > copy ? mma : copy), rounding = fuse ? 250 + (weights < 2 && g.gated ? 1000 : 450) * ((mean + 3) / 4) : 0;
         const int64_t ctas = (tiles < units ? tiles : units) * split;
         const int64_t cost = rounds8 * ((groups + split - 1) / split * (group > rounding ? group : rounding) + (cols > 224 ? 2500 : 500)) / 8 +
-                             (fuse ? 30 * ctas + (split == 1 ? 0 : 1200 + 200 * split) : 10 * cols + (split == 1 ? 0 : 8000));
+                             (fuse ? 30 * ctas + (split == 1 ? 0 : 1200 + 200 * split) :
+                                     10 * cols + (split == 1 ? 0 : 8000) + (cg == 2 ? 700 : 0));
         if (cost < best_cost) {
             best_cost = cost;
             best = {cg, tile, split};
         }
     };
     if (!fuse && (g.E == 0 || mean >= 512))
-        for (int cols = 256; cols >= 64; cols -= 32)
+        for (int cols = 256; cols >= 64; cols -= g.bwd ? 64 : 32)
             offer(2, cols, 1);
     // (what shared memory holds of the others' sums)
     const int most = fuse ? (weights == 2 ? (g.M > 16 ? 3 : 6) : g.M > 16 ? 6 : kFMaxSplit) : weights == 2 ? 6 : kFMaxSplit;
