@@ -411,7 +411,7 @@ sq_status fp8_product(const Fp8Call &c, bool gated, uint32_t flags, void *ws, si
         return SQ_ERR_NULL;
     if (c.E > 0 && M == 0)                            // no rows: nothing to do
         return SQ_OK;
-    const bool fused = sq::fp8_rounds_rows((int)c.E, M, gated && c.bwd);      // (needs no workspace)
+    const bool fused = sq::fp8_rounds_rows((int)c.E, M, N, K, gated && c.bwd);      // (needs no workspace)
     if (!c.x || !c.y || (!ws && !fused) || (gated && c.bwd && (!c.g || !c.u)) || (c.g_out == nullptr) != (c.u_out == nullptr))
         return SQ_ERR_NULL;
     if (!aligned(c.x, 16) || !aligned(c.y, 16) || !aligned(c.g, 16) || !aligned(c.u, 16) || !aligned(c.g_out, 16) ||
@@ -565,11 +565,11 @@ size_t sq_workspace_bytes(int op, int64_t M, int64_t N, int64_t K)
         return i8_layout(true, M, N, K).total;
     case SQ_OP_LINEAR_FWD_FP8:
     case SQ_OP_GATED_FWD_FP8:
-        return sq::fp8_rounds_rows(0, M, false) ? 0 : fp8_layout(false, false, M, N, K).total;
+        return sq::fp8_rounds_rows(0, M, N, K, false) ? 0 : fp8_layout(false, false, M, N, K).total;
     case SQ_OP_LINEAR_BWD_DX_FP8:
-        return sq::fp8_rounds_rows(0, M, false) ? 0 : fp8_layout(true, false, M, N, K).total;
+        return sq::fp8_rounds_rows(0, M, N, K, false) ? 0 : fp8_layout(true, false, M, N, K).total;
     case SQ_OP_GATED_BWD_DX_FP8:
-        return sq::fp8_rounds_rows(0, M, true) ? 0 : fp8_layout(true, true, M, N, K).total;
+        return sq::fp8_rounds_rows(0, M, N, K, true) ? 0 : fp8_layout(true, true, M, N, K).total;
     default:
         return 0;
     }
@@ -586,11 +586,11 @@ size_t sq_grouped_workspace_bytes(int op, int64_t E, int64_t M, int64_t N, int64
         return i8_layout(true, M, N, K).total;
     case SQ_OP_GROUPED_FWD_FP8:
     case SQ_OP_GROUPED_GATED_FWD_FP8:
-        return sq::fp8_rounds_rows((int)E, M, false) ? 0 : fp8_layout(false, false, M, N, K).total;
+        return sq::fp8_rounds_rows((int)E, M, N, K, false) ? 0 : fp8_layout(false, false, M, N, K).total;
     case SQ_OP_GROUPED_BWD_DX_FP8:
-        return sq::fp8_rounds_rows((int)E, M, false) ? 0 : fp8_layout(true, false, M, N, K).total;
+        return sq::fp8_rounds_rows((int)E, M, N, K, false) ? 0 : fp8_layout(true, false, M, N, K).total;
     case SQ_OP_GROUPED_GATED_BWD_DX_FP8:
-        return sq::fp8_rounds_rows((int)E, M, true) ? 0 : fp8_layout(true, true, M, N, K).total;
+        return sq::fp8_rounds_rows((int)E, M, N, K, true) ? 0 : fp8_layout(true, true, M, N, K).total;
     default:
         return 0;
     }

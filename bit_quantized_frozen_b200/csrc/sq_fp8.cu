@@ -1475,14 +1475,17 @@ cudaError_t launch_mode(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8
 
 }  // namespace
 
-// Every CTA rounds the rows for itself: that saves a launch (some 3 us), and costs more with each row, most
-// for a gated pair's gradients.  Measured, us a call, one kernel and two: 7 x 4128 x 1536 6.2, 8.5;
+// Every CTA rounds the rows for itself: that saves a launch (some 3 us, and 2.5 of the host's time), and costs
+// more with each row, most for a gated pair's gradients.  Measured, us a call, one kernel and two: 7 x 4128 x 1536 6.2, 8.5;
 // 16 x 6784 x 880 5.7, 8.7; gradients of 15 x 6784 x 1584 8.5, 13.6, 24 x 8192 x 9216 26.8, 23.4 and
 // 31 x 7680 x 11136 49.8, 21.9; gated gradients of 6 x 1248 x 1248 6.4, 10.5, 7 x 9216 x 4224 24.6, 23.7 and
-// 17 x 3712 x 4560 21.1, 18.0.  Of experts a tile has only some of the rows.
-bool fp8_rounds_rows(int E, int64_t M, bool gated_bwd)
+// 17 x 3712 x 4560 21.1, 18.0.  Of experts a tile has only some of the rows; and small weights are shared by
+// fewer CTAs: of 45 calls with N K <= 2^24 and 17 to 32 rows (gated gradients 9 to 16) one kernel took 0.91 of the
+// time of two (24 x 1280 x 6032 9.4, 13.5; at worst 32 x 7200 x 1392 10.6, 8.7), called one by one 0.86.
+bool fp8_rounds_rows(int E, int64_t M, int64_t N, int64_t K, bool gated_bwd)
 {
-    return M <= kFuseRows * (E > 1 ? 2 : 1) / (gated_bwd ? 2 : 1);
+    const bool twice = E > 1 || (K > 0 && N <= (int64_t(1) << 24) / K);
+    return M <= kFuseRows * (twice ? 2 : 1) / (gated_bwd ? 2 : 1);
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, int sms, cudaStream_t stream)
@@ -1494,7 +1497,7 @@ cudaError_t launch_fp8_gemm(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, int s
     const Fp8Room *room = nullptr;
     if (cudaError_t e = room_of(dev, ctx, sms, &room); e != cudaSuccess)
         return e;
-    const bool fuse = fp8_rounds_rows(g.E, g.M, g.bwd && g.gated);
+    const bool fuse = fp8_rounds_rows(g.E, g.M, g.N, g.K, g.bwd && g.gated);
     const Fp8Shape sh = pick(g, fuse, *room);
     if (sh.cg == 2)
         return launch_mode<2, false>(g, q, sh, dev, *room, stream);

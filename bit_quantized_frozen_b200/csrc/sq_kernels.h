@@ -173,7 +173,7 @@ struct Fp8GemmLaunch {
 };
 cudaError_t launch_fp8_gemm(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, int sms, cudaStream_t stream);
 // whether that kernel rounds the rows itself (few rows: launch_fp8_quant is not called)
-bool fp8_rounds_rows(int E, int64_t M, bool gated_bwd);
+bool fp8_rounds_rows(int E, int64_t M, int64_t N, int64_t K, bool gated_bwd);
 
 // ID of the current CUDA context (unique for the life of the process; a context created
 // after cudaDeviceReset gets a new one), 0 if it cannot be read.  Per-device caches of

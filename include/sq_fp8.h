@@ -23,8 +23,8 @@
  * pass fp32's range is infinite or NaN).  A row with a NaN or an infinity gives a row
  * of NaN; other rows are not affected.
  *
- * Few rows are rounded by the product itself: M <= 16, for E > 1 experts M <= 32; the
- * gradient of a gated pair M <= 8, for E > 1 experts M <= 16.  Such a call needs no
+ * Few rows are rounded by the product itself: M <= 16, and M <= 32 where N K <= 2^24
+ * or E > 1 (the gradient of a gated pair: M <= 8 and 16).  Such a call needs no
  * workspace: its size is 0 and ws may be NULL; the status word is then the library's
  * own (sq_check_device_status(NULL, stream)), to which calls only add.  A workspace
  * given all the same holds at least 256 bytes.

@@ -54,9 +54,9 @@ def size(fn, op, M, N, K, E=4):
     return sq.sq_grouped_workspace_bytes(op, E, M, N, K) if "grouped" in fn else sq.sq_workspace_bytes(op, M, N, K)
 
 
-def few_rows(fn, e):
+def few_rows(fn, e, n=256, k=512):
     """Rows that the product rounds itself: calls that need no workspace."""
-    return (8 if "gated_bwd" in fn else 16) * (2 if "grouped" in fn and e > 1 else 1)
+    return (8 if "gated_bwd" in fn else 16) * (2 if "grouped" in fn and e > 1 or n * k <= 1 << 24 else 1)
 
 
 @pytest.mark.parametrize("call,fn,op", CALLS)
@@ -196,11 +196,12 @@ def test_workspace_covers_its_parts():
     """Header, row codes and scale words, and little more."""
     for _, fn, op in CALLS:
         back, halves = "bwd" in fn, 2 if "gated_bwd" in fn else 1
-        for m, n, k in ((1, 6144, 6144), (4480, 16384, 6144), (333, 144, 16), (7, 16, 2064), (33, 256, 512), (17, 256, 512)):
+        for m, n, k in ((1, 6144, 6144), (4480, 16384, 6144), (333, 144, 16), (7, 16, 2064), (33, 256, 512), (17, 256, 512), (32, 4096, 4096), (17, 4096, 4112),
+                        (16, 4096, 4112), (9, 4096, 4112), (8, 4096, 4112)):
             wide = n if back else k
             need = 256 + halves * m * (wide + 4 * ((wide + 511) // 512))
             for e in (1, 64, 1024):
-                if m <= few_rows(fn, e):
+                if m <= few_rows(fn, e, n, k):
                     assert size(fn, op, m, n, k, e) == 0
                 else:
                     assert need <= size(fn, op, m, n, k, e) <= need + 4 * 1024

@@ -448,7 +448,7 @@ def test_few_rows_need_no_workspace():
     assert e.value.status == 9
     sq.sq_check_device_status(None)
     with pytest.raises(sq.SqError):
-        sq.sq_linear_fwd_fp8(w, torch.zeros(17, 272, dtype=BF, device="cuda"), torch.empty(17, 400, device="cuda"))
+        sq.sq_linear_fwd_fp8(w, torch.zeros(33, 272, dtype=BF, device="cuda"), torch.empty(33, 400, device="cuda"))
 
 
 def test_views_and_streams():
@@ -594,7 +594,8 @@ def test_device_checks(monkeypatch):
         sq.linear_fwd_fp8(w, x)
 
 
-@pytest.mark.parametrize("M,off", [(5, None), (8, None), (9, None), (16, None), (17, None), (16, [0, 0, 16, 16]), (17, [0, 17, 17, 17]),
+@pytest.mark.parametrize("M,off", [(5, None), (8, None), (9, None), (16, None), (17, None), (32, None), (33, None), (16, [0, 16]), (17, [0, 17]), (32, [0, 32]),
+                                   (33, [1, 33]), (16, [0, 0, 16, 16]), (17, [0, 17, 17, 17]),
                                    (32, [0, 1, 31, 32]), (33, [0, 33, 33, 33])])
 def test_rows_around_the_border_of_one_kernel(M, off):
     """The most rows that the product rounds itself and one more, all of one expert among them; tiles that end
