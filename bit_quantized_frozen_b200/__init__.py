@@ -63,6 +63,7 @@ SQ_OP_GROUPED_BWD_DX_FP8 = 20
 SQ_OP_GROUPED_GATED_FWD_FP8 = 21
 SQ_OP_GROUPED_GATED_BWD_DX_FP8 = 22
 SQ_IN_BF16 = 0x40
+SQ_STATUS_LIBRARY = 0x100
 SQ_ACT_SILU = 0
 SQ_ACT_GELU_TANH = 1
 RANK = 32
@@ -918,7 +919,8 @@ def build_fp8_grouped(W: torch.Tensor, stream=None) -> GroupedWeight:
 
 
 def _fp8_out(fn, op, weights, rows, offsets, act, save, ws, flags, out_bf16, stream):
-    """The outputs and workspace of a block-scaled call, and the call."""
+    """The outputs and workspace of a block-scaled call, and the call.  With the caller's ws its first word is the
+    call's status; without, it goes to the library's word (sq_check_device_status(None)), however many rows."""
     if stream is not None:
         with _allocating_on(stream):
             return _fp8_out_here(fn, op, weights, rows, offsets, act, save, ws, flags, out_bf16, stream)
@@ -938,8 +940,9 @@ def _fp8_out_here(fn, op, weights, rows, offsets, act, save, ws, flags, out_bf16
     fresh = ws is None
     if fresh:
         n = _w8a8_bytes(op, E, M, N, K)
-        if n:
+        if n:                                                # (gone when the status is asked for)
             ws = x.new_empty(n, dtype=torch.uint8)
+            flags |= SQ_STATUS_LIBRARY
     outs = (y,)
     if act is not None:
         act = _fp8_act(fn, act)

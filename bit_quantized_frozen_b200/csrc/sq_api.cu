@@ -401,7 +401,7 @@ sq_status fp8_product(const Fp8Call &c, bool gated, uint32_t flags, void *ws, si
         if (!aligned(w->codes, 16))
             return SQ_ERR_ALIGN;
     }
-    if ((flags & ~(SQ_OUT_BF16 | SQ_CHECK_FINITE | (c.E > 0 ? SQ_ZERO_UNGROUPED : 0u))) ||
+    if ((flags & ~(SQ_OUT_BF16 | SQ_CHECK_FINITE | SQ_STATUS_LIBRARY | (c.E > 0 ? SQ_ZERO_UNGROUPED : 0u))) ||
         (gated && c.act != SQ_ACT_SILU && c.act != SQ_ACT_GELU_TANH))
         return SQ_ERR_ARG;
     const int64_t N = c.w[0]->N, K = c.w[0]->K, M = c.M;
@@ -425,7 +425,10 @@ sq_status fp8_product(const Fp8Call &c, bool gated, uint32_t flags, void *ws, si
     if (st != SQ_OK)
         return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    uint32_t *status = reinterpret_cast<uint32_t *>(ws);      // NULL: the library's own word
+    const bool shared = !ws || (flags & SQ_STATUS_LIBRARY);
+    uint32_t *status = reinterpret_cast<uint32_t *>(ws);
+    if (shared)
+        SQ_CUDA(sq::fp8_status_word(sms, &status), "status symbol");
     sq::Fp8QuantArgs q;
     memset(&q, 0, sizeof(q));
     q.x = c.x;
@@ -449,8 +452,8 @@ sq_status fp8_product(const Fp8Call &c, bool gated, uint32_t flags, void *ws, si
     q.finite_check = (flags & SQ_CHECK_FINITE) ? 1 : 0;
     // the first block of the rounding writes the workspace's status word; with a finite check any block
     // may set it, so it is cleared first.  (The library's word is shared: calls only add to it.)
-    q.keep_status = q.finite_check || !status;
-    if (q.finite_check && status)
+    q.keep_status = q.finite_check || shared;
+    if (q.finite_check && !shared)
         SQ_CUDA(cudaMemsetAsync(status, 0, 4, s), "memset");
     if (!fused) {
         SQ_CUDA(stage_event(SQ_STAGE_ACT_QUANT, 0, s), "event record");

@@ -1323,7 +1323,7 @@ cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8S
     a.y = g.y;
     a.g_out = g.g_out;
     a.u_out = g.u_out;
-    a.status = g.status ? g.status : room.status;
+    a.status = g.status;
     for (int i = 0; i < 3; ++i) {
         a.zero[i] = q.zero[i];
         a.zero_row_bytes[i] = q.zero_row_bytes[i];
@@ -1488,14 +1488,28 @@ bool fp8_rounds_rows(int E, int64_t M, int64_t N, int64_t K, bool gated_bwd)
     return M <= kFuseRows * (twice ? 2 : 1) / (gated_bwd ? 2 : 1);
 }
 
+static cudaError_t current_room(int sms, int *dev, const Fp8Room **room)
+{
+    if (cudaGetDevice(dev) != cudaSuccess || *dev < 0 || *dev >= kMaxDev)
+        return cudaErrorInvalidDevice;
+    return room_of(*dev, current_context_id(), sms, room);
+}
+
+cudaError_t fp8_status_word(int sms, uint32_t **p)
+{
+    int dev = 0;
+    const Fp8Room *room = nullptr;
+    const cudaError_t e = current_room(sms, &dev, &room);
+    if (e == cudaSuccess)
+        *p = room->status;
+    return e;
+}
+
 cudaError_t launch_fp8_gemm(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, int sms, cudaStream_t stream)
 {
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev)
-        return cudaErrorInvalidDevice;
-    const unsigned long long ctx = current_context_id();
     const Fp8Room *room = nullptr;
-    if (cudaError_t e = room_of(dev, ctx, sms, &room); e != cudaSuccess)
+    if (cudaError_t e = current_room(sms, &dev, &room); e != cudaSuccess)
         return e;
     const bool fuse = fp8_rounds_rows(g.E, g.M, g.N, g.K, g.bwd && g.gated);
     const Fp8Shape sh = pick(g, fuse, *room);

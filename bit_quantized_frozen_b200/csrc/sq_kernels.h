@@ -169,11 +169,13 @@ struct Fp8GemmLaunch {
     void *y;                    // [M, N] (backward [M, K]) fp32 or bf16
     uint16_t *g_out, *u_out;    // gated forward: [M, N] bf16, or NULL
     int out_bf16;
-    uint32_t *status;           // NULL (few rows): the library's own word
+    uint32_t *status;
 };
 cudaError_t launch_fp8_gemm(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, int sms, cudaStream_t stream);
 // whether that kernel rounds the rows itself (few rows: launch_fp8_quant is not called)
 bool fp8_rounds_rows(int E, int64_t M, int64_t N, int64_t K, bool gated_bwd);
+// library_status_word() from what these products keep of the device
+cudaError_t fp8_status_word(int sms, uint32_t **p);
 
 // ID of the current CUDA context (unique for the life of the process; a context created
 // after cudaDeviceReset gets a new one), 0 if it cannot be read.  Per-device caches of

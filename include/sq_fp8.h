@@ -25,9 +25,13 @@
  *
  * Few rows are rounded by the product itself: M <= 16, and M <= 32 where N K <= 2^24
  * or E > 1 (the gradient of a gated pair: M <= 8 and 16).  Such a call needs no
- * workspace: its size is 0 and ws may be NULL; the status word is then the library's
- * own (sq_check_device_status(NULL, stream)), to which calls only add.  A workspace
- * given all the same holds at least 256 bytes.
+ * workspace: its size is 0 and ws may be NULL.  A workspace given all the same holds at
+ * least 256 bytes.
+ *
+ * The status of a call is the first word of its workspace, as in sq.h.  Without a
+ * workspace, or with SQ_STATUS_LIBRARY, it is the library's own word on the device
+ * (sq_check_device_status(NULL, stream)), to which calls only add: what the calls on
+ * all streams have found since it was last read.
  */
 #ifndef SQ_FP8_H
 #define SQ_FP8_H
@@ -51,8 +55,11 @@ extern "C" {
 #define SQ_OP_GROUPED_GATED_FWD_FP8    21
 #define SQ_OP_GROUPED_GATED_BWD_DX_FP8 22
 
-/* a flag beside those of sq.h and sq_w8a8.h */
+/* flags beside those of sq.h and sq_w8a8.h */
 #define SQ_IN_BF16             0x40u /* sq_build_fp8: W is bf16 instead of fp32 */
+#define SQ_STATUS_LIBRARY      0x100u /* the products: report to the library's status word,
+                                         not to the workspace's (which may be gone when
+                                         somebody asks) */
 
 /* activations of the gated projections */
 #define SQ_ACT_SILU            0     /* g / (1 + e^-g) */
@@ -69,7 +76,7 @@ SQ_API sq_status sq_build_fp8(const void *W, int64_t N, int64_t K, uint32_t flag
 /*
  * y [M, N] = x W^T, x [M, K] bf16; y fp32, or bf16 with SQ_OUT_BF16 (one more
  * rounding).  M >= 1.  flags: SQ_OUT_BF16, SQ_CHECK_FINITE (a NaN or an infinity in x
- * sets SQ_ERR_NONFINITE in the status word).
+ * sets SQ_ERR_NONFINITE in the status word), SQ_STATUS_LIBRARY.
  * ws: sq_workspace_bytes(SQ_OP_LINEAR_FWD_FP8, M, N, K) bytes.
  */
 SQ_API sq_status sq_linear_fwd_fp8(const sq_weight *w, const uint16_t *x, int64_t M, void *y, uint32_t flags,
