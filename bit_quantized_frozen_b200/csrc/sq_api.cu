@@ -77,6 +77,14 @@ static __global__ void selftest_wait_kernel(uint32_t *status, unsigned long long
         (void)sq::mbar_wait(sq::smem_u32(&bar), 0u, &abort_flag, status, limit_ns);
 }
 
+// Reads and clears the library's status word at once: what a call on another stream adds is in this
+// report or stays for the next one.
+static __device__ uint32_t g_taken_status;
+static __global__ void take_status_kernel(uint32_t *word)
+{
+    g_taken_status = atomicExch(word, 0u);
+}
+
 namespace {
 
 constexpr int kMaxDevices = 64;
@@ -1141,27 +1149,37 @@ sq_status sq_selftest_index_check(void *ws, void *stream)
 
 sq_status sq_check_device_status(void *ws, void *stream)
 {
-    if (!ws) {                                         // the library's own word (calls without a workspace)
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    uint32_t word = 0;
+    if (!ws) {                                         // the library's own word
         int sms = 0;
         sq_status st = check_device(&sms);
         if (st != SQ_OK)
             return st;
-        uint32_t *word = nullptr;
-        SQ_CUDA(sq::library_status_word(&word), "status symbol");
-        ws = word;
-    } else if (!aligned(ws, 256)) {
-        return SQ_ERR_ALIGN;
+        uint32_t *from = nullptr, *taken = nullptr;
+        SQ_CUDA(sq::library_status_word(&from), "status symbol");
+        SQ_CUDA(cudaGetSymbolAddress(reinterpret_cast<void **>(&taken), g_taken_status), "status symbol");
+        static std::mutex one_at_a_time;               // (g_taken_status)
+        std::lock_guard<std::mutex> hold(one_at_a_time);
+        take_status_kernel<<<1, 1, 0, s>>>(from);
+        SQ_CUDA(cudaGetLastError(), "status read");
+        SQ_CUDA(cudaMemcpyAsync(&word, taken, 4, cudaMemcpyDeviceToHost, s), "status read");
+        SQ_CUDA(cudaStreamSynchronize(s), "status sync");
+    } else {
+        if (!aligned(ws, 256))
+            return SQ_ERR_ALIGN;
+        SQ_CUDA(cudaMemcpyAsync(&word, ws, 4, cudaMemcpyDeviceToHost, s), "status read");
+        SQ_CUDA(cudaStreamSynchronize(s), "status sync");
+        if (word != 0)
+            SQ_CUDA(cudaMemsetAsync(ws, 0, 4, s), "status clear");
     }
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    uint32_t word = 0;
-    SQ_CUDA(cudaMemcpyAsync(&word, ws, 4, cudaMemcpyDeviceToHost, s), "status read");
-    SQ_CUDA(cudaStreamSynchronize(s), "status sync");
-    if (word != 0) {
-        SQ_CUDA(cudaMemsetAsync(ws, 0, 4, s), "status clear");
-        // bit 0 timeout, bit 2 failed index check, bit 1 non-finite input
-        return (word & 1u) ? SQ_ERR_TIMEOUT : (word & sq::kStatusIndex) ? SQ_ERR_INDEX : SQ_ERR_NONFINITE;
-    }
-    return SQ_OK;
+    if (word == 0)
+        return SQ_OK;
+    snprintf(g_detail, sizeof(g_detail), "status word:%s%s%s", (word & sq::kStatusTimeout) ? " timeout" : "",
+             (word & sq::kStatusIndex) ? " index" : "", (word & sq::kStatusNonfinite) ? " non-finite" : "");
+    return (word & sq::kStatusTimeout) ? SQ_ERR_TIMEOUT
+           : (word & sq::kStatusIndex) ? SQ_ERR_INDEX
+                                       : SQ_ERR_NONFINITE;
 }
 
 }  // extern "C"

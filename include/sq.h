@@ -402,12 +402,14 @@ SQ_API sq_status sq_set_stage_events(int32_t stage, void *start_event, void *sto
 /*
  * Read back and clear the device status word that a kernel sets when it gives
  * up a bounded wait (SQ_ERR_TIMEOUT), or that the SQ_CHECK_FINITE scan sets
- * on a NaN or an infinity in x (SQ_ERR_NONFINITE; a timeout is reported
- * first); ws is the workspace of the sq_linear_fwd
+ * on a NaN or an infinity in x (SQ_ERR_NONFINITE).  Where it holds several findings a
+ * timeout is returned first, then a failed index check; sq_last_error_detail() names
+ * all of them.  ws is the workspace of the sq_linear_fwd
  * call to check (each such call clears the word when it starts).  With ws ==
  * NULL it reads the library's own word on the current device, which the calls
- * without a workspace (sq_reconstruct_bf16) set instead.  This call
- * synchronises `stream` and copies 4 bytes to the host.
+ * without a workspace (sq_reconstruct_bf16) set instead; it is read and cleared at
+ * once, so that what a call on any stream finds meanwhile is in this report or the
+ * next.  This call synchronises `stream` and copies 4 bytes to the host.
  */
 SQ_API sq_status sq_check_device_status(void *ws, void *stream);
 

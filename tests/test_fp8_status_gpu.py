@@ -1,4 +1,7 @@
 """Where the block-scaled products report what they found on the device."""
+import threading
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -72,3 +75,75 @@ def test_clamped_offsets_are_reported_without_a_workspace(M):
             call(1.0)
             assert status() == INDEX, name
             assert status() == sq.SQ_OK, name
+
+
+def test_no_report_is_lost_between_streams():
+    """One thread asks all the time and another one's calls find NaN all the time, each on a stream of its own: the
+    offsets that a call on a third stream clamps are in a report all the same."""
+    rng = np.random.default_rng(1)
+    w, bad = weight(*layer(rng, N, K, E)), torch.full((4, K), float("nan"), dtype=BF, device="cuda")
+    fine, off = torch.zeros_like(bad), dev(np.array([0, 1, 2, 4], np.int32))
+    wrong = dev(np.array([0, 2, 1, 4], np.int32))
+    assert status() == sq.SQ_OK
+    done, asked, found = threading.Event(), [0], [0]
+
+    def ask():
+        stream = torch.cuda.Stream()
+        while not done.is_set():
+            try:
+                sq.sq_check_device_status(None, stream=stream)
+            except sq.SqError as e:
+                found[0] += e.status == INDEX
+            asked[0] += 1
+
+    sq.grouped_fwd_fp8(w, bad, off, flags=sq.SQ_CHECK_FINITE)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(200):
+            sq.grouped_fwd_fp8(w, bad, off, flags=sq.SQ_CHECK_FINITE)
+
+    def find():
+        with torch.cuda.stream(torch.cuda.Stream()):
+            while not done.is_set():
+                graph.replay()
+                torch.cuda.current_stream().synchronize()
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=f) for f in (ask, find)]
+    for t in threads:
+        t.start()
+    lost = []
+    stream = torch.cuda.Stream()
+    try:
+        for i in range(400):
+            before, wait = found[0], time.perf_counter() + rng.uniform(0, 1e-4)
+            while time.perf_counter() < wait:
+                pass
+            sq.grouped_fwd_fp8(w, fine, wrong, stream=stream)
+            stream.synchronize()
+            n, until = asked[0], time.monotonic() + 20
+            while asked[0] < n + 2 and time.monotonic() < until:      # (one that began after the call)
+                time.sleep(0)
+            assert asked[0] >= n + 2, "nobody asks"
+            # (two of the call's CTAs may find it, and a report lie between them)
+            if found[0] == before:
+                lost.append(i)
+    finally:
+        done.set()
+        for t in threads:
+            t.join()
+    assert not lost, lost
+    status()
+
+
+def test_a_report_names_all_findings():
+    rng = np.random.default_rng(2)
+    w, bad = weight(*layer(rng, N, K, E)), torch.full((4, K), float("nan"), dtype=BF, device="cuda")
+    off = torch.tensor([0, 2, 1, 4], dtype=torch.int32, device="cuda")
+    for ws in (None, torch.zeros(256, dtype=torch.uint8, device="cuda")):
+        sq.grouped_fwd_fp8(w, bad, off, ws=ws, flags=sq.SQ_CHECK_FINITE)
+        with pytest.raises(sq.SqError, match="index non-finite") as e:
+            sq.sq_check_device_status(ws)
+        assert e.value.status == INDEX
+        assert status(ws) == sq.SQ_OK
