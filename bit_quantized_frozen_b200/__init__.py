@@ -469,14 +469,21 @@ def sq_grouped_workspace_bytes(op: int, E: int, M: int, N: int, K: int) -> int:
     return lib().sq_grouped_workspace_bytes(op, E, M, N, K)
 
 
-_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+# (None in a PyTorch that lacks them, e8m0 before 2.7: the block-scaled calls refuse, the others do not need them)
+_E4M3, _E8M0 = getattr(torch, "float8_e4m3fn", None), getattr(torch, "float8_e8m0fnu", None)
 _FP8 = {}                                # _fp8_entry's
 _byref = ctypes.byref
 _FP8_ACTS = {"silu": SQ_ACT_SILU, "gelu": SQ_ACT_GELU_TANH}
 
 
+def _need_float8(fn):
+    if _E4M3 is None or _E8M0 is None:
+        raise RuntimeError(f"{fn}: needs a PyTorch with float8_e4m3fn and float8_e8m0fnu, this is {torch.__version__}")
+
+
 def _fp8_refuse(fn, weights, rows, outs, offsets, flags, ws):
     """Names what is wrong with the arguments of a block-scaled call (returns if nothing is)."""
+    _need_float8(fn)
     w, x = weights[0], rows[0]
     N, K, E = w.N, w.K, getattr(w, "E", None)
     back, gated = "bwd" in fn, len(weights) == 2
@@ -899,6 +906,7 @@ def grouped_bwd_dx_w8a8(w: GroupedWeight, dy: torch.Tensor, offsets: torch.Tenso
 
 def build_fp8(W: torch.Tensor, stream=None) -> Weight:
     """Block-scaled e4m3 weight of W [N, K] (fp32 or bf16); N and K multiples of 16."""
+    _need_float8("build_fp8")
     N, K = W.shape
     with _allocating_on(stream):
         codes = torch.empty((N, K), dtype=_E4M3, device=W.device)
@@ -909,6 +917,7 @@ def build_fp8(W: torch.Tensor, stream=None) -> Weight:
 
 def build_fp8_grouped(W: torch.Tensor, stream=None) -> GroupedWeight:
     """Block-scaled e4m3 weights of E experts from W [E, N, K] (fp32 or bf16)."""
+    _need_float8("build_fp8_grouped")
     E, N, K = W.shape
     with _allocating_on(stream):
         codes = torch.empty((E, N, K), dtype=_E4M3, device=W.device)
