@@ -610,7 +610,7 @@ def _fp8_outs_fit(outs, shape, flags, ws, dev):
 
 
 def _fp8_act(fn, act):
-    code = _FP8_ACTS.get(act)
+    code = _FP8_ACTS.get(act) if isinstance(act, str) else None
     if code is None:
         raise ValueError(f"{fn}: act must be one of {sorted(_FP8_ACTS)}, got {act!r}")
     return code
@@ -953,7 +953,7 @@ def _fp8_out_here(fn, op, weights, rows, offsets, act, save, ws, flags, out_bf16
             ws = x.new_empty(n, dtype=torch.uint8)
             flags |= SQ_STATUS_LIBRARY
     outs = (y,)
-    if act is not None:
+    if len(weights) == 2:
         act = _fp8_act(fn, act)
         if op & 1:
             outs = (y, x.new_empty(M, width), x.new_empty(M, width)) if save else (y, None, None)

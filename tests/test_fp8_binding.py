@@ -3,6 +3,12 @@ import os
 import subprocess
 import sys
 
+import pytest
+import torch
+
+import bit_quantized_frozen_b200 as sq
+from test_fp8 import OFF, E, K, M, N, raw, t, weight
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 OLD_TORCH = r'''
@@ -39,3 +45,16 @@ def test_a_torch_without_the_8_bit_types():
     for names in (["float8_e8m0fnu"], ["float8_e4m3fn", "float8_e8m0fnu"]):
         r = subprocess.run([sys.executable, "-c", OLD_TORCH, ROOT, *names], capture_output=True, text=True, timeout=600)
         assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("act", [None, 0, "relu", ["silu"]])
+def test_activations_are_refused_by_name(act):
+    w, e, x, dy = weight(), weight(E), t((M, K)), t((M, N))
+    for f in (lambda: sq.gated_fwd_fp8(w, w, x, act=act), lambda: sq.gated_fwd_fp8(w, w, x, act=act, save=True),
+              lambda: sq.gated_bwd_dx_fp8(w, w, dy, dy, dy, act=act),
+              lambda: sq.grouped_gated_fwd_fp8(e, e, x, OFF, act=act, save=True),
+              lambda: sq.grouped_gated_bwd_dx_fp8(e, e, dy, dy, dy, OFF, act=act),
+              lambda: raw("sq_gated_fwd_fp8", w, x, t((M, N), torch.float32), act=act),
+              lambda: raw("sq_grouped_gated_bwd_dx_fp8", e, dy, t((M, K), torch.float32), act=act)):
+        with pytest.raises(ValueError, match="act must be one of"):
+            f()
