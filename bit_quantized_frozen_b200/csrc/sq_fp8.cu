@@ -695,6 +695,9 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
     } else if (warp == kIssuer) {
         // ------------------------------------------------------------ MMA issuer (leader)
         if (leader) {
+            // (few rows: the kernel in front may be any, and longer than a wait for the feeders may take)
+            if (FUSE && args.E == 0)
+                grid_dep_wait();
             const bool issue = one_lane();
             const uint32_t s0 = smem_u32(smem) + ring0;
             // the rows' and the weight's descriptors (backward: from 128 columns of the weight to the next 128 it
