@@ -106,14 +106,15 @@ def operands(op, M, N, K):
 
 
 # Two to five rounds of tiles of pairs, or just less than one; sums that bring buffers of scales and stages round
-# again; last row tiles of 1 to 128 rows (the second CTA of the pair has none) and of more; odd widths.  The last of
-# each: one row tile and many columns, one CTA with tiles of 256 columns, more tiles than CTAs for few rows.
+# again; last row tiles of 1 to 128 rows (the second CTA of the pair has none) and of more; odd widths.  Then one row
+# tile and many columns, more tiles than CTAs for few rows, and (the last line) one-CTA tiles wider than 128 columns.
 DENSE = [("fwd", 2305, 8192, 4624), ("fwd", 2100, 4096, 2064), ("fwd", 777, 4240, 2832), ("fwd", 200, 9008, 2064),
          ("bwd_dx", 2305, 4624, 8192), ("bwd_dx", 2100, 2064, 8208), ("bwd_dx", 1300, 2064, 2832),
          ("bwd_dx", 140, 2064, 30000),
          ("gated_fwd", 1854, 3376, 4112), ("gated_fwd", 2100, 4096, 2064), ("gated_fwd", 250, 9232, 1040),
          ("gated_fwd", 8, 16384, 1552),
-         ("gated_bwd_dx", 2100, 2064, 4096), ("gated_bwd_dx", 1290, 3600, 4112), ("gated_bwd_dx", 300, 1040, 25616)]
+         ("gated_bwd_dx", 2100, 2064, 4096), ("gated_bwd_dx", 1290, 3600, 4112), ("gated_bwd_dx", 300, 1040, 25616),
+         ("fwd", 353, 6384, 992), ("bwd_dx", 798, 3296, 4992), ("gated_fwd", 278, 8624, 2176), ("gated_bwd_dx", 318, 3168, 10784)]
 
 
 @pytest.mark.parametrize("op,M,N,K", DENSE)
