@@ -66,6 +66,10 @@ constexpr int kFuseRows = 16;
 constexpr int kFMaxSplit = 8;
 constexpr int kFPartBytes = 24 * 1024;            // FUSE: places for the other CTAs' sums
 constexpr int kFUpRow = 64;                       // FUSE, gated: lane of the up projection's first channel
+// An fp32 result's sum takes at most so many groups of a CTA's accumulator at a time: each tensor-core step of 32
+// products cuts the sum that it adds to towards zero, and the loss grows faster than the length.  Relative to the result's
+// size it is 5e-7 for 6144 values, 2e-6 for 16384, 5e-6 for 32768; it was 3e-5 for 2^17 and 4e-4 for 2^20.
+constexpr int kSumGroups = 64;
 constexpr int kPrefetchBytes = 64 * 1024;         // of weight into L2 before the kernel in front has ended, each CTA
 
 template <int CG, int MODE, bool FUSE>
@@ -118,6 +122,7 @@ struct Fp8Args {
     int prefetch;             // FUSE: chunks of a tile fetched into L2 before the kernel in front has ended
     int split;                // CTAs of a cluster that share a tile (CG = 1)
     int slot1;                // column of the second accumulator
+    int lo, hi;               // groups of the sum that this launch takes
 };
 
 template <int CG>
@@ -150,10 +155,16 @@ struct Fp8Patch {
     int lane, turn;
 };
 
+__device__ __forceinline__ uint32_t sum_bits(uint32_t a, uint32_t b)
+{
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+}
+
 // One warp's 32 rows x 64 bytes to y through its patch: by TMA (map, box of 64 bytes x 32 rows at x, y),
 // or where not all of them exist (map NULL) row by row, so that a row's 64 bytes leave in one run.
-// dst: row 0's first byte; the first `rows` rows and `bytes` bytes (a multiple of 16) of each exist.
-template <int PATCHES>
+// dst: row 0's first byte; the first `rows` rows and `bytes` bytes (a multiple of 16) of each exist.  ADDS (map
+// NULL): fp32 values, added to what is there.
+template <int PATCHES, bool ADDS>
 __device__ __forceinline__ void store_rows64(const uint32_t (&v)[16], Fp8Patch &out, const CUtensorMap *map, int x,
                                              int y, uint8_t *dst, int64_t row_bytes, int rows, int bytes)
 {
@@ -181,9 +192,15 @@ __device__ __forceinline__ void store_rows64(const uint32_t (&v)[16], Fp8Patch &
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = 8 * i + (lane >> 2), p = lane & 3;
-            const uint4 w = *reinterpret_cast<const uint4 *>(patch + row * 64 + ((p ^ ((row >> 1) & 3)) << 4));
-            if (row < rows && 16 * p < bytes)
-                *reinterpret_cast<uint4 *>(dst + row * row_bytes + 16 * p) = w;
+            uint4 w = *reinterpret_cast<const uint4 *>(patch + row * 64 + ((p ^ ((row >> 1) & 3)) << 4));
+            if (row < rows && 16 * p < bytes) {
+                uint4 *to = reinterpret_cast<uint4 *>(dst + row * row_bytes + 16 * p);
+                if constexpr (ADDS) {
+                    const uint4 o = *to;
+                    w = make_uint4(sum_bits(w.x, o.x), sum_bits(w.y, o.y), sum_bits(w.z, o.z), sum_bits(w.w, o.w));
+                }
+                *to = w;
+            }
         }
         __syncwarp();
     }
@@ -193,7 +210,7 @@ __device__ __forceinline__ void store_rows64(const uint32_t (&v)[16], Fp8Patch &
 
 // 32 neighbouring columns of y from fp32 values, as bf16 or fp32, through the patch; the first `cols` of them
 // and `rows` rows exist.
-template <int PATCHES>
+template <int PATCHES, bool ADDS>
 __device__ __forceinline__ void store_cols(const float (&o)[32], Fp8Patch &out, const CUtensorMap *map, void *y,
                                            int64_t row, int64_t col, int64_t width, int rows, int cols, bool bf16)
 {
@@ -203,14 +220,15 @@ __device__ __forceinline__ void store_cols(const float (&o)[32], Fp8Patch &out, 
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             v[i] = f32x2_to_bf16x2_bits(o[2 * i], o[2 * i + 1]);
-        store_rows64<PATCHES>(v, out, map, (int)col, (int)row, dst, 2 * width, rows, 2 * cols);
+        store_rows64<PATCHES, false>(v, out, map, (int)col, (int)row, dst, 2 * width, rows, 2 * cols);
     } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 v[i] = __float_as_uint(o[16 * h + i]);
-            store_rows64<PATCHES>(v, out, map, (int)col + 16 * h, (int)row, dst + 64 * h, 4 * width, rows, 4 * (cols - 16 * h));
+            store_rows64<PATCHES, ADDS>(v, out, map, (int)col + 16 * h, (int)row, dst + 64 * h, 4 * width, rows,
+                                        4 * (cols - 16 * h));
         }
     }
 }
@@ -228,7 +246,8 @@ struct Fp8Walk {
     }
 };
 
-template <int CG, int MODE, bool FUSE>
+// ADDS: fp32 results, added to what y holds
+template <int CG, int MODE, bool FUSE, bool ADDS>
 __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
     sq_fp8_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmX32,
                   const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmW2,
@@ -238,6 +257,7 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
     using Cfg = Fp8Cfg<CG, MODE, FUSE>;
     constexpr bool BWD = MODE == kFp8Bwd, GATED = MODE == kFp8Gated;
     static_assert(!FUSE || CG == 1, "few rows take tiles of one CTA");
+    static_assert(!ADDS || !GATED, "the activation needs the whole sums");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *rest = smem + Cfg::kRing;
@@ -347,8 +367,9 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
     Fp8Walk walk;
     walk.blocks = args.blocks;
     walk.groups = (args.blocks + kFp8Group - 1) / kFp8Group;
-    walk.lo = walk.groups * args.halves * part / split;
-    walk.hi = walk.groups * args.halves * (part + 1) / split;
+    const int first = GATED ? 0 : args.lo, many = GATED ? walk.groups * args.halves : args.hi - args.lo;
+    walk.lo = first + many * part / split;
+    walk.hi = first + many * (part + 1) / split;
 
     if (producer) {
         // ------------------------------------------------------------ producers (every CTA)
@@ -840,9 +861,9 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
                 } else {
                     float *dst = reinterpret_cast<float *>(to) + at + i * args.width;
                     if (i < rows)
-                        dst[0] = v[i];
+                        dst[0] = ADDS ? dst[0] + v[i] : v[i];
                     if (i + 1 < rows)
-                        dst[args.width] = v[i + 1];
+                        dst[args.width] = ADDS ? dst[args.width] + v[i + 1] : v[i + 1];
                 }
             }
         };
@@ -996,9 +1017,9 @@ __global__ void __launch_bounds__(Fp8Cfg<CG, MODE, FUSE>::kThreads, 1)
             if (live <= 0 || !SQ_DCHECK(rows <= 0 || (row + rows <= args.M && col + live <= args.width), args.status))
                 return;
             // all 32 rows and C columns are the tile's, or lie behind the matrix's end
-            const bool whole = (rows == 32 || args.E == 0) && (live == C || col + live == args.width);
+            const bool whole = !ADDS && (rows == 32 || args.E == 0) && (live == C || col + live == args.width);
             auto put_out = [&](const float (&o)[C], const CUtensorMap &m, void *to, bool bf16) {
-                store_cols<Cfg::kPatches>(o, out, whole ? &m : nullptr, to, row, col, args.width, rows, live, bf16);
+                store_cols<Cfg::kPatches, ADDS>(o, out, whole ? &m : nullptr, to, row, col, args.width, rows, live, bf16);
             };
             if constexpr (GATED) {
                 if (args.g_out) {
@@ -1248,13 +1269,13 @@ bool out_map(CUtensorMap *m, const void *base, int64_t width, int64_t rows, bool
               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int CG, int MODE, bool FUSE>
+template <int CG, int MODE, bool FUSE, bool ADDS>
 cudaError_t allow_smem(int dev, unsigned long long ctx)
 {
     static unsigned long long seen[kMaxDev];
     if (ctx != 0 && seen[dev] == ctx)
         return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(sq_fp8_kernel<CG, MODE, FUSE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(sq_fp8_kernel<CG, MODE, FUSE, ADDS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                Fp8Cfg<CG, MODE, FUSE>::kSmemBytes);
     if (e == cudaSuccess)
         seen[dev] = ctx;
@@ -1275,7 +1296,7 @@ int resident_clusters(int size, int sms)
     o.attrs = at;
     o.numAttrs = 1;
     int n = 0;
-    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, sq_fp8_kernel<CG, MODE, false>, &o);
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, sq_fp8_kernel<CG, MODE, false, false>, &o);
     (void)cudaGetLastError();
     return e == cudaSuccess && n > 0 && n < sms / size ? n : sms / size;
 }
@@ -1285,9 +1306,9 @@ cudaError_t room_of(int dev, unsigned long long ctx, int sms, const Fp8Room **ou
     static Fp8Room rooms[kMaxDev];
     Fp8Room &r = rooms[dev];
     if (ctx == 0 || r.ctx != ctx) {
-        cudaError_t e = allow_smem<2, kFp8Fwd, false>(dev, ctx);
+        cudaError_t e = allow_smem<2, kFp8Fwd, false, false>(dev, ctx);
         if (e == cudaSuccess)
-            e = allow_smem<1, kFp8Fwd, false>(dev, ctx);
+            e = allow_smem<1, kFp8Fwd, false, false>(dev, ctx);
         if (e == cudaSuccess)
             e = library_status_word(&r.status);
         if (e != cudaSuccess)
@@ -1306,9 +1327,10 @@ template <int CG, int MODE, bool FUSE>
 cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8Shape &sh, int dev, const Fp8Room &room,
                        cudaStream_t stream)
 {
+    static_assert(kSumGroups >= kFMaxSplit, "every CTA of a cluster has a group");
     using Cfg = Fp8Cfg<CG, MODE, FUSE>;
     constexpr bool BWD = MODE == kFp8Bwd, GATED = MODE == kFp8Gated;
-    if (cudaError_t e = allow_smem<CG, MODE, FUSE>(dev, room.ctx); e != cudaSuccess)
+    if (cudaError_t e = allow_smem<CG, MODE, FUSE, false>(dev, room.ctx); e != cudaSuccess)
         return e;
     const int tile = sh.tile;
     const int64_t Em = g.E > 0 ? g.E : 1;
@@ -1396,7 +1418,29 @@ cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8S
     cfg.stream = stream;
     cfg.attrs = at;
     cfg.numAttrs = CG * sh.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, sq_fp8_kernel<CG, MODE, FUSE>, tmX, tmX32, tmW, tmW2, tmY, tmG, tmU, a);
+    // Long sums of fp32 results: a launch for each part, which adds to the ones before (the gated forward needs both
+    // sums whole; a bf16 result's own rounding is larger than what is lost).  Each waits for the one in front before it
+    // touches y.
+    const int groups = (int)fp8_groups(summed) * halves;
+    const int most_groups = kSumGroups * sh.split;
+    const int parts = GATED || g.out_bf16 ? 1 : (groups + most_groups - 1) / most_groups;
+    for (int i = 0; i < parts; ++i) {
+        a.lo = (int)((int64_t)groups * i / parts);
+        a.hi = (int)((int64_t)groups * (i + 1) / parts);
+        cudaError_t e = cudaSuccess;
+        if (i == 0) {
+            e = cudaLaunchKernelEx(&cfg, sq_fp8_kernel<CG, MODE, FUSE, false>, tmX, tmX32, tmW, tmW2, tmY, tmG, tmU, a);
+        } else if constexpr (!GATED) {
+            a.keep_status = 1;
+            a.zero[0] = a.zero[1] = a.zero[2] = nullptr;
+            e = allow_smem<CG, MODE, FUSE, true>(dev, room.ctx);
+            if (e == cudaSuccess)
+                e = cudaLaunchKernelEx(&cfg, sq_fp8_kernel<CG, MODE, FUSE, true>, tmX, tmX32, tmW, tmW2, tmY, tmG, tmU, a);
+        }
+        if (e != cudaSuccess)
+            return e;
+    }
+    return cudaSuccess;
 }
 
 // How a call's tiles are cut: the candidate with the least time by a simple count of cycles.  A chunk

@@ -179,9 +179,9 @@ def test_these_sizes_run_on_pairs():
     if not any(names):
         pytest.skip("the profiler records no kernels here")
     flat = [n for s in names for n in s]
-    for want in ("<2,0,0>", "<2,1,0>", "<2,2,0>"):
+    for want in ("<2,0,0", "<2,1,0", "<2,2,0"):
         assert sum(want in n for n in flat) >= 3, (want, flat)
-    assert all("<2,0,0>" in n for s in names[-2:] for n in s), names[-2:]
+    assert all("<2,0,0" in n for s in names[-2:] for n in s), names[-2:]
 
 
 DEBUG = r'''
