@@ -27,7 +27,10 @@
 // CTA (CG = 1, tiles of 128 tokens x up to 224 columns, backward 256) or CTA pair (CG = 2, 256 x up to
 // 256), one CTA per SM, persistent: 8 epilogue warps (few rows: 4), TMA producers, feeders (few rows: two
 // sets), and an issuer that also allocates tensor memory.  Outputs leave by TMA where a warp's 32 rows
-// are all the tile's.
+// are all the tile's.  Gated forwards are at the limit of 128 registers a thread, by which the
+// pair's spills 24 bytes (its epilogue holds 32 columns of both sums).
+//
+// Accuracy: see kSumGroups.
 //
 // Few tiles (CG = 1): a cluster of CTAs shares a tile, each with some of the groups, and joins the
 // partial sums over distributed shared memory, in the order of the CTAs' ranks.
@@ -66,9 +69,11 @@ constexpr int kFuseRows = 16;
 constexpr int kFMaxSplit = 8;
 constexpr int kFPartBytes = 24 * 1024;            // FUSE: places for the other CTAs' sums
 constexpr int kFUpRow = 64;                       // FUSE, gated: lane of the up projection's first channel
-// An fp32 result's sum takes at most so many groups of a CTA's accumulator at a time: each tensor-core step of 32
-// products cuts the sum that it adds to towards zero, and the loss grows faster than the length.  Relative to the result's
-// size it is 5e-7 for 6144 values, 2e-6 for 16384, 5e-6 for 32768; it was 3e-5 for 2^17 and 4e-4 for 2^20.
+// Accuracy: each tensor-core step of 32 products cuts the fp32 sum that it adds to towards zero, and the loss grows
+// faster than the length.  Relative to the result's size it is 1e-7 for 2048 values, 5e-7 for 6144, 2e-6 for 16384, 5e-6 for
+// 32768 (3e-5 for 2^17, 4e-4 for 2^20).  So a CTA's accumulator takes at most so many groups of an fp32 result's sum at a
+// time, and the parts, a launch each, are added to y.  (In tensor memory there is no room for a third accumulator
+// beside wide tiles.)  Gradient of 4480 x 131072 x 6144: 2.98 ms, in one part 2.91; 300 x 131072 x 4096: 0.48, 0.38.
 constexpr int kSumGroups = 64;
 constexpr int kPrefetchBytes = 64 * 1024;         // of weight into L2 before the kernel in front has ended, each CTA
 
@@ -1449,7 +1454,9 @@ cudaError_t launch_fp8(const Fp8GemmLaunch &g, const Fp8QuantArgs &q, const Fp8S
 // groups may be shared by a cluster where all tiles run at once, which costs some 8000 cycles (of clusters
 // larger than two, some room is left: the last one waited for SMs that other kernels still held, 262 x 1616 x
 // 14080 in 45 clusters of three of 45 that fit took 31.6 us, with 39 of them 24.1).  A pair's start takes 700
-// more.  Backward a CTA's columns start at 32-byte sectors (4480 x 16384 x 6144, pairs of 192, 224 and 256
+// more.  One-CTA tiles are wider than 128 columns too: of 22 dense calls that take such, 0.91 of the time with 128
+// (gradient of 301 x 11664 x 11040 58 us, 76; gated 278 x 8624 x 2176 20.5, 24.4; at worst gated 192 x 6272 x 304
+// 9.6, 9.4).  Backward a CTA's columns start at 32-byte sectors (4480 x 16384 x 6144, pairs of 192, 224 and 256
 // columns: 423, 450, 361 us).
 // Few rows: products of 128 channels whatever the tile has, 190 cycles and 2 a row of the operand; a group at
 // least as long as its rounding; 30 for each CTA, which all read the rows; 1200 and 200 a CTA for a shared

@@ -28,7 +28,8 @@ constexpr int kQuantThreads = 128;
 // first wait too.  Fewer CTAs have more registers each (92 instead of 56 hold a gated pair's operands without
 // spills) and end closer together: a call of 2049 rows, gated gradient, 8192 x 4096, takes 133.8, 132.5, 132.0,
 // 130.4, 131.3 us with 9, 7, 6, 5, 4 of them; 777 x 4240 x 2832, forward, 22.4, 21.0, 21.1, 21.1 us with 8, 6,
-// 5, 4; 4480 x 16384 x 6144 334, 334, 336, 337.
+// 5, 4; 4480 x 16384 x 6144 334, 334, 336, 337.  (The product's CTAs take 46 to 64 K of an SM's 64 K registers, one of
+// these 10 to 12 K: a product's CTA starts where at most one of them is left, a gated forward's where none is.)
 constexpr int quant_ctas(int gated)
 {
     return gated ? 5 : 6;

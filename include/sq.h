@@ -391,7 +391,8 @@ SQ_API sq_status sq_set_gemm_events(void *start_event, void *stop_event);
  * NVFP4 sq_linear_fwd), SQ_STAGE_ACT_QUANT the pass that quantises H x.  An
  * event between two launches keeps the second one from starting its set-up
  * early (the launches overlap otherwise), so a timed call is a little slower
- * than an untimed one.  Returns SQ_ERR_ARG for an unknown stage.
+ * than an untimed one.  A call without such a launch records nothing (few rows of the
+ * calls of sq_fp8.h are rounded by the product: SQ_STAGE_ACT_QUANT).  Returns SQ_ERR_ARG for an unknown stage.
  */
 #define SQ_STAGE_GEMM       0
 #define SQ_STAGE_ACT_PASS1  1

@@ -20,8 +20,12 @@
  *   s = the least power of two >= 2^-127 with max|r| <= 448 s,   code = e4m3(r / s),
  * r / s is exact, the conversion rounds to nearest even.  The products of codes and
  * scales are exact in the tensor cores and summed there in fp32 (a sum whose parts
- * pass fp32's range is infinite or NaN).  A row with a NaN or an infinity gives a row
- * of NaN; other rows are not affected.
+ * pass fp32's range is infinite or NaN).  Each step of 32 products cuts the sum that it
+ * adds to towards zero, by at most 2^-22 of the magnitudes summed so far: measured 5e-7 of
+ * a result's size for 6144 values, 2e-6 for 16384 and 5e-6 for 32768 and more; for bf16
+ * results and the gated forward 3e-5 for 2^17 and 4e-4 for 2^20.  Equal calls on equal
+ * devices give equal bits; a row among another number of rows may be summed in another
+ * order.  A row with a NaN or an infinity gives a row of NaN; other rows are not affected.
  *
  * Few rows are rounded by the product itself: M <= 16, and M <= 32 where N K <= 2^24
  * or E > 1 (the gradient of a gated pair: M <= 8 and 16).  Such a call needs no
